@@ -75,16 +75,19 @@ def step_min_bytes(p, n_ckpt: int) -> int:
 
 # The C entry points' host-side validation: no device or launch code.
 HOST_ONLY_SOURCES = ("gdn_api.hip",)
+# The softmax-attention layers' cache and attention: no part of the scan.
+OTHER_KERNELS = ("cache_", "attn_")
 
 
 def csrc_digest() -> str:
     """sha256 over the device and launch sources (names and bytes, sorted by
-    name): every file of csrc/ except the host-only validation of the entry
-    points, which changes no kernel and no launch."""
+    name) of the gated-delta-rule layer: every file of csrc/ except the
+    host-only validation of the entry points, which changes no kernel and no
+    launch, and the kernels of the attention layers."""
     import hashlib
     h = hashlib.sha256()
     for name in sorted(os.listdir(CSRC)):
-        if name in HOST_ONLY_SOURCES:
+        if name in HOST_ONLY_SOURCES or name.startswith(OTHER_KERNELS):
             continue
         h.update(name.encode())
         with open(os.path.join(CSRC, name), "rb") as f:

@@ -1,5 +1,6 @@
 """Python binding of libgdn (packed gated-delta-rule prefill, checkpoints,
-decode, short conv and checkpoint copy on MI355X / gfx950).
+decode, short conv and checkpoint copy, and the paged 8-bit key/value cache of
+the softmax-attention layers with the attention over it, on MI355X / gfx950).
 
 Argument marshalling only: every function here passes torch tensor data
 pointers, sizes and the current HIP stream to the C entry point of the same
@@ -25,16 +26,20 @@ __all__ = [
     "gdn_status_string", "gdn_plan_checkpoints", "gdn_prefill_packed", "gdn_prefill_conv_packed",
     "gdn_decode_step", "gdn_decode_tokens",
     "gdn_conv1d_silu_packed", "gdn_snapshot_copy", "LIB_PATH", "EXPORTED",
+    "gdn_cache", "gdn_rope", "make_cache", "make_rope", "GDN_E4M3", "GDN_I8",
+    "gdn_plan_pages", "gdn_rope_append", "gdn_cache_gather", "gdn_attn_packed", "gdn_attn_decode",
+    "gdn_attn_decode_workspace",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgdn.so")
-GDN_BF16, GDN_F32 = 0, 1
+GDN_BF16, GDN_F32, GDN_E4M3, GDN_I8 = 0, 1, 2, 3
 GDN_QK_L2NORM = 1
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_UNSUPPORTED",
           4: "GDN_ERR_SEQLENS", 5: "GDN_ERR_CKPT", 6: "GDN_ERR_CAPACITY", 7: "GDN_ERR_HIP"}
 EXPORTED = ("gdn_status_string", "gdn_plan_checkpoints", "gdn_conv1d_silu_packed",
             "gdn_prefill_packed", "gdn_prefill_conv_packed", "gdn_decode_step",
-            "gdn_decode_tokens", "gdn_snapshot_copy")
+            "gdn_decode_tokens", "gdn_snapshot_copy", "gdn_plan_pages", "gdn_rope_append",
+            "gdn_cache_gather", "gdn_attn_packed", "gdn_attn_decode", "gdn_attn_decode_workspace")
 
 
 class GdnError(RuntimeError):
@@ -59,6 +64,56 @@ def make_shape(Hqk: int, Hv: int, dk: int, dv: int, chunk: int = 64, io_dtype: i
                q_tok_stride: int = 0, k_tok_stride: int = 0, v_tok_stride: int = 0) -> gdn_shape:
     return gdn_shape(Hqk, Hv, dk, dv, chunk, io_dtype, GDN_QK_L2NORM if l2norm else 0,
                      scale, l2_eps, 0, q_tok_stride, k_tok_stride, v_tok_stride)
+
+
+class gdn_cache(ctypes.Structure):
+    _fields_ = [
+        ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page", ctypes.c_int32),
+        ("code_dtype", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+    ]
+
+
+class gdn_rope(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("adjacent", ctypes.c_int32),
+        ("scale", ctypes.c_float), ("freq", ctypes.c_float * 128), ("axis", ctypes.c_uint8 * 128),
+    ]
+
+
+_CODES = {torch.float8_e4m3fn: GDN_E4M3, torch.int8: GDN_I8}
+
+
+def make_cache(k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
+               v_scale: torch.Tensor) -> gdn_cache:
+    """Handle of a paged cache: k [n_pages, Hkv, page, d] and v [n_pages, Hkv,
+    page/16, d, 16] of torch.float8_e4m3fn or torch.int8, scales [n_pages, Hkv]
+    fp32.  The handle keeps its tensors alive; nothing needs clearing."""
+    if k.dim() != 4 or k.dtype not in _CODES:
+        raise ValueError("k must be [n_pages, Hkv, page, d] of float8_e4m3fn or int8")
+    n, h, page, d = k.shape
+    if v.dtype != k.dtype or tuple(v.shape) != (n, h, page // 16, d, 16):
+        raise ValueError("v must be [n_pages, Hkv, page/16, d, 16] of k's dtype")
+    for t in (k_scale, v_scale):
+        if t.dtype != torch.float32 or tuple(t.shape) != (n, h):
+            raise ValueError("scales must be fp32 [n_pages, Hkv]")
+    c = gdn_cache(h, d, page, _CODES[k.dtype], n, 0, _buf(k, k.dtype), _buf(v, v.dtype),
+                  _buf(k_scale, torch.float32), _buf(v_scale, torch.float32))
+    c.tensors = (k, v, k_scale, v_scale)
+    return c
+
+
+def make_rope(freq: Sequence[float], axis: Optional[Sequence[int]] = None, n_axes: int = 1,
+              adjacent: bool = False, scale: float = 1.0) -> gdn_rope:
+    """Rotary plan: freq in radians per position of each of rot_dim / 2 pairs,
+    axis the position row (below n_axes) that turns each pair (default 0)."""
+    freq = [float(f) for f in freq]
+    axis = [0] * len(freq) if axis is None else [int(i) for i in axis]
+    if len(freq) > 128 or len(axis) != len(freq) or any(not 0 <= i < n_axes for i in axis):
+        raise ValueError("at most 128 pairs, each with an axis below n_axes")
+    return gdn_rope(2 * len(freq), n_axes, int(adjacent), scale, (ctypes.c_float * 128)(*freq),
+                    (ctypes.c_uint8 * 128)(*axis))
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -97,6 +152,22 @@ def load() -> ctypes.CDLL:
                                            _P, _P, _P, _I32, _P, _P]
     lib.gdn_snapshot_copy.restype = _I32
     lib.gdn_snapshot_copy.argtypes = [_P, _I32, _I64, _P, _I64, _P, _P, _P, _P, _P]
+    lib.gdn_plan_pages.restype = _I32
+    lib.gdn_plan_pages.argtypes = [_I32, _I32, _P, _P, _P, _P, _I32, _P, _P, _P, _I32, _P, _P, _I32,
+                                   _P, _P, _P]
+    lib.gdn_rope_append.restype = _I32
+    lib.gdn_rope_append.argtypes = [_P, _P, _I32, _P, _P, _I32, _I32, _P, _I64, _P, _I64, _P, _I64,
+                                    _P, _I64, _P, _P, _I64, _P]
+    lib.gdn_cache_gather.restype = _I32
+    lib.gdn_cache_gather.argtypes = [_P, _I32, _P, _P, _P, _P]
+    lib.gdn_attn_packed.restype = _I32
+    lib.gdn_attn_packed.argtypes = [_P, _I32, ctypes.c_float, _P, _P, _I32, _I32, _P, _P, _I32, _P,
+                                    _I64, _P, _P]
+    lib.gdn_attn_decode.restype = _I32
+    lib.gdn_attn_decode.argtypes = [_P, _I32, ctypes.c_float, _I32, _I32, _P, _P, _I32, _I32, _P,
+                                    _I64, _P, _P, _I64, _P]
+    lib.gdn_attn_decode_workspace.restype = _I32
+    lib.gdn_attn_decode_workspace.argtypes = [_P, _I32, _I32, _I32, _I32, _P]
     _lib = lib
     return lib
 
@@ -118,7 +189,41 @@ def _dev(t) -> Optional[int]:
     return t.data_ptr()
 
 
+def _buf(t: Optional[torch.Tensor], dtype: torch.dtype, what: str = "argument") -> Optional[int]:
+    """Device pointer of a dense tensor of one type on the current device."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return _here(t, what)
+
+
+def _here(t: torch.Tensor, what: str) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{what} is not on the GPU")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what} is not on the current device")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, rows: int, heads: Optional[int], d: int, what: str):
+    """Pointer, token stride and head count of bf16 rows [>= rows, heads, d]
+    whose heads are dense (columns of a wider row will do)."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{what} must be torch.bfloat16, got {t.dtype}")
+    sh, st = t.shape, t.stride()
+    if len(sh) != 3 or sh[2] != d or sh[0] < rows or (heads is not None and sh[1] != heads):
+        raise ValueError(f"{what} must be [{rows}, {'heads' if heads is None else heads}, {d}], got {tuple(sh)}")
+    if st[2] != 1 or (sh[1] > 1 and st[1] != d):
+        raise ValueError(f"{what}: the heads of a token must be dense")
+    return _here(t, what), (st[0] if sh[0] > 1 else sh[1] * d), sh[1]
+
+
 def _host_i32(a) -> Optional[np.ndarray]:
+    if type(a) is np.ndarray and a.dtype == np.int32 and a.flags.c_contiguous:
+        return a
     if a is None:
         return None
     if isinstance(a, torch.Tensor):
@@ -269,3 +374,119 @@ def gdn_snapshot_copy(ckpt_buf, n: int, bytes_each: int, dst_pool, dst_slot, dst
     _check(load().gdn_snapshot_copy(
         _dev(ckpt_buf), int(n), int(bytes_each), dst, int(pool_slots), _dev(dst_slot), _hp(sl_h),
         _event(wait_event), _stream(copy_stream), _record_target(done_event)), "gdn_snapshot_copy")
+
+
+def gdn_plan_pages(page: int, want_len, kv_len, kv_len_out, block_table, free_pages, free_count,
+                   free_count_out, cu_seqlens, slot_map, positions, status, stream=None) -> None:
+    """Block tables, the pack of new tokens and its slot map, from the lengths
+    that the requests hold (kv_len) and want; all on the device."""
+    i32 = torch.int32
+    n, (rows, max_pages) = want_len.numel(), block_table.shape
+    if (rows < n or kv_len.numel() < n or kv_len_out.numel() < n or status.numel() < n or
+            cu_seqlens.numel() < n + 1):
+        raise ValueError("a buffer is shorter than the requests")
+    if positions is not None and positions.numel() < slot_map.numel():
+        raise ValueError("positions is shorter than slot_map")
+    if free_count.numel() < 1 or free_count_out.numel() < 1:
+        raise ValueError("free_count is empty")
+    _check(load().gdn_plan_pages(
+        page, n, _buf(want_len, i32, "want_len"), _buf(kv_len, i32, "kv_len"),
+        _buf(kv_len_out, i32, "kv_len_out"), _buf(block_table, i32, "block_table"), max_pages,
+        _buf(free_pages, i32, "free_pages"), _buf(free_count, i32, "free_count"),
+        _buf(free_count_out, i32, "free_count_out"), free_pages.numel(),
+        _buf(cu_seqlens, i32, "cu_seqlens"), _buf(slot_map, torch.int64, "slot_map"),
+        slot_map.numel(), _buf(positions, i32, "positions"), _buf(status, i32, "status"),
+        _stream(stream)), "gdn_plan_pages")
+
+
+def gdn_rope_append(rope: gdn_rope, cache: gdn_cache, cu_seqlens, cu_seqlens_host, q, k, v, positions,
+                    slot_map, q_out, stream=None) -> None:
+    """q_out = rotated q; rotated k and v into their cache slots.  q, k, v are
+    [T, heads, d] bf16, views of one wider row if need be; positions [n_axes, T],
+    or [T] for every axis; q and q_out None: only the cache is written."""
+    cu_h = _host_i32(cu_seqlens_host)
+    n = len(cu_h) - 1
+    T, d, hkv = int(cu_h[-1]), cache.head_dim, cache.num_kv_heads
+    qp = qs = qo = qos = None
+    hq = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        qp, qs, hq = _rows(q, T, None, d, "q")
+        qo, qos, _ = _rows(q_out, T, hq, d, "q_out")
+    kp, ks, _ = _rows(k, T, hkv, d, "k")
+    vp, vs, _ = _rows(v, T, hkv, d, "v")
+    pos_stride = 0
+    if positions is not None:
+        if positions.shape[-1] < T or (positions.dim() == 2 and positions.shape[0] < rope.n_axes) or positions.dim() > 2:
+            raise ValueError("positions must be [T] or [n_axes, T]")
+        pos_stride = positions.shape[-1] if positions.dim() == 2 else 0
+    if slot_map.numel() < T or cu_seqlens.numel() < n + 1:
+        raise ValueError("slot_map or cu_seqlens is shorter than the pack")
+    _check(load().gdn_rope_append(
+        ctypes.addressof(rope), ctypes.addressof(cache), hq, _buf(cu_seqlens, torch.int32, "cu_seqlens"),
+        cu_h.ctypes.data, n, T, qp, qs or 0, kp, ks, vp, vs, _buf(positions, torch.int32, "positions"),
+        pos_stride, _buf(slot_map, torch.int64, "slot_map"), qo, qos or 0, _stream(stream)),
+        "gdn_rope_append")
+
+
+def gdn_cache_gather(cache: gdn_cache, slot_map, k_out=None, v_out=None, stream=None) -> None:
+    """k_out, v_out [T, Hkv, d] bf16: the values held at the T slots."""
+    T = slot_map.numel()
+    for t in (k_out, v_out):
+        if t is not None and tuple(t.shape) != (T, cache.num_kv_heads, cache.head_dim):
+            raise ValueError("outputs must be [T, Hkv, d]")
+    _check(load().gdn_cache_gather(
+        ctypes.addressof(cache), T, _buf(slot_map, torch.int64, "slot_map"),
+        _buf(k_out, torch.bfloat16, "k_out"), _buf(v_out, torch.bfloat16, "v_out"), _stream(stream)),
+        "gdn_cache_gather")
+
+
+def gdn_attn_packed(cache: gdn_cache, cu_seqlens, cu_seqlens_host, kv_len, block_table, q, out,
+                    scale: Optional[float] = None, stream=None) -> None:
+    """Causal attention of a pack's rows over the cache (which holds them);
+    scale defaults to d ** -0.5."""
+    cu_h = _host_i32(cu_seqlens_host)
+    n = len(cu_h) - 1
+    T, d = int(cu_h[-1]), cache.head_dim
+    qp, qs, hq = _rows(q, T, None, d, "q")
+    if tuple(out.shape[1:]) != (hq, d) or out.shape[0] < T:
+        raise ValueError("out must be [T, Hq, d]")
+    if kv_len.numel() < n or block_table.shape[0] < n or cu_seqlens.numel() < n + 1:
+        raise ValueError("kv_len, block_table or cu_seqlens is shorter than the prompts")
+    _check(load().gdn_attn_packed(
+        ctypes.addressof(cache), hq, d ** -0.5 if scale is None else scale,
+        _buf(cu_seqlens, torch.int32, "cu_seqlens"), cu_h.ctypes.data, n, T,
+        _buf(kv_len, torch.int32, "kv_len"), _buf(block_table, torch.int32, "block_table"),
+        block_table.shape[1], qp, qs, _buf(out, torch.bfloat16, "out"), _stream(stream)),
+        "gdn_attn_packed")
+
+
+def gdn_attn_decode_workspace(cache: gdn_cache, num_q_heads: int, batch: int, n_tok: int,
+                              max_kv_len: int) -> int:
+    """Bytes of workspace of gdn_attn_decode."""
+    n = ctypes.c_int64(0)
+    _check(load().gdn_attn_decode_workspace(ctypes.addressof(cache), num_q_heads, batch, n_tok,
+                                            max_kv_len, ctypes.byref(n)), "gdn_attn_decode_workspace")
+    return n.value
+
+
+def gdn_attn_decode(cache: gdn_cache, n_tok: int, kv_len, block_table, q, out,
+                    max_kv_len: Optional[int] = None, scale: Optional[float] = None, workspace=None,
+                    stream=None) -> None:
+    """Causal attention of n_tok rows per request (q [batch * n_tok, Hq, d])
+    over the cache.  workspace: a uint8 tensor of gdn_attn_decode_workspace()
+    bytes; max_kv_len: an upper bound of kv_len (default: the table's pages)."""
+    B, max_pages = kv_len.numel(), block_table.shape[1]
+    d = cache.head_dim
+    qp, qs, hq = _rows(q, B * n_tok, None, d, "q")
+    if tuple(out.shape[1:]) != (hq, d) or out.shape[0] < B * n_tok:
+        raise ValueError("out must be [batch * n_tok, Hq, d]")
+    if block_table.shape[0] < B:
+        raise ValueError("block_table is shorter than the batch")
+    _check(load().gdn_attn_decode(
+        ctypes.addressof(cache), hq, d ** -0.5 if scale is None else scale, B, n_tok,
+        _buf(kv_len, torch.int32, "kv_len"), _buf(block_table, torch.int32, "block_table"), max_pages,
+        min(max_pages * cache.page, 2**31 - 1) if max_kv_len is None else max_kv_len, qp, qs,
+        _buf(out, torch.bfloat16, "out"), _buf(workspace, torch.uint8, "workspace"),
+        0 if workspace is None else workspace.numel(), _stream(stream)), "gdn_attn_decode")

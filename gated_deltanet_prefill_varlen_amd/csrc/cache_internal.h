@@ -1,0 +1,88 @@
+// Internal interface between the C-ABI host layer and the launchers of the
+// paged 8-bit key/value cache and the attention over it.  Every struct here is
+// filled only after the host layer validated the call.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gdn {
+
+// The paged 8-bit key/value cache as the kernels see it.
+struct CacheRef {
+  int32_t Hkv, dim;
+  int32_t page_shift;      // log2 of the page's tokens
+  int32_t n_pages;
+  int32_t i8;              // codes are int8 (else e4m3)
+  uint8_t* k;              // [n_pages, Hkv, page, dim]
+  uint8_t* v;              // [n_pages, Hkv, page/16, dim, 16]
+  float* ks;               // [n_pages, Hkv]
+  float* vs;
+};
+
+struct PlanArgs {
+  int32_t page_shift, n_seqs, max_pages, n_pages, slot_cap;
+  const int32_t* want;
+  const int32_t* kv;
+  int32_t* kv_out;         // may equal kv
+  int32_t* table;          // [n_seqs, max_pages]
+  int32_t* free_pages;     // [n_pages]
+  const int32_t* free_count;
+  int32_t* free_count_out; // may equal free_count
+  int32_t* cu;             // [n_seqs + 1]
+  int64_t* slot;           // [slot_cap]
+  int32_t* pos;            // [slot_cap] or nullptr
+  int32_t* status;         // [n_seqs]
+};
+
+struct RopeRef {
+  int32_t rot, n_axes, adjacent;
+  float scale;
+  float freq[128];
+  uint8_t axis[128];
+};
+
+struct AppendArgs {
+  RopeRef rope;
+  CacheRef c;
+  int32_t Hq, n_seqs, n_tokens;
+  const int32_t* cu;
+  const uint16_t* q;       // [T, Hq, d] or nullptr
+  const uint16_t* k;       // [T, Hkv, d]
+  const uint16_t* v;
+  uint16_t* q_out;
+  int64_t q_stride, k_stride, v_stride, qo_stride;
+  const int32_t* pos;      // axis a of token t at a * pos_stride + t
+  int64_t pos_stride;
+  const int64_t* slot;     // [T]
+};
+
+struct GatherArgs {
+  CacheRef c;
+  int32_t n_tokens;
+  const int64_t* slot;
+  uint16_t* k_out;         // [T, Hkv, d] or nullptr
+  uint16_t* v_out;
+};
+
+struct AttnArgs {
+  CacheRef c;
+  int32_t Hq, n_seqs, n_tokens;
+  int32_t n_tok;           // rows per request (decode), 0 = rows by cu
+  float scale;
+  const int32_t* cu;
+  const int32_t* kv_len;   // [n_seqs]
+  const int32_t* table;    // [n_seqs, max_pages]
+  int32_t max_pages;
+  int32_t max_kv;          // lengths over it make NaN rows
+  const uint16_t* q;
+  int64_t q_stride;
+  uint16_t* out;           // [T, Hq, d]
+};
+
+hipError_t launch_plan_pages(const PlanArgs& a, hipStream_t stream);
+hipError_t launch_rope_append(const AppendArgs& a, hipStream_t stream);
+hipError_t launch_cache_gather(const GatherArgs& a, hipStream_t stream);
+hipError_t launch_attn(const AttnArgs& a, hipStream_t stream);
+
+}  // namespace gdn

@@ -1,0 +1,424 @@
+// Rotary positions with the cache's write, and the cache's read back.
+//
+// One launch rotates the queries and writes the keys and values.  A workgroup
+// of the write owns one (page, kv head) of one prompt, because the page's
+// scale depends on every token that this call puts there: it loads the page's
+// new keys and values once into registers, rotates the keys, takes both
+// maxima, settles the scales and stores the codes.  A query workgroup forms
+// the angles of its tokens once in LDS and turns every head with them.
+#include <algorithm>
+
+#include "cache_device.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+
+// cos and sin of position * freq.  In 64 bits the angle becomes turns, of
+// which the nearest quarter is taken off; what is left lies in [-pi/4, pi/4],
+// where the Taylor sums through x^9 and x^10 are exact to fp32 rounding
+// (next terms below 2e-9 and 2e-11).
+__device__ __forceinline__ void cos_sin(int pos, float freq, float scale, float* c, float* s) {
+  const double quarters = (double)pos * (double)freq * 0.63661977236758134308;   // 2 / pi
+  const double n = rint(quarters);
+  const float x = (float)((quarters - n) * 1.57079632679489661923);              // pi / 2
+  const float y = x * x;
+  float sn = fmaf(y, 2.7557319e-6f, -1.9841270e-4f);
+  sn = fmaf(y, sn, 8.3333333e-3f);
+  sn = fmaf(y, sn, -1.6666667e-1f);
+  sn = fmaf(x * y, sn, x);
+  float cs = fmaf(y, -2.7557319e-7f, 2.4801587e-5f);
+  cs = fmaf(y, cs, -1.3888889e-3f);
+  cs = fmaf(y, cs, 4.1666667e-2f);
+  cs = fmaf(y, cs, -0.5f);
+  cs = fmaf(y, cs, 1.f);
+  const int k = (int)(long long)n & 3;
+  const float a = (k & 1) ? sn : cs, b = (k & 1) ? cs : sn;
+  *c = scale * (k == 1 || k == 2 ? -a : a);
+  *s = scale * (k >= 2 ? -b : b);
+}
+
+// Positions of a token on every axis.
+struct Positions {
+  int32_t p[4];
+  __device__ __forceinline__ void load(const AppendArgs& a, int t) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) p[x] = x < a.rope.n_axes ? a.pos[x * a.pos_stride + t] : 0;
+  }
+  __device__ __forceinline__ int32_t at(int axis) const {
+    return axis == 0 ? p[0] : axis == 1 ? p[1] : axis == 2 ? p[2] : p[3];
+  }
+};
+
+// A head's channels in chunks of 16: two groups of 8, at e0 and e1.  The first
+// rot / 16 chunks hold the pairs 8 chunk .. 8 chunk + 7.
+struct Chunk {
+  int e0, e1;
+  bool turned;
+  __device__ __forceinline__ Chunk(const RopeRef& r, int c) {
+    turned = c < r.rot / 16;
+    e0 = turned && !r.adjacent ? 8 * c : 16 * c;
+    e1 = turned && !r.adjacent ? e0 + r.rot / 2 : e0 + 8;
+  }
+};
+
+// Turns the 8 pairs of a chunk (x: 16 channels, e0's 8 then e1's 8).
+template <typename CosSin>
+__device__ __forceinline__ void turn(float* x, int adjacent, CosSin cs) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float c, s;
+    cs(i, &c, &s);
+    float& a = adjacent ? x[2 * i] : x[i];
+    float& b = adjacent ? x[2 * i + 1] : x[8 + i];
+    const float ra = a * c - b * s, rb = a * s + b * c;
+    a = ra;
+    b = rb;
+  }
+}
+
+__device__ __forceinline__ void unpack8(uint4 w, float* x) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = lo_bf16(u[i]);
+    x[2 * i + 1] = hi_bf16(u[i]);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+
+// ---------------------------------------------------------------- queries --
+__device__ __forceinline__ void rotate_q(const AppendArgs& a, int dim, int t0, int n, float2* cs) {
+  const int half = a.rope.rot / 2;
+  for (int e = threadIdx.x; e < n * half; e += kThreads) {
+    const int t = e / half, i = e - t * half;
+    float c, s;
+    cos_sin(a.pos[a.rope.axis[i] * a.pos_stride + t0 + t], a.rope.freq[i], a.rope.scale, &c, &s);
+    cs[e] = make_float2(c, s);
+  }
+  __syncthreads();
+  const int chunks = dim / 16, per = a.Hq * chunks;
+  for (int e = threadIdx.x; e < n * per; e += kThreads) {
+    const int t = e / per, hc = e - t * per, h = hc / chunks, c = hc - h * chunks;
+    const Chunk ch(a.rope, c);
+    const uint16_t* src = a.q + (t0 + t) * a.q_stride + (int64_t)h * dim;
+    uint16_t* dst = a.q_out + (t0 + t) * a.qo_stride + (int64_t)h * dim;
+    uint4 w0 = *reinterpret_cast<const uint4*>(src + ch.e0);
+    uint4 w1 = *reinterpret_cast<const uint4*>(src + ch.e1);
+    if (ch.turned) {
+      float x[16];
+      unpack8(w0, x);
+      unpack8(w1, x + 8);
+      const float2* row = cs + t * half + 8 * c;
+      turn(x, a.rope.adjacent, [&](int i, float* co, float* si) { *co = row[i].x; *si = row[i].y; });
+      w0 = pack8(x);
+      w1 = pack8(x + 8);
+    }
+    *reinterpret_cast<uint4*>(dst + ch.e0) = w0;
+    *reinterpret_cast<uint4*>(dst + ch.e1) = w1;
+  }
+}
+
+// Largest value over the workgroup of x >= 0 and y >= 0.
+__device__ __forceinline__ void block_max(float* x, float* y, float2* lds) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) {
+    *x = fmaxf(*x, __shfl_xor(*x, d));
+    *y = fmaxf(*y, __shfl_xor(*y, d));
+  }
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = make_float2(*x, *y);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kThreads / 64; ++i) {
+    *x = fmaxf(*x, lds[i].x);
+    *y = fmaxf(*y, lds[i].y);
+  }
+}
+
+__device__ __forceinline__ float old_scale(const float* p) {
+  const float s = *p;
+  return s >= kMinScale && s < __builtin_inff() ? s : kMinScale;   // a page never written holds anything
+}
+
+// ---------------------------------------------------------- keys, values --
+// NV: value items (16 tokens x 2 channels) per thread; a key item (1 token x
+// 16 channels) is half as large, so there are 2 NV of them.
+template <int D, bool I8, int NV>
+__device__ __forceinline__ void write_page(const AppendArgs& a, int unit, int h, uint8_t* valid, float2* red) {
+  const int tid = threadIdx.x, shift = a.c.page_shift, P = 1 << shift;
+  // unit -> (prompt s, its j-th page of this call): prompt s has the units
+  // cu[s] / P + 2 s on, more than its ceil(len / P) + 1 pages
+  int lo = 0, hi = a.n_seqs;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((a.cu[mid] >> shift) + 2 * mid <= unit) lo = mid; else hi = mid;
+  }
+  const int j = unit - (a.cu[lo] >> shift) - 2 * lo;
+  const int i0 = a.cu[lo], i1 = min(a.cu[lo + 1], a.n_tokens);
+  if (i0 < 0 || i0 >= i1 || j < 0) return;
+  const int64_t slot0 = a.slot[i0];
+  const int off0 = slot0 >= 0 ? (int)(slot0 & (P - 1)) : 0;
+  const int64_t begin = j == 0 ? i0 : (int64_t)i0 + ((int64_t)j << shift) - off0;
+  if (begin >= i1) return;
+  const int tl = (int)begin, off = j == 0 ? off0 : 0;
+  const int cnt = min(P - off, i1 - tl);
+  const int64_t lead = a.slot[tl];
+  if (lead < 0 || (lead & (P - 1)) != off || (lead >> shift) >= a.c.n_pages) return;
+  const int64_t page = lead >> shift;
+
+  if (tid < P) valid[tid] = tid >= off && tid < off + cnt && a.slot[tl + tid - off] == lead + (tid - off);
+  __syncthreads();
+
+  uint32_t v[NV][16];
+  float vmax = 0.f, kmax = 0.f;
+  const int tiles = P / 16;
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    const int item = tid + n * kThreads, u = item / (D / 2), c2 = item % (D / 2);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int o = u * 16 + i;
+      v[n][i] = 0;
+      if (u < tiles && valid[o])
+        v[n][i] = *reinterpret_cast<const uint32_t*>(a.v + (tl + o - off) * a.v_stride + (int64_t)h * D + 2 * c2);
+    }
+  }
+  uint4 k[2 * NV][2];
+#pragma unroll
+  for (int n = 0; n < 2 * NV; ++n) {
+    const int item = tid + n * kThreads, o = item / (D / 16), c = item % (D / 16);
+    k[n][0] = k[n][1] = make_uint4(0, 0, 0, 0);
+    if (o < P && valid[o]) {
+      const int t = tl + o - off;
+      const Chunk ch(a.rope, c);
+      const uint16_t* src = a.k + t * a.k_stride + (int64_t)h * D;
+      k[n][0] = *reinterpret_cast<const uint4*>(src + ch.e0);
+      k[n][1] = *reinterpret_cast<const uint4*>(src + ch.e1);
+      float x[16];
+      unpack8(k[n][0], x);
+      unpack8(k[n][1], x + 8);
+      if (ch.turned) {
+        Positions pos;
+        pos.load(a, t);
+        turn(x, a.rope.adjacent, [&](int i, float* co, float* si) {
+          cos_sin(pos.at(a.rope.axis[8 * c + i]), a.rope.freq[8 * c + i], a.rope.scale, co, si);
+        });
+        k[n][0] = pack8(x);
+        k[n][1] = pack8(x + 8);
+        unpack8(k[n][0], x);
+        unpack8(k[n][1], x + 8);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) kmax = fmaxf(kmax, finite_abs(x[i]));
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NV; ++n)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      vmax = fmaxf(vmax, fmaxf(finite_abs(lo_bf16(v[n][i])), finite_abs(hi_bf16(v[n][i]))));
+  block_max(&kmax, &vmax, red);
+
+  float* const ksp = a.c.ks + page * a.c.Hkv + h;
+  float* const vsp = a.c.vs + page * a.c.Hkv + h;
+  const float k_old = off ? old_scale(ksp) : kMinScale, v_old = off ? old_scale(vsp) : kMinScale;
+  const float k_new = fmaxf(k_old, scale_for<I8>(kmax)), v_new = fmaxf(v_old, scale_for<I8>(vmax));
+  __syncthreads();   // every thread has the old scales
+  if (tid == 0) {
+    *ksp = k_new;
+    *vsp = v_new;
+  }
+  // powers of two up to 2^121: the reciprocals are exact and normal
+  const float k_inv = 1.f / k_new, v_inv = 1.f / v_new;
+  const float k_ratio = k_old * k_inv, v_ratio = v_old * v_inv;
+  const bool k_grew = k_new > k_old, v_grew = v_new > v_old;
+
+  uint8_t* const kb = a.c.k + page_base(a.c, page, h);
+#pragma unroll
+  for (int n = 0; n < 2 * NV; ++n) {
+    const int item = tid + n * kThreads, o = item / (D / 16), c = item % (D / 16);
+    if (o >= P) continue;
+    const Chunk ch(a.rope, c);
+    uint2* const d0 = reinterpret_cast<uint2*>(kb + o * D + ch.e0);
+    uint2* const d1 = reinterpret_cast<uint2*>(kb + o * D + ch.e1);
+    if (valid[o]) {
+      float x[16];
+      unpack8(k[n][0], x);
+      unpack8(k[n][1], x + 8);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] *= k_inv;
+      *d0 = make_uint2(encode4<I8>(x), encode4<I8>(x + 4));
+      *d1 = make_uint2(encode4<I8>(x + 8), encode4<I8>(x + 12));
+    } else if (o < off && k_grew) {
+      const uint2 w0 = *d0, w1 = *d1;
+      *d0 = make_uint2(recode4<I8>(w0.x, k_ratio), recode4<I8>(w0.y, k_ratio));
+      *d1 = make_uint2(recode4<I8>(w1.x, k_ratio), recode4<I8>(w1.y, k_ratio));
+    }
+  }
+
+  uint8_t* const vb = a.c.v + page_base(a.c, page, h);
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    const int item = tid + n * kThreads, u = item / (D / 2), c2 = item % (D / 2);
+    if (u >= tiles) continue;
+    uint32_t mask[4];   // the bytes of this tile that are new
+    bool any = false, all = true;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      mask[g] = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (valid[u * 16 + 4 * g + i]) mask[g] |= 0xFFu << (8 * i);
+      any |= mask[g] != 0;
+      all &= mask[g] == 0xFFFFFFFFu;
+    }
+    const bool again = v_grew && u * 16 < off;
+    if (!any && !again) continue;
+    uint4* const dst = reinterpret_cast<uint4*>(vb + (u * D + 2 * c2) * 16);
+    uint4 old[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (!all) {
+      old[0] = dst[0];
+      old[1] = dst[1];
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t w[4] = {old[half].x, old[half].y, old[half].z, old[half].w};
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (again) {
+          const int before = off - (u * 16 + 4 * g);   // older tokens among these four
+          const uint32_t m = before >= 4 ? 0xFFFFFFFFu : before <= 0 ? 0u : (1u << (8 * before)) - 1;
+          w[g] = (recode4<I8>(w[g], v_ratio) & m) | (w[g] & ~m);
+        }
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t two = v[n][4 * g + i];
+          x[i] = (half ? hi_bf16(two) : lo_bf16(two)) * v_inv;
+        }
+        w[g] = (encode4<I8>(x) & mask[g]) | (w[g] & ~mask[g]);
+      }
+      dst[half] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+constexpr int kQTokens = 4;
+
+template <int D, bool I8, int NV>
+__global__ void __launch_bounds__(kThreads) rope_append_kernel(const AppendArgs a, const int64_t page_blocks) {
+  __shared__ union {
+    struct { uint8_t valid[128]; float2 red[kThreads / 64]; } w;
+    float2 cs[kQTokens * 128];
+  } lds;
+  const int64_t b = blockIdx.x;
+  if (b < page_blocks) {
+    write_page<D, I8, NV>(a, (int)(b / a.c.Hkv), (int)(b % a.c.Hkv), lds.w.valid, lds.w.red);
+  } else {
+    const int t0 = (int)(b - page_blocks) * kQTokens;
+    rotate_q(a, D, t0, min(kQTokens, a.n_tokens - t0), lds.cs);
+  }
+}
+
+// ---------------------------------------------------------------- gather --
+// A workgroup reads back 16 rows of one head.
+template <int D, bool I8>
+__global__ void __launch_bounds__(kThreads) cache_gather_kernel(const GatherArgs a) {
+  const int h = blockIdx.y;
+  const int64_t row0 = (int64_t)blockIdx.x * 16;
+  const int64_t slots = (int64_t)a.c.n_pages << a.c.page_shift;
+  const int page_mask = (1 << a.c.page_shift) - 1;
+  if (a.k_out) {
+    for (int e = threadIdx.x; e < D; e += kThreads) {   // 16 rows x D / 16 chunks
+      const int64_t t = row0 + e / (D / 16);
+      const int c = e % (D / 16);
+      if (t >= a.n_tokens) continue;
+      const int64_t s = a.slot[t];
+      const bool ok = s >= 0 && s < slots;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      float scale = 0.f;
+      if (ok) {
+        const int64_t page = s >> a.c.page_shift;
+        w = *reinterpret_cast<const uint4*>(a.c.k + page_base(a.c, page, h) + (s & page_mask) * D + 16 * c);
+        scale = a.c.ks[page * a.c.Hkv + h];
+      }
+      float x[16];
+      decode4<I8>(w.x, x);
+      decode4<I8>(w.y, x + 4);
+      decode4<I8>(w.z, x + 8);
+      decode4<I8>(w.w, x + 12);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = ok ? x[i] * scale : 0.f;
+      uint4* dst = reinterpret_cast<uint4*>(a.k_out + (t * a.c.Hkv + h) * D + 16 * c);
+      dst[0] = pack8(x);
+      dst[1] = pack8(x + 8);
+    }
+  }
+  if (a.v_out) {
+    for (int e = threadIdx.x; e < 8 * D; e += kThreads) {   // 16 rows x D / 2 channel pairs
+      const int64_t t = row0 + e / (D / 2);
+      const int c2 = e % (D / 2);
+      if (t >= a.n_tokens) continue;
+      const int64_t s = a.slot[t];
+      float x0 = 0.f, x1 = 0.f;
+      if (s >= 0 && s < slots) {
+        const int64_t page = s >> a.c.page_shift;
+        const int o = (int)(s & page_mask);
+        const uint8_t* p = a.c.v + page_base(a.c, page, h) + ((o >> 4) * D + 2 * c2) * 16 + (o & 15);
+        const float scale = a.c.vs[page * a.c.Hkv + h];
+        float f[4];
+        decode4<I8>((uint32_t)p[0] | (uint32_t)p[16] << 8, f);
+        x0 = f[0] * scale;
+        x1 = f[1] * scale;
+      }
+      *reinterpret_cast<uint32_t*>(a.v_out + (t * a.c.Hkv + h) * D + 2 * c2) = pack_bf16(x0, x1);
+    }
+  }
+}
+
+template <int D, bool I8>
+hipError_t append_nv(const AppendArgs& a, dim3 grid, int64_t page_blocks, hipStream_t st) {
+  const int nv = std::max(1, (D << a.c.page_shift) / (32 * kThreads));
+  if (nv == 1) hipLaunchKernelGGL((rope_append_kernel<D, I8, 1>), grid, dim3(kThreads), 0, st, a, page_blocks);
+  else if (nv == 2) hipLaunchKernelGGL((rope_append_kernel<D, I8, 2>), grid, dim3(kThreads), 0, st, a, page_blocks);
+  else hipLaunchKernelGGL((rope_append_kernel<D, I8, 4>), grid, dim3(kThreads), 0, st, a, page_blocks);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rope_append(const AppendArgs& a, hipStream_t st) {
+  const int64_t units = (a.n_tokens >> a.c.page_shift) + 2 * (int64_t)a.n_seqs;
+  const int64_t page_blocks = units * a.c.Hkv;
+  const int64_t q_blocks = a.q ? (a.n_tokens + kQTokens - 1) / kQTokens : 0;
+  const dim3 grid((uint32_t)(page_blocks + q_blocks));
+  switch (a.c.dim) {
+    case 64: return a.c.i8 ? append_nv<64, true>(a, grid, page_blocks, st) : append_nv<64, false>(a, grid, page_blocks, st);
+    case 128: return a.c.i8 ? append_nv<128, true>(a, grid, page_blocks, st) : append_nv<128, false>(a, grid, page_blocks, st);
+    default: return a.c.i8 ? append_nv<256, true>(a, grid, page_blocks, st) : append_nv<256, false>(a, grid, page_blocks, st);
+  }
+}
+
+hipError_t launch_cache_gather(const GatherArgs& a, hipStream_t st) {
+  const dim3 grid((uint32_t)((a.n_tokens + 15) / 16), a.c.Hkv);
+  const dim3 block(kThreads);
+  switch (a.c.dim) {
+    case 64:
+      if (a.c.i8) hipLaunchKernelGGL((cache_gather_kernel<64, true>), grid, block, 0, st, a);
+      else hipLaunchKernelGGL((cache_gather_kernel<64, false>), grid, block, 0, st, a);
+      break;
+    case 128:
+      if (a.c.i8) hipLaunchKernelGGL((cache_gather_kernel<128, true>), grid, block, 0, st, a);
+      else hipLaunchKernelGGL((cache_gather_kernel<128, false>), grid, block, 0, st, a);
+      break;
+    default:
+      if (a.c.i8) hipLaunchKernelGGL((cache_gather_kernel<256, true>), grid, block, 0, st, a);
+      else hipLaunchKernelGGL((cache_gather_kernel<256, false>), grid, block, 0, st, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace gdn

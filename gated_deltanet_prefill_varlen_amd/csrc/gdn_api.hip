@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <vector>
 
+#include "cache_internal.h"
 #include "gdn.h"
 #include "gdn_internal.h"
 
@@ -82,6 +83,67 @@ gdn_status check_slots(const T* slots, int64_t n, int64_t pool_slots) {
   return GDN_OK;
 }
 
+int log2_of(int32_t x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+bool supported_page(int32_t p) { return p == 16 || p == 32 || p == 64 || p == 128; }
+
+// Checks of a cache's handle, and the kernels' form of it.  `data` is false
+// where only its sizes are used.
+gdn_status check_cache(const gdn_cache* c, bool data, gdn::CacheRef* out) {
+  if (!c) return GDN_ERR_NULL;
+  if (c->num_kv_heads < 1 || c->n_pages < 1) return GDN_ERR_SHAPE;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return GDN_ERR_UNSUPPORTED;
+  if (!supported_page(c->page)) return GDN_ERR_UNSUPPORTED;
+  if (c->code_dtype != GDN_E4M3 && c->code_dtype != GDN_I8) return GDN_ERR_UNSUPPORTED;
+  if (data) {
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale) return GDN_ERR_NULL;
+    if (!aligned16(c->k) || !aligned16(c->v)) return GDN_ERR_SHAPE;
+  }
+  *out = gdn::CacheRef{c->num_kv_heads, c->head_dim, log2_of(c->page), c->n_pages, c->code_dtype == GDN_I8,
+                       static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), c->k_scale, c->v_scale};
+  return GDN_OK;
+}
+
+// Token stride of bf16 rows [tokens, heads, d]: 0 = dense, else at least that,
+// with every row 16-byte aligned.
+gdn_status bf16_stride(int64_t given, int64_t dense, int64_t* out) {
+  const int64_t st = given == 0 ? dense : given;
+  if (st < dense || st % 8 != 0 || st > INT32_MAX) return GDN_ERR_SHAPE;
+  *out = st;
+  return GDN_OK;
+}
+
+// What both attention calls check alike.
+gdn_status check_attn(const gdn_cache* cache, int32_t Hq, float scale, int32_t n_seqs, int32_t max_pages,
+                      const int32_t* kv_len, const int32_t* table, const void* q, int64_t q_stride,
+                      const void* out, int64_t rows, gdn::AttnArgs* a) {
+  gdn_status st = check_cache(cache, true, &a->c);
+  if (st != GDN_OK) return st;
+  if (Hq < 1 || max_pages < 0 || !std::isfinite(scale)) return GDN_ERR_SHAPE;
+  if (Hq % a->c.Hkv != 0 || Hq / a->c.Hkv > 64) return GDN_ERR_UNSUPPORTED;
+  if (rows * Hq > INT32_MAX) return GDN_ERR_SHAPE;
+  if (n_seqs > 0 && (!kv_len || (max_pages > 0 && !table))) return GDN_ERR_NULL;
+  if (rows > 0 && (!q || !out)) return GDN_ERR_NULL;
+  if ((st = bf16_stride(q_stride, (int64_t)Hq * a->c.dim, &a->q_stride)) != GDN_OK) return st;
+  if ((q && !aligned16(q)) || (out && !aligned16(out))) return GDN_ERR_SHAPE;
+  if (rows > 0) {   // out must not overlap q
+    const char* qb = static_cast<const char*>(q);
+    const char* ob = static_cast<const char*>(out);
+    const char* qe = qb + ((rows - 1) * a->q_stride + (int64_t)Hq * a->c.dim) * 2;
+    const char* oe = ob + rows * Hq * a->c.dim * 2;
+    if (qb < oe && ob < qe) return GDN_ERR_SHAPE;
+  }
+  a->Hq = Hq; a->n_seqs = n_seqs; a->n_tokens = (int32_t)rows; a->scale = scale;
+  a->kv_len = kv_len; a->table = table; a->max_pages = max_pages;
+  a->max_kv = (int32_t)std::min<int64_t>((int64_t)max_pages << a->c.page_shift, INT32_MAX);
+  a->q = static_cast<const uint16_t*>(q); a->out = static_cast<uint16_t*>(const_cast<void*>(out));
+  return GDN_OK;
+}
+
 gdn_status finish_launch(hipError_t e, hipStream_t stream) {
   if (e == hipSuccess) e = hipGetLastError();
   if (e != hipSuccess) {
@@ -103,7 +165,7 @@ const char* gdn_status_string(int32_t status) {
     case GDN_ERR_UNSUPPORTED: return "GDN_ERR_UNSUPPORTED: head dims, chunk, dtype, flags or head ratio not supported";
     case GDN_ERR_SEQLENS: return "GDN_ERR_SEQLENS: cu_seqlens must start at 0, not decrease and end at n_tokens";
     case GDN_ERR_CKPT: return "GDN_ERR_CKPT: checkpoints must increase and each lie inside a prompt";
-    case GDN_ERR_CAPACITY: return "GDN_ERR_CAPACITY: output list too short or slot outside the pool";
+    case GDN_ERR_CAPACITY: return "GDN_ERR_CAPACITY: output list or workspace too short, or slot outside the pool";
     case GDN_ERR_HIP: return "GDN_ERR_HIP: a HIP call or kernel launch failed";
     default: return "unknown gdn_status";
   }
@@ -386,6 +448,136 @@ gdn_status gdn_snapshot_copy(const void* ckpt_buf, int32_t n, int64_t bytes_each
     if (e != hipSuccess) return finish_launch(e, s);
   }
   return GDN_OK;
+}
+
+gdn_status gdn_plan_pages(int32_t page, int32_t n_seqs, const int32_t* want_len, const int32_t* kv_len,
+                          int32_t* kv_len_out, int32_t* block_table, int32_t max_pages,
+                          int32_t* free_pages, const int32_t* free_count, int32_t* free_count_out,
+                          int32_t n_pages, int32_t* cu_seqlens, int64_t* slot_map, int32_t slot_cap,
+                          int32_t* positions, int32_t* status, void* stream) {
+  if (!supported_page(page)) return GDN_ERR_UNSUPPORTED;
+  if (n_seqs < 0 || max_pages < 0 || n_pages < 1 || slot_cap < 0) return GDN_ERR_SHAPE;
+  if (!free_pages || !free_count || !free_count_out || !cu_seqlens) return GDN_ERR_NULL;
+  if (n_seqs > 0 && (!want_len || !kv_len || !kv_len_out || !status || (max_pages > 0 && !block_table)))
+    return GDN_ERR_NULL;
+  if (slot_cap > 0 && !slot_map) return GDN_ERR_NULL;
+  gdn::PlanArgs a{};
+  a.page_shift = log2_of(page); a.n_seqs = n_seqs; a.max_pages = max_pages; a.n_pages = n_pages;
+  a.slot_cap = slot_cap; a.want = want_len; a.kv = kv_len; a.kv_out = kv_len_out; a.table = block_table;
+  a.free_pages = free_pages; a.free_count = free_count; a.free_count_out = free_count_out;
+  a.cu = cu_seqlens; a.slot = slot_map; a.pos = positions; a.status = status;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  return finish_launch(gdn::launch_plan_pages(a, s), s);
+}
+
+gdn_status gdn_rope_append(const gdn_rope* rope, const gdn_cache* cache, int32_t num_q_heads,
+                           const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, int32_t n_seqs,
+                           int32_t n_tokens, const void* q, int64_t q_tok_stride, const void* k,
+                           int64_t k_tok_stride, const void* v, int64_t v_tok_stride,
+                           const int32_t* positions, int64_t pos_axis_stride, const int64_t* slot_map,
+                           void* q_out, int64_t q_out_tok_stride, void* stream) {
+  gdn::AppendArgs a{};
+  if (!rope) return GDN_ERR_NULL;
+  gdn_status st = check_cache(cache, true, &a.c);
+  if (st != GDN_OK) return st;
+  if (rope->rot_dim < 0 || rope->rot_dim % 16 != 0 || rope->rot_dim > a.c.dim) return GDN_ERR_UNSUPPORTED;
+  if (rope->n_axes < 1 || rope->n_axes > 4 || (rope->adjacent != 0 && rope->adjacent != 1)) return GDN_ERR_UNSUPPORTED;
+  if (!std::isfinite(rope->scale) || pos_axis_stride < 0) return GDN_ERR_SHAPE;
+  for (int32_t i = 0; i < rope->rot_dim / 2; ++i)
+    if (!std::isfinite(rope->freq[i]) || rope->axis[i] >= rope->n_axes) return GDN_ERR_SHAPE;
+  st = check_seqlens(cu_seqlens_host, n_seqs, n_tokens);
+  if (st != GDN_OK) return st;
+  if (!q != !q_out) return GDN_ERR_NULL;
+  if (q && num_q_heads < 1) return GDN_ERR_SHAPE;
+  if (n_seqs > 0 && !cu_seqlens) return GDN_ERR_NULL;
+  if (n_tokens > 0 && (!k || !v || !slot_map || (rope->rot_dim > 0 && !positions))) return GDN_ERR_NULL;
+  const int64_t d = a.c.dim, hkv = a.c.Hkv, hq = q ? num_q_heads : 1;
+  if ((st = bf16_stride(q_tok_stride, hq * d, &a.q_stride)) != GDN_OK) return st;
+  if ((st = bf16_stride(q_out_tok_stride, hq * d, &a.qo_stride)) != GDN_OK) return st;
+  if ((st = bf16_stride(k_tok_stride, hkv * d, &a.k_stride)) != GDN_OK) return st;
+  if ((st = bf16_stride(v_tok_stride, hkv * d, &a.v_stride)) != GDN_OK) return st;
+  if (q == q_out && a.q_stride != a.qo_stride) return GDN_ERR_SHAPE;
+  const void* ptrs[] = {q, k, v, q_out};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return GDN_ERR_SHAPE;
+  // one workgroup per page and head, and per few rows of queries
+  if (((int64_t)n_tokens / cache->page + 2 * (int64_t)n_seqs) * hkv + n_tokens > INT32_MAX) return GDN_ERR_SHAPE;
+  if (n_tokens == 0) return GDN_OK;
+  a.rope.rot = rope->rot_dim; a.rope.n_axes = rope->n_axes; a.rope.adjacent = rope->adjacent;
+  a.rope.scale = rope->scale;
+  std::copy(rope->freq, rope->freq + 128, a.rope.freq);
+  std::copy(rope->axis, rope->axis + 128, a.rope.axis);
+  a.Hq = num_q_heads; a.n_seqs = n_seqs; a.n_tokens = n_tokens; a.cu = cu_seqlens;
+  a.q = static_cast<const uint16_t*>(q); a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v); a.q_out = static_cast<uint16_t*>(q_out);
+  a.pos = positions; a.pos_stride = pos_axis_stride; a.slot = slot_map;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  return finish_launch(gdn::launch_rope_append(a, s), s);
+}
+
+gdn_status gdn_cache_gather(const gdn_cache* cache, int32_t n_tokens, const int64_t* slot_map, void* k_out,
+                            void* v_out, void* stream) {
+  gdn::GatherArgs a{};
+  gdn_status st = check_cache(cache, true, &a.c);
+  if (st != GDN_OK) return st;
+  if (n_tokens < 0 || a.c.Hkv > 65535) return GDN_ERR_SHAPE;
+  if (!k_out && !v_out) return GDN_ERR_NULL;
+  if (n_tokens > 0 && !slot_map) return GDN_ERR_NULL;
+  if ((k_out && !aligned16(k_out)) || (v_out && !aligned16(v_out))) return GDN_ERR_SHAPE;
+  if (n_tokens == 0) return GDN_OK;
+  a.n_tokens = n_tokens; a.slot = slot_map;
+  a.k_out = static_cast<uint16_t*>(k_out); a.v_out = static_cast<uint16_t*>(v_out);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  return finish_launch(gdn::launch_cache_gather(a, s), s);
+}
+
+gdn_status gdn_attn_packed(const gdn_cache* cache, int32_t num_q_heads, float scale, const int32_t* cu_seqlens,
+                           const int32_t* cu_seqlens_host, int32_t n_seqs, int32_t n_tokens,
+                           const int32_t* kv_len, const int32_t* block_table, int32_t max_pages,
+                           const void* q, int64_t q_tok_stride, void* out, void* stream) {
+  gdn::AttnArgs a{};
+  gdn_status st = check_seqlens(cu_seqlens_host, n_seqs, n_tokens);
+  if (st != GDN_OK) return st;
+  st = check_attn(cache, num_q_heads, scale, n_seqs, max_pages, kv_len, block_table, q, q_tok_stride, out,
+                  n_tokens, &a);
+  if (st != GDN_OK) return st;
+  if (n_seqs > 0 && !cu_seqlens) return GDN_ERR_NULL;
+  if (n_tokens == 0) return GDN_OK;
+  a.cu = cu_seqlens;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  return finish_launch(gdn::launch_attn(a, s), s);
+}
+
+gdn_status gdn_attn_decode_workspace(const gdn_cache* cache, int32_t num_q_heads, int32_t batch, int32_t n_tok,
+                                     int32_t max_kv_len, int64_t* bytes) {
+  gdn::CacheRef c;
+  if (!bytes) return GDN_ERR_NULL;
+  const gdn_status st = check_cache(cache, false, &c);
+  if (st != GDN_OK) return st;
+  if (num_q_heads < 1 || batch < 0 || n_tok < 1 || max_kv_len < 0) return GDN_ERR_SHAPE;
+  *bytes = 0;
+  return GDN_OK;
+}
+
+gdn_status gdn_attn_decode(const gdn_cache* cache, int32_t num_q_heads, float scale, int32_t batch,
+                           int32_t n_tok, const int32_t* kv_len, const int32_t* block_table,
+                           int32_t max_pages, int32_t max_kv_len, const void* q, int64_t q_tok_stride,
+                           void* out, void* workspace, int64_t workspace_bytes, void* stream) {
+  gdn::AttnArgs a{};
+  if (batch < 0 || n_tok < 1 || max_kv_len < 0) return GDN_ERR_SHAPE;
+  gdn_status st = check_attn(cache, num_q_heads, scale, batch, max_pages, kv_len, block_table, q, q_tok_stride,
+                             out, (int64_t)batch * n_tok, &a);
+  if (st != GDN_OK) return st;
+  if (max_kv_len > a.max_kv) return GDN_ERR_SHAPE;
+  a.max_kv = max_kv_len; a.n_tok = n_tok;
+  int64_t need;
+  if ((st = gdn_attn_decode_workspace(cache, num_q_heads, batch, n_tok, max_kv_len, &need)) != GDN_OK) return st;
+  if (need > 0 && !workspace) return GDN_ERR_NULL;
+  if (workspace_bytes < need) return GDN_ERR_CAPACITY;
+  if (workspace && !aligned16(workspace)) return GDN_ERR_SHAPE;
+  if (batch == 0) return GDN_OK;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  return finish_launch(gdn::launch_attn(a, s), s);
 }
 
 }  // extern "C"

@@ -1,7 +1,11 @@
 /*
  * libgdn: packed (varlen) gated-delta-rule prefill with prefix-cache
  * checkpoints, a one-token decode step, the short convolution ahead of them
- * and a checkpoint copy on its own stream, for AMD Instinct MI355X (gfx950).
+ * and a checkpoint copy on its own stream, for AMD Instinct MI355X (gfx950);
+ * and, for the softmax-attention layers of the same hybrid models, a paged
+ * key/value cache held in 8 bits: its page planner, rotary positions with the
+ * cache's write, its read back, and attention over it for packed prompts and
+ * for decoding requests.
  *
  * What the layer computes
  *   Per prompt s and value head h (qk head j = h / (Hv / Hqk)), starting from
@@ -57,11 +61,13 @@ typedef enum gdn_status {
   GDN_ERR_UNSUPPORTED = 3, /* head dims, chunk, dtype, flags or head ratio not built      */
   GDN_ERR_SEQLENS = 4,     /* cu_seqlens not 0-based, non-decreasing, ending at n_tokens  */
   GDN_ERR_CKPT = 5,        /* checkpoints not strictly increasing, or outside every prompt */
-  GDN_ERR_CAPACITY = 6,    /* an output list is too short, or a slot outside the pool      */
+  GDN_ERR_CAPACITY = 6,    /* an output list or workspace too short, a slot outside the pool */
   GDN_ERR_HIP = 7          /* a HIP runtime call or kernel launch failed                  */
 } gdn_status;
 
-typedef enum gdn_dtype { GDN_BF16 = 0, GDN_F32 = 1 } gdn_dtype;
+/* GDN_E4M3 (4 exponent and 3 fraction bits, largest value 448) and GDN_I8
+ * (-127 .. 127) are codes of a gdn_cache. */
+typedef enum gdn_dtype { GDN_BF16 = 0, GDN_F32 = 1, GDN_E4M3 = 2, GDN_I8 = 3 } gdn_dtype;
 
 /* shape.flags */
 #define GDN_QK_L2NORM 1u
@@ -325,6 +331,190 @@ GDN_API gdn_status gdn_snapshot_copy(const void* ckpt_buf, int32_t n, int64_t by
                              int64_t pool_slots, const int64_t* dst_slot,
                              const int64_t* dst_slot_host, void* wait_event, void* copy_stream,
                              void* done_event);
+
+/* ------------------------------------------------------------------------
+ * The softmax-attention layers: a paged key/value cache held in 8 bits.
+ *
+ * A page holds `page` consecutive tokens of one request for every kv head.
+ * Its keys (and its values) are 8-bit codes with one fp32 scale per page and
+ * head: value = code * scale.  Scales are powers of two: the smallest one with
+ * |x| <= scale * (448 or 127) for every x written since the page's token 0
+ * was, and at least 2^-100.  When a later token needs a larger scale, the
+ * page's older codes are rounded again to it.  Multiplying by a power of two
+ * is exact, so a stored value is off by at most half a step of its code plus,
+ * per growth, half a step of the smaller scales before (together under one
+ * int8 step; e4m3 codes only lose what falls below the subnormals).
+ * code * scale is exact in bf16.
+ *
+ *   num_kv_heads:  Hkv >= 1.      head_dim: d, one of 64, 128, 256.
+ *   page:          tokens per page, one of 16, 32, 64, 128.
+ *   code_dtype:    GDN_E4M3 or GDN_I8.        n_pages: >= 1.
+ *   k:             device [n_pages, Hkv, page, d] codes.
+ *   v:             device [n_pages, Hkv, page/16, d, 16] codes: 16-token tiles,
+ *                  the token innermost (the product of the probabilities and
+ *                  the values contracts over tokens and reads 16 as a vector).
+ *   k_scale, v_scale: device fp32 [n_pages, Hkv].
+ * Pages need no clearing before their first use.  A request's row of a block
+ * table (device int32 [.., max_pages]) names its pages in order; a slot is
+ * page id * page + offset.  Entries of block tables and slot maps live on the
+ * device, so the host cannot check them: the kernels neither read nor write a
+ * page outside [0, n_pages).
+ * ------------------------------------------------------------------------ */
+typedef struct gdn_cache {
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t page;
+  int32_t code_dtype;
+  int32_t n_pages;
+  int32_t reserved;
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+} gdn_cache;
+
+/* Rotary positions with up to four axes (text: one; images and video: time,
+ * height, width).  Pair i < rot_dim / 2 of a head turns by the angle
+ * position[axis[i]] * freq[i]:  (a, b) -> (a c - b s, a s + b c), with
+ * c, s = scale * cos, scale * sin.  The angle is formed in 64 bits, so far
+ * positions lose nothing.  Channels from rot_dim on are passed through.
+ *   rot_dim:   a multiple of 16 in [0, min(d, 256)].   n_axes: 1 .. 4.
+ *   adjacent:  0: pair i is channels (i, i + rot_dim/2); 1: (2i, 2i + 1).
+ *   scale:     factor on cos and sin (1.0 for none).
+ *   freq:      radians per position, finite.   axis: each below n_axes (in
+ *              sections, or dealt out in turn). */
+typedef struct gdn_rope {
+  int32_t rot_dim;
+  int32_t n_axes;
+  int32_t adjacent;
+  float scale;
+  float freq[128];
+  uint8_t axis[128];
+} gdn_rope;
+
+/* Page planner on the device: from the lengths that requests hold and want,
+ * their block tables, the pack of their new tokens and its slot map.  Request
+ * i goes from kv_len[i] to want_len[i] tokens:
+ *   - shorter (ended: 0; drafted tokens rejected): the pages from
+ *     ceil(want / page) on go back on the free stack, in request order;
+ *   - longer: the pages it lacks are taken from the top of the stack, after
+ *     every page given back by this call, in request order.
+ * A request that cannot grow keeps its length and pages, and status says why:
+ *   0 done; 1 the stack is short: the pages needed by it and the growing
+ *   requests before it are more than there are; 2 want_len is over
+ *   max_pages * page; 3 kv_len or want_len negative, or kv_len over
+ *   max_pages * page; 4 its new tokens end beyond slot_cap.
+ * (2, 3 and 4 need no pages.)  The pack has max(0, want - kv) tokens per
+ * request, granted or not (status 3: none), one request after the other.
+ *   want_len, kv_len: device int32 [n_seqs].   kv_len_out: int32 [n_seqs], the
+ *                     lengths after the call; may equal kv_len.
+ *   block_table:      device int32 [n_seqs, max_pages], in place: entries of
+ *                     held pages are read, of taken pages written.
+ *   free_pages:       device int32 [n_pages], a stack: the first *free_count
+ *                     are free.   free_count, free_count_out: device int32 [1];
+ *                     may be equal.
+ *   cu_seqlens:       device int32 [n_seqs + 1], the pack's offsets.
+ *   slot_map:         device int64 [slot_cap]: slot of each new token; -1 for
+ *                     refused requests and from cu_seqlens[n_seqs] on.
+ *   positions:        device int32 [slot_cap] or NULL: each new token's index
+ *                     in its request (0 behind the last).
+ *   status:           device int32 [n_seqs].
+ * Buffers not said to be equal must not overlap.  Errors: GDN_ERR_NULL,
+ * GDN_ERR_SHAPE, GDN_ERR_UNSUPPORTED (page), GDN_ERR_HIP. */
+GDN_API gdn_status gdn_plan_pages(int32_t page, int32_t n_seqs, const int32_t* want_len,
+                                  const int32_t* kv_len, int32_t* kv_len_out, int32_t* block_table,
+                                  int32_t max_pages, int32_t* free_pages, const int32_t* free_count,
+                                  int32_t* free_count_out, int32_t n_pages, int32_t* cu_seqlens,
+                                  int64_t* slot_map, int32_t slot_cap, int32_t* positions,
+                                  int32_t* status, void* stream);
+
+/* Rotary positions for a pack's queries and keys, and the keys and values
+ * written into the cache: q_out = rotated q; the rotated keys (rounded to
+ * bf16, as a tensor of keys is) and the values, as codes, into their slots.
+ *   cu_seqlens(_host), n_seqs, n_tokens: as in gdn_prefill_packed.
+ *   q, k, v:        device bf16 [n_tokens, Hq | Hkv | Hkv, d], token strides in
+ *                   elements (0 = dense), so they may be columns of one row.
+ *   positions:      device int32 [n_axes, n_tokens], axis a at a *
+ *                   pos_axis_stride (0: one row for every axis); NULL iff
+ *                   rot_dim = 0.
+ *   slot_map:       device int64 [n_tokens].  Within a prompt, slots count up
+ *                   by one inside a page and each page starts at its token 0;
+ *                   a prompt's first slot may be anywhere in its page.  Tokens
+ *                   whose slot is not what the first one of their page in the
+ *                   prompt implies (-1 among them) are not written.  A write
+ *                   at a page's token 0 starts its scale anew.  No page may
+ *                   be written by two prompts of one call.
+ *   q_out:          device bf16 [n_tokens, Hq, d], token stride q_out_tok_stride
+ *                   (0 = dense); may be q itself with the same stride, must
+ *                   not overlap k, v or another part of q.  NULL with q NULL:
+ *                   only the cache is written.
+ * Infinities are stored as the largest code; NaN as e4m3's NaN, or as 0 in
+ * int8; neither counts for a scale.  Tokens of a page behind the last one
+ * written are left as they were.
+ * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_UNSUPPORTED, GDN_ERR_SEQLENS,
+ * GDN_ERR_HIP. */
+GDN_API gdn_status gdn_rope_append(const gdn_rope* rope, const gdn_cache* cache, int32_t num_q_heads,
+                                   const int32_t* cu_seqlens, const int32_t* cu_seqlens_host,
+                                   int32_t n_seqs, int32_t n_tokens, const void* q,
+                                   int64_t q_tok_stride, const void* k, int64_t k_tok_stride,
+                                   const void* v, int64_t v_tok_stride, const int32_t* positions,
+                                   int64_t pos_axis_stride, const int64_t* slot_map, void* q_out,
+                                   int64_t q_out_tok_stride, void* stream);
+
+/* The cache read back: row t of k_out and v_out gets the values of slot_map[t]
+ * (zeros for a slot outside the cache), for prefixes moved out of the pages.
+ *   slot_map:       device int64 [n_tokens], any slots in any order.
+ *   k_out, v_out:   device bf16 [n_tokens, Hkv, d], or NULL (not both).
+ * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_UNSUPPORTED, GDN_ERR_HIP. */
+GDN_API gdn_status gdn_cache_gather(const gdn_cache* cache, int32_t n_tokens, const int64_t* slot_map,
+                                    void* k_out, void* v_out, void* stream);
+
+/* Causal softmax attention of a pack over the cache: row i of prompt s (n_s
+ * rows of the pack, kv_len[s] = L tokens in the cache, these among them) sees
+ * the keys 0 .. L - n_s + i:
+ *     o = sum_j softmax_j(scale * q . k_j) v_j.
+ * Query head h reads kv head h / (Hq / Hkv).  A row that sees no key
+ * (kv_len < n_s) is 0.  A prompt whose kv_len is negative or over max_pages *
+ * page gets NaN rows.  A block-table entry outside [0, n_pages) below kv_len
+ * is a page that is not held: its tokens are not seen.
+ *   num_q_heads:    Hq, a multiple of Hkv, Hq / Hkv <= 64.
+ *   scale:          finite; d^-1/2 as a rule.
+ *   kv_len:         device int32 [n_seqs];  block_table: [n_seqs, max_pages].
+ *   q:              device bf16 [n_tokens, Hq, d], token stride q_tok_stride.
+ *   out:            device bf16 [n_tokens, Hq, d] (dense), not overlapping q.
+ * Rows of out behind the last prompt are not written.
+ * Arithmetic: products of bf16 queries and the codes (exact in bf16) sum in
+ * fp32 on the matrix cores; the softmax runs in fp32 with a running maximum;
+ * its probabilities times the values' scale are rounded to bf16 once.
+ * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_UNSUPPORTED, GDN_ERR_SEQLENS,
+ * GDN_ERR_HIP. */
+GDN_API gdn_status gdn_attn_packed(const gdn_cache* cache, int32_t num_q_heads, float scale,
+                                   const int32_t* cu_seqlens, const int32_t* cu_seqlens_host,
+                                   int32_t n_seqs, int32_t n_tokens, const int32_t* kv_len,
+                                   const int32_t* block_table, int32_t max_pages, const void* q,
+                                   int64_t q_tok_stride, void* out, void* stream);
+
+/* The same for a decode batch: n_tok rows for each of `batch` requests (row
+ * b * n_tok + i sees the keys 0 .. kv_len[b] - n_tok + i), the keys split over
+ * workgroups and joined.  Nothing but the pointers and sizes of the call is
+ * fixed on the host, so a captured call follows kv_len and block_table.
+ *   max_kv_len:     upper bound of kv_len, 0 .. max_pages * page (requests over
+ *                   it get NaN rows): the launch is sized for it.
+ *   workspace:      device memory, gdn_attn_decode_workspace() bytes at least
+ *                   (may be NULL if that is 0), 16-byte aligned; its contents
+ *                   mean nothing before or after the call, and calls that may
+ *                   run at the same time need one each.
+ * How a request's keys are split depends on its own length alone.
+ * Errors: as gdn_attn_packed; GDN_ERR_CAPACITY (workspace too small). */
+GDN_API gdn_status gdn_attn_decode(const gdn_cache* cache, int32_t num_q_heads, float scale,
+                                   int32_t batch, int32_t n_tok, const int32_t* kv_len,
+                                   const int32_t* block_table, int32_t max_pages, int32_t max_kv_len,
+                                   const void* q, int64_t q_tok_stride, void* out, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that gdn_attn_decode needs for these sizes. */
+GDN_API gdn_status gdn_attn_decode_workspace(const gdn_cache* cache, int32_t num_q_heads, int32_t batch,
+                                             int32_t n_tok, int32_t max_kv_len, int64_t* bytes);
 
 #ifdef __cplusplus
 }
