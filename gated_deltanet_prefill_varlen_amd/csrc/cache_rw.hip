@@ -15,24 +15,27 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// cos and sin of position * freq.  In 64 bits the angle becomes turns, of
-// which the nearest quarter is taken off; what is left lies in [-pi/4, pi/4],
-// where the Taylor sums through x^9 and x^10 are exact to fp32 rounding
-// (next terms below 2e-9 and 2e-11).
+// cos and sin of position * freq, to a little over half an ulp.  In 64 bits
+// the angle becomes quarter turns, of which the nearest whole number is taken
+// off; what is left is x + x_lo in [-pi/4, pi/4], where the Taylor sums through
+// x^9 and x^10 leave 2e-9 and 3e-11.  Each sum's last addition is the only
+// rounding at the result's size: the lower part of x, of x^2 and of 1 - x^2/2
+// goes into the small terms.
 __device__ __forceinline__ void cos_sin(int pos, float freq, float scale, float* c, float* s) {
   const double quarters = (double)pos * (double)freq * 0.63661977236758134308;   // 2 / pi
   const double n = rint(quarters);
-  const float x = (float)((quarters - n) * 1.57079632679489661923);              // pi / 2
-  const float y = x * x;
+  const double xd = (quarters - n) * 1.57079632679489661923;                     // pi / 2
+  const float x = (float)xd, x_lo = (float)(xd - (double)x);
+  const float y = x * x, y_lo = fmaf(2.f * x, x_lo, fmaf(x, x, -y));
   float sn = fmaf(y, 2.7557319e-6f, -1.9841270e-4f);
   sn = fmaf(y, sn, 8.3333333e-3f);
   sn = fmaf(y, sn, -1.6666667e-1f);
-  sn = fmaf(x * y, sn, x);
+  sn = x + fmaf(x * y, sn, x_lo);
   float cs = fmaf(y, -2.7557319e-7f, 2.4801587e-5f);
   cs = fmaf(y, cs, -1.3888889e-3f);
   cs = fmaf(y, cs, 4.1666667e-2f);
-  cs = fmaf(y, cs, -0.5f);
-  cs = fmaf(y, cs, 1.f);
+  const float h = 0.5f * y, w = 1.f - h;
+  cs = w + ((1.f - w) - h + fmaf(y * y, cs, -0.5f * y_lo));
   const int k = (int)(long long)n & 3;
   const float a = (k & 1) ? sn : cs, b = (k & 1) ? cs : sn;
   *c = scale * (k == 1 || k == 2 ? -a : a);
@@ -72,7 +75,10 @@ __device__ __forceinline__ void turn(float* x, int adjacent, CosSin cs) {
     cs(i, &c, &s);
     float& a = adjacent ? x[2 * i] : x[i];
     float& b = adjacent ? x[2 * i + 1] : x[8 + i];
-    const float ra = a * c - b * s, rb = a * s + b * c;
+    // the second product's rounding error goes back in, so that fewer results
+    // land on the other side of a bf16 step
+    const float bs = b * s, bc = b * c;
+    const float ra = fmaf(a, c, -bs) - fmaf(b, s, -bs), rb = fmaf(a, s, bc) + fmaf(b, c, -bc);
     a = ra;
     b = rb;
   }

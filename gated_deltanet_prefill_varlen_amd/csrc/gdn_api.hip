@@ -555,7 +555,8 @@ gdn_status gdn_attn_decode_workspace(const gdn_cache* cache, int32_t num_q_heads
   const gdn_status st = check_cache(cache, false, &c);
   if (st != GDN_OK) return st;
   if (num_q_heads < 1 || batch < 0 || n_tok < 1 || max_kv_len < 0) return GDN_ERR_SHAPE;
-  *bytes = 0;
+  if ((int64_t)batch * n_tok * num_q_heads > INT32_MAX) return GDN_ERR_SHAPE;
+  *bytes = gdn::attn_decode_bytes(c.dim, num_q_heads, batch, n_tok, max_kv_len);
   return GDN_OK;
 }
 
@@ -576,8 +577,9 @@ gdn_status gdn_attn_decode(const gdn_cache* cache, int32_t num_q_heads, float sc
   if (workspace_bytes < need) return GDN_ERR_CAPACITY;
   if (workspace && !aligned16(workspace)) return GDN_ERR_SHAPE;
   if (batch == 0) return GDN_OK;
+  if (batch > 65535 || a.c.Hkv * (((int64_t)n_tok * (num_q_heads / a.c.Hkv) + 15) / 16) > 65535) return GDN_ERR_SHAPE;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  return finish_launch(gdn::launch_attn(a, s), s);
+  return finish_launch(gdn::launch_attn_decode(a, workspace, s), s);
 }
 
 }  // extern "C"
