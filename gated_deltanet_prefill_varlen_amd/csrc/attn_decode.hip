@@ -1,0 +1,346 @@
+// Decode attention over the paged 8-bit cache: few query rows per request, the
+// whole cache read once, so HBM bounds it.
+//
+// The rows of a request that share a kv head (n_tok tokens x Hq / Hkv heads)
+// are packed into tiles of 16.  A wave takes 64 keys at a time straight from
+// the pages into registers, with no LDS between:
+//   S^T = K Q^T   (16x16x32 products, rows = keys, columns = query rows)
+//   O^T += V^T P^T  (rows = channels, columns = query rows).
+// A product's result holds in lane group g (16 lanes) the rows 4g .. 4g + 3 of
+// every column, and its second operand wants in lane group g the eight
+// contraction indices 8g .. 8g + 7 of the column.  The order of keys is free,
+// so row 4g + i of score tile s is key 16 g + 4 s + i of the 64: then group g
+// has, over the four score tiles, exactly the keys 16 g .. 16 g + 15, which is
+// one 16-byte vector of the cache's transposed value tile, and the
+// probabilities go from one product into the next without leaving their lane.
+//
+// Keys are split over workgroups by the request's own length (split_keys), the
+// four waves of a workgroup take 64-key tiles in turn, and partial results
+// (fp32 sums against the running maximum) are joined in a fixed order, so a
+// request's bits do not depend on its batch.
+#include <algorithm>
+
+#include "attn_device.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kTile = 64;
+
+// Keys per workgroup for a request of L keys.
+__host__ __device__ inline int split_keys(int L) { return L <= 16384 ? 512 : 1024; }
+__host__ __device__ inline int n_splits(int L) {
+  const int k = split_keys(L);
+  return L <= 0 ? 1 : (L + k - 1) / k;
+}
+
+struct Partial {
+  float* o;    // [B][splits][n_tok * Hq][D]
+  float2* ml;  // [B][splits][n_tok * Hq] maximum (of log2 scores), sum
+  int splits;
+};
+
+template <int D, bool I8, int NT>
+__global__ void __launch_bounds__(64 * kWaves) attn_decode_kernel(const AttnArgs a, const Partial part) {
+  constexpr int KL = D / 64;    // 16-byte loads of a key per lane
+  constexpr int KS = D / 32;    // contraction steps of a score
+  constexpr int OB = D / 16;    // 16-channel blocks of the output
+  const int b = blockIdx.z, sp = blockIdx.x;
+  const int G = a.Hq / a.c.Hkv, R = a.n_tok * G;
+  const int groups = (R + 16 * NT - 1) / (16 * NT);
+  const int hk = blockIdx.y / groups, r0 = (blockIdx.y % groups) * 16 * NT;
+  const int L = a.kv_len[b];
+  const bool bad = L < 0 || L > a.max_kv;
+  const int splits = bad ? 1 : n_splits(L);
+  if (sp >= splits) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c16 = lane & 15, g = lane >> 4;
+
+  // the query row of this lane's column, per tile
+  int64_t row[NT];
+  int last[NT];      // the last key it sees
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int r = min(r0 + 16 * t + c16, R - 1), i = r / G;
+    row[t] = ((int64_t)b * a.n_tok + i) * a.Hq + hk * G + (r - i * G);
+    last[t] = L - a.n_tok + i;
+  }
+  if (bad || L == 0) {
+    for (int e = tid; e < 16 * NT * D; e += 64 * kWaves) {
+      const int r = r0 + e / D;
+      if (r < R) {
+        const int i = r / G;
+        a.out[(((int64_t)b * a.n_tok + i) * a.Hq + hk * G + (r - i * G)) * D + e % D] = bad ? 0x7FC0 : 0;
+      }
+    }
+    return;
+  }
+
+  bf16x8 q[NT][KS];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int64_t tok = row[t] / a.Hq, h = row[t] % a.Hq;
+    const uint16_t* p = a.q + tok * a.q_stride + h * D + 16 * g;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+      q[t][k] = *reinterpret_cast<const bf16x8*>(p + 64 * (k >> 1) + 8 * (k & 1));
+  }
+
+  f32x4 o[NT][OB];
+  float m[NT], l[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    m[t] = -__builtin_inff();
+    l[t] = 0.f;
+#pragma unroll
+    for (int x = 0; x < OB; ++x) o[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  const int per = split_keys(L);
+  const int key0 = sp * per, key1 = min(L, key0 + per);
+  const int shift = a.c.page_shift, pmask = (1 << shift) - 1;
+  const int32_t* table = a.table + (int64_t)b * a.max_pages;
+  const float log_scale = a.scale * kLog2e;
+
+  for (int t0 = key0 + wave * kTile; t0 < key1; t0 += kWaves * kTile) {
+    // pages: of the 16 keys whose values (and scores) this lane has, and of
+    // the key whose codes it loads.  A page that is not held is read as page 0
+    // and masked.
+    const int kv = t0 + 16 * g, kk = t0 + 16 * (c16 >> 2);
+    int pv = kv < key1 ? table[kv >> shift] : -1;
+    int pk = kk < key1 ? table[kk >> shift] : -1;
+    const bool held = pv >= 0 && pv < a.c.n_pages;
+    pv = held ? pv : 0;
+    pk = pk >= 0 && pk < a.c.n_pages ? pk : 0;
+    const uint8_t* kp = a.c.k + page_base(a.c, pk, hk) + ((kk & pmask) + (c16 & 3)) * D + 16 * g;
+    const uint8_t* vp = a.c.v + page_base(a.c, pv, hk) + ((kv & pmask) * D + c16 * 16);
+    uint4 kc[4][KL], vc[OB];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < KL; ++i) kc[s][i] = *reinterpret_cast<const uint4*>(kp + 4 * s * D + 64 * i);
+#pragma unroll
+    for (int x = 0; x < OB; ++x) vc[x] = *reinterpret_cast<const uint4*>(vp + x * 256);
+    const float ks = a.c.ks[(int64_t)pv * a.c.Hkv + hk] * log_scale;
+    const float vs = held ? a.c.vs[(int64_t)pv * a.c.Hkv + hk] : 0.f;
+
+    f32x4 s4[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) s4[t][s] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < KL; ++i) {
+        const bf16x8 k0 = codes_to_operand<I8>(kc[s][i].x, kc[s][i].y);
+        const bf16x8 k1 = codes_to_operand<I8>(kc[s][i].z, kc[s][i].w);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          s4[t][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[t][2 * i], s4[t][s], 0, 0, 0);
+          s4[t][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[t][2 * i + 1], s4[t][s], 0, 0, 0);
+        }
+      }
+
+    // scores to probabilities; in units of log2
+    const bool whole = t0 + kTile <= key1 - (a.n_tok - 1);   // every row sees the tile
+    bf16x8 p[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float mx = -__builtin_inff();
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x = s4[t][s][i] * ks;
+          if (!held || (!whole && kv + 4 * s + i > last[t])) x = -__builtin_inff();
+          s4[t][s][i] = x;
+          mx = fmaxf(mx, x);
+        }
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      const float m1 = fmaxf(m[t], mx);
+      const float base = m1 == -__builtin_inff() ? 0.f : m1;
+      if (__any(m1 > m[t])) {
+        const float again = exp2_fast(m[t] - base);
+        l[t] *= again;
+#pragma unroll
+        for (int x = 0; x < OB; ++x) o[t][x] *= again;
+        m[t] = m1;
+      }
+      u32x4 w[2];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e[i] = exp2_fast(s4[t][s][i] - base);
+          l[t] += e[i];
+          e[i] *= vs;   // the probability times its value's scale is rounded to bf16 once
+        }
+        w[s >> 1][2 * (s & 1)] = pack_bf16(e[0], e[1]);
+        w[s >> 1][2 * (s & 1) + 1] = pack_bf16(e[2], e[3]);
+      }
+      p[t][0] = __builtin_bit_cast(bf16x8, w[0]);
+      p[t][1] = __builtin_bit_cast(bf16x8, w[1]);
+    }
+
+    // codes behind the last key (or of a page not held) may be anything, NaN
+    // among them, which a probability of 0 would not silence
+    const int left = held ? key1 - kv : 0;
+    if (__any(left < 16)) {
+      uint32_t keep[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = left - 4 * j;
+        keep[j] = n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << (8 * n)) - 1;
+      }
+#pragma unroll
+      for (int x = 0; x < OB; ++x) {
+        vc[x].x &= keep[0];
+        vc[x].y &= keep[1];
+        vc[x].z &= keep[2];
+        vc[x].w &= keep[3];
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < OB; ++x) {
+      const bf16x8 v0 = codes_to_operand<I8>(vc[x].x, vc[x].y);
+      const bf16x8 v1 = codes_to_operand<I8>(vc[x].z, vc[x].w);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        o[t][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, p[t][0], o[t][x], 0, 0, 0);
+        o[t][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, p[t][1], o[t][x], 0, 0, 0);
+      }
+    }
+  }
+
+  // the four waves, in order
+  __shared__ float sm[kWaves][16 * NT], sl[kWaves][16 * NT];
+  __shared__ __align__(16) float so[16 * NT][D + 4];   // + 4: rows on other banks
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    l[t] += __shfl_xor(l[t], 16);
+    l[t] += __shfl_xor(l[t], 32);
+    if (g == 0) {
+      sm[wave][16 * t + c16] = m[t];
+      sl[wave][16 * t + c16] = l[t];
+    }
+  }
+  __syncthreads();
+  float mt[NT], lt[NT], mine[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    mt[t] = -__builtin_inff();
+    lt[t] = 0.f;
+    for (int w = 0; w < kWaves; ++w) mt[t] = fmaxf(mt[t], sm[w][16 * t + c16]);
+    const float base = mt[t] == -__builtin_inff() ? 0.f : mt[t];
+    for (int w = 0; w < kWaves; ++w) lt[t] += sl[w][16 * t + c16] * exp2_fast(sm[w][16 * t + c16] - base);
+    mine[t] = exp2_fast(m[t] - base);
+  }
+  for (int w = 0; w < kWaves; ++w) {
+    if (wave == w) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int x = 0; x < OB; ++x) {
+          f32x4* const d = reinterpret_cast<f32x4*>(&so[16 * t + c16][16 * x + 4 * g]);
+          const f32x4 y = o[t][x] * mine[t];
+          *d = w == 0 ? y : *d + y;
+        }
+    }
+    __syncthreads();
+  }
+  if (wave == 0 && g == 0) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      sm[0][16 * t + c16] = mt[t];
+      sl[0][16 * t + c16] = lt[t];
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < 16 * NT * D / 4; e += 64 * kWaves) {
+    const int rl = e / (D / 4), c = e % (D / 4) * 4, r = r0 + rl;
+    if (r >= R) continue;
+    const int i = r / G, h = hk * G + (r - i * G);
+    const f32x4 x = *reinterpret_cast<const f32x4*>(&so[rl][c]);
+    if (splits == 1) {
+      const float inv = sl[0][rl] > 0.f ? 1.f / sl[0][rl] : (sm[0][rl] == -__builtin_inff() ? 0.f : 1.f / sl[0][rl]);
+      *reinterpret_cast<uint2*>(a.out + (((int64_t)b * a.n_tok + i) * a.Hq + h) * D + c) =
+          make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+    } else {
+      const int64_t pr = ((int64_t)b * part.splits + sp) * a.n_tok * a.Hq + i * a.Hq + h;
+      *reinterpret_cast<f32x4*>(part.o + pr * D + c) = x;
+      if (c == 0) part.ml[pr] = make_float2(sm[0][rl], sl[0][rl]);
+    }
+  }
+}
+
+// Joins the splits of one row, in order.
+template <int D>
+__global__ void __launch_bounds__(64) attn_join_kernel(const AttnArgs a, const Partial part) {
+  const int rows = a.n_tok * a.Hq;
+  const int b = (int)(blockIdx.x / rows), r = (int)(blockIdx.x % rows), lane = threadIdx.x;
+  const int L = a.kv_len[b];
+  if (L < 0 || L > a.max_kv) return;
+  const int splits = n_splits(L);
+  if (splits == 1) return;
+  constexpr int C = D / 64;
+  const int64_t p0 = (int64_t)b * part.splits * rows + r;
+  float mt = -__builtin_inff();
+  for (int s = 0; s < splits; ++s) mt = fmaxf(mt, part.ml[p0 + (int64_t)s * rows].x);
+  const float base = mt == -__builtin_inff() ? 0.f : mt;
+  float o[C] = {}, l = 0.f;
+  for (int s = 0; s < splits; ++s) {
+    const int64_t pr = p0 + (int64_t)s * rows;
+    const float2 ml = part.ml[pr];
+    const float w = exp2_fast(ml.x - base);
+    l += w * ml.y;
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] += w * part.o[pr * D + C * lane + c];
+  }
+  const float inv = mt == -__builtin_inff() ? 0.f : 1.f / l;
+  uint16_t* const out = a.out + ((int64_t)b * rows + r) * D + C * lane;
+#pragma unroll
+  for (int c = 0; c < C; ++c) out[c] = (uint16_t)pack_bf16(o[c] * inv, 0.f);
+}
+
+template <int D, bool I8>
+hipError_t launch_d(const AttnArgs& a, const Partial& part, hipStream_t st) {
+  const int R = a.n_tok * (a.Hq / a.c.Hkv);
+  const int nt = R <= 16 ? 1 : R <= 32 || D == 256 ? 2 : 4;
+  const dim3 grid(part.splits, a.c.Hkv * ((R + 16 * nt - 1) / (16 * nt)), a.n_seqs), block(64 * kWaves);
+  if (nt == 1) hipLaunchKernelGGL((attn_decode_kernel<D, I8, 1>), grid, block, 0, st, a, part);
+  else if (nt == 2) hipLaunchKernelGGL((attn_decode_kernel<D, I8, 2>), grid, block, 0, st, a, part);
+  else if constexpr (D < 256) hipLaunchKernelGGL((attn_decode_kernel<D, I8, 4>), grid, block, 0, st, a, part);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || part.splits == 1) return e;
+  hipLaunchKernelGGL((attn_join_kernel<D>), dim3((uint32_t)(a.n_seqs * a.n_tok * a.Hq)), dim3(64), 0, st, a, part);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// Most splits of any length up to max_kv: the rule steps up at 16,384.
+static int most_splits(int max_kv) {
+  int s = n_splits(max_kv);
+  if (max_kv > 16384) s = std::max(s, n_splits(16384));
+  return s;
+}
+
+int64_t attn_decode_bytes(int dim, int Hq, int batch, int n_tok, int max_kv) {
+  const int64_t s = most_splits(max_kv);
+  return s == 1 ? 0 : s * batch * n_tok * Hq * (dim + 2) * 4;
+}
+
+hipError_t launch_attn_decode(const AttnArgs& a, void* workspace, hipStream_t st) {
+  Partial part{static_cast<float*>(workspace), nullptr, most_splits(a.max_kv)};
+  part.ml = reinterpret_cast<float2*>(part.o + (int64_t)a.n_seqs * part.splits * a.n_tok * a.Hq * a.c.dim);
+  switch (a.c.dim) {
+    case 64: return a.c.i8 ? launch_d<64, true>(a, part, st) : launch_d<64, false>(a, part, st);
+    case 128: return a.c.i8 ? launch_d<128, true>(a, part, st) : launch_d<128, false>(a, part, st);
+    default: return a.c.i8 ? launch_d<256, true>(a, part, st) : launch_d<256, false>(a, part, st);
+  }
+}
+
+}  // namespace gdn

@@ -545,7 +545,7 @@ gdn_status gdn_attn_packed(const gdn_cache* cache, int32_t num_q_heads, float sc
   if (n_tokens == 0) return GDN_OK;
   a.cu = cu_seqlens;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  return finish_launch(gdn::launch_attn(a, s), s);
+  return finish_launch(gdn::launch_attn_packed(a, s), s);
 }
 
 gdn_status gdn_attn_decode_workspace(const gdn_cache* cache, int32_t num_q_heads, int32_t batch, int32_t n_tok,
