@@ -109,9 +109,12 @@ def filled(rng, lens, hkv, page, d, code, k_scale=1.0, v_scale=1.0):
 def attn_bound(o, mass, dot, d, keys):
     """Largest error of a bf16 output: half a step of the output (2^-8 of its
     value), half a bf16 step of each probability (2^-8 of sum p |v|), and the
-    fp32 work.  A score of `dot` = scale sum |q k| is summed from d products,
+    fp32 work.  Where the sum is of the rounded probabilities p (1 + e), |e| <=
+    2^-8, the quotient sum p (1 + e) v / sum p (1 + e) has besides those e of
+    the numerator a denominator between 1 - 2^-8 and 1 + 2^-8: another 2^-8 of
+    the output (and a second order, below).  A score of `dot` = scale sum |q k| is summed from d products,
     each sum off by 2^-24 of it at most, and exponentiated with a relative error
     of 2^-22 of its size: p is off by that much of itself twice (numerator and
     sum); the sums over the keys add keys 2^-24."""
     p = 2 * dot * ((d + 4) * 2.0 ** -24 + 2.0 ** -22) + (keys + 8) * 2.0 ** -24 + 2.0 ** -20
-    return 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + p) * (1 + 2.0 ** -8) * mass + 2.0 ** -126
+    return (2 * 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + p) * mass) * (1 + 2.0 ** -7) + 2.0 ** -126
