@@ -3,11 +3,11 @@
 //
 // The rows of a prompt that share a kv head (tokens x Hq / Hkv heads) are
 // packed and dealt out to workgroups of four waves, 32 MB rows a wave.  Every
-// wave computes, for 64 keys at a time,
+// wave computes, for 32 keys at a time,
 //   S^T = K Q^T and O^T += V^T P^T   (32x32x16 products; columns = query rows)
-// from tiles that the workgroup stages in LDS as bf16: the 8-bit codes are
-// converted once per workgroup, exactly, and a tile's operand is read once for
-// all MB row blocks of a wave.
+// from tiles of 64 keys that the workgroup stages in LDS as bf16: the 8-bit
+// codes are converted once per workgroup, exactly, and a tile's operand is read
+// once for all MB row blocks of a wave.
 //
 // A product's result holds in lane half h the rows 8 a + 4 h + b of a column
 // (a, b = 0 .. 3), and its second operand wants there the contraction indices
@@ -19,39 +19,37 @@
 // LDS rows are permuted in 16-byte chunks (chunk ^ row), so that the reads of
 // eight lanes at one chunk of eight rows touch all banks.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_device.h"
 
 namespace gdn {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 8;
+constexpr int kTile = 64;      // keys staged at a time; a step takes 32
 constexpr float kLazy = 8.f;   // the running maximum follows once it lags by this many powers of two
 
-__device__ __forceinline__ float max_halves(float x) {
+__device__ __forceinline__ uint2 both_halves(float x) {
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   const uint32_t u = __float_as_uint(x);
   const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(u, u, false, false));
+  return make_uint2(r.x, r.y);
+}
+__device__ __forceinline__ float max_halves(float x) {
+  const uint2 r = both_halves(x);
   return fmaxf(__uint_as_float(r.x), __uint_as_float(r.y));
 }
 __device__ __forceinline__ float add_halves(float x) {
-  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-  const uint32_t u = __float_as_uint(x);
-  const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(u, u, false, false));
+  const uint2 r = both_halves(x);
   return __uint_as_float(r.x) + __uint_as_float(r.y);
 }
 
 // The permutation of a key row's chunks; the eight keys that eight lanes read
 // together are 0 .. 3 and 8 .. 11 of 16, or the others.
-template <int KC>
+template <int D>
 __device__ __forceinline__ int swizzle(int key) {
-  return KC == 8 ? (key & 3) | ((key >> 1) & 4) : key & 15;
-}
-
-// The same for a channel row of KT keys (128 or 64 bytes) of the value tile.
-template <int KT>
-__device__ __forceinline__ int swizzle_v(int c) {
-  return KT == 64 ? c & 7 : (c >> 2) & 3;
+  return D == 64 ? (key & 3) | ((key >> 1) & 4) : key & 15;
 }
 
 // x + both bf16 of a dword.
@@ -63,28 +61,17 @@ __device__ __forceinline__ float add_pair(uint32_t two, float x) {
 typedef const int32_t __attribute__((address_space(4)))* ConstI32;
 typedef const float __attribute__((address_space(4)))* ConstF32;
 
-// One 16-key piece of a tile: its page (-1: not held) and scales, uniform.
-struct Piece {
-  int page;
-  float ks, vs;
-};
-
-// KT: keys per staged tile (64 or 32); a step of the loop takes 32 keys.
-template <int D, bool I8, int MB, int KT>
-__global__ void __launch_bounds__(64 * kWaves, 1) attn_packed_kernel(const AttnArgs a, const int units) {
+template <int D, bool I8, int MB>
+__global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnArgs a, const int units) {
   constexpr int M = 32 * MB * kWaves;   // rows of a workgroup
-  constexpr int KC = D / 8;             // 16-byte chunks of a key row
   constexpr int KS = D / 16;            // contraction steps of a score
   constexpr int OB = D / 32;            // 32-channel blocks of the output
-  constexpr int SUB = KT / 32;          // steps per tile
-  constexpr int AHEAD = SUB == 2 ? 1 : 2;   // tiles staged ahead of the one in use
-  constexpr int VRING = AHEAD + 2;
-  constexpr int NP = KT / 16;           // 16-key pieces of a tile
-  constexpr int NL = KT * D / (64 * kWaves * 16);   // 16-byte loads of codes per lane, keys and values each
-  constexpr int PER = kWaves / NP;      // waves that share a piece
-  __shared__ __align__(16) uint16_t kl[2][KT * D];       // [key][d]
-  __shared__ __align__(16) uint16_t vl[VRING][D * KT];   // [channel][key]
-  __shared__ uint32_t nan_keys[VRING][kWaves];           // keys of a tile with a NaN value, per staging wave
+  constexpr int NU = D / 64;            // units of 8 codes per lane and tile, keys and values each
+  constexpr int KBYTES = kTile * D * 2; // a staged tile of keys [key][d], or of values [channel][key]
+  __shared__ __align__(16) char lds[4 * KBYTES];        // keys of two tiles, values of two tiles
+  __shared__ __align__(16) float4 pieces[4][4];         // of four tiles: each 16 keys' scales
+  __shared__ uint32_t nan_keys[4][kWaves];              // of four tiles: keys with a NaN value
+  char* const vlds = lds + 2 * KBYTES;
 
   const int hk = blockIdx.x % a.c.Hkv;
   const int unit = units - 1 - (int)(blockIdx.x / a.c.Hkv);   // late rows see most keys: first
@@ -149,158 +136,176 @@ __global__ void __launch_bounds__(64 * kWaves, 1) attn_packed_kernel(const AttnA
       for (int e = 0; e < 16; ++e) o[t][x][e] = 0.f;
   }
 
+  // ---- staging: two waves bring a 16-key piece of a tile ----
+  const int piece = wave >> 1, part = wave & 1;
   const int shift = a.c.page_shift, pmask = (1 << shift) - 1;
   const ConstI32 table = (ConstI32)(a.table + (int64_t)s * a.max_pages);
-  auto page_at = [&](int key) -> int {
-    const int p = table[min(key, max(keys, 1) - 1) >> shift];   // no branch
-    return key < keys && p >= 0 && p < a.c.n_pages ? p : -1;
+  uint2 kr[NU], vr[NU];
+  int page = -1, key = 0;   // the wave's piece of the tile looked up last: its page (-1: none) and first key
+  int64_t base = 0;         // its codes
+  float ks = 0.f, vs = 0.f;
+  auto look_up = [&](int tile) {
+    key = tile * kTile + 16 * piece;
+    const int p = table[min(key, max(keys, 1) - 1) >> shift];
+    page = key < keys && p >= 0 && p < a.c.n_pages ? p : -1;
+    const int64_t e = (int64_t)max(page, 0) * a.c.Hkv + hk;
+    base = ((e << shift) + (key & pmask)) * D;
+    ks = ((ConstF32)a.c.ks)[e];
+    vs = ((ConstF32)a.c.vs)[e];
   };
-  auto piece_at = [&](int key) -> Piece {
-    Piece p;
-    p.page = page_at(key);
-    const int64_t e = (int64_t)max(p.page, 0) * a.c.Hkv + hk;
-    p.ks = ((ConstF32)a.c.ks)[e];
-    p.vs = ((ConstF32)a.c.vs)[e];
-    return p;
-  };
-
-  // ---- staging: a wave brings 1 / PER of one 16-key piece of a tile ----
-  uint4 kr[NL], vr[NL];
-  const int my_piece = wave / PER, my_part = wave % PER;
-  int fetched = 0, page = -1;   // the tile in kr, vr and its page
-  auto fetch = [&](int tile) {
-    fetched = tile;
-    const int key = tile * KT + 16 * my_piece;
-    page = page_at(key);
-    const int64_t base = page_base(a.c, max(page, 0), hk) + (key & pmask) * D + my_part * (NL * 1024) + lane * 16;
+  auto fetch = [&](const uint8_t* from, uint2(&r)[NU]) {
+    const uint8_t* const p = from + base + part * 8 * D;
+    if constexpr (NU == 1) {
+      r[0] = *reinterpret_cast<const uint2*>(p + lane * 8);
+    } else {
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      kr[i] = *reinterpret_cast<const uint4*>(a.c.k + base + i * 1024);
-      vr[i] = *reinterpret_cast<const uint4*>(a.c.v + base + i * 1024);
+      for (int i = 0; i < NU / 2; ++i) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p + i * 1024 + lane * 16);
+        r[2 * i] = make_uint2(w.x, w.y);
+        r[2 * i + 1] = make_uint2(w.z, w.w);
+      }
     }
   };
+  auto value_scale = [&]() { return page < 0 ? 1.f : fmaxf(vs, kMinScale); };
   // Values that not every row of the workgroup may see: what lies behind the
   // last key or in a page not held may be anything, and a NaN that a row does
   // not see would get into it as 0 * NaN.  The former become 0; so do NaN
   // values, whose keys then score NaN for the rows that see them.
-  auto clean = [&]() {
-    if ((fetched + 1) * KT <= wg_free && page >= 0) return;
-    const int left = page < 0 ? 0 : keys - (fetched * KT + 16 * my_piece);
+  auto clean = [&](int tile) {
+    if ((tile + 1) * kTile <= wg_free && page >= 0) return;
     uint32_t found = 0;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      uint32_t w[4] = {vr[i].x, vr[i].y, vr[i].z, vr[i].w};
+    for (int x = 0; x < NU; ++x) {
+      const int second = NU == 1 ? lane & 1 : x & 1;   // which 8 of the 16 keys
+      const int left = (page < 0 ? 0 : keys - key) - 8 * second;
+      uint32_t w[2] = {vr[x].x, vr[x].y};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 2; ++j) {
         const int c = left - 4 * j;
         w[j] &= c >= 4 ? 0xFFFFFFFFu : c <= 0 ? 0u : (1u << (8 * c)) - 1;
         if constexpr (!I8) {
           const uint32_t nan = (((w[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
           w[j] &= ~(nan * 0xFFu);
-          found |= ((nan * 0x10204080u) >> 28) << (4 * j);   // the four flags side by side
+          found |= ((nan * 0x10204080u) >> 28) << (8 * second + 4 * j);   // the four flags side by side
         }
       }
-      vr[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      vr[x] = make_uint2(w[0], w[1]);
     }
     if constexpr (!I8) {
 #pragma unroll
       for (int d = 32; d; d >>= 1) found |= __shfl_xor(found, d);
-      if (lane == 0) nan_keys[fetched % VRING][wave] = found;
+      if (lane == 0) nan_keys[tile & 3][wave] = found;
     }
   };
-  auto stage = [&]() {
-    uint16_t* const kd = kl[fetched & 1];
-    uint16_t* const vd = vl[fetched % VRING];
+  // The scales as the steps use them: the scores' factor (at least 2^-126: its
+  // product with a masked score stays -inf), the values' as a power of two and
+  // the inverse of that, which is 0 for a piece that is not held.  Values are
+  // measured in units of the first page's scale, within limits that keep zero
+  // pages and huge ones from pushing the others out of range.
+  float unit_log = 0.f;
+  auto put_scales = [&](int tile) {
+    const float lv = __builtin_amdgcn_logf(value_scale()) - unit_log;
+    if (lane == 0 && part == 0)
+      pieces[tile & 3][piece] = page < 0 ? make_float4(1.f, 0.f, 0.f, 0.f)
+                                        : make_float4(fmaxf(ks * log_scale, 0x1p-126f), lv, exp2_fast(-lv), 0.f);
+  };
+  // LDS addresses of a lane's units of a tile: 8 channels of a key, 8 keys of a channel
+  constexpr int NA = NU == 1 ? 1 : 2;
+  int kput[NA], vput[NA];
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      // 16 codes of one key
-      const int e = my_part * (NL * 1024) + i * 1024 + lane * 16, key = 16 * my_piece + e / D, ch = (e % D) / 8;
-      bf16x8* row = reinterpret_cast<bf16x8*>(kd + key * D);
-      row[ch ^ swizzle<KC>(key)] = codes_to_operand<I8>(kr[i].x, kr[i].y);
-      row[(ch + 1) ^ swizzle<KC>(key)] = codes_to_operand<I8>(kr[i].z, kr[i].w);
-      // 16 keys of one channel
-      const int c = e / 16;
-      bf16x8* col = reinterpret_cast<bf16x8*>(vd + c * KT);
-      col[(2 * my_piece) ^ swizzle_v<KT>(c)] = codes_to_operand<I8>(vr[i].x, vr[i].y);
-      col[(2 * my_piece + 1) ^ swizzle_v<KT>(c)] = codes_to_operand<I8>(vr[i].z, vr[i].w);
-    }
+  for (int x = 0; x < NA; ++x) {
+    const int e = part * 8 * D + (NU == 1 ? lane * 8 : lane * 16 + x * 8), k = 16 * piece + e / D, c = e / 16;
+    kput[x] = k * D * 2 + (((e % D / 8) ^ swizzle<D>(k)) * 16);
+    vput[x] = c * kTile * 2 + (((2 * piece + (e >> 3 & 1)) ^ (c & 7)) * 16);
+  }
+  // (units 2 and 3, D = 256: keys 4 on, channels 64 on)
+  auto put_keys = [&](int buf, int x) {
+    *reinterpret_cast<bf16x8*>(lds + ((kput[x % NA] ^ (x >= 2 ? 4 * 16 : 0)) + buf * KBYTES + (x >= 2 ? 4 * D * 2 : 0))) =
+        codes_to_operand<I8>(kr[x].x, kr[x].y);
+  };
+  auto put_values = [&](int buf, int x) {
+    *reinterpret_cast<bf16x8*>(vlds + (vput[x % NA] + buf * KBYTES + (x >= 2 ? 64 * kTile * 2 : 0))) =
+        codes_to_operand<I8>(vr[x].x, vr[x].y);
   };
 
+  // ---- operands: even ones 16 channels of 32 keys, odd ones 16 keys of 32 channels ----
+  constexpr int OPS = 2 * KS, KA = KS < 8 ? KS : 8;
   const int krow = 16 * (c32 >> 4) + 8 * ((c32 >> 2) & 1) + 4 * ((c32 >> 3) & 1) + (c32 & 3);
-  // scores of step j (32 keys)
-  auto qk = [&](int j, f32x16(&sc)[MB]) {
-    const int key = 32 * (j % SUB) + krow;
-    const bf16x8* row = reinterpret_cast<const bf16x8*>(kl[(j / SUB) & 1] + key * D);
+  int kget[KA], vget[4];
 #pragma unroll
-    for (int t = 0; t < MB; ++t)
+  for (int k = 0; k < KA; ++k) kget[k] = krow * D * 2 + (((2 * k + h) ^ swizzle<D>(krow)) * 16);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) sc[t][e] = 0.f;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const bf16x8 kk = row[(2 * k + h) ^ swizzle<KC>(key)];
-#pragma unroll
-      for (int t = 0; t < MB; ++t) sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kk, q[t][k], sc[t], 0, 0, 0);
+  for (int u = 0; u < 4; ++u) vget[u] = c32 * kTile * 2 + (((2 * u + h) ^ (c32 & 7)) * 16);
+  // jk, jv: steps modulo 4 of the keys and of the values
+  auto operand = [&](int c, int jk, int jv) -> bf16x8 {
+    if (c & 1) {
+      const int x = c >> 2, u = (c >> 1) & 1;
+      return *reinterpret_cast<const bf16x8*>(vlds + (vget[2 * (jv & 1) + u] + (jv >> 1) * KBYTES + x * 32 * kTile * 2));
     }
+    const int k = c >> 1;
+    return *reinterpret_cast<const bf16x8*>(lds + (kget[k % KA] + (jk >> 1) * KBYTES + (jk & 1) * 32 * D * 2 + k / KA * 256));
   };
-  // output blocks x0 .. x1 - 1 gain step j's probabilities times values
-  auto pv = [&](int j, bf16x8(&p)[MB][2], int x0, int x1) {
-    const uint16_t* const vd = vl[(j / SUB) % VRING];
+  // products with operand c: next += keys x queries, or o += values x p
+  auto product = [&](int c, bf16x8 x, f32x16(&next)[MB], bf16x8(&p)[MB][2]) {
 #pragma unroll
-    for (int x = x0; x < x1; ++x) {
-      const int c = 32 * x + c32;
-      const bf16x8* col = reinterpret_cast<const bf16x8*>(vd + c * KT);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const bf16x8 vv = col[(4 * (j % SUB) + 2 * u + h) ^ swizzle_v<KT>(c)];
-#pragma unroll
-        for (int t = 0; t < MB; ++t) o[t][x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vv, p[t][u], o[t][x], 0, 0, 0);
-      }
+    for (int t = 0; t < MB; ++t) {
+      if (c & 1) o[t][c >> 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, p[t][(c >> 1) & 1], o[t][c >> 2], 0, 0, 0);
+      else next[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, q[t][c >> 1], next[t], 0, 0, 0);
     }
   };
 
-  const int steps = (keys + KT - 1) / KT * SUB;
+  const int steps = (keys + kTile - 1) / kTile * 2;
   if (steps > 0) {
+    look_up(0);
+    const int p0 = table[0];
+    const float v0 = ((ConstF32)a.c.vs)[(int64_t)(p0 >= 0 && p0 < a.c.n_pages ? p0 : 0) * a.c.Hkv + hk];
+    unit_log = fminf(fmaxf(__builtin_amdgcn_logf(p0 >= 0 && p0 < a.c.n_pages ? fmaxf(v0, kMinScale) : 1.f), -30.f), 60.f);
+    fetch(a.c.k, kr);
+    fetch(a.c.v, vr);
+    clean(0);
+    put_scales(0);
 #pragma unroll
-    for (int t = 0; t < AHEAD; ++t) {
-      fetch(t);
-      clean();
-      stage();
+    for (int x = 0; x < NU; ++x) {
+      put_keys(0, x);
+      put_values(0, x);
+      put_values(1, x);   // step 0 multiplies these by probabilities of 0: no NaN of old may be there
     }
-    fetch(AHEAD);
+    look_up(1);
+    fetch(a.c.k, kr);
+    fetch(a.c.v, vr);
   }
   __syncthreads();
 
-  Piece pc[2] = {piece_at(0), piece_at(16)};
-  // Values are measured in units of the first page's scale, within limits that
-  // keep zero pages and huge ones from pushing the others out of range.
-  const float unit_log = fminf(fmaxf(__builtin_amdgcn_logf(pc[0].page >= 0 ? fmaxf(pc[0].vs, kMinScale) : 1.f), -30.f), 60.f);
-  // A step finishes the scores of its 32 keys (formed a step before), and
-  // between their exponentials forms the next step's scores and adds the step
-  // before's probabilities times values.
-  auto step = [&](int j, f32x16(&sc)[MB], f32x16(&next)[MB], bf16x8(&before)[MB][2], bf16x8(&p)[MB][2]) {
-    const int key0 = 32 * j, jb = max(j - 1, 0);
-    const bool put = j % SUB == 0;
-    if (put) clean();
-    {
-      const bool held0 = pc[0].page >= 0, held1 = pc[1].page >= 0;
-      if (key0 + 32 > w_free || !held0 || !held1) {
+  // A step turns the scores of its 32 keys (formed a step before) into
+  // probabilities, and meanwhile forms the next step's scores and adds the
+  // step before's probabilities times values.  One wave has a SIMD to itself
+  // and issues one instruction at a time, so what counts is how few there are:
+  // LDS addresses are fixed (four steps are laid out one after the other: two
+  // tiles of two steps), the scales come from LDS, and products are dealt out
+  // evenly between the vector instructions, each operand read LEAD products
+  // before its use; the first EARLY of them run beside the maximum.
+  // Even steps stage the next tile's keys, odd ones its values: a tile's last
+  // reader is past the barrier (at the end of even steps) by then.
+  constexpr int LEAD = 3, EARLY = OPS / 5, PAIRS = 8 * MB;
+  auto step = [&](auto jc, int j, f32x16(&sc)[MB], f32x16(&next)[MB], bf16x8(&before)[MB][2], bf16x8(&p)[MB][2]) {
+    constexpr int J = decltype(jc)::value, JK = (J + 1) & 3, JV = (J + 3) & 3;
+    const int key0 = 32 * j, tile = j >> 1;
+    if ((J & 1) == 0) clean(tile + 1);
+    const float4 pc0 = pieces[tile & 3][2 * (J & 1)], pc1 = pieces[tile & 3][2 * (J & 1) + 1];
+    bf16x8 x[OPS];
 #pragma unroll
-        for (int t = 0; t < MB; ++t)
+    for (int c = 0; c < LEAD; ++c) x[c] = operand(c, JK, JV);
+    if (key0 + 32 > w_free || __any(fminf(pc0.z, pc1.z) == 0.f)) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (!(e < 8 ? held0 : held1) || key0 + 16 * (e >> 3) + 8 * h + (e & 7) > last[t]) sc[t][e] = -__builtin_inff();
-      }
+      for (int t = 0; t < MB; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if ((e < 8 ? pc0.z : pc1.z) == 0.f || key0 + 16 * (e >> 3) + 8 * h + (e & 7) > last[t]) sc[t][e] = -__builtin_inff();
       if constexpr (!I8) {
-        if ((j / SUB + 1) * KT > wg_free) {
-          const uint32_t* const f = nan_keys[(j / SUB) % VRING];
-          const int pa = 2 * (j % SUB);
-          uint32_t nan[2] = {0, 0};
-#pragma unroll
-          for (int w = 0; w < PER; ++w) {
-            nan[0] |= f[pa * PER + w];
-            nan[1] |= f[(pa + 1) * PER + w];
-          }
-          if (nan[0] | nan[1]) {
+        if ((tile + 1) * kTile > wg_free) {
+          const uint32_t* const f = nan_keys[tile & 3] + 4 * (J & 1);
+          const uint32_t nan[2] = {f[0] | f[1], f[2] | f[3]};
+          if (__any(nan[0] | nan[1])) {
 #pragma unroll
             for (int t = 0; t < MB; ++t)
 #pragma unroll
@@ -309,84 +314,97 @@ __global__ void __launch_bounds__(64 * kWaves, 1) attn_packed_kernel(const AttnA
           }
         }
       }
-      // at least 2^-126: a product with a masked score stays -inf
-      float ks[2], lv[2], iv[2];
+    }
+#pragma unroll
+    for (int t = 0; t < MB; ++t)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) next[t][e] = 0.f;
+#pragma unroll
+    for (int c = 0; c < EARLY; ++c) {
+      x[c + LEAD] = operand(c + LEAD, JK, JV);
+      product(c, x[c], next, before);
+    }
+    float mx[MB];
+    bool grow = false;
+#pragma unroll
+    for (int t = 0; t < MB; ++t) {
+      float y[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const bool held = u ? held1 : held0;
-        ks[u] = held ? fmaxf(pc[u].ks * log_scale, 0x1p-126f) : 1.f;
-        const float vs = held ? fmaxf(pc[u].vs, kMinScale) : 1.f;
-        lv[u] = __builtin_amdgcn_logf(vs) - unit_log;
-        iv[u] = exp2_fast(-lv[u]);
+        y[u] = sc[t][8 * u];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) y[u] = fmaxf(y[u], sc[t][8 * u + e]);
       }
-      pc[0] = piece_at(key0 + 32);
-      pc[1] = piece_at(key0 + 48);
-      float mx[MB];
-      bool grow = false;
+      mx[t] = max_halves(fmaxf(y[0] * pc0.x, y[1] * pc1.x));
+      grow |= mx[t] > m[t] + kLazy;
+    }
+    if (__any(grow)) {
+      // the measure is a whole number, so the factor is a power of two and
+      // exact, also for the probabilities that are still to be added
 #pragma unroll
       for (int t = 0; t < MB; ++t) {
-        float x[2];
+        const float m1 = mx[t] > m[t] + kLazy ? ceilf(mx[t]) : m[t];
+        const float again = m1 == m[t] ? 1.f : exp2_fast(m[t] - m1);
+        l[t] *= again;
+#pragma unroll
+        for (int b = 0; b < OB; ++b) {
+          o[t][b] *= again;
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          x[u] = sc[t][8 * u];
+          u32x4 w = __builtin_bit_cast(u32x4, before[t][u]);
 #pragma unroll
-          for (int e = 1; e < 8; ++e) x[u] = fmaxf(x[u], sc[t][8 * u + e]);
+          for (int i = 0; i < 4; ++i) w[i] = pack_bf16(lo_bf16(w[i]) * again, hi_bf16(w[i]) * again);
+          before[t][u] = __builtin_bit_cast(bf16x8, w);
         }
-        mx[t] = max_halves(fmaxf(x[0] * ks[0], x[1] * ks[1]));
-        grow |= mx[t] > m[t] + kLazy;
-      }
-      if (__any(grow)) {
-        // the measure is a whole number, so the factor is a power of two and
-        // exact, also for the probabilities that are still to be added
-#pragma unroll
-        for (int t = 0; t < MB; ++t) {
-          const float m1 = mx[t] > m[t] + kLazy ? ceilf(mx[t]) : m[t];
-          const float again = m1 == m[t] ? 1.f : exp2_fast(m[t] - m1);
-          l[t] *= again;
-#pragma unroll
-          for (int x = 0; x < OB; ++x) {
-            asm volatile("" : "+a"(o[t][x]));   // its registers are read here, not before the branch
-            o[t][x] *= again;
-          }
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            u32x4 w = __builtin_bit_cast(u32x4, before[t][u]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = pack_bf16(lo_bf16(w[i]) * again, hi_bf16(w[i]) * again);
-            before[t][u] = __builtin_bit_cast(bf16x8, w);
-          }
-          m[t] = m1;
-        }
-      }
-      qk(j + 1, next);
-      pv(jb, before, 0, OB);
-      if (put) stage();
-#pragma unroll
-      for (int t = 0; t < MB; ++t) {
-        const float base = m[t] == -__builtin_inff() ? 0.f : m[t];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          // p times its value's scale, a power of two, rounded to bf16 once;
-          // the sum is of the rounded ones, so a row that one key takes is
-          // that key's value exactly
-          const float b = base - lv[u];
-          u32x4 w;
-          float sum = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t two = pack_bf16(exp2_fast(fmaf(sc[t][8 * u + 2 * i], ks[u], -b)),
-                                           exp2_fast(fmaf(sc[t][8 * u + 2 * i + 1], ks[u], -b)));
-            w[i] = two;
-            sum = add_pair(two, sum);
-          }
-          l[t] = fmaf(sum, iv[u], l[t]);
-          asm volatile("" : "+v"(w));   // here, not at its use in the next step
-          p[t][u] = __builtin_bit_cast(bf16x8, w);
-        }
+        m[t] = m1;
       }
     }
-    if (put) {
-      fetch(fetched + 1);
+    float off[MB][2], sum[MB][2];
+#pragma unroll
+    for (int t = 0; t < MB; ++t) {
+      const float b = m[t] == -__builtin_inff() ? 0.f : m[t];
+      off[t][0] = pc0.y - b;
+      off[t][1] = pc1.y - b;
+      sum[t][0] = sum[t][1] = 0.f;
+    }
+    u32x4 w[MB][2];
+#pragma unroll
+    for (int c = EARLY; c < OPS; ++c) {
+      if (c + LEAD < OPS) x[c + LEAD] = operand(c + LEAD, JK, JV);
+      product(c, x[c], next, before);
+      // p times its value's scale, a power of two, rounded to bf16 once; the
+      // sum is of the rounded ones, so a row that one key takes is that key's
+      // value exactly
+#pragma unroll
+      for (int e = (c - EARLY) * PAIRS / (OPS - EARLY); e < (c - EARLY + 1) * PAIRS / (OPS - EARLY); ++e) {
+        const int t = e / 8, u = (e / 4) & 1, i = e & 3;
+        const float f = u ? pc1.x : pc0.x;
+        uint32_t two = pack_bf16(exp2_fast(fmaf(sc[t][8 * u + 2 * i], f, off[t][u])),
+                                 exp2_fast(fmaf(sc[t][8 * u + 2 * i + 1], f, off[t][u])));
+        asm volatile("" : "+v"(two));   // formed here, not at its use in the next step
+        w[t][u][i] = two;
+        sum[t][u] = add_pair(two, sum[t][u]);
+      }
+#pragma unroll
+      for (int e = (c - EARLY) * NU / (OPS - EARLY); e < (c - EARLY + 1) * NU / (OPS - EARLY); ++e) {
+        if (J & 1) put_values((J >> 1) ^ 1, e);
+        else put_keys((J >> 1) ^ 1, e);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int t = 0; t < MB; ++t) {
+      l[t] = fmaf(sum[t][1], pc1.z, fmaf(sum[t][0], pc0.z, l[t]));
+#pragma unroll
+      for (int u = 0; u < 2; ++u) p[t][u] = __builtin_bit_cast(bf16x8, w[t][u]);
+    }
+    if (J & 1) {
+      fetch(a.c.v, vr);      // of the tile looked up a step before
+    } else {
+      put_scales(tile + 1);
+      look_up(tile + 2);
+      fetch(a.c.k, kr);
       __syncthreads();
     }
   };
@@ -394,15 +412,31 @@ __global__ void __launch_bounds__(64 * kWaves, 1) attn_packed_kernel(const AttnA
   f32x16 sa[MB], sb[MB];
   bf16x8 pa[MB][2], pb[MB][2];
 #pragma unroll
-  for (int t = 0; t < MB; ++t) pa[t][0] = pa[t][1] = pb[t][0] = pb[t][1] = bf16x8{};
-  if (steps > 0) qk(0, sa);
-  for (int j = 0; j < steps; j += 2) {
-    step(j, sa, sb, pb, pa);
-    if (j + 1 < steps) step(j + 1, sb, sa, pa, pb);
+  for (int t = 0; t < MB; ++t) {
+    pa[t][0] = pa[t][1] = pb[t][0] = pb[t][1] = bf16x8{};
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sa[t][e] = sb[t][e] = 0.f;
   }
   if (steps > 0) {
-    if (steps & 1) pv(steps - 1, pa, 0, OB);
-    else pv(steps - 1, pb, 0, OB);
+#pragma unroll
+    for (int c = 0; c < OPS; c += 2) product(c, operand(c, 0, 0), sa, pa);
+  }
+  int j = 0;
+  for (; j + 4 <= steps; j += 4) {   // (a way out of its middle would cost registers)
+    step(std::integral_constant<int, 0>(), j, sa, sb, pb, pa);
+    step(std::integral_constant<int, 1>(), j + 1, sb, sa, pa, pb);
+    step(std::integral_constant<int, 2>(), j + 2, sa, sb, pb, pa);
+    step(std::integral_constant<int, 3>(), j + 3, sb, sa, pa, pb);
+  }
+  if (steps & 2) {
+    step(std::integral_constant<int, 0>(), j, sa, sb, pb, pa);
+    step(std::integral_constant<int, 1>(), j + 1, sb, sa, pa, pb);
+  }
+  if (steps > 0) {   // the last step's probabilities
+    const char* const tail = vlds + ((steps >> 1) - 1 & 1) * KBYTES;
+#pragma unroll
+    for (int c = 1; c < OPS; c += 2)
+      product(c, *reinterpret_cast<const bf16x8*>(tail + vget[2 + ((c >> 1) & 1)] + (c >> 2) * 32 * kTile * 2), sa, pb);
   }
 
 #pragma unroll
@@ -423,11 +457,10 @@ __global__ void __launch_bounds__(64 * kWaves, 1) attn_packed_kernel(const AttnA
 
 template <int D, bool I8>
 hipError_t launch_d(const AttnArgs& a, hipStream_t st) {
-  constexpr int MB = D == 256 ? 1 : 2;
+  constexpr int MB = 1;
   constexpr int M = 32 * MB * kWaves;
   const int64_t units = (int64_t)a.n_tokens * (a.Hq / a.c.Hkv) / M + a.n_seqs;
-  constexpr int KT = D == 256 ? 32 : 64;
-  hipLaunchKernelGGL((attn_packed_kernel<D, I8, MB, KT>), dim3((uint32_t)(units * a.c.Hkv)), dim3(64 * kWaves), 0, st, a, (int)units);
+  hipLaunchKernelGGL((attn_packed_kernel<D, I8, MB>), dim3((uint32_t)(units * a.c.Hkv)), dim3(64 * kWaves), 0, st, a, (int)units);
   return hipGetLastError();
 }
 
