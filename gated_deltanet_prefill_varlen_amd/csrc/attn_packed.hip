@@ -2,12 +2,11 @@
 // prompt, so the matrix cores bound it.
 //
 // The rows of a prompt that share a kv head (tokens x Hq / Hkv heads) are
-// packed and dealt out to workgroups of four waves, 32 MB rows a wave.  Every
-// wave computes, for 32 keys at a time,
+// packed and dealt out to workgroups of eight waves, 32 rows a wave.  Every
+// wave computes, a tile of 64 (head_dim 256: 32) keys at a time,
 //   S^T = K Q^T and O^T += V^T P^T   (32x32x16 products; columns = query rows)
-// from tiles of 64 keys that the workgroup stages in LDS as bf16: the 8-bit
-// codes are converted once per workgroup, exactly, and a tile's operand is read
-// once for all MB row blocks of a wave.
+// from tiles that the workgroup stages in LDS as bf16, so the 8-bit codes are
+// converted once per workgroup, exactly.
 //
 // A product's result holds in lane half h the rows 8 a + 4 h + b of a column
 // (a, b = 0 .. 3), and its second operand wants there the contraction indices
@@ -16,8 +15,8 @@
 // next product's operand without leaving their lane.  Register group a / 2 is
 // then one 16-key piece of a page: its scales are the same for every lane.
 //
-// LDS rows are permuted in 16-byte chunks (chunk ^ row), so that the reads of
-// eight lanes at one chunk of eight rows touch all banks.
+// LDS rows are permuted in 16-byte chunks, so that the reads of sixteen lanes
+// at one chunk of sixteen rows touch all banks.
 #include <algorithm>
 #include <type_traits>
 
@@ -27,8 +26,8 @@ namespace gdn {
 namespace {
 
 constexpr int kWaves = 8;
-constexpr int kTile = 64;      // keys staged at a time; a step takes 32
-constexpr float kLazy = 8.f;   // the running maximum follows once it lags by this many powers of two
+constexpr int kRows = 32 * kWaves;   // of a workgroup
+constexpr float kLazy = 16.f;  // the running maximum follows once it lags by this many powers of two
 
 __device__ __forceinline__ uint2 both_halves(float x) {
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -45,11 +44,16 @@ __device__ __forceinline__ float add_halves(float x) {
   return __uint_as_float(r.x) + __uint_as_float(r.y);
 }
 
-// The permutation of a key row's chunks; the eight keys that eight lanes read
-// together are 0 .. 3 and 8 .. 11 of 16, or the others.
+// The permutation of a key row's chunks (D = 64: two rows share the banks, and
+// the sixteen keys read together are 0 .. 15 in the order of krow below).
 template <int D>
-__device__ __forceinline__ int swizzle(int key) {
-  return D == 64 ? (key & 3) | ((key >> 1) & 4) : key & 15;
+__device__ __forceinline__ int swizzle_k(int key) {
+  return D == 64 ? (key >> 1) & 7 : key & 15;
+}
+// The same for a channel's row of KT keys.
+template <int KT>
+__device__ __forceinline__ int swizzle_v(int c) {
+  return KT == 64 ? (c >> 1) & 7 : (c >> 2) & 3;
 }
 
 // x + both bf16 of a dword.
@@ -61,123 +65,120 @@ __device__ __forceinline__ float add_pair(uint32_t two, float x) {
 typedef const int32_t __attribute__((address_space(4)))* ConstI32;
 typedef const float __attribute__((address_space(4)))* ConstF32;
 
-template <int D, bool I8, int MB>
+template <int D, bool I8>
 __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnArgs a, const int units) {
-  constexpr int M = 32 * MB * kWaves;   // rows of a workgroup
-  constexpr int KS = D / 16;            // contraction steps of a score
-  constexpr int OB = D / 32;            // 32-channel blocks of the output
-  constexpr int NU = D / 64;            // units of 8 codes per lane and tile, keys and values each
-  constexpr int KBYTES = kTile * D * 2; // a staged tile of keys [key][d], or of values [channel][key]
-  __shared__ __align__(16) char lds[4 * KBYTES];        // keys of two tiles, values of two tiles
-  __shared__ __align__(16) float4 pieces[4][4];         // of four tiles: each 16 keys' scales
-  __shared__ uint32_t nan_keys[4][kWaves];              // of four tiles: keys with a NaN value
-  char* const vlds = lds + 2 * KBYTES;
+  constexpr int KT = D == 256 ? 32 : 64;   // keys of a tile, and of a step
+  constexpr int KB = KT / 32;              // blocks of 32 keys
+  constexpr int NP = KT / 16;              // 16-key pieces, each in one page
+  constexpr int KS = D / 16;               // contraction steps of a score
+  constexpr int OB = D / 32;               // 32-channel blocks of the output
+  constexpr int PARTS = kWaves / NP;       // waves that bring a piece
+  constexpr int NU = KT * D / (64 * kWaves * 8);   // units of 8 codes per lane and tile, keys and values each
+  constexpr int BYTES = KT * D * 2;        // a staged tile of keys [key][d], or of values [channel][key]
+  __shared__ __align__(16) char lds[6 * BYTES];      // three tiles of keys, three of values
+  __shared__ __align__(16) float4 pieces[4][NP];     // of four tiles: each piece's scales
+  __shared__ uint32_t nan_keys[4][kWaves];           // of four tiles: keys with a NaN value
+  char* const vlds = lds + 3 * BYTES;
 
   const int hk = blockIdx.x % a.c.Hkv;
   const int unit = units - 1 - (int)(blockIdx.x / a.c.Hkv);   // late rows see most keys: first
   const int G = a.Hq / a.c.Hkv;
   // unit -> (prompt, its j-th tile of rows): prompt s has the units
-  // cu[s] G / M + s on, at least as many as its tiles
+  // cu[s] G / kRows + s on, at least as many as its tiles
   const ConstI32 cu = (ConstI32)a.cu;
   int lo = 0, hi = a.n_seqs;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if ((int)((int64_t)cu[mid] * G / M) + mid <= unit) lo = mid; else hi = mid;
+    if ((int)((int64_t)cu[mid] * G / kRows) + mid <= unit) lo = mid; else hi = mid;
   }
   const int s = lo, i0 = cu[s], n = min(cu[s + 1], a.n_tokens) - i0;
-  const int64_t first = (int64_t)(unit - (int)((int64_t)i0 * G / M) - s) * M;
+  const int64_t first = (int64_t)(unit - (int)((int64_t)i0 * G / kRows) - s) * kRows;
   const int64_t rows = (int64_t)n * G;
   if (i0 < 0 || first < 0 || first >= rows) return;
   const int L = ((ConstI32)a.kv_len)[s];
   const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  int64_t at[MB];   // this lane's query rows
-  int last[MB];     // the last key each sees
-  const int r0 = (int)first + wave * 32 * MB;
-#pragma unroll
-  for (int t = 0; t < MB; ++t) {
-    const int r = min(r0 + 32 * t + c32, (int)rows - 1), i = r / G;
-    at[t] = (int64_t)(i0 + i) * a.Hq + hk * G + (r - i * G);
-    last[t] = L - n + i;
-  }
+  // this lane's query row and the last key it sees
+  const int r0 = (int)first + wave * 32;
+  const int r = min(r0 + c32, (int)rows - 1), i = r / G, hq = hk * G + (r - i * G);
+  const int64_t at = (int64_t)(i0 + i) * a.Hq + hq;
+  const int last = L - n + i;
   const bool bad = L < 0 || L > a.max_kv;
   // keys that the workgroup's last row sees, and that all of its rows and all
   // of the wave's rows see.  Waves whose rows see fewer keys keep step with the
   // others, their scores masked.
-  const int wg_last = (int)min(first + M, rows) - 1;
+  const int wg_last = (int)min(first + kRows, rows) - 1;
   const int keys = bad ? 0 : max(0, min(L, L - n + wg_last / G + 1));
   const int wg_free = L - n + (int)first / G + 1, w_free = L - n + min(r0, (int)rows - 1) / G + 1;
 
   // queries: the factor's sign goes into them, so that it leaves maxima maxima
-  bf16x8 q[MB][KS];
+  bf16x8 q[KS];
+  const uint16_t* const qp = a.q + (int64_t)(i0 + i) * a.q_stride + hq * D + 8 * h;
 #pragma unroll
-  for (int t = 0; t < MB; ++t) {
-    const int64_t tok = at[t] / a.Hq, hd = at[t] % a.Hq;
-    const uint16_t* p = a.q + tok * a.q_stride + hd * D + 8 * h;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      u32x4 w = *reinterpret_cast<const u32x4*>(p + 16 * k);
-      if (a.scale < 0.f) w ^= 0x80008000u;
-      q[t][k] = __builtin_bit_cast(bf16x8, w);
-    }
+  for (int k = 0; k < KS; ++k) {
+    u32x4 w = *reinterpret_cast<const u32x4*>(qp + 16 * k);
+    if (a.scale < 0.f) w ^= 0x80008000u;
+    q[k] = __builtin_bit_cast(bf16x8, w);
   }
   const float log_scale = fabsf(a.scale) * kLog2e;
 
-  f32x16 o[MB][OB];
-  float m[MB], l[MB];
+  f32x16 o[OB];
+  float m = -__builtin_inff(), l = 0.f;
 #pragma unroll
-  for (int t = 0; t < MB; ++t) {
-    m[t] = -__builtin_inff();
-    l[t] = 0.f;
+  for (int x = 0; x < OB; ++x)
 #pragma unroll
-    for (int x = 0; x < OB; ++x)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) o[t][x][e] = 0.f;
-  }
+    for (int e = 0; e < 16; ++e) o[x][e] = 0.f;
 
-  // ---- staging: two waves bring a 16-key piece of a tile ----
-  const int piece = wave >> 1, part = wave & 1;
+  // ---- staging: PARTS waves bring a 16-key piece of a tile ----
+  const int piece = wave / PARTS, part = wave % PARTS;
   const int shift = a.c.page_shift, pmask = (1 << shift) - 1;
   const ConstI32 table = (ConstI32)(a.table + (int64_t)s * a.max_pages);
-  uint2 kr[NU], vr[NU];
-  int page = -1, key = 0;   // the wave's piece of the tile looked up last: its page (-1: none) and first key
-  int64_t base = 0;         // its codes
+  // The piece of the tile looked up last: its first key, page (-1: none), codes
+  // and scales.  A tile's entry of the table is asked for a tile ahead, and its
+  // scales when the page is known, both early in a half step, so that the waits
+  // at its end cover them.
+  auto entry_of = [&](int tile) -> int { return table[min(tile * KT + 16 * piece, max(keys, 1) - 1) >> shift]; };
+  int entry = 0, key = 0, page = -1;
+  int64_t base = 0;
   float ks = 0.f, vs = 0.f;
   auto look_up = [&](int tile) {
-    key = tile * kTile + 16 * piece;
-    const int p = table[min(key, max(keys, 1) - 1) >> shift];
-    page = key < keys && p >= 0 && p < a.c.n_pages ? p : -1;
+    key = tile * KT + 16 * piece;
+    page = key < keys && entry >= 0 && entry < a.c.n_pages ? entry : -1;
+    entry = entry_of(tile + 1);
     const int64_t e = (int64_t)max(page, 0) * a.c.Hkv + hk;
     base = ((e << shift) + (key & pmask)) * D;
     ks = ((ConstF32)a.c.ks)[e];
     vs = ((ConstF32)a.c.vs)[e];
   };
-  auto fetch = [&](const uint8_t* from, uint2(&r)[NU]) {
-    const uint8_t* const p = from + base + part * 8 * D;
+  uint2 kr[NU], vr[NU];
+  int v_key = 0, v_page = -1;   // of the values in vr
+  auto fetch = [&](const uint8_t* from, uint2(&to)[NU]) {
+    const uint8_t* const p = from + base + part * (16 * D / PARTS);
     if constexpr (NU == 1) {
-      r[0] = *reinterpret_cast<const uint2*>(p + lane * 8);
+      to[0] = *reinterpret_cast<const uint2*>(p + lane * 8);
     } else {
-#pragma unroll
-      for (int i = 0; i < NU / 2; ++i) {
-        const uint4 w = *reinterpret_cast<const uint4*>(p + i * 1024 + lane * 16);
-        r[2 * i] = make_uint2(w.x, w.y);
-        r[2 * i + 1] = make_uint2(w.z, w.w);
-      }
+      const uint4 w = *reinterpret_cast<const uint4*>(p + lane * 16);
+      to[0] = make_uint2(w.x, w.y);
+      to[1] = make_uint2(w.z, w.w);
     }
   };
-  auto value_scale = [&]() { return page < 0 ? 1.f : fmaxf(vs, kMinScale); };
+  auto fetch_values = [&]() {
+    v_key = key;
+    v_page = page;
+    fetch(a.c.v, vr);
+  };
   // Values that not every row of the workgroup may see: what lies behind the
   // last key or in a page not held may be anything, and a NaN that a row does
   // not see would get into it as 0 * NaN.  The former become 0; so do NaN
   // values, whose keys then score NaN for the rows that see them.
   auto clean = [&](int tile) {
-    if ((tile + 1) * kTile <= wg_free && page >= 0) return;
+    if ((tile + 1) * KT <= wg_free && v_page >= 0) return;
     uint32_t found = 0;
 #pragma unroll
     for (int x = 0; x < NU; ++x) {
       const int second = NU == 1 ? lane & 1 : x & 1;   // which 8 of the 16 keys
-      const int left = (page < 0 ? 0 : keys - key) - 8 * second;
+      const int left = (v_page < 0 ? 0 : keys - v_key) - 8 * second;
       uint32_t w[2] = {vr[x].x, vr[x].y};
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -204,263 +205,246 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
   // pages and huge ones from pushing the others out of range.
   float unit_log = 0.f;
   auto put_scales = [&](int tile) {
-    const float lv = __builtin_amdgcn_logf(value_scale()) - unit_log;
+    const float lv = __builtin_amdgcn_logf(page < 0 ? 1.f : fmaxf(vs, kMinScale)) - unit_log;
     if (lane == 0 && part == 0)
       pieces[tile & 3][piece] = page < 0 ? make_float4(1.f, 0.f, 0.f, 0.f)
-                                        : make_float4(fmaxf(ks * log_scale, 0x1p-126f), lv, exp2_fast(-lv), 0.f);
+                                         : make_float4(fmaxf(ks * log_scale, 0x1p-126f), lv, exp2_fast(-lv), 0.f);
   };
   // LDS addresses of a lane's units of a tile: 8 channels of a key, 8 keys of a channel
-  constexpr int NA = NU == 1 ? 1 : 2;
-  int kput[NA], vput[NA];
+  int kput[NU], vput[NU];
 #pragma unroll
-  for (int x = 0; x < NA; ++x) {
-    const int e = part * 8 * D + (NU == 1 ? lane * 8 : lane * 16 + x * 8), k = 16 * piece + e / D, c = e / 16;
-    kput[x] = k * D * 2 + (((e % D / 8) ^ swizzle<D>(k)) * 16);
-    vput[x] = c * kTile * 2 + (((2 * piece + (e >> 3 & 1)) ^ (c & 7)) * 16);
+  for (int x = 0; x < NU; ++x) {
+    const int e = part * (16 * D / PARTS) + (lane * NU + x) * 8, k = 16 * piece + e / D, c = e / 16;
+    kput[x] = k * D * 2 + (((e % D / 8) ^ swizzle_k<D>(k)) * 16);
+    vput[x] = c * KT * 2 + (((2 * piece + (e >> 3 & 1)) ^ swizzle_v<KT>(c)) * 16);
   }
-  // (units 2 and 3, D = 256: keys 4 on, channels 64 on)
   auto put_keys = [&](int buf, int x) {
-    *reinterpret_cast<bf16x8*>(lds + ((kput[x % NA] ^ (x >= 2 ? 4 * 16 : 0)) + buf * KBYTES + (x >= 2 ? 4 * D * 2 : 0))) =
-        codes_to_operand<I8>(kr[x].x, kr[x].y);
+    *reinterpret_cast<bf16x8*>(lds + (kput[x] + buf * BYTES)) = codes_to_operand<I8>(kr[x].x, kr[x].y);
   };
   auto put_values = [&](int buf, int x) {
-    *reinterpret_cast<bf16x8*>(vlds + (vput[x % NA] + buf * KBYTES + (x >= 2 ? 64 * kTile * 2 : 0))) =
-        codes_to_operand<I8>(vr[x].x, vr[x].y);
+    *reinterpret_cast<bf16x8*>(vlds + (vput[x] + buf * BYTES)) = codes_to_operand<I8>(vr[x].x, vr[x].y);
   };
 
   // ---- operands: even ones 16 channels of 32 keys, odd ones 16 keys of 32 channels ----
-  constexpr int OPS = 2 * KS, KA = KS < 8 ? KS : 8;
+  constexpr int OPS = 2 * KB * KS, KA = KS < 8 ? KS : 8;
+  static_assert(KB * KS == NP * OB, "as many operands of keys as of values");
   const int krow = 16 * (c32 >> 4) + 8 * ((c32 >> 2) & 1) + 4 * ((c32 >> 3) & 1) + (c32 & 3);
-  int kget[KA], vget[4];
+  int kget[KA], vget[NP];
 #pragma unroll
-  for (int k = 0; k < KA; ++k) kget[k] = krow * D * 2 + (((2 * k + h) ^ swizzle<D>(krow)) * 16);
+  for (int k = 0; k < KA; ++k) kget[k] = krow * D * 2 + (((2 * k + h) ^ swizzle_k<D>(krow)) * 16);
 #pragma unroll
-  for (int u = 0; u < 4; ++u) vget[u] = c32 * kTile * 2 + (((2 * u + h) ^ (c32 & 7)) * 16);
-  // jk, jv: steps modulo 4 of the keys and of the values
-  auto operand = [&](int c, int jk, int jv) -> bf16x8 {
+  for (int u = 0; u < NP; ++u) vget[u] = c32 * KT * 2 + (((2 * u + h) ^ swizzle_v<KT>(c32)) * 16);
+  auto operand = [&](int c, int kbuf, int vbuf) -> bf16x8 {
     if (c & 1) {
-      const int x = c >> 2, u = (c >> 1) & 1;
-      return *reinterpret_cast<const bf16x8*>(vlds + (vget[2 * (jv & 1) + u] + (jv >> 1) * KBYTES + x * 32 * kTile * 2));
+      const int x = (c >> 1) / NP, u = (c >> 1) % NP;
+      return *reinterpret_cast<const bf16x8*>(vlds + (vget[u] + vbuf * BYTES + x * 32 * KT * 2));
     }
-    const int k = c >> 1;
-    return *reinterpret_cast<const bf16x8*>(lds + (kget[k % KA] + (jk >> 1) * KBYTES + (jk & 1) * 32 * D * 2 + k / KA * 256));
-  };
-  // products with operand c: next += keys x queries, or o += values x p
-  auto product = [&](int c, bf16x8 x, f32x16(&next)[MB], bf16x8(&p)[MB][2]) {
-#pragma unroll
-    for (int t = 0; t < MB; ++t) {
-      if (c & 1) o[t][c >> 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, p[t][(c >> 1) & 1], o[t][c >> 2], 0, 0, 0);
-      else next[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, q[t][c >> 1], next[t], 0, 0, 0);
-    }
+    const int b = (c >> 1) / KS, k = (c >> 1) % KS;
+    return *reinterpret_cast<const bf16x8*>(lds + (kget[k % KA] + kbuf * BYTES + b * 32 * D * 2 + k / KA * 256));
   };
 
-  const int steps = (keys + kTile - 1) / kTile * 2;
-  if (steps > 0) {
-    look_up(0);
-    const int p0 = table[0];
-    const float v0 = ((ConstF32)a.c.vs)[(int64_t)(p0 >= 0 && p0 < a.c.n_pages ? p0 : 0) * a.c.Hkv + hk];
-    unit_log = fminf(fmaxf(__builtin_amdgcn_logf(p0 >= 0 && p0 < a.c.n_pages ? fmaxf(v0, kMinScale) : 1.f), -30.f), 60.f);
-    fetch(a.c.k, kr);
-    fetch(a.c.v, vr);
-    clean(0);
-    put_scales(0);
+  // The waves of one SIMD take turns: while waves 0 - 3 form products, waves
+  // 4 - 7 do everything else, and the other way round after a barrier, so the
+  // matrix cores and the vector units of a SIMD both have work all the time.
+  // (Products dealt out between the vector instructions of one wave overlap
+  // worse: 190 ns for 8 products and 56 vector instructions of a SIMD's two
+  // waves, against 147 ns in turns; the products alone take 136.)
+  //
+  // Step t of a wave: the scores of tile t and the products of step t - 1's
+  // probabilities with its values, and between them tile t + 2's keys and tile
+  // t + 1's values converted; a barrier; the probabilities; a barrier.  Waves
+  // 0 - 3 do the first in half step 2 t, waves 4 - 7 in 2 t + 1.  Tile t's keys
+  // are read in the half steps 2 t - 1 to 2 t + 1, its values in 2 t + 1 to
+  // 2 t + 3 (the first LEAD operands a half step early), and are staged in
+  // 2 t - 4 and 2 t - 3, and in 2 t - 2 and 2 t - 1: three buffers of each do.
+  auto barrier = [&]() {
+    __builtin_amdgcn_sched_barrier(0);   // the halves stay apart
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr int LEAD = D == 256 ? 2 : 4;
+  bf16x8 x[LEAD];     // the first operands of the next products
+  bf16x8 p[NP];       // probabilities
+  auto step = [&](auto jc, int tile) {
+    constexpr int J = decltype(jc)::value, J1 = (J + 1) % 3, J2 = (J + 2) % 3;   // buffers of tiles t, t + 1 and t - 1 or t + 2
+    const int key0 = KT * tile;
+    clean(tile + 1);
+    f32x16 sc[KB];
 #pragma unroll
-    for (int x = 0; x < NU; ++x) {
-      put_keys(0, x);
-      put_values(0, x);
-      put_values(1, x);   // step 0 multiplies these by probabilities of 0: no NaN of old may be there
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sc[b][e] = 0.f;
+    {
+      bf16x8 y[OPS];
+#pragma unroll
+      for (int c = 0; c < LEAD; ++c) y[c] = x[c];
+#pragma unroll
+      for (int c = 0; c < OPS; ++c) {
+        if (c + LEAD < OPS) y[c + LEAD] = operand(c + LEAD, J, J2);
+        const int i = c >> 1;
+        if (c & 1) o[i / NP] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(y[c], p[i % NP], o[i / NP], 0, 0, 0);
+        else sc[i / KS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(y[c], q[i % KS], sc[i / KS], 0, 0, 0);
+        if (c >= OPS / 2) {   // in the second half: the codes have had time to come
+#pragma unroll
+          for (int e = (c - OPS / 2) * 2 * NU / (OPS / 2); e < (c + 1 - OPS / 2) * 2 * NU / (OPS / 2); ++e) {
+            if (e < NU) put_keys(J2, e);
+            else put_values(J1, e - NU);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);   // operands stay LEAD ahead
+      }
     }
-    look_up(1);
-    fetch(a.c.k, kr);
-    fetch(a.c.v, vr);
-  }
-  __syncthreads();
+    float4 pc[NP];
+#pragma unroll
+    for (int u = 0; u < NP; ++u) pc[u] = pieces[tile & 3][u];
+    barrier();
 
-  // A step turns the scores of its 32 keys (formed a step before) into
-  // probabilities, and meanwhile forms the next step's scores and adds the
-  // step before's probabilities times values.  One wave has a SIMD to itself
-  // and issues one instruction at a time, so what counts is how few there are:
-  // LDS addresses are fixed (four steps are laid out one after the other: two
-  // tiles of two steps), the scales come from LDS, and products are dealt out
-  // evenly between the vector instructions, each operand read LEAD products
-  // before its use; the first EARLY of them run beside the maximum.
-  // Even steps stage the next tile's keys, odd ones its values: a tile's last
-  // reader is past the barrier (at the end of even steps) by then.
-  constexpr int LEAD = 3, EARLY = OPS / 5, PAIRS = 8 * MB;
-  auto step = [&](auto jc, int j, f32x16(&sc)[MB], f32x16(&next)[MB], bf16x8(&before)[MB][2], bf16x8(&p)[MB][2]) {
-    constexpr int J = decltype(jc)::value, JK = (J + 1) & 3, JV = (J + 3) & 3;
-    const int key0 = 32 * j, tile = j >> 1;
-    if ((J & 1) == 0) clean(tile + 1);
-    const float4 pc0 = pieces[tile & 3][2 * (J & 1)], pc1 = pieces[tile & 3][2 * (J & 1) + 1];
-    bf16x8 x[OPS];
+    put_scales(tile + 2);
+    fetch_values();        // of tile t + 2
+    look_up(tile + 3);
+    fetch(a.c.k, kr);
+    float held = pc[0].z;
 #pragma unroll
-    for (int c = 0; c < LEAD; ++c) x[c] = operand(c, JK, JV);
-    if (key0 + 32 > w_free || __any(fminf(pc0.z, pc1.z) == 0.f)) {
+    for (int u = 1; u < NP; ++u) held = fminf(held, pc[u].z);
+    if (key0 + KT > w_free || __any(held == 0.f)) {
 #pragma unroll
-      for (int t = 0; t < MB; ++t)
+      for (int b = 0; b < KB; ++b)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if ((e < 8 ? pc0.z : pc1.z) == 0.f || key0 + 16 * (e >> 3) + 8 * h + (e & 7) > last[t]) sc[t][e] = -__builtin_inff();
+          if (pc[2 * b + (e >> 3)].z == 0.f || key0 + 32 * b + 16 * (e >> 3) + 8 * h + (e & 7) > last) sc[b][e] = -__builtin_inff();
       if constexpr (!I8) {
-        if ((tile + 1) * kTile > wg_free) {
-          const uint32_t* const f = nan_keys[tile & 3] + 4 * (J & 1);
-          const uint32_t nan[2] = {f[0] | f[1], f[2] | f[3]};
-          if (__any(nan[0] | nan[1])) {
+        if (key0 + KT > wg_free) {
+          uint32_t nan[NP], any = 0;
 #pragma unroll
-            for (int t = 0; t < MB; ++t)
+          for (int u = 0; u < NP; ++u) {
+            nan[u] = 0;
+#pragma unroll
+            for (int w = 0; w < PARTS; ++w) nan[u] |= nan_keys[tile & 3][u * PARTS + w];
+            any |= nan[u];
+          }
+          if (__any(any)) {
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                if ((nan[e >> 3] >> (8 * h + (e & 7)) & 1) && sc[t][e] != -__builtin_inff()) sc[t][e] = __builtin_nanf("");
+                if ((nan[2 * b + (e >> 3)] >> (8 * h + (e & 7)) & 1) && sc[b][e] != -__builtin_inff()) sc[b][e] = __builtin_nanf("");
           }
         }
       }
     }
+    float mx = -__builtin_inff();
 #pragma unroll
-    for (int t = 0; t < MB; ++t)
+    for (int u = 0; u < NP; ++u) {
+      float y = sc[u >> 1][8 * (u & 1)];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) next[t][e] = 0.f;
-#pragma unroll
-    for (int c = 0; c < EARLY; ++c) {
-      x[c + LEAD] = operand(c + LEAD, JK, JV);
-      product(c, x[c], next, before);
+      for (int e = 1; e < 8; ++e) y = fmaxf(y, sc[u >> 1][8 * (u & 1) + e]);
+      mx = fmaxf(mx, y * pc[u].x);
     }
-    float mx[MB];
-    bool grow = false;
-#pragma unroll
-    for (int t = 0; t < MB; ++t) {
-      float y[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        y[u] = sc[t][8 * u];
-#pragma unroll
-        for (int e = 1; e < 8; ++e) y[u] = fmaxf(y[u], sc[t][8 * u + e]);
-      }
-      mx[t] = max_halves(fmaxf(y[0] * pc0.x, y[1] * pc1.x));
-      grow |= mx[t] > m[t] + kLazy;
-    }
+    mx = max_halves(mx);
+    const bool grow = mx > m + kLazy;
     if (__any(grow)) {
-      // the measure is a whole number, so the factor is a power of two and
-      // exact, also for the probabilities that are still to be added
+      // the measure is a whole number, so the factor is a power of two and exact
+      const float m1 = grow ? ceilf(mx) : m;
+      const float again = grow ? exp2_fast(m - m1) : 1.f;
+      l *= again;
 #pragma unroll
-      for (int t = 0; t < MB; ++t) {
-        const float m1 = mx[t] > m[t] + kLazy ? ceilf(mx[t]) : m[t];
-        const float again = m1 == m[t] ? 1.f : exp2_fast(m[t] - m1);
-        l[t] *= again;
+      for (int b = 0; b < OB; ++b) o[b] *= again;
+      m = m1;
+    }
+    const float less = m == -__builtin_inff() ? 0.f : m;
+    // p times its value's scale, a power of two, rounded to bf16 once; the sum
+    // is of the rounded ones, so a row that one key takes is that key's value
+    // exactly
 #pragma unroll
-        for (int b = 0; b < OB; ++b) {
-          o[t][b] *= again;
-        }
+    for (int u = 0; u < NP; ++u) {
+      const float off = pc[u].y - less;
+      float sum = 0.f;
+      u32x4 w;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          u32x4 w = __builtin_bit_cast(u32x4, before[t][u]);
+      for (int i = 0; i < 4; ++i) {
+        const float s0 = sc[u >> 1][8 * (u & 1) + 2 * i], s1 = sc[u >> 1][8 * (u & 1) + 2 * i + 1];
+        w[i] = pack_bf16(exp2_fast(fmaf(s0, pc[u].x, off)), exp2_fast(fmaf(s1, pc[u].x, off)));
+        sum = add_pair(w[i], sum);
+      }
+      l = fmaf(sum, pc[u].z, l);
+      asm volatile("" : "+v"(w), "+v"(l));   // formed here, not beside the next products
+      p[u] = __builtin_bit_cast(bf16x8, w);
+      if (u == NP - 2) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = pack_bf16(lo_bf16(w[i]) * again, hi_bf16(w[i]) * again);
-          before[t][u] = __builtin_bit_cast(bf16x8, w);
-        }
-        m[t] = m1;
+        for (int c = 0; c < LEAD; ++c) x[c] = operand(c, J1, J);
       }
     }
-    float off[MB][2], sum[MB][2];
-#pragma unroll
-    for (int t = 0; t < MB; ++t) {
-      const float b = m[t] == -__builtin_inff() ? 0.f : m[t];
-      off[t][0] = pc0.y - b;
-      off[t][1] = pc1.y - b;
-      sum[t][0] = sum[t][1] = 0.f;
-    }
-    u32x4 w[MB][2];
-#pragma unroll
-    for (int c = EARLY; c < OPS; ++c) {
-      if (c + LEAD < OPS) x[c + LEAD] = operand(c + LEAD, JK, JV);
-      product(c, x[c], next, before);
-      // p times its value's scale, a power of two, rounded to bf16 once; the
-      // sum is of the rounded ones, so a row that one key takes is that key's
-      // value exactly
-#pragma unroll
-      for (int e = (c - EARLY) * PAIRS / (OPS - EARLY); e < (c - EARLY + 1) * PAIRS / (OPS - EARLY); ++e) {
-        const int t = e / 8, u = (e / 4) & 1, i = e & 3;
-        const float f = u ? pc1.x : pc0.x;
-        uint32_t two = pack_bf16(exp2_fast(fmaf(sc[t][8 * u + 2 * i], f, off[t][u])),
-                                 exp2_fast(fmaf(sc[t][8 * u + 2 * i + 1], f, off[t][u])));
-        asm volatile("" : "+v"(two));   // formed here, not at its use in the next step
-        w[t][u][i] = two;
-        sum[t][u] = add_pair(two, sum[t][u]);
-      }
-#pragma unroll
-      for (int e = (c - EARLY) * NU / (OPS - EARLY); e < (c - EARLY + 1) * NU / (OPS - EARLY); ++e) {
-        if (J & 1) put_values((J >> 1) ^ 1, e);
-        else put_keys((J >> 1) ^ 1, e);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int t = 0; t < MB; ++t) {
-      l[t] = fmaf(sum[t][1], pc1.z, fmaf(sum[t][0], pc0.z, l[t]));
-#pragma unroll
-      for (int u = 0; u < 2; ++u) p[t][u] = __builtin_bit_cast(bf16x8, w[t][u]);
-    }
-    if (J & 1) {
-      fetch(a.c.v, vr);      // of the tile looked up a step before
-    } else {
-      put_scales(tile + 1);
-      look_up(tile + 2);
-      fetch(a.c.k, kr);
-      __syncthreads();
-    }
+    barrier();
   };
 
-  f32x16 sa[MB], sb[MB];
-  bf16x8 pa[MB][2], pb[MB][2];
+  const int steps = (keys + KT - 1) / KT;
 #pragma unroll
-  for (int t = 0; t < MB; ++t) {
-    pa[t][0] = pa[t][1] = pb[t][0] = pb[t][1] = bf16x8{};
-#pragma unroll
-    for (int e = 0; e < 16; ++e) sa[t][e] = sb[t][e] = 0.f;
-  }
+  for (int u = 0; u < NP; ++u) p[u] = bf16x8{};
   if (steps > 0) {
+    const int p0 = table[0];
+    const bool held = p0 >= 0 && p0 < a.c.n_pages;
+    const float v0 = ((ConstF32)a.c.vs)[(int64_t)(held ? p0 : 0) * a.c.Hkv + hk];
+    unit_log = fminf(fmaxf(__builtin_amdgcn_logf(held ? fmaxf(v0, kMinScale) : 1.f), -30.f), 60.f);
+    entry = entry_of(0);
+    look_up(0);
+    fetch(a.c.k, kr);
+    fetch_values();
+    put_scales(0);
+    clean(0);
 #pragma unroll
-    for (int c = 0; c < OPS; c += 2) product(c, operand(c, 0, 0), sa, pa);
-  }
-  int j = 0;
-  for (; j + 4 <= steps; j += 4) {   // (a way out of its middle would cost registers)
-    step(std::integral_constant<int, 0>(), j, sa, sb, pb, pa);
-    step(std::integral_constant<int, 1>(), j + 1, sb, sa, pa, pb);
-    step(std::integral_constant<int, 2>(), j + 2, sa, sb, pb, pa);
-    step(std::integral_constant<int, 3>(), j + 3, sb, sa, pa, pb);
-  }
-  if (steps & 2) {
-    step(std::integral_constant<int, 0>(), j, sa, sb, pb, pa);
-    step(std::integral_constant<int, 1>(), j + 1, sb, sa, pa, pb);
-  }
-  if (steps > 0) {   // the last step's probabilities
-    const char* const tail = vlds + ((steps >> 1) - 1 & 1) * KBYTES;
+    for (int x = 0; x < NU; ++x) {
+      put_keys(0, x);
+      put_values(0, x);
+      put_values(2, x);   // step 0 multiplies these by probabilities of 0: no NaN of old may be there
+    }
+    look_up(1);
+    fetch(a.c.k, kr);
+    fetch_values();       // stay in vr for step 0
+    put_scales(1);
 #pragma unroll
-    for (int c = 1; c < OPS; c += 2)
-      product(c, *reinterpret_cast<const bf16x8*>(tail + vget[2 + ((c >> 1) & 1)] + (c >> 2) * 32 * kTile * 2), sa, pb);
+    for (int x = 0; x < NU; ++x) put_keys(1, x);
+    look_up(2);
+    fetch(a.c.k, kr);     // stay in kr for step 0
+    barrier();
+    if (wave >= 4) barrier();
+#pragma unroll
+    for (int c = 0; c < LEAD; ++c) x[c] = operand(c, 0, 2);
+    int t = 0;
+    for (; t + 3 <= steps; t += 3) {   // (a way out of its middle would cost registers)
+      step(std::integral_constant<int, 0>(), t);
+      step(std::integral_constant<int, 1>(), t + 1);
+      step(std::integral_constant<int, 2>(), t + 2);
+    }
+    if (t < steps) step(std::integral_constant<int, 0>(), t);
+    if (t + 1 < steps) step(std::integral_constant<int, 1>(), t + 1);
+    // the last step's probabilities
+    const char* const tail = vlds + (steps - 1) % 3 * BYTES;
+#pragma unroll
+    for (int c = 0; c < NP * OB; ++c)
+      o[c / NP] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+          *reinterpret_cast<const bf16x8*>(tail + vget[c % NP] + c / NP * 32 * KT * 2), p[c % NP], o[c / NP], 0, 0, 0);
+    if (wave < 4) barrier();
   }
 
+  if (r0 + c32 >= rows) return;
+  const float sum = add_halves(l);
+  const float inv = bad ? __builtin_nanf("") : m == -__builtin_inff() ? 0.f : exp2_fast(unit_log) / sum;
+  uint16_t* out = a.out + at * D + 4 * h;
 #pragma unroll
-  for (int t = 0; t < MB; ++t) {
-    if (r0 + 32 * t + c32 >= rows) continue;
-    const float sum = add_halves(l[t]);
-    const float inv = bad ? __builtin_nanf("") : m[t] == -__builtin_inff() ? 0.f : exp2_fast(unit_log) / sum;
-    uint16_t* out = a.out + at[t] * D + 4 * h;
+  for (int x = 0; x < OB; ++x)
 #pragma unroll
-    for (int x = 0; x < OB; ++x)
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<uint2*>(out + 32 * x + 8 * g) =
-            make_uint2(pack_bf16(o[t][x][4 * g] * inv, o[t][x][4 * g + 1] * inv),
-                       pack_bf16(o[t][x][4 * g + 2] * inv, o[t][x][4 * g + 3] * inv));
-  }
+    for (int g = 0; g < 4; ++g)
+      *reinterpret_cast<uint2*>(out + 32 * x + 8 * g) =
+          make_uint2(pack_bf16(o[x][4 * g] * inv, o[x][4 * g + 1] * inv),
+                     pack_bf16(o[x][4 * g + 2] * inv, o[x][4 * g + 3] * inv));
 }
 
 template <int D, bool I8>
 hipError_t launch_d(const AttnArgs& a, hipStream_t st) {
-  constexpr int MB = 1;
-  constexpr int M = 32 * MB * kWaves;
-  const int64_t units = (int64_t)a.n_tokens * (a.Hq / a.c.Hkv) / M + a.n_seqs;
-  hipLaunchKernelGGL((attn_packed_kernel<D, I8, MB>), dim3((uint32_t)(units * a.c.Hkv)), dim3(64 * kWaves), 0, st, a, (int)units);
+  const int64_t units = (int64_t)a.n_tokens * (a.Hq / a.c.Hkv) / kRows + a.n_seqs;
+  hipLaunchKernelGGL((attn_packed_kernel<D, I8>), dim3((uint32_t)(units * a.c.Hkv)), dim3(64 * kWaves), 0, st, a, (int)units);
   return hipGetLastError();
 }
 
