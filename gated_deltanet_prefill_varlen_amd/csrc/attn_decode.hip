@@ -76,15 +76,27 @@ __global__ void __launch_bounds__(64 * kWaves) attn_decode_kernel(const AttnArgs
     return;
   }
 
-  bf16x8 q[NT][KS];
+  // Queries: in registers, or in LDS (the same for every wave) where they would
+  // take 64 registers: those are needed for the codes in flight.
+  constexpr bool QL = NT * KS * 4 >= 64;
+  __shared__ __align__(16) bf16x8 ql[QL ? NT * KS : 1][64];
+  bf16x8 q[NT][QL ? 1 : KS];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int64_t tok = row[t] / a.Hq, h = row[t] % a.Hq;
     const uint16_t* p = a.q + tok * a.q_stride + h * D + 16 * g;
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
-      q[t][k] = *reinterpret_cast<const bf16x8*>(p + 64 * (k >> 1) + 8 * (k & 1));
+    for (int k = 0; k < KS; ++k) {
+      const uint16_t* const from = p + 64 * (k >> 1) + 8 * (k & 1);
+      if constexpr (!QL) q[t][k] = *reinterpret_cast<const bf16x8*>(from);
+      else if (wave == k % kWaves) ql[t * KS + k][lane] = *reinterpret_cast<const bf16x8*>(from);
+    }
   }
+  if constexpr (QL) __syncthreads();
+  auto query = [&](int t, int k) -> bf16x8 {
+    if constexpr (QL) return ql[t * KS + k][lane];
+    else return q[t][k];
+  };
 
   f32x4 o[NT][OB];
   float m[NT], l[NT];
@@ -102,27 +114,47 @@ __global__ void __launch_bounds__(64 * kWaves) attn_decode_kernel(const AttnArgs
   const int32_t* table = a.table + (int64_t)b * a.max_pages;
   const float log_scale = a.scale * kLog2e;
 
-  for (int t0 = key0 + wave * kTile; t0 < key1; t0 += kWaves * kTile) {
-    // pages: of the 16 keys whose values (and scores) this lane has, and of
-    // the key whose codes it loads.  A page that is not held is read as page 0
-    // and masked.
-    const int kv = t0 + 16 * g, kk = t0 + 16 * (c16 >> 2);
-    int pv = kv < key1 ? table[kv >> shift] : -1;
-    int pk = kk < key1 ? table[kk >> shift] : -1;
-    const bool held = pv >= 0 && pv < a.c.n_pages;
-    pv = held ? pv : 0;
-    pk = pk >= 0 && pk < a.c.n_pages ? pk : 0;
-    const uint8_t* kp = a.c.k + page_base(a.c, pk, hk) + ((kk & pmask) + (c16 & 3)) * D + 16 * g;
-    const uint8_t* vp = a.c.v + page_base(a.c, pv, hk) + ((kv & pmask) * D + c16 * 16);
-    uint4 kc[4][KL], vc[OB];
+  // A tile's pages: of the 16 keys whose values (and scores) this lane has, and
+  // of the key whose codes it loads (-1: not held, read as page 0 and masked).
+  auto page_at = [&](int key) -> int {
+    const int p = key < key1 ? table[key >> shift] : -1;
+    return p < a.c.n_pages ? p : -1;
+  };
+  uint4 kc[4][KL], vc[OB];
+  float ks, vs;
+  auto load_keys = [&](int t0, int pk, int pv) {
+    const int kk = t0 + 16 * (c16 >> 2);
+    const uint8_t* kp = a.c.k + page_base(a.c, max(pk, 0), hk) + ((kk & pmask) + (c16 & 3)) * D + 16 * g;
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
       for (int i = 0; i < KL; ++i) kc[s][i] = *reinterpret_cast<const uint4*>(kp + 4 * s * D + 64 * i);
+    ks = a.c.ks[(int64_t)max(pv, 0) * a.c.Hkv + hk];
+  };
+  auto load_values = [&](int t0, int pv) {
+    const int kv = t0 + 16 * g;
+    const uint8_t* vp = a.c.v + page_base(a.c, max(pv, 0), hk) + ((kv & pmask) * D + c16 * 16);
 #pragma unroll
     for (int x = 0; x < OB; ++x) vc[x] = *reinterpret_cast<const uint4*>(vp + x * 256);
-    const float ks = a.c.ks[(int64_t)pv * a.c.Hkv + hk] * log_scale;
-    const float vs = held ? a.c.vs[(int64_t)pv * a.c.Hkv + hk] : 0.f;
+    vs = a.c.vs[(int64_t)max(pv, 0) * a.c.Hkv + hk];
+  };
+
+  // Loads run ahead: a tile's keys are asked for when the scores before them
+  // are done, its values after the products before them, its pages a tile
+  // earlier.
+  constexpr int kStep = kWaves * kTile;
+  int t0 = key0 + wave * kTile;
+  int pk = page_at(t0 + 16 * (c16 >> 2)), pv = page_at(t0 + 16 * g);
+  int pk1 = page_at(t0 + kStep + 16 * (c16 >> 2)), pv1 = page_at(t0 + kStep + 16 * g);
+  if (t0 < key1) {
+    load_keys(t0, pk, pv);
+    load_values(t0, pv);
+  }
+  for (; t0 < key1; t0 += kStep) {
+    const bool more = t0 + kStep < key1;
+    const int pk2 = page_at(t0 + 2 * kStep + 16 * (c16 >> 2)), pv2 = page_at(t0 + 2 * kStep + 16 * g);
+    const int kv = t0 + 16 * g;
+    const bool held = pv >= 0;
 
     f32x4 s4[NT][4];
 #pragma unroll
@@ -130,20 +162,51 @@ __global__ void __launch_bounds__(64 * kWaves) attn_decode_kernel(const AttnArgs
 #pragma unroll
       for (int s = 0; s < 4; ++s) s4[t][s] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int i = 0; i < KL; ++i) {
+      bf16x8 q0[NT], q1[NT];
 #pragma unroll
-      for (int i = 0; i < KL; ++i) {
+      for (int t = 0; t < NT; ++t) {
+        q0[t] = query(t, 2 * i);
+        q1[t] = query(t, 2 * i + 1);
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
         const bf16x8 k0 = codes_to_operand<I8>(kc[s][i].x, kc[s][i].y);
         const bf16x8 k1 = codes_to_operand<I8>(kc[s][i].z, kc[s][i].w);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          s4[t][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[t][2 * i], s4[t][s], 0, 0, 0);
-          s4[t][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[t][2 * i + 1], s4[t][s], 0, 0, 0);
+          s4[t][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q0[t], s4[t][s], 0, 0, 0);
+          s4[t][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q1[t], s4[t][s], 0, 0, 0);
         }
       }
+    }
+    const float kf = ks * log_scale;
+    __builtin_amdgcn_sched_barrier(0);
+    if (more) load_keys(t0 + kStep, pk1, pv1);
+    __builtin_amdgcn_sched_barrier(0);
+
+    // codes behind the last key (or of a page not held) may be anything, NaN
+    // among them, which a probability of 0 would not silence; so would a NaN
+    // value that only some rows see: it becomes 0, and its key's score NaN for
+    // the rows that see it
+    const bool whole = t0 + kTile <= key1 - (a.n_tok - 1);   // every row sees the tile
+    uint32_t nan = 0;
+    if (!whole || __any(!held)) {
+      const int left = held ? key1 - kv : 0;
+#pragma unroll
+      for (int x = 0; x < OB; ++x) {
+        uint32_t w[4] = {vc[x].x, vc[x].y, vc[x].z, vc[x].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = without_nan<I8>(w[j] & first_bytes(left - 4 * j), 4 * j, &nan);
+        vc[x] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if constexpr (!I8)
+#pragma unroll
+        for (int d = 8; d; d >>= 1) nan |= __shfl_xor(nan, d);
+    }
 
     // scores to probabilities; in units of log2
-    const bool whole = t0 + kTile <= key1 - (a.n_tok - 1);   // every row sees the tile
+    const float vf = held ? vs : 0.f;
     bf16x8 p[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -152,7 +215,8 @@ __global__ void __launch_bounds__(64 * kWaves) attn_decode_kernel(const AttnArgs
       for (int s = 0; s < 4; ++s)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float x = s4[t][s][i] * ks;
+          float x = s4[t][s][i] * kf;
+          if (!I8 && (nan >> (4 * s + i) & 1)) x = __builtin_nanf("");
           if (!held || (!whole && kv + 4 * s + i > last[t])) x = -__builtin_inff();
           s4[t][s][i] = x;
           mx = fmaxf(mx, x);
@@ -176,32 +240,13 @@ __global__ void __launch_bounds__(64 * kWaves) attn_decode_kernel(const AttnArgs
         for (int i = 0; i < 4; ++i) {
           e[i] = exp2_fast(s4[t][s][i] - base);
           l[t] += e[i];
-          e[i] *= vs;   // the probability times its value's scale is rounded to bf16 once
+          e[i] *= vf;   // the probability times its value's scale is rounded to bf16 once
         }
         w[s >> 1][2 * (s & 1)] = pack_bf16(e[0], e[1]);
         w[s >> 1][2 * (s & 1) + 1] = pack_bf16(e[2], e[3]);
       }
       p[t][0] = __builtin_bit_cast(bf16x8, w[0]);
       p[t][1] = __builtin_bit_cast(bf16x8, w[1]);
-    }
-
-    // codes behind the last key (or of a page not held) may be anything, NaN
-    // among them, which a probability of 0 would not silence
-    const int left = held ? key1 - kv : 0;
-    if (__any(left < 16)) {
-      uint32_t keep[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = left - 4 * j;
-        keep[j] = n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << (8 * n)) - 1;
-      }
-#pragma unroll
-      for (int x = 0; x < OB; ++x) {
-        vc[x].x &= keep[0];
-        vc[x].y &= keep[1];
-        vc[x].z &= keep[2];
-        vc[x].w &= keep[3];
-      }
     }
 #pragma unroll
     for (int x = 0; x < OB; ++x) {
@@ -213,6 +258,11 @@ __global__ void __launch_bounds__(64 * kWaves) attn_decode_kernel(const AttnArgs
         o[t][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, p[t][1], o[t][x], 0, 0, 0);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
+    if (more) load_values(t0 + kStep, pv1);
+    pk1 = pk2;
+    pv = pv1;
+    pv1 = pv2;
   }
 
   // the four waves, in order
@@ -276,7 +326,8 @@ __global__ void __launch_bounds__(64 * kWaves) attn_decode_kernel(const AttnArgs
   }
 }
 
-// Joins the splits of one row, in order.
+// Joins the splits of one row, in order: lanes take the splits' maxima and
+// sums at once, then all channels of each split.
 template <int D>
 __global__ void __launch_bounds__(64) attn_join_kernel(const AttnArgs a, const Partial part) {
   const int rows = a.n_tok * a.Hq;
@@ -288,16 +339,27 @@ __global__ void __launch_bounds__(64) attn_join_kernel(const AttnArgs a, const P
   constexpr int C = D / 64;
   const int64_t p0 = (int64_t)b * part.splits * rows + r;
   float mt = -__builtin_inff();
-  for (int s = 0; s < splits; ++s) mt = fmaxf(mt, part.ml[p0 + (int64_t)s * rows].x);
+  for (int s = lane; s < splits; s += 64) mt = fmaxf(mt, part.ml[p0 + (int64_t)s * rows].x);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) mt = fmaxf(mt, __shfl_xor(mt, d));
   const float base = mt == -__builtin_inff() ? 0.f : mt;
   float o[C] = {}, l = 0.f;
-  for (int s = 0; s < splits; ++s) {
-    const int64_t pr = p0 + (int64_t)s * rows;
-    const float2 ml = part.ml[pr];
-    const float w = exp2_fast(ml.x - base);
-    l += w * ml.y;
+  for (int s0 = 0; s0 < splits; s0 += 64) {
+    float w = 0.f, lw = 0.f;
+    if (s0 + lane < splits) {
+      const float2 ml = part.ml[p0 + (int64_t)(s0 + lane) * rows];
+      w = exp2_fast(ml.x - base);
+      lw = w * ml.y;
+    }
+    const int n = min(64, splits - s0);
+#pragma unroll 8
+    for (int s = 0; s < n; ++s) {
+      const float ws = __shfl(w, s);
+      l += __shfl(lw, s);
+      const float* const from = part.o + (p0 + (int64_t)(s0 + s) * rows) * D + C * lane;
 #pragma unroll
-    for (int c = 0; c < C; ++c) o[c] += w * part.o[pr * D + C * lane + c];
+      for (int c = 0; c < C; ++c) o[c] += ws * from[c];
+    }
   }
   const float inv = mt == -__builtin_inff() ? 0.f : 1.f / l;
   uint16_t* const out = a.out + ((int64_t)b * rows + r) * D + C * lane;

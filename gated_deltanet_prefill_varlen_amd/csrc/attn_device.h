@@ -41,6 +41,18 @@ __device__ __forceinline__ bf16x8 codes_to_operand(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(bf16x8, r);
 }
 
+// The first n bytes of a dword.
+__device__ __forceinline__ uint32_t first_bytes(int n) { return n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << (8 * n)) - 1; }
+
+// Four codes with 0 for each NaN, whose places become bits at, at + 1, .. of *found.
+template <bool I8>
+__device__ __forceinline__ uint32_t without_nan(uint32_t w, int at, uint32_t* found) {
+  if constexpr (I8) return w;
+  const uint32_t nan = (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
+  *found |= ((nan * 0x10204080u) >> 28) << at;   // the four flags side by side
+  return w & ~(nan * 0xFFu);
+}
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 }  // namespace gdn

@@ -179,18 +179,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
     for (int x = 0; x < NU; ++x) {
       const int second = NU == 1 ? lane & 1 : x & 1;   // which 8 of the 16 keys
       const int left = (v_page < 0 ? 0 : keys - v_key) - 8 * second;
-      uint32_t w[2] = {vr[x].x, vr[x].y};
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int c = left - 4 * j;
-        w[j] &= c >= 4 ? 0xFFFFFFFFu : c <= 0 ? 0u : (1u << (8 * c)) - 1;
-        if constexpr (!I8) {
-          const uint32_t nan = (((w[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
-          w[j] &= ~(nan * 0xFFu);
-          found |= ((nan * 0x10204080u) >> 28) << (8 * second + 4 * j);   // the four flags side by side
-        }
-      }
-      vr[x] = make_uint2(w[0], w[1]);
+      vr[x].x = without_nan<I8>(vr[x].x & first_bytes(left), 8 * second, &found);
+      vr[x].y = without_nan<I8>(vr[x].y & first_bytes(left - 4), 8 * second + 4, &found);
     }
     if constexpr (!I8) {
 #pragma unroll
