@@ -14,7 +14,7 @@
 // one 16-byte vector of the cache's transposed value tile, and the
 // probabilities go from one product into the next without leaving their lane.
 //
-// Keys are split over workgroups by the request's own length (split_keys), the
+// Keys are split over workgroups in runs of fixed length (split_keys), the
 // four waves of a workgroup take 64-key tiles in turn, and partial results
 // (fp32 sums against the running maximum) are joined in a fixed order, so a
 // request's bits do not depend on its batch.
@@ -28,12 +28,10 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kTile = 64;
 
-// Keys per workgroup for a request of L keys.
-__host__ __device__ inline int split_keys(int L) { return L <= 16384 ? 512 : 1024; }
-__host__ __device__ inline int n_splits(int L) {
-  const int k = split_keys(L);
-  return L <= 0 ? 1 : (L + k - 1) / k;
-}
+// Keys per workgroup: by the head size alone, so that how a request's keys are
+// split never depends on its batch.
+__host__ __device__ constexpr int split_keys(int dim) { return dim == 256 ? 2048 : 1024; }
+__host__ __device__ inline int n_splits(int L, int dim) { return L <= 0 ? 1 : (L + split_keys(dim) - 1) / split_keys(dim); }
 
 struct Partial {
   float* o;    // [B][splits][n_tok * Hq][D]
@@ -42,27 +40,39 @@ struct Partial {
 };
 
 template <int D, bool I8, int NT>
-__global__ void __launch_bounds__(64 * kWaves) attn_decode_kernel(const AttnArgs a, const Partial part) {
+__global__ void __launch_bounds__(64 * kWaves, NT * D <= 128 ? 2 : 1) attn_decode_kernel(const AttnArgs a, const Partial part) {
   constexpr int KL = D / 64;    // 16-byte loads of a key per lane
   constexpr int KS = D / 32;    // contraction steps of a score
   constexpr int OB = D / 16;    // 16-channel blocks of the output
-  const int b = blockIdx.z, sp = blockIdx.x;
+  // heads first, then requests, then splits: workgroups go to the eight XCDs in
+  // turn, and an order by splits would send every first split to one of them
+  const int b = blockIdx.y, sp = blockIdx.z;
   const int G = a.Hq / a.c.Hkv, R = a.n_tok * G;
   const int groups = (R + 16 * NT - 1) / (16 * NT);
-  const int hk = blockIdx.y / groups, r0 = (blockIdx.y % groups) * 16 * NT;
+  const int hk = blockIdx.x / groups, r0 = (blockIdx.x % groups) * 16 * NT;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c16 = lane & 15, g = lane >> 4;
+  const int shift = a.c.page_shift, pmask = (1 << shift) - 1;
+  const int32_t* table = a.table + (int64_t)b * a.max_pages;
+  constexpr int kStep = kWaves * kTile, per = split_keys(D);
+  const int key0 = sp * per;
+  // the first tile's entries do not wait for the length
+  int t0 = key0 + wave * kTile;
+  auto entry_of = [&](int key) -> int { return a.max_pages > 0 ? table[min(key >> shift, a.max_pages - 1)] : -1; };
+  const int ek = entry_of(t0 + 16 * (c16 >> 2)), ev = entry_of(t0 + 16 * g);
+  const int ek1 = entry_of(t0 + kStep + 16 * (c16 >> 2)), ev1 = entry_of(t0 + kStep + 16 * g);
   const int L = a.kv_len[b];
   const bool bad = L < 0 || L > a.max_kv;
-  const int splits = bad ? 1 : n_splits(L);
+  const int splits = bad ? 1 : n_splits(L, D);
   if (sp >= splits) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c16 = lane & 15, g = lane >> 4;
 
   // the query row of this lane's column, per tile
-  int64_t row[NT];
-  int last[NT];      // the last key it sees
+  int64_t tok[NT];
+  int hq[NT], last[NT];      // its head, and the last key it sees
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int r = min(r0 + 16 * t + c16, R - 1), i = r / G;
-    row[t] = ((int64_t)b * a.n_tok + i) * a.Hq + hk * G + (r - i * G);
+    tok[t] = (int64_t)b * a.n_tok + i;
+    hq[t] = hk * G + (r - i * G);
     last[t] = L - a.n_tok + i;
   }
   if (bad || L == 0) {
@@ -83,8 +93,7 @@ __global__ void __launch_bounds__(64 * kWaves) attn_decode_kernel(const AttnArgs
   bf16x8 q[NT][QL ? 1 : KS];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int64_t tok = row[t] / a.Hq, h = row[t] % a.Hq;
-    const uint16_t* p = a.q + tok * a.q_stride + h * D + 16 * g;
+    const uint16_t* p = a.q + tok[t] * a.q_stride + hq[t] * D + 16 * g;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       const uint16_t* const from = p + 64 * (k >> 1) + 8 * (k & 1);
@@ -108,18 +117,12 @@ __global__ void __launch_bounds__(64 * kWaves) attn_decode_kernel(const AttnArgs
     for (int x = 0; x < OB; ++x) o[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  const int per = split_keys(L);
-  const int key0 = sp * per, key1 = min(L, key0 + per);
-  const int shift = a.c.page_shift, pmask = (1 << shift) - 1;
-  const int32_t* table = a.table + (int64_t)b * a.max_pages;
+  const int key1 = min(L, key0 + per);
   const float log_scale = a.scale * kLog2e;
 
   // A tile's pages: of the 16 keys whose values (and scores) this lane has, and
   // of the key whose codes it loads (-1: not held, read as page 0 and masked).
-  auto page_at = [&](int key) -> int {
-    const int p = key < key1 ? table[key >> shift] : -1;
-    return p < a.c.n_pages ? p : -1;
-  };
+  auto page_of = [&](int entry, int key) -> int { return key < key1 && entry < a.c.n_pages ? entry : -1; };
   uint4 kc[4][KL], vc[OB];
   float ks, vs;
   auto load_keys = [&](int t0, int pk, int pv) {
@@ -142,17 +145,16 @@ __global__ void __launch_bounds__(64 * kWaves) attn_decode_kernel(const AttnArgs
   // Loads run ahead: a tile's keys are asked for when the scores before them
   // are done, its values after the products before them, its pages a tile
   // earlier.
-  constexpr int kStep = kWaves * kTile;
-  int t0 = key0 + wave * kTile;
-  int pk = page_at(t0 + 16 * (c16 >> 2)), pv = page_at(t0 + 16 * g);
-  int pk1 = page_at(t0 + kStep + 16 * (c16 >> 2)), pv1 = page_at(t0 + kStep + 16 * g);
+  int pv = page_of(ev, t0 + 16 * g);
+  int pk1 = page_of(ek1, t0 + kStep + 16 * (c16 >> 2)), pv1 = page_of(ev1, t0 + kStep + 16 * g);
   if (t0 < key1) {
-    load_keys(t0, pk, pv);
+    load_keys(t0, page_of(ek, t0 + 16 * (c16 >> 2)), pv);
     load_values(t0, pv);
   }
   for (; t0 < key1; t0 += kStep) {
     const bool more = t0 + kStep < key1;
-    const int pk2 = page_at(t0 + 2 * kStep + 16 * (c16 >> 2)), pv2 = page_at(t0 + 2 * kStep + 16 * g);
+    const int kk2 = t0 + 2 * kStep + 16 * (c16 >> 2), kv2 = t0 + 2 * kStep + 16 * g;
+    const int pk2 = page_of(table[min(kk2, key1 - 1) >> shift], kk2), pv2 = page_of(table[min(kv2, key1 - 1) >> shift], kv2);
     const int kv = t0 + 16 * g;
     const bool held = pv >= 0;
 
@@ -265,9 +267,11 @@ __global__ void __launch_bounds__(64 * kWaves) attn_decode_kernel(const AttnArgs
     pv1 = pv2;
   }
 
-  // the four waves, in order
+  // The four waves, in order: each sums a quarter of the 16 x 16 blocks of the
+  // output, which the other three leave for it in LDS.
   __shared__ float sm[kWaves][16 * NT], sl[kWaves][16 * NT];
-  __shared__ __align__(16) float so[16 * NT][D + 4];   // + 4: rows on other banks
+  constexpr int NB = NT * OB / kWaves;
+  __shared__ __align__(16) f32x4 so[kWaves][kWaves - 1][NB][64];   // for wave, from (its number - 1 after mine)
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     l[t] += __shfl_xor(l[t], 16);
@@ -278,50 +282,46 @@ __global__ void __launch_bounds__(64 * kWaves) attn_decode_kernel(const AttnArgs
     }
   }
   __syncthreads();
-  float mt[NT], lt[NT], mine[NT];
+  float mt[NT], lt[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     mt[t] = -__builtin_inff();
     lt[t] = 0.f;
+#pragma unroll
     for (int w = 0; w < kWaves; ++w) mt[t] = fmaxf(mt[t], sm[w][16 * t + c16]);
     const float base = mt[t] == -__builtin_inff() ? 0.f : mt[t];
+#pragma unroll
     for (int w = 0; w < kWaves; ++w) lt[t] += sl[w][16 * t + c16] * exp2_fast(sm[w][16 * t + c16] - base);
-    mine[t] = exp2_fast(m[t] - base);
-  }
-  for (int w = 0; w < kWaves; ++w) {
-    if (wave == w) {
+    const float mine = exp2_fast(m[t] - base);
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int x = 0; x < OB; ++x) {
-          f32x4* const d = reinterpret_cast<f32x4*>(&so[16 * t + c16][16 * x + 4 * g]);
-          const f32x4 y = o[t][x] * mine[t];
-          *d = w == 0 ? y : *d + y;
-        }
-    }
-    __syncthreads();
-  }
-  if (wave == 0 && g == 0) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      sm[0][16 * t + c16] = mt[t];
-      sl[0][16 * t + c16] = lt[t];
+    for (int x = 0; x < OB; ++x) {
+      const int n = t * OB + x, to = n % kWaves;
+      o[t][x] *= mine;
+      if (to != wave) so[to][(wave - to - 1) & (kWaves - 1)][n / kWaves][lane] = o[t][x];
     }
   }
   __syncthreads();
-  for (int e = tid; e < 16 * NT * D / 4; e += 64 * kWaves) {
-    const int rl = e / (D / 4), c = e % (D / 4) * 4, r = r0 + rl;
-    if (r >= R) continue;
-    const int i = r / G, h = hk * G + (r - i * G);
-    const f32x4 x = *reinterpret_cast<const f32x4*>(&so[rl][c]);
-    if (splits == 1) {
-      const float inv = sl[0][rl] > 0.f ? 1.f / sl[0][rl] : (sm[0][rl] == -__builtin_inff() ? 0.f : 1.f / sl[0][rl]);
-      *reinterpret_cast<uint2*>(a.out + (((int64_t)b * a.n_tok + i) * a.Hq + h) * D + c) =
-          make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
-    } else {
-      const int64_t pr = ((int64_t)b * part.splits + sp) * a.n_tok * a.Hq + i * a.Hq + h;
-      *reinterpret_cast<f32x4*>(part.o + pr * D + c) = x;
-      if (c == 0) part.ml[pr] = make_float2(sm[0][rl], sl[0][rl]);
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const float inv = mt[t] == -__builtin_inff() ? 0.f : 1.f / lt[t];
+    const bool mine = r0 + 16 * t + c16 < R;
+#pragma unroll
+    for (int x = 0; x < OB; ++x) {
+      const int n = t * OB + x, to = n % kWaves, c = 16 * x + 4 * g;
+      if (to != wave) continue;
+      f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) y += w == to ? o[t][x] : so[to][(w - to - 1) & (kWaves - 1)][n / kWaves][lane];
+      if (!mine) continue;
+      const int64_t row = tok[t] * a.Hq + hq[t];
+      if (splits == 1) {
+        *reinterpret_cast<uint2*>(a.out + row * D + c) = make_uint2(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv));
+      } else {
+        const int rows = a.n_tok * a.Hq;
+        const int64_t pr = row + ((int64_t)b * (part.splits - 1) + sp) * rows;   // [b][split][row of the request]
+        *reinterpret_cast<f32x4*>(part.o + pr * D + c) = y;
+        if (c == 0) part.ml[pr] = make_float2(mt[t], lt[t]);
+      }
     }
   }
 }
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(64) attn_join_kernel(const AttnArgs a, const P
   const int b = (int)(blockIdx.x / rows), r = (int)(blockIdx.x % rows), lane = threadIdx.x;
   const int L = a.kv_len[b];
   if (L < 0 || L > a.max_kv) return;
-  const int splits = n_splits(L);
+  const int splits = n_splits(L, D);
   if (splits == 1) return;
   constexpr int C = D / 64;
   const int64_t p0 = (int64_t)b * part.splits * rows + r;
@@ -371,7 +371,7 @@ template <int D, bool I8>
 hipError_t launch_d(const AttnArgs& a, const Partial& part, hipStream_t st) {
   const int R = a.n_tok * (a.Hq / a.c.Hkv);
   const int nt = R <= 16 ? 1 : R <= 32 || D == 256 ? 2 : 4;
-  const dim3 grid(part.splits, a.c.Hkv * ((R + 16 * nt - 1) / (16 * nt)), a.n_seqs), block(64 * kWaves);
+  const dim3 grid(a.c.Hkv * ((R + 16 * nt - 1) / (16 * nt)), a.n_seqs, part.splits), block(64 * kWaves);
   if (nt == 1) hipLaunchKernelGGL((attn_decode_kernel<D, I8, 1>), grid, block, 0, st, a, part);
   else if (nt == 2) hipLaunchKernelGGL((attn_decode_kernel<D, I8, 2>), grid, block, 0, st, a, part);
   else if constexpr (D < 256) hipLaunchKernelGGL((attn_decode_kernel<D, I8, 4>), grid, block, 0, st, a, part);
@@ -383,20 +383,13 @@ hipError_t launch_d(const AttnArgs& a, const Partial& part, hipStream_t st) {
 
 }  // namespace
 
-// Most splits of any length up to max_kv: the rule steps up at 16,384.
-static int most_splits(int max_kv) {
-  int s = n_splits(max_kv);
-  if (max_kv > 16384) s = std::max(s, n_splits(16384));
-  return s;
-}
-
 int64_t attn_decode_bytes(int dim, int Hq, int batch, int n_tok, int max_kv) {
-  const int64_t s = most_splits(max_kv);
+  const int64_t s = n_splits(max_kv, dim);
   return s == 1 ? 0 : s * batch * n_tok * Hq * (dim + 2) * 4;
 }
 
 hipError_t launch_attn_decode(const AttnArgs& a, void* workspace, hipStream_t st) {
-  Partial part{static_cast<float*>(workspace), nullptr, most_splits(a.max_kv)};
+  Partial part{static_cast<float*>(workspace), nullptr, n_splits(a.max_kv, a.c.dim)};
   part.ml = reinterpret_cast<float2*>(part.o + (int64_t)a.n_seqs * part.splits * a.n_tok * a.Hq * a.c.dim);
   switch (a.c.dim) {
     case 64: return a.c.i8 ? launch_d<64, true>(a, part, st) : launch_d<64, false>(a, part, st);
