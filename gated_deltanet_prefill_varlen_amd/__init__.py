@@ -73,6 +73,7 @@ class gdn_cache(ctypes.Structure):
         ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
         ("v_scale", ctypes.c_void_p),
     ]
+    device = -1
 
 
 class gdn_rope(ctypes.Structure):
@@ -98,8 +99,12 @@ def make_cache(k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
     for t in (k_scale, v_scale):
         if t.dtype != torch.float32 or tuple(t.shape) != (n, h):
             raise ValueError("scales must be fp32 [n_pages, Hkv]")
-    c = gdn_cache(h, d, page, _CODES[k.dtype], n, 0, _buf(k, k.dtype), _buf(v, v.dtype),
-                  _buf(k_scale, torch.float32), _buf(v_scale, torch.float32))
+    dev = k.get_device()
+    c = gdn_cache(h, d, page, _CODES[k.dtype], n, 0, _buf(k, k.dtype, dev, "k"), _buf(v, k.dtype, dev, "v"),
+                  _buf(k_scale, torch.float32, dev, "k_scale"), _buf(v_scale, torch.float32, dev, "v_scale"))
+    if dev < 0:
+        raise ValueError("the cache is not on the GPU")
+    c.device = dev
     c.tensors = (k, v, k_scale, v_scale)
     return c
 
@@ -189,36 +194,43 @@ def _dev(t) -> Optional[int]:
     return t.data_ptr()
 
 
-def _buf(t: Optional[torch.Tensor], dtype: torch.dtype, what: str = "argument") -> Optional[int]:
-    """Device pointer of a dense tensor of one type on the current device."""
+def _buf(t: Optional[torch.Tensor], dtype: torch.dtype, dev: int, what: str = "argument") -> Optional[int]:
+    """Device pointer of a dense tensor of one type on device dev."""
     if t is None:
         return None
-    if t.dtype != dtype:
-        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return _here(t, what)
-
-
-def _here(t: torch.Tensor, what: str) -> int:
-    if not t.is_cuda:
-        raise ValueError(f"{what} is not on the GPU")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{what} is not on the current device")
+    if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(t, dtype, what)
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, rows: int, heads: Optional[int], d: int, what: str):
+def _refuse(t: torch.Tensor, dtype: torch.dtype, what: str) -> None:
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{what} must be contiguous" if t.is_cuda and not t.is_contiguous() else
+                     f"{what} is not on the current device" if t.is_cuda else f"{what} is not on the GPU")
+
+
+def _rows(t: torch.Tensor, rows: int, heads: Optional[int], d: int, dev: int, what: str):
     """Pointer, token stride and head count of bf16 rows [>= rows, heads, d]
     whose heads are dense (columns of a wider row will do)."""
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{what} must be torch.bfloat16, got {t.dtype}")
-    sh, st = t.shape, t.stride()
-    if len(sh) != 3 or sh[2] != d or sh[0] < rows or (heads is not None and sh[1] != heads):
-        raise ValueError(f"{what} must be [{rows}, {'heads' if heads is None else heads}, {d}], got {tuple(sh)}")
-    if st[2] != 1 or (sh[1] > 1 and st[1] != d):
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        _refuse(t, torch.bfloat16, what)
+    n, h, e = t.shape if t.dim() == 3 else (0, 0, 0)
+    if e != d or n < rows or (heads is not None and h != heads):
+        raise ValueError(f"{what} must be [{rows}, {'heads' if heads is None else heads}, {d}], got {tuple(t.shape)}")
+    st = t.stride()
+    if st[2] != 1 or (h > 1 and st[1] != d):
         raise ValueError(f"{what}: the heads of a token must be dense")
-    return _here(t, what), (st[0] if sh[0] > 1 else sh[1] * d), sh[1]
+    return t.data_ptr(), (st[0] if n > 1 else h * d), h
+
+
+def _where(stream):
+    """Current device (one that no tensor is on while there is none) and the
+    stream's handle."""
+    if not torch.cuda.is_initialized():
+        return -2, None
+    dev = torch.cuda.current_device()
+    return dev, (torch._C._cuda_getCurrentRawStream(dev) or None) if stream is None else _stream(stream)
 
 
 def _host_i32(a) -> Optional[np.ndarray]:
@@ -376,11 +388,19 @@ def gdn_snapshot_copy(ckpt_buf, n: int, bytes_each: int, dst_pool, dst_slot, dst
         _event(wait_event), _stream(copy_stream), _record_target(done_event)), "gdn_snapshot_copy")
 
 
+def _cache(cache: gdn_cache, dev: int) -> int:
+    """Address of a cache's handle; its tensors must be on device dev."""
+    if cache.device != dev:
+        raise ValueError("the cache is not on the current device")
+    return ctypes.addressof(cache)
+
+
 def gdn_plan_pages(page: int, want_len, kv_len, kv_len_out, block_table, free_pages, free_count,
                    free_count_out, cu_seqlens, slot_map, positions, status, stream=None) -> None:
     """Block tables, the pack of new tokens and its slot map, from the lengths
     that the requests hold (kv_len) and want; all on the device."""
     i32 = torch.int32
+    dev, st = _where(stream)
     n, (rows, max_pages) = want_len.numel(), block_table.shape
     if (rows < n or kv_len.numel() < n or kv_len_out.numel() < n or status.numel() < n or
             cu_seqlens.numel() < n + 1):
@@ -390,13 +410,13 @@ def gdn_plan_pages(page: int, want_len, kv_len, kv_len_out, block_table, free_pa
     if free_count.numel() < 1 or free_count_out.numel() < 1:
         raise ValueError("free_count is empty")
     _check(load().gdn_plan_pages(
-        page, n, _buf(want_len, i32, "want_len"), _buf(kv_len, i32, "kv_len"),
-        _buf(kv_len_out, i32, "kv_len_out"), _buf(block_table, i32, "block_table"), max_pages,
-        _buf(free_pages, i32, "free_pages"), _buf(free_count, i32, "free_count"),
-        _buf(free_count_out, i32, "free_count_out"), free_pages.numel(),
-        _buf(cu_seqlens, i32, "cu_seqlens"), _buf(slot_map, torch.int64, "slot_map"),
-        slot_map.numel(), _buf(positions, i32, "positions"), _buf(status, i32, "status"),
-        _stream(stream)), "gdn_plan_pages")
+        page, n, _buf(want_len, i32, dev, "want_len"), _buf(kv_len, i32, dev, "kv_len"),
+        _buf(kv_len_out, i32, dev, "kv_len_out"), _buf(block_table, i32, dev, "block_table"), max_pages,
+        _buf(free_pages, i32, dev, "free_pages"), _buf(free_count, i32, dev, "free_count"),
+        _buf(free_count_out, i32, dev, "free_count_out"), free_pages.numel(),
+        _buf(cu_seqlens, i32, dev, "cu_seqlens"), _buf(slot_map, torch.int64, dev, "slot_map"),
+        slot_map.numel(), _buf(positions, i32, dev, "positions"), _buf(status, i32, dev, "status"),
+        st), "gdn_plan_pages")
 
 
 def gdn_rope_append(rope: gdn_rope, cache: gdn_cache, cu_seqlens, cu_seqlens_host, q, k, v, positions,
@@ -404,6 +424,7 @@ def gdn_rope_append(rope: gdn_rope, cache: gdn_cache, cu_seqlens, cu_seqlens_hos
     """q_out = rotated q; rotated k and v into their cache slots.  q, k, v are
     [T, heads, d] bf16, views of one wider row if need be; positions [n_axes, T],
     or [T] for every axis; q and q_out None: only the cache is written."""
+    dev, st = _where(stream)
     cu_h = _host_i32(cu_seqlens_host)
     n = len(cu_h) - 1
     T, d, hkv = int(cu_h[-1]), cache.head_dim, cache.num_kv_heads
@@ -412,10 +433,10 @@ def gdn_rope_append(rope: gdn_rope, cache: gdn_cache, cu_seqlens, cu_seqlens_hos
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     if q is not None:
-        qp, qs, hq = _rows(q, T, None, d, "q")
-        qo, qos, _ = _rows(q_out, T, hq, d, "q_out")
-    kp, ks, _ = _rows(k, T, hkv, d, "k")
-    vp, vs, _ = _rows(v, T, hkv, d, "v")
+        qp, qs, hq = _rows(q, T, None, d, dev, "q")
+        qo, qos, _ = _rows(q_out, T, hq, d, dev, "q_out")
+    kp, ks, _ = _rows(k, T, hkv, d, dev, "k")
+    vp, vs, _ = _rows(v, T, hkv, d, dev, "v")
     pos_stride = 0
     if positions is not None:
         if positions.shape[-1] < T or (positions.dim() == 2 and positions.shape[0] < rope.n_axes) or positions.dim() > 2:
@@ -424,21 +445,22 @@ def gdn_rope_append(rope: gdn_rope, cache: gdn_cache, cu_seqlens, cu_seqlens_hos
     if slot_map.numel() < T or cu_seqlens.numel() < n + 1:
         raise ValueError("slot_map or cu_seqlens is shorter than the pack")
     _check(load().gdn_rope_append(
-        ctypes.addressof(rope), ctypes.addressof(cache), hq, _buf(cu_seqlens, torch.int32, "cu_seqlens"),
-        cu_h.ctypes.data, n, T, qp, qs or 0, kp, ks, vp, vs, _buf(positions, torch.int32, "positions"),
-        pos_stride, _buf(slot_map, torch.int64, "slot_map"), qo, qos or 0, _stream(stream)),
+        ctypes.addressof(rope), _cache(cache, dev), hq, _buf(cu_seqlens, torch.int32, dev, "cu_seqlens"),
+        cu_h.ctypes.data, n, T, qp, qs or 0, kp, ks, vp, vs, _buf(positions, torch.int32, dev, "positions"),
+        pos_stride, _buf(slot_map, torch.int64, dev, "slot_map"), qo, qos or 0, st),
         "gdn_rope_append")
 
 
 def gdn_cache_gather(cache: gdn_cache, slot_map, k_out=None, v_out=None, stream=None) -> None:
     """k_out, v_out [T, Hkv, d] bf16: the values held at the T slots."""
+    dev, st = _where(stream)
     T = slot_map.numel()
     for t in (k_out, v_out):
         if t is not None and tuple(t.shape) != (T, cache.num_kv_heads, cache.head_dim):
             raise ValueError("outputs must be [T, Hkv, d]")
     _check(load().gdn_cache_gather(
-        ctypes.addressof(cache), T, _buf(slot_map, torch.int64, "slot_map"),
-        _buf(k_out, torch.bfloat16, "k_out"), _buf(v_out, torch.bfloat16, "v_out"), _stream(stream)),
+        _cache(cache, dev), T, _buf(slot_map, torch.int64, dev, "slot_map"),
+        _buf(k_out, torch.bfloat16, dev, "k_out"), _buf(v_out, torch.bfloat16, dev, "v_out"), st),
         "gdn_cache_gather")
 
 
@@ -446,19 +468,20 @@ def gdn_attn_packed(cache: gdn_cache, cu_seqlens, cu_seqlens_host, kv_len, block
                     scale: Optional[float] = None, stream=None) -> None:
     """Causal attention of a pack's rows over the cache (which holds them);
     scale defaults to d ** -0.5."""
+    dev, st = _where(stream)
     cu_h = _host_i32(cu_seqlens_host)
     n = len(cu_h) - 1
     T, d = int(cu_h[-1]), cache.head_dim
-    qp, qs, hq = _rows(q, T, None, d, "q")
+    qp, qs, hq = _rows(q, T, None, d, dev, "q")
     if tuple(out.shape[1:]) != (hq, d) or out.shape[0] < T:
         raise ValueError("out must be [T, Hq, d]")
     if kv_len.numel() < n or block_table.shape[0] < n or cu_seqlens.numel() < n + 1:
         raise ValueError("kv_len, block_table or cu_seqlens is shorter than the prompts")
     _check(load().gdn_attn_packed(
-        ctypes.addressof(cache), hq, d ** -0.5 if scale is None else scale,
-        _buf(cu_seqlens, torch.int32, "cu_seqlens"), cu_h.ctypes.data, n, T,
-        _buf(kv_len, torch.int32, "kv_len"), _buf(block_table, torch.int32, "block_table"),
-        block_table.shape[1], qp, qs, _buf(out, torch.bfloat16, "out"), _stream(stream)),
+        _cache(cache, dev), hq, d ** -0.5 if scale is None else scale,
+        _buf(cu_seqlens, torch.int32, dev, "cu_seqlens"), cu_h.ctypes.data, n, T,
+        _buf(kv_len, torch.int32, dev, "kv_len"), _buf(block_table, torch.int32, dev, "block_table"),
+        block_table.shape[1], qp, qs, _buf(out, torch.bfloat16, dev, "out"), st),
         "gdn_attn_packed")
 
 
@@ -477,16 +500,17 @@ def gdn_attn_decode(cache: gdn_cache, n_tok: int, kv_len, block_table, q, out,
     """Causal attention of n_tok rows per request (q [batch * n_tok, Hq, d])
     over the cache.  workspace: a uint8 tensor of gdn_attn_decode_workspace()
     bytes; max_kv_len: an upper bound of kv_len (default: the table's pages)."""
+    dev, st = _where(stream)
     B, max_pages = kv_len.numel(), block_table.shape[1]
     d = cache.head_dim
-    qp, qs, hq = _rows(q, B * n_tok, None, d, "q")
+    qp, qs, hq = _rows(q, B * n_tok, None, d, dev, "q")
     if tuple(out.shape[1:]) != (hq, d) or out.shape[0] < B * n_tok:
         raise ValueError("out must be [batch * n_tok, Hq, d]")
     if block_table.shape[0] < B:
         raise ValueError("block_table is shorter than the batch")
     _check(load().gdn_attn_decode(
-        ctypes.addressof(cache), hq, d ** -0.5 if scale is None else scale, B, n_tok,
-        _buf(kv_len, torch.int32, "kv_len"), _buf(block_table, torch.int32, "block_table"), max_pages,
+        _cache(cache, dev), hq, d ** -0.5 if scale is None else scale, B, n_tok,
+        _buf(kv_len, torch.int32, dev, "kv_len"), _buf(block_table, torch.int32, dev, "block_table"), max_pages,
         min(max_pages * cache.page, 2**31 - 1) if max_kv_len is None else max_kv_len, qp, qs,
-        _buf(out, torch.bfloat16, "out"), _buf(workspace, torch.uint8, "workspace"),
-        0 if workspace is None else workspace.numel(), _stream(stream)), "gdn_attn_decode")
+        _buf(out, torch.bfloat16, dev, "out"), _buf(workspace, torch.uint8, dev, "workspace"),
+        0 if workspace is None else workspace.numel(), st), "gdn_attn_decode")
