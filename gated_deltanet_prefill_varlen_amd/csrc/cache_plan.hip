@@ -1,12 +1,16 @@
 // Page planner: block tables, the pack of new tokens and its slot map from
 // the lengths that requests hold and want, without a host round trip.
 //
-// One workgroup plans: prefix sums over the requests (1,024 at a time, their
-// results in LDS) turn lengths into stack positions and pack offsets, and the
-// pages and tokens are then dealt out flat, each finding its request by a
-// binary search of the prefix in LDS, so a request of many pages does not
-// hold up its lane.  Everything is integer work on a few kB: latency bounds
-// it.
+// One workgroup plans: prefix sums over the requests turn lengths into stack
+// positions and pack offsets, and the pages and tokens are then dealt out flat,
+// each finding its request by a binary search of the prefix in LDS, so a
+// request of many pages does not hold up its lane.  Everything is integer work
+// on a few kB, so the number of dependent steps through memory bounds it.  Up
+// to 1,024 requests there are two: the lengths, and then everything else at
+// once, since the page at any place of the stack is known without the stack
+// having been written (below its old top it is read there, above it it comes
+// from the row that gives it back).  More requests go 1,024 at a time, through
+// the stack in memory.
 #include "cache_internal.h"
 #include "gdn_device.h"
 
@@ -80,6 +84,102 @@ __device__ __forceinline__ int64_t slot_of(const PlanArgs& a, int i, int64_t p) 
   const int32_t id = a.table[(int64_t)i * a.max_pages + (p >> a.page_shift)];
   if (id < 0 || id >= a.n_pages) return -1;
   return ((int64_t)id << a.page_shift) + (p & ((1 << a.page_shift) - 1));
+}
+
+struct SmallLds {
+  int64_t back[kPlan + 1], more[kPlan + 1], fresh[kPlan + 1];   // exclusive prefixes
+  int32_t kv[kPlan], have[kPlan], need[kPlan], status[kPlan];
+  int64_t wave[kPlan / 64][3];
+  unsigned long long got;
+};
+
+// n_seqs <= kPlan
+__global__ void __launch_bounds__(kPlan) plan_few_kernel(const PlanArgs a, const int fill) {
+  __shared__ SmallLds l;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int n = a.n_seqs, shift = a.page_shift;
+  const int64_t old_top = min(max(*a.free_count, 0), a.n_pages);
+  const Lengths r = lengths_of(a, tid);
+  int64_t x[3];   // given back, asked for, new tokens
+  x[2] = r.status != 3 && r.want > r.kv ? r.want - r.kv : 0;
+  x[0] = r.have > r.need ? r.have - r.need : 0;
+  // (a request refused for the slot map's end asks for no pages, but then no
+  // later one gets any either)
+  x[1] = r.status == 0 && r.need > r.have ? r.need - r.have : 0;
+  int64_t s[3] = {x[0], x[1], x[2]};
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1)
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const int64_t y = __shfl_up(s[q], d);
+      if (lane >= d) s[q] += y;
+    }
+  if (lane == 63)
+#pragma unroll
+    for (int q = 0; q < 3; ++q) l.wave[w][q] = s[q];
+  if (tid == 0) l.got = 0;
+  __syncthreads();
+  int64_t all[3] = {0, 0, 0};
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    s[q] -= x[q];
+    for (int i = 0; i * 64 < n; ++i) {
+      const int64_t y = l.wave[i][q];
+      if (i < w) s[q] += y;
+      all[q] += y;
+    }
+  }
+  const int64_t left = min(old_top + all[0], (int64_t)a.n_pages);   // the stack's top after the pushes
+  int32_t status = r.status;
+  if (status == 0 && x[2] && s[2] + x[2] > a.slot_cap) status = 4;
+  // granted: every page asked for up to here is there; the requests that take
+  // pages are so a prefix of those that ask, and take the first ones
+  if (status == 0 && x[1] && s[1] + x[1] > left) status = 1;
+  l.back[tid] = s[0];
+  l.more[tid] = s[1];
+  l.fresh[tid] = s[2];
+  l.kv[tid] = (int32_t)r.kv;
+  l.have[tid] = r.have;
+  l.need[tid] = r.need;
+  l.status[tid] = status;
+  if (status == 0 && x[1]) atomicMax(&l.got, (unsigned long long)(s[1] + x[1]));
+  __syncthreads();
+  const int64_t got = (int64_t)l.got;
+  if (tid < n) {
+    a.kv_out[tid] = (int32_t)(status == 0 ? r.want : r.kv);
+    a.status[tid] = status;
+    a.cu[tid] = (int32_t)min(s[2], (int64_t)INT32_MAX);
+  }
+  if (tid == 0) {
+    a.cu[n] = (int32_t)min(all[2], (int64_t)INT32_MAX);
+    *a.free_count_out = (int32_t)(left - got);
+  }
+  auto given_back = [&](int64_t e) -> int32_t {   // the e-th page pushed
+    const int i = owner(l.back, n, e);
+    return a.table[(int64_t)i * a.max_pages + l.need[i] + (e - l.back[i])];
+  };
+  auto page_at = [&](int64_t place) -> int32_t { return place < old_top ? a.free_pages[place] : given_back(place - old_top); };
+  if (fill)
+    for (int64_t t = tid; t < a.slot_cap; t += kPlan) {
+      int64_t slot = -1, p = 0;
+      if (t < all[2]) {
+        const int i = owner(l.fresh, n, t);
+        p = l.kv[i] + (t - l.fresh[i]);
+        if (l.status[i] == 0) {
+          const int32_t col = (int32_t)(p >> shift);
+          const int32_t id = col < l.have[i] ? a.table[(int64_t)i * a.max_pages + col]
+                                             : page_at(left - 1 - (l.more[i] + (col - l.have[i])));
+          if (id >= 0 && id < a.n_pages) slot = ((int64_t)id << shift) + (p & ((1 << shift) - 1));
+        }
+      }
+      a.slot[t] = slot;
+      if (a.pos) a.pos[t] = (int32_t)p;
+    }
+  for (int64_t e = tid; e < got; e += kPlan) {
+    const int i = owner(l.more, n, e);
+    a.table[(int64_t)i * a.max_pages + l.have[i] + (e - l.more[i])] = page_at(left - 1 - e);
+  }
+  for (int64_t e = tid; e < all[0] && old_top + e < a.n_pages; e += kPlan) a.free_pages[old_top + e] = given_back(e);
 }
 
 __global__ void __launch_bounds__(kPlan) plan_pages_kernel(const PlanArgs a, const int fill) {
@@ -182,7 +282,8 @@ __global__ void __launch_bounds__(kFill) plan_slots_kernel(const PlanArgs a) {
 
 hipError_t launch_plan_pages(const PlanArgs& a, hipStream_t st) {
   const int fill = a.slot_cap <= 4 * kPlan;
-  hipLaunchKernelGGL(plan_pages_kernel, dim3(1), dim3(kPlan), 0, st, a, fill);
+  if (a.n_seqs <= kPlan) hipLaunchKernelGGL(plan_few_kernel, dim3(1), dim3(kPlan), 0, st, a, fill);
+  else hipLaunchKernelGGL(plan_pages_kernel, dim3(1), dim3(kPlan), 0, st, a, fill);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || fill) return e;
   hipLaunchKernelGGL(plan_slots_kernel, dim3((a.slot_cap + kFill - 1) / kFill), dim3(kFill), 0, st, a);
