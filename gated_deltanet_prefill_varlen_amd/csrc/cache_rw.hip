@@ -157,10 +157,11 @@ __device__ __forceinline__ void write_page(const AppendArgs& a, int unit, int h,
   const int tid = threadIdx.x, shift = a.c.page_shift, P = 1 << shift;
   // unit -> (prompt s, its j-th page of this call): prompt s has the units
   // cu[s] / P + 2 s on, more than its ceil(len / P) + 1 pages
-  int lo = 0, hi = a.n_seqs;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((a.cu[mid] >> shift) + 2 * mid <= unit) lo = mid; else hi = mid;
+  // (counted 64 prompts at a time: one round through memory, not log2 n)
+  int lo = -1;
+  for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
+    const int s = s0 + (tid & 63);
+    lo += __popcll(__ballot(s < a.n_seqs && (a.cu[min(s, a.n_seqs)] >> shift) + 2 * s <= unit));
   }
   const int j = unit - (a.cu[lo] >> shift) - 2 * lo;
   const int i0 = a.cu[lo], i1 = min(a.cu[lo + 1], a.n_tokens);
@@ -330,58 +331,107 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const AppendArgs 
 }
 
 // ---------------------------------------------------------------- gather --
-// A workgroup reads back 16 rows of one head.
+// A workgroup reads back 16 rows of one head.  Keys: 16 channels of a row per
+// thread.  Values lie 16 tokens to a vector, so a wave takes 4 rows, reads a
+// vector per channel for each run of rows that lie in one 16-token tile (one or
+// two for rows that follow each other) and hands its bytes out row by row; the
+// next run's vectors are on their way meanwhile.  Bound by HBM: 32,768 rows of 8
+// heads of 128 take 31 us, 0.20 GB (6.4 TB/s with a part of it still cached,
+// 48 us from cold); a prefix of 1,000 rows takes 4 us.  16 rows a wave read
+// each vector once, but are no faster anywhere (49 and 5.4 us).
 template <int D, bool I8>
 __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const GatherArgs a) {
+  constexpr int C = D / 64;   // a lane's channels of the values
+  constexpr int R = 4;        // a wave's rows
   const int h = blockIdx.y;
-  const int64_t row0 = (int64_t)blockIdx.x * 16;
+  const int64_t row0 = (int64_t)blockIdx.x * (4 * R);
+  const int lane = threadIdx.x & 63;
+  const int64_t t0 = row0 + R * (threadIdx.x >> 6);
+  const int n = (int)max(min((int64_t)R, a.n_tokens - t0), (int64_t)0);
   const int64_t slots = (int64_t)a.c.n_pages << a.c.page_shift;
   const int page_mask = (1 << a.c.page_shift) - 1;
+
+  // the wave's slots, a lane each; -1 for one outside the cache (which ends
+  // with a tile's end, so a tile is inside as a whole or not at all)
+  int64_t mine = lane < n ? a.slot[t0 + lane] : -1;
+  if (mine < 0 || mine >= slots) mine = -1;
+  const int64_t before = __shfl_up(mine, 1);
+  uint64_t runs = __ballot(lane < n && (lane == 0 || (mine >> 4) != (before >> 4)));
+  uint4 w[C], next[C];
+  float scale = 0.f, next_scale = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) w[c] = next[c] = make_uint4(0, 0, 0, 0);
+  auto slot_of = [&](int r) {
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(mine >> 32), r) << 32 |
+                     (uint32_t)__builtin_amdgcn_readlane((int)mine, r));
+  };
+  auto load = [&](int r, uint4 (&to)[C], float& to_scale) {
+    const int64_t s = slot_of(r);
+    to_scale = 0.f;
+    if (s < 0) return;
+    const int64_t page = s >> a.c.page_shift;
+    const uint8_t* p = a.c.v + page_base(a.c, page, h) + (((s & page_mask) >> 4) * D + C * lane) * 16;
+#pragma unroll
+    for (int c = 0; c < C; ++c) to[c] = reinterpret_cast<const uint4*>(p)[c];
+    to_scale = a.c.vs[page * a.c.Hkv + h];
+  };
+  if (a.v_out && n) load(0, w, scale);
+
   if (a.k_out) {
-    for (int e = threadIdx.x; e < D; e += kThreads) {   // 16 rows x D / 16 chunks
+#pragma unroll
+    for (int e = threadIdx.x; e < R * D / 4; e += kThreads) {   // 4 R rows x D / 16 chunks
       const int64_t t = row0 + e / (D / 16);
       const int c = e % (D / 16);
       if (t >= a.n_tokens) continue;
       const int64_t s = a.slot[t];
       const bool ok = s >= 0 && s < slots;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      float scale = 0.f;
+      uint4 k = make_uint4(0, 0, 0, 0);
+      float k_scale = 0.f;
       if (ok) {
         const int64_t page = s >> a.c.page_shift;
-        w = *reinterpret_cast<const uint4*>(a.c.k + page_base(a.c, page, h) + (s & page_mask) * D + 16 * c);
-        scale = a.c.ks[page * a.c.Hkv + h];
+        k = *reinterpret_cast<const uint4*>(a.c.k + page_base(a.c, page, h) + (s & page_mask) * D + 16 * c);
+        k_scale = a.c.ks[page * a.c.Hkv + h];
       }
       float x[16];
-      decode4<I8>(w.x, x);
-      decode4<I8>(w.y, x + 4);
-      decode4<I8>(w.z, x + 8);
-      decode4<I8>(w.w, x + 12);
+      decode4<I8>(k.x, x);
+      decode4<I8>(k.y, x + 4);
+      decode4<I8>(k.z, x + 8);
+      decode4<I8>(k.w, x + 12);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = ok ? x[i] * scale : 0.f;
+      for (int i = 0; i < 16; ++i) x[i] = ok ? x[i] * k_scale : 0.f;
       uint4* dst = reinterpret_cast<uint4*>(a.k_out + (t * a.c.Hkv + h) * D + 16 * c);
       dst[0] = pack8(x);
       dst[1] = pack8(x + 8);
     }
   }
-  if (a.v_out) {
-    for (int e = threadIdx.x; e < 8 * D; e += kThreads) {   // 16 rows x D / 2 channel pairs
-      const int64_t t = row0 + e / (D / 2);
-      const int c2 = e % (D / 2);
-      if (t >= a.n_tokens) continue;
-      const int64_t s = a.slot[t];
-      float x0 = 0.f, x1 = 0.f;
-      if (s >= 0 && s < slots) {
-        const int64_t page = s >> a.c.page_shift;
-        const int o = (int)(s & page_mask);
-        const uint8_t* p = a.c.v + page_base(a.c, page, h) + ((o >> 4) * D + 2 * c2) * 16 + (o & 15);
-        const float scale = a.c.vs[page * a.c.Hkv + h];
+  if (!a.v_out) return;
+  while (runs) {
+    const int r0 = __builtin_ctzll(runs);
+    runs &= runs - 1;
+    const int r1 = runs ? __builtin_ctzll(runs) : n;
+    if (runs) load(r1, next, next_scale);
+    const bool ok = slot_of(r0) >= 0;
+    for (int r = r0; r < r1; ++r) {
+      const int o = (int)(slot_of(r) & 15);
+      const uint32_t pick = (uint32_t)(o & 7) | 0x0C0C0C00u;   // that byte, zeros above
+      float x[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
         float f[4];
-        decode4<I8>((uint32_t)p[0] | (uint32_t)p[16] << 8, f);
-        x0 = f[0] * scale;
-        x1 = f[1] * scale;
+        decode4<I8>(o < 8 ? __builtin_amdgcn_perm(w[c].y, w[c].x, pick) : __builtin_amdgcn_perm(w[c].w, w[c].z, pick), f);
+        x[c] = ok ? f[0] * scale : 0.f;
       }
-      *reinterpret_cast<uint32_t*>(a.v_out + (t * a.c.Hkv + h) * D + 2 * c2) = pack_bf16(x0, x1);
+      uint16_t* dst = a.v_out + ((t0 + r) * a.c.Hkv + h) * D + C * lane;
+      if constexpr (C == 1) {
+        dst[0] = (uint16_t)pack_bf16(x[0], 0.f);
+      } else {
+#pragma unroll
+        for (int c = 0; c < C; c += 2) reinterpret_cast<uint32_t*>(dst)[c / 2] = pack_bf16(x[c], x[c + 1]);
+      }
     }
+#pragma unroll
+    for (int c = 0; c < C; ++c) w[c] = next[c];
+    scale = next_scale;
   }
 }
 
@@ -409,7 +459,7 @@ hipError_t launch_rope_append(const AppendArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_cache_gather(const GatherArgs& a, hipStream_t st) {
-  const dim3 grid((uint32_t)((a.n_tokens + 15) / 16), a.c.Hkv);
+  const dim3 grid((uint32_t)(((int64_t)a.n_tokens + 15) / 16), a.c.Hkv);
   const dim3 block(kThreads);
   switch (a.c.dim) {
     case 64:
