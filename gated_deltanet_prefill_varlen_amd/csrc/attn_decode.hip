@@ -29,8 +29,10 @@ constexpr int kWaves = 4;
 constexpr int kTile = 64;
 
 // Keys per workgroup: by the head size alone, so that how a request's keys are
-// split never depends on its batch.
-__host__ __device__ constexpr int split_keys(int dim) { return dim == 256 ? 2048 : 1024; }
+// split never depends on its batch.  Fewer make more partial sums to write and
+// join, more leave the last workgroups to run alone (16 requests of 4,096 to
+// 32,768 keys, 2 kv heads of 256: 1,024 keys 120 us, 1,536 105, 2,048 120).
+__host__ __device__ constexpr int split_keys(int dim) { return dim == 256 ? 1536 : 1024; }
 __host__ __device__ inline int n_splits(int L, int dim) { return L <= 0 ? 1 : (L + split_keys(dim) - 1) / split_keys(dim); }
 
 struct Partial {
@@ -40,17 +42,19 @@ struct Partial {
 };
 
 template <int D, bool I8, int NT>
-__global__ void __launch_bounds__(64 * kWaves, NT * D <= 128 ? 2 : 1) attn_decode_kernel(const AttnArgs a, const Partial part) {
+__global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 ? 2 : 1) attn_decode_kernel(const AttnArgs a, const Partial part) {
   constexpr int KL = D / 64;    // 16-byte loads of a key per lane
   constexpr int KS = D / 32;    // contraction steps of a score
   constexpr int OB = D / 16;    // 16-channel blocks of the output
-  // heads first, then requests, then splits: workgroups go to the eight XCDs in
-  // turn, and an order by splits would send every first split to one of them
-  const int b = blockIdx.y, sp = blockIdx.z;
+  // Workgroups go to the eight XCDs in turn: heads first, then requests, then
+  // splits, and the requests one further on with every split, so that neither
+  // the first splits nor a long request's all go to one of them (16 requests of
+  // 4,096 to 32,768 keys, 2 kv heads of 256: 114 us, without the turn 155).
+  const int sp = blockIdx.z, b = (int)((blockIdx.y + blockIdx.z) % gridDim.y);
   const int G = a.Hq / a.c.Hkv, R = a.n_tok * G;
   const int groups = (R + 16 * NT - 1) / (16 * NT);
-  const int hk = blockIdx.x / groups, r0 = (blockIdx.x % groups) * 16 * NT;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c16 = lane & 15, g = lane >> 4;
+  const int hk = blockIdx.x / groups, r0 = (blockIdx.x % groups) * 16 * NT;
   const int shift = a.c.page_shift, pmask = (1 << shift) - 1;
   const int32_t* table = a.table + (int64_t)b * a.max_pages;
   constexpr int kStep = kWaves * kTile, per = split_keys(D);
@@ -65,16 +69,11 @@ __global__ void __launch_bounds__(64 * kWaves, NT * D <= 128 ? 2 : 1) attn_decod
   const int splits = bad ? 1 : n_splits(L, D);
   if (sp >= splits) return;
 
-  // the query row of this lane's column, per tile
-  int64_t tok[NT];
-  int hq[NT], last[NT];      // its head, and the last key it sees
+  // this lane's column: its query row per tile, and the last key that it sees
+  auto row_of = [&](int t) -> int { return min(r0 + 16 * t + c16, R - 1); };
+  int last[NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int r = min(r0 + 16 * t + c16, R - 1), i = r / G;
-    tok[t] = (int64_t)b * a.n_tok + i;
-    hq[t] = hk * G + (r - i * G);
-    last[t] = L - a.n_tok + i;
-  }
+  for (int t = 0; t < NT; ++t) last[t] = L - a.n_tok + row_of(t) / G;
   if (bad || L == 0) {
     for (int e = tid; e < 16 * NT * D; e += 64 * kWaves) {
       const int r = r0 + e / D;
@@ -86,36 +85,22 @@ __global__ void __launch_bounds__(64 * kWaves, NT * D <= 128 ? 2 : 1) attn_decod
     return;
   }
 
-  // Queries: in registers, or in LDS (the same for every wave) where they would
-  // take 64 registers: those are needed for the codes in flight.
-  constexpr bool QL = NT * KS * 4 >= 64;
+  // Queries: in registers, or in LDS (the same for every wave) where the
+  // registers are needed for the codes in flight.
+  constexpr bool QL = NT * D >= 256;
+  constexpr int QN = QL ? NT * KS / kWaves : NT * KS;
   __shared__ __align__(16) bf16x8 ql[QL ? NT * KS : 1][64];
-  bf16x8 q[NT][QL ? 1 : KS];
+  bf16x8 q[QN];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const uint16_t* p = a.q + tok[t] * a.q_stride + hq[t] * D + 16 * g;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const uint16_t* const from = p + 64 * (k >> 1) + 8 * (k & 1);
-      if constexpr (!QL) q[t][k] = *reinterpret_cast<const bf16x8*>(from);
-      else if (wave == k % kWaves) ql[t * KS + k][lane] = *reinterpret_cast<const bf16x8*>(from);
-    }
+  for (int n = 0; n < QN; ++n) {
+    const int e = QL ? n * kWaves + wave : n, t = e / KS, k = e % KS, r = row_of(t), i = r / G;
+    const uint16_t* p = a.q + ((int64_t)b * a.n_tok + i) * a.q_stride + (hk * G + (r - i * G)) * D + 16 * g;
+    q[n] = *reinterpret_cast<const bf16x8*>(p + 64 * (k >> 1) + 8 * (k & 1));
   }
-  if constexpr (QL) __syncthreads();
   auto query = [&](int t, int k) -> bf16x8 {
     if constexpr (QL) return ql[t * KS + k][lane];
-    else return q[t][k];
+    else return q[t * KS + k];
   };
-
-  f32x4 o[NT][OB];
-  float m[NT], l[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    m[t] = -__builtin_inff();
-    l[t] = 0.f;
-#pragma unroll
-    for (int x = 0; x < OB; ++x) o[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
 
   const int key1 = min(L, key0 + per);
   const float log_scale = a.scale * kLog2e;
@@ -151,6 +136,21 @@ __global__ void __launch_bounds__(64 * kWaves, NT * D <= 128 ? 2 : 1) attn_decod
     load_keys(t0, page_of(ek, t0 + 16 * (c16 >> 2)), pv);
     load_values(t0, pv);
   }
+  if constexpr (QL) {
+#pragma unroll
+    for (int n = 0; n < QN; ++n) ql[n * kWaves + wave][lane] = q[n];
+    __syncthreads();
+  }
+  f32x4 o[NT][OB];
+  float m[NT], l[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    m[t] = -__builtin_inff();
+    l[t] = 0.f;
+#pragma unroll
+    for (int x = 0; x < OB; ++x) o[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
   for (; t0 < key1; t0 += kStep) {
     const bool more = t0 + kStep < key1;
     const int kk2 = t0 + 2 * kStep + 16 * (c16 >> 2), kv2 = t0 + 2 * kStep + 16 * g;
@@ -267,11 +267,10 @@ __global__ void __launch_bounds__(64 * kWaves, NT * D <= 128 ? 2 : 1) attn_decod
     pv1 = pv2;
   }
 
-  // The four waves, in order: each sums a quarter of the 16 x 16 blocks of the
-  // output, which the other three leave for it in LDS.
+  // The waves' sums meet in LDS, each against the common maximum; then each
+  // wave adds up a quarter of the 16 x 16 blocks, in the waves' order.
   __shared__ float sm[kWaves][16 * NT], sl[kWaves][16 * NT];
-  constexpr int NB = NT * OB / kWaves;
-  __shared__ __align__(16) f32x4 so[kWaves][kWaves - 1][NB][64];   // for wave, from (its number - 1 after mine)
+  __shared__ __align__(16) f32x4 so[kWaves][NT * OB][64];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     l[t] += __shfl_xor(l[t], 16);
@@ -282,46 +281,39 @@ __global__ void __launch_bounds__(64 * kWaves, NT * D <= 128 ? 2 : 1) attn_decod
     }
   }
   __syncthreads();
-  float mt[NT], lt[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    mt[t] = -__builtin_inff();
-    lt[t] = 0.f;
+    float mt = -__builtin_inff();
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) mt[t] = fmaxf(mt[t], sm[w][16 * t + c16]);
-    const float base = mt[t] == -__builtin_inff() ? 0.f : mt[t];
+    for (int w = 0; w < kWaves; ++w) mt = fmaxf(mt, sm[w][16 * t + c16]);
+    const float mine = m[t] == -__builtin_inff() ? 0.f : exp2_fast(m[t] - mt);
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) lt[t] += sl[w][16 * t + c16] * exp2_fast(sm[w][16 * t + c16] - base);
-    const float mine = exp2_fast(m[t] - base);
-#pragma unroll
-    for (int x = 0; x < OB; ++x) {
-      const int n = t * OB + x, to = n % kWaves;
-      o[t][x] *= mine;
-      if (to != wave) so[to][(wave - to - 1) & (kWaves - 1)][n / kWaves][lane] = o[t][x];
-    }
+    for (int x = 0; x < OB; ++x) so[wave][t * OB + x][lane] = o[t][x] * mine;
   }
   __syncthreads();
+#pragma unroll 1
+  for (int n = wave; n < NT * OB; n += kWaves) {
+    const int t = n / OB, c = 16 * (n % OB) + 4 * g, r = r0 + 16 * t + c16;
+    f32x4 y = so[0][n][lane];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const float inv = mt[t] == -__builtin_inff() ? 0.f : 1.f / lt[t];
-    const bool mine = r0 + 16 * t + c16 < R;
+    for (int w = 1; w < kWaves; ++w) y += so[w][n][lane];
+    float mt = -__builtin_inff(), lt = 0.f;
 #pragma unroll
-    for (int x = 0; x < OB; ++x) {
-      const int n = t * OB + x, to = n % kWaves, c = 16 * x + 4 * g;
-      if (to != wave) continue;
-      f32x4 y = {0.f, 0.f, 0.f, 0.f};
+    for (int w = 0; w < kWaves; ++w) mt = fmaxf(mt, sm[w][16 * t + c16]);
+    const float base = mt == -__builtin_inff() ? 0.f : mt;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) y += w == to ? o[t][x] : so[to][(w - to - 1) & (kWaves - 1)][n / kWaves][lane];
-      if (!mine) continue;
-      const int64_t row = tok[t] * a.Hq + hq[t];
-      if (splits == 1) {
-        *reinterpret_cast<uint2*>(a.out + row * D + c) = make_uint2(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv));
-      } else {
-        const int rows = a.n_tok * a.Hq;
-        const int64_t pr = row + ((int64_t)b * (part.splits - 1) + sp) * rows;   // [b][split][row of the request]
-        *reinterpret_cast<f32x4*>(part.o + pr * D + c) = y;
-        if (c == 0) part.ml[pr] = make_float2(mt[t], lt[t]);
-      }
+    for (int w = 0; w < kWaves; ++w) lt += sl[w][16 * t + c16] * exp2_fast(sm[w][16 * t + c16] - base);
+    if (r >= R) continue;
+    const int i = r / G;
+    const int64_t row = ((int64_t)b * a.n_tok + i) * a.Hq + hk * G + (r - i * G);
+    if (splits == 1) {
+      const float inv = mt == -__builtin_inff() ? 0.f : 1.f / lt;
+      *reinterpret_cast<uint2*>(a.out + row * D + c) = make_uint2(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv));
+    } else {
+      const int rows = a.n_tok * a.Hq;
+      const int64_t pr = row + ((int64_t)b * (part.splits - 1) + sp) * rows;   // [b][split][row of the request]
+      *reinterpret_cast<f32x4*>(part.o + pr * D + c) = y;
+      if (c == 0) part.ml[pr] = make_float2(mt, lt);
     }
   }
 }
@@ -370,11 +362,14 @@ __global__ void __launch_bounds__(64) attn_join_kernel(const AttnArgs a, const P
 template <int D, bool I8>
 hipError_t launch_d(const AttnArgs& a, const Partial& part, hipStream_t st) {
   const int R = a.n_tok * (a.Hq / a.c.Hkv);
-  const int nt = R <= 16 ? 1 : R <= 32 || D == 256 ? 2 : 4;
+  // Two tiles of rows a wave where there are more than one: they share the
+  // codes' conversion (32 rows, 2 kv heads of 128, 16 x 4,096 .. 32,768 keys:
+  // 59 us, with one tile a wave 69).  Four leave room for one wave a SIMD only,
+  // which loses more than it saves (64 rows of 128: 83 us, with four 113).
+  const int nt = R <= 16 ? 1 : 2;
   const dim3 grid(a.c.Hkv * ((R + 16 * nt - 1) / (16 * nt)), a.n_seqs, part.splits), block(64 * kWaves);
   if (nt == 1) hipLaunchKernelGGL((attn_decode_kernel<D, I8, 1>), grid, block, 0, st, a, part);
-  else if (nt == 2) hipLaunchKernelGGL((attn_decode_kernel<D, I8, 2>), grid, block, 0, st, a, part);
-  else if constexpr (D < 256) hipLaunchKernelGGL((attn_decode_kernel<D, I8, 4>), grid, block, 0, st, a, part);
+  else hipLaunchKernelGGL((attn_decode_kernel<D, I8, 2>), grid, block, 0, st, a, part);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || part.splits == 1) return e;
   hipLaunchKernelGGL((attn_join_kernel<D>), dim3((uint32_t)(a.n_seqs * a.n_tok * a.Hq)), dim3(64), 0, st, a, part);
