@@ -62,6 +62,11 @@ __device__ __forceinline__ float add_pair(uint32_t two, float x) {
   return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, two), __builtin_bit_cast(bf16x2, 0x3F803F80u), x, false);
 }
 
+// A value that is the same in every lane, in a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
+
 typedef const int32_t __attribute__((address_space(4)))* ConstI32;
 typedef const float __attribute__((address_space(4)))* ConstF32;
 
@@ -102,7 +107,6 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
   // this lane's query row and the last key it sees
   const int r0 = (int)first + wave * 32;
   const int r = min(r0 + c32, (int)rows - 1), i = r / G, hq = hk * G + (r - i * G);
-  const int64_t at = (int64_t)(i0 + i) * a.Hq + hq;
   const int last = L - n + i;
   const bool bad = L < 0 || L > a.max_kv;
   // keys that the workgroup's last row sees, and that all of its rows and all
@@ -121,7 +125,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
     if (a.scale < 0.f) w ^= 0x80008000u;
     q[k] = __builtin_bit_cast(bf16x8, w);
   }
-  const float log_scale = fabsf(a.scale) * kLog2e;
+  const float log_scale = uniform(fabsf(a.scale) * kLog2e);
 
   f32x16 o[OB];
   float m = -__builtin_inff(), l = 0.f;
@@ -201,36 +205,38 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
                                          : make_float4(fmaxf(ks * log_scale, 0x1p-126f), lv, exp2_fast(-lv), 0.f);
   };
   // LDS addresses of a lane's units of a tile: 8 channels of a key, 8 keys of a channel
-  int kput[NU], vput[NU];
-#pragma unroll
-  for (int x = 0; x < NU; ++x) {
-    const int e = part * (16 * D / PARTS) + (lane * NU + x) * 8, k = 16 * piece + e / D, c = e / 16;
-    kput[x] = k * D * 2 + (((e % D / 8) ^ swizzle_k<D>(k)) * 16);
-    vput[x] = c * KT * 2 + (((2 * piece + (e >> 3 & 1)) ^ swizzle_v<KT>(c)) * 16);
-  }
+  // (of two units: in chunks that differ in their last bit)
+  const int put_e = part * (16 * D / PARTS) + lane * NU * 8, put_k = 16 * piece + put_e / D, put_c = put_e / 16;
+  const int kput = put_k * D * 2 + (((put_e % D / 8) ^ swizzle_k<D>(put_k)) * 16);
+  const int vput = put_c * KT * 2 + (((2 * piece + (put_e >> 3 & 1)) ^ swizzle_v<KT>(put_c)) * 16);
   auto put_keys = [&](int buf, int x) {
-    *reinterpret_cast<bf16x8*>(lds + (kput[x] + buf * BYTES)) = codes_to_operand<I8>(kr[x].x, kr[x].y);
+    *reinterpret_cast<bf16x8*>(lds + ((kput ^ 16 * x) + buf * BYTES)) = codes_to_operand<I8>(kr[x].x, kr[x].y);
   };
   auto put_values = [&](int buf, int x) {
-    *reinterpret_cast<bf16x8*>(vlds + (vput[x] + buf * BYTES)) = codes_to_operand<I8>(vr[x].x, vr[x].y);
+    *reinterpret_cast<bf16x8*>(vlds + ((vput ^ 16 * x) + buf * BYTES)) = codes_to_operand<I8>(vr[x].x, vr[x].y);
   };
 
   // ---- operands: even ones 16 channels of 32 keys, odd ones 16 keys of 32 channels ----
   constexpr int OPS = 2 * KB * KS, KA = KS < 8 ? KS : 8;
   static_assert(KB * KS == NP * OB, "as many operands of keys as of values");
   const int krow = 16 * (c32 >> 4) + 8 * ((c32 >> 2) & 1) + 4 * ((c32 >> 3) & 1) + (c32 & 3);
-  int kget[KA], vget[NP];
+  // Heads of 256 leave no registers for the addresses of every chunk: those are
+  // formed from the first one's, by its bits (the others keep them: a vector
+  // instruction a product costs more).
+  constexpr bool FORM = D == 256;
+  int kget[FORM ? 1 : KA], vget[FORM ? 1 : NP];
 #pragma unroll
-  for (int k = 0; k < KA; ++k) kget[k] = krow * D * 2 + (((2 * k + h) ^ swizzle_k<D>(krow)) * 16);
+  for (int k = 0; k < (FORM ? 1 : KA); ++k) kget[k] = krow * D * 2 + (((2 * k + h) ^ swizzle_k<D>(krow)) * 16);
 #pragma unroll
-  for (int u = 0; u < NP; ++u) vget[u] = c32 * KT * 2 + (((2 * u + h) ^ swizzle_v<KT>(c32)) * 16);
+  for (int u = 0; u < (FORM ? 1 : NP); ++u) vget[u] = c32 * KT * 2 + (((2 * u + h) ^ swizzle_v<KT>(c32)) * 16);
+  auto v_at = [&](int u) -> int { return FORM ? vget[0] ^ 32 * u : vget[u]; };
   auto operand = [&](int c, int kbuf, int vbuf) -> bf16x8 {
     if (c & 1) {
       const int x = (c >> 1) / NP, u = (c >> 1) % NP;
-      return *reinterpret_cast<const bf16x8*>(vlds + (vget[u] + vbuf * BYTES + x * 32 * KT * 2));
+      return *reinterpret_cast<const bf16x8*>(vlds + (v_at(u) + vbuf * BYTES + x * 32 * KT * 2));
     }
     const int b = (c >> 1) / KS, k = (c >> 1) % KS;
-    return *reinterpret_cast<const bf16x8*>(lds + (kget[k % KA] + kbuf * BYTES + b * 32 * D * 2 + k / KA * 256));
+    return *reinterpret_cast<const bf16x8*>(lds + ((FORM ? kget[0] ^ 32 * (k % KA) : kget[k % KA]) + kbuf * BYTES + b * 32 * D * 2 + k / KA * 256));
   };
 
   // The waves of one SIMD take turns: while waves 0 - 3 form products, waves
@@ -260,6 +266,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
   auto step = [&](auto jc, int tile) {
     constexpr int J = decltype(jc)::value, J1 = (J + 1) % 3, J2 = (J + 2) % 3;   // buffers of tiles t, t + 1 and t - 1 or t + 2
     const int key0 = KT * tile;
+    if constexpr (FORM) asm volatile("" : "+v"(kget[0]), "+v"(vget[0]));   // in every step anew
     clean(tile + 1);
     f32x16 sc[KB];
 #pragma unroll
@@ -313,13 +320,14 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
 #pragma unroll
             for (int w = 0; w < PARTS; ++w) nan[u] |= nan_keys[tile & 3][u * PARTS + w];
             any |= nan[u];
+            nan[u] >>= 8 * h;
           }
           if (__any(any)) {
 #pragma unroll
             for (int b = 0; b < KB; ++b)
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                if ((nan[2 * b + (e >> 3)] >> (8 * h + (e & 7)) & 1) && sc[b][e] != -__builtin_inff()) sc[b][e] = __builtin_nanf("");
+                if ((nan[2 * b + (e >> 3)] >> (e & 7) & 1) && sc[b][e] != -__builtin_inff()) sc[b][e] = __builtin_nanf("");
           }
         }
       }
@@ -376,7 +384,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
     const int p0 = table[0];
     const bool held = p0 >= 0 && p0 < a.c.n_pages;
     const float v0 = ((ConstF32)a.c.vs)[(int64_t)(held ? p0 : 0) * a.c.Hkv + hk];
-    unit_log = fminf(fmaxf(__builtin_amdgcn_logf(held ? fmaxf(v0, kMinScale) : 1.f), -30.f), 60.f);
+    unit_log = uniform(fminf(fmaxf(__builtin_amdgcn_logf(held ? fmaxf(v0, kMinScale) : 1.f), -30.f), 60.f));
     entry = entry_of(0);
     look_up(0);
     fetch(a.c.k, kr);
@@ -414,14 +422,17 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
 #pragma unroll
     for (int c = 0; c < NP * OB; ++c)
       o[c / NP] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-          *reinterpret_cast<const bf16x8*>(tail + vget[c % NP] + c / NP * 32 * KT * 2), p[c % NP], o[c / NP], 0, 0, 0);
+          *reinterpret_cast<const bf16x8*>(tail + v_at(c % NP) + c / NP * 32 * KT * 2), p[c % NP], o[c / NP], 0, 0, 0);
     if (wave < 4) barrier();
   }
 
-  if (r0 + c32 >= rows) return;
+  // (the row formed again: it would cost registers all the way)
+  const int lane1 = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+  const int r1 = r0 + (lane1 & 31), i1 = r1 / G;
+  if (r1 >= rows) return;
   const float sum = add_halves(l);
   const float inv = bad ? __builtin_nanf("") : m == -__builtin_inff() ? 0.f : exp2_fast(unit_log) / sum;
-  uint16_t* out = a.out + at * D + 4 * h;
+  uint16_t* out = a.out + ((int64_t)(i0 + i1) * a.Hq + hk * G + (r1 - i1 * G)) * D + 4 * (lane1 >> 5);
 #pragma unroll
   for (int x = 0; x < OB; ++x)
 #pragma unroll
