@@ -14,6 +14,12 @@
 // one 16-byte vector of the cache's transposed value tile, and the
 // probabilities go from one product into the next without leaving their lane.
 //
+// Measured: 32 requests of 17 to 8,192 keys, 8 kv heads of 128, e4m3: 64 us,
+// 4.1 TB/s of codes (a plain sum reads 4.0 TB/s); 16 of 4,096 to 32,768 keys with
+// 4 tokens each, 2 kv heads of 256, int8: 104 us, 2.9 TB/s.  There 32 rows of
+// sums leave one wave a SIMD, whose conversions (45 % of its cycles) do not
+// overlap its waits.
+//
 // Keys are split over workgroups in runs of fixed length (split_keys), the
 // four waves of a workgroup take 64-key tiles in turn, and partial results
 // (fp32 sums against the running maximum) are joined in a fixed order, so a
