@@ -39,7 +39,7 @@ constexpr int kTile = 64;
 // join, more leave the last workgroups to run alone (16 requests of 4,096 to
 // 32,768 keys, 2 kv heads of 256: 1,024 keys 120 us, 1,536 105, 2,048 120).
 __host__ __device__ constexpr int split_keys(int dim) { return dim == 256 ? 1536 : 1024; }
-__host__ __device__ inline int n_splits(int L, int dim) { return L <= 0 ? 1 : (L + split_keys(dim) - 1) / split_keys(dim); }
+__host__ __device__ inline int n_splits(int L, int dim) { return L <= 0 ? 1 : (L - 1) / split_keys(dim) + 1; }
 
 struct Partial {
   float* o;    // [B][splits][n_tok * Hq][D]
@@ -383,6 +383,8 @@ hipError_t launch_d(const AttnArgs& a, const Partial& part, hipStream_t st) {
 }
 
 }  // namespace
+
+int attn_decode_splits(int dim, int max_kv) { return n_splits(max_kv, dim); }
 
 int64_t attn_decode_bytes(int dim, int Hq, int batch, int n_tok, int max_kv) {
   const int64_t s = n_splits(max_kv, dim);

@@ -84,6 +84,7 @@ hipError_t launch_plan_pages(const PlanArgs& a, hipStream_t stream);
 hipError_t launch_rope_append(const AppendArgs& a, hipStream_t stream);
 hipError_t launch_cache_gather(const GatherArgs& a, hipStream_t stream);
 hipError_t launch_attn_packed(const AttnArgs& a, hipStream_t stream);
+int attn_decode_splits(int dim, int max_kv);   // workgroups that share a request's keys
 int64_t attn_decode_bytes(int dim, int Hq, int batch, int n_tok, int max_kv);
 hipError_t launch_attn_decode(const AttnArgs& a, void* workspace, hipStream_t stream);
 

@@ -117,6 +117,9 @@ gdn_status bf16_stride(int64_t given, int64_t dense, int64_t* out) {
   return GDN_OK;
 }
 
+// A launch holds fewer than 2^32 threads along its first axis.
+bool fits_grid(int64_t groups, int64_t threads) { return groups * threads <= UINT32_MAX; }
+
 // What both attention calls check alike.
 gdn_status check_attn(const gdn_cache* cache, int32_t Hq, float scale, int32_t n_seqs, int32_t max_pages,
                       const int32_t* kv_len, const int32_t* table, const void* q, int64_t q_stride,
@@ -500,8 +503,8 @@ gdn_status gdn_rope_append(const gdn_rope* rope, const gdn_cache* cache, int32_t
   const void* ptrs[] = {q, k, v, q_out};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return GDN_ERR_SHAPE;
-  // one workgroup per page and head, and per few rows of queries
-  if (((int64_t)n_tokens / cache->page + 2 * (int64_t)n_seqs) * hkv + n_tokens > INT32_MAX) return GDN_ERR_SHAPE;
+  // a workgroup of 256 per page and head, and per few rows of queries
+  if (!fits_grid(((int64_t)n_tokens / cache->page + 2 * (int64_t)n_seqs) * hkv + n_tokens, 256)) return GDN_ERR_SHAPE;
   if (n_tokens == 0) return GDN_OK;
   a.rope.rot = rope->rot_dim; a.rope.n_axes = rope->n_axes; a.rope.adjacent = rope->adjacent;
   a.rope.scale = rope->scale;
@@ -520,7 +523,7 @@ gdn_status gdn_cache_gather(const gdn_cache* cache, int32_t n_tokens, const int6
   gdn::GatherArgs a{};
   gdn_status st = check_cache(cache, true, &a.c);
   if (st != GDN_OK) return st;
-  if (n_tokens < 0 || a.c.Hkv > 65535) return GDN_ERR_SHAPE;
+  if (n_tokens < 0 || a.c.Hkv > 65535 || !fits_grid((int64_t)n_tokens / 16 + 1, 256)) return GDN_ERR_SHAPE;
   if (!k_out && !v_out) return GDN_ERR_NULL;
   if (n_tokens > 0 && !slot_map) return GDN_ERR_NULL;
   if ((k_out && !aligned16(k_out)) || (v_out && !aligned16(v_out))) return GDN_ERR_SHAPE;
@@ -542,6 +545,8 @@ gdn_status gdn_attn_packed(const gdn_cache* cache, int32_t num_q_heads, float sc
                   n_tokens, &a);
   if (st != GDN_OK) return st;
   if (n_seqs > 0 && !cu_seqlens) return GDN_ERR_NULL;
+  // a workgroup of 512 per 256 rows of a prompt and kv head
+  if (!fits_grid(((int64_t)n_tokens * (num_q_heads / a.c.Hkv) / 256 + n_seqs) * a.c.Hkv, 512)) return GDN_ERR_SHAPE;
   if (n_tokens == 0) return GDN_OK;
   a.cu = cu_seqlens;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -576,7 +581,17 @@ gdn_status gdn_attn_decode(const gdn_cache* cache, int32_t num_q_heads, float sc
   if (need > 0 && !workspace) return GDN_ERR_NULL;
   if (workspace_bytes < need) return GDN_ERR_CAPACITY;
   if (workspace && !aligned16(workspace)) return GDN_ERR_SHAPE;
+  if (need > 0) {   // nor may the workspace overlap out or q
+    const char* wb = static_cast<const char*>(workspace);
+    const char* ob = static_cast<const char*>(out);
+    const char* qb = static_cast<const char*>(q);
+    const int64_t rows = (int64_t)batch * n_tok, row = (int64_t)num_q_heads * a.c.dim * 2;
+    if (wb < ob + rows * row && ob < wb + need) return GDN_ERR_SHAPE;
+    if (wb < qb + (rows - 1) * a.q_stride * 2 + row && qb < wb + need) return GDN_ERR_SHAPE;
+  }
   if (batch == 0) return GDN_OK;
+  if (gdn::attn_decode_splits(a.c.dim, max_kv_len) > 65535) return GDN_ERR_SHAPE;
+  if (!fits_grid((int64_t)batch * n_tok * num_q_heads, 64)) return GDN_ERR_SHAPE;
   if (batch > 65535 || a.c.Hkv * (((int64_t)n_tok * (num_q_heads / a.c.Hkv) + 15) / 16) > 65535) return GDN_ERR_SHAPE;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return finish_launch(gdn::launch_attn_decode(a, workspace, s), s);

@@ -501,9 +501,9 @@ GDN_API gdn_status gdn_attn_packed(const gdn_cache* cache, int32_t num_q_heads, 
  *   max_kv_len:     upper bound of kv_len, 0 .. max_pages * page (requests over
  *                   it get NaN rows): the launch is sized for it.
  *   workspace:      device memory, gdn_attn_decode_workspace() bytes at least
- *                   (may be NULL if that is 0), 16-byte aligned; its contents
- *                   mean nothing before or after the call, and calls that may
- *                   run at the same time need one each.
+ *                   (may be NULL if that is 0), 16-byte aligned, not overlapping
+ *                   q or out; its contents mean nothing before or after the
+ *                   call, and calls that may run at the same time need one each.
  * How a request's keys are split depends on its own length alone.
  * Errors: as gdn_attn_packed; GDN_ERR_CAPACITY (workspace too small). */
 GDN_API gdn_status gdn_attn_decode(const gdn_cache* cache, int32_t num_q_heads, float scale,

@@ -146,6 +146,36 @@ def test_packed_and_decode_refusals_of_their_own():
     assert lib.gdn_attn_decode_workspace(None, 4, 2, 1, 256, ctypes.byref(n)) == NULL
 
 
+@no_gpu
+def test_sizes_that_no_launch_holds_are_refused():
+    """A launch has fewer than 2^32 threads along its first axis, and 65,535
+    workgroups along the others."""
+    zeros = np.zeros((1 << 22) + 1, np.int32)
+    assert packed(cu=zeros) == SHAPE and packed(cu=zeros[:-1]) == 0
+    assert append(cu=zeros) == SHAPE and append(cu=zeros[:-1]) == 0
+    assert append(T=1 << 25, cu=(0, 1 << 25), ps=1 << 25) == SHAPE
+    assert gdn.load().gdn_cache_gather(ref(cache()), 2 ** 31 - 1, FAKE, FAKE, FAKE, None) == SHAPE
+    far = dict(m=1 << 24, out=1 << 45, size=1 << 60, ws=1 << 50)
+    assert decode(most=65535 * 1024, **far) == HIP and decode(most=65535 * 1024 + 1, **far) == SHAPE
+    assert decode(most=2 ** 30, **far) == SHAPE
+    assert decode(b=65535, n_tok=256, most=64, **far) == HIP and decode(b=65535, n_tok=257, most=64, **far) == SHAPE
+    n = ctypes.c_int64()
+    big = cache(page=128)
+    assert gdn.load().gdn_attn_decode_workspace(ref(big), 4, 1, 1, 2 ** 31 - 1, ctypes.byref(n)) == 0
+    assert n.value == (1 << 21) * 4 * 130 * 4
+
+
+@no_gpu
+def test_workspace_apart_from_the_rows():
+    assert gdn.load().gdn_attn_decode_workspace(ref(cache()), 4, 2, 1, 4096, ctypes.byref(n := ctypes.c_int64())) == 0 and n.value
+    ok = dict(m=64, most=4096, q=1 << 30, out=1 << 31, ws=1 << 32)
+    assert decode(**ok) == HIP
+    for at in ("q", "out"):
+        base = ok[at]
+        for ws, st in [(base, SHAPE), (base + 1024, SHAPE), (base - n.value + 16, SHAPE), (base - n.value, HIP), (base + 2 * 4 * 128 * 2, HIP)]:
+            assert decode(**{**ok, "ws": ws}) == st, (at, ws - base)
+
+
 def test_binding_refusals():
     """Wrong shapes, types and places are Python errors before any call."""
     f8, i8 = torch.float8_e4m3fn, torch.int8
