@@ -77,6 +77,50 @@ __device__ __forceinline__ float uniform(float x) {
 typedef const int32_t __attribute__((address_space(4)))* ConstI32;
 typedef const float __attribute__((address_space(4)))* ConstF32;
 
+// Sum of x over the lanes up to this one.
+__device__ __forceinline__ int scan_lanes(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, true);    // one to the right in each row of 16
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, true);    // two
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, true);    // four
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, true);    // eight
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);   // a row's sum to the next, for rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);   // the first two rows' sum to the others
+  return x;
+}
+
+// Workgroups start in order of their index, so the tiles with the most keys
+// (counted in 256s) go first and the short ones fill the end.  For up to 64
+// prompts, a lane each: how many tiles of a prompt see at least 256 q keys has
+// a closed form, the rank-th tile's q is found by halving, and its prompt by a
+// sum over the lanes.  More prompts are taken last row first, in the pack's
+// order: they are short beside the card's 256 workgroups.  (8 prompts of 17 to
+// 2,048 tokens on up to 4,096: heads of 64 412 -> 384 us, of 128 521 -> 507 us.)
+__device__ __forceinline__ bool tile_of_rank(const AttnArgs& a, int G, int rank, int* prompt, int* first) {
+  const int lane = threadIdx.x & 63, s = min(lane, a.n_seqs - 1);
+  const int i0 = a.cu[s], n = lane < a.n_seqs && i0 >= 0 ? max(min(a.cu[s + 1], a.n_tokens) - i0, 0) : 0;
+  const int tiles = (int)(((int64_t)n * G + kRows - 1) / kRows), len = a.kv_len[s];
+  const int L = len < 0 || len > a.max_kv ? 0 : len;
+  auto count = [&](int q) -> int {   // tiles whose last row sees 256 q keys or more
+    if (q == 0) return tiles;
+    const int64_t d = (int64_t)256 * q - 1 - L + n;   // the first of the prompt's tokens that sees them
+    return d >= n || L == 0 ? 0 : d <= 0 ? tiles : tiles - (int)((G * d + 1 + kRows - 1) / kRows - 1);
+  };
+  auto total = [&](int q) -> int { return __builtin_amdgcn_readlane(scan_lanes(count(q)), 63); };
+  if (total(0) <= rank) return false;
+  int lo = 0, hi = 1;
+  while (__any(n > 0 && (L >> 8) >= hi)) hi *= 2;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (total(mid) > rank) lo = mid; else hi = mid;
+  }
+  const int more = count(lo + 1), same = count(lo) - more;
+  const int past = scan_lanes(same) - (rank - __builtin_amdgcn_readlane(scan_lanes(more), 63));   // > 0 from the tile's prompt on
+  const int at = __builtin_ctzll(__ballot(past > 0));
+  *prompt = at;
+  *first = __builtin_amdgcn_readlane((tiles - more - same + past - 1) * kRows, at);
+  return true;
+}
+
 template <int D, bool I8>
 __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnArgs a, const int units) {
   constexpr int KT = D == 256 ? 32 : 64;   // keys of a tile, and of a step
@@ -93,35 +137,41 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
   char* const vlds = lds + 3 * BYTES;
 
   const int hk = blockIdx.x % a.c.Hkv;
-  const int unit = units - 1 - (int)(blockIdx.x / a.c.Hkv);   // late rows see most keys: first
   const int G = a.Hq / a.c.Hkv;
-  // unit -> (prompt, its j-th tile of rows): prompt s has the units
-  // cu[s] G / kRows + s on, at least as many as its tiles
   const ConstI32 cu = (ConstI32)a.cu;
-  int lo = 0, hi = a.n_seqs;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((int)((int64_t)cu[mid] * G / kRows) + mid <= unit) lo = mid; else hi = mid;
+  int s = 0, first = 0;
+  if (a.n_seqs <= 64) {
+    if (!tile_of_rank(a, G, (int)(blockIdx.x / a.c.Hkv), &s, &first)) return;
+  } else {
+    // unit -> (prompt, its j-th tile of rows): prompt s has the units
+    // cu[s] G / kRows + s on, at least as many as its tiles
+    const int unit = units - 1 - (int)(blockIdx.x / a.c.Hkv);
+    int hi = a.n_seqs;
+    while (hi - s > 1) {
+      const int mid = (s + hi) >> 1;
+      if ((int)((int64_t)cu[mid] * G / kRows) + mid <= unit) s = mid; else hi = mid;
+    }
+    const int64_t at = (int64_t)(unit - (int)((int64_t)cu[s] * G / kRows) - s) * kRows;
+    if (cu[s] < 0 || at < 0 || at >= (int64_t)(min(cu[s + 1], a.n_tokens) - cu[s]) * G) return;
+    first = (int)at;
   }
-  const int s = lo, i0 = cu[s], n = min(cu[s + 1], a.n_tokens) - i0;
-  const int64_t first = (int64_t)(unit - (int)((int64_t)i0 * G / kRows) - s) * kRows;
+  const int i0 = cu[s], n = min(cu[s + 1], a.n_tokens) - i0;
   const int64_t rows = (int64_t)n * G;
-  if (i0 < 0 || first < 0 || first >= rows) return;
   const int L = ((ConstI32)a.kv_len)[s];
   const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
   // this lane's query row and the last key it sees
-  const int r0 = (int)first + wave * 32;
+  const int r0 = first + wave * 32;
   const int r = min(r0 + c32, (int)rows - 1), i = r / G, hq = hk * G + (r - i * G);
   const int last = L - n + i;
   const bool bad = L < 0 || L > a.max_kv;
   // keys that the workgroup's last row sees, and that all of its rows and all
   // of the wave's rows see.  Waves whose rows see fewer keys keep step with the
   // others, their scores masked.
-  const int wg_last = (int)min(first + kRows, rows) - 1;
+  const int wg_last = (int)min((int64_t)first + kRows, rows) - 1;
   const int keys = bad ? 0 : max(0, min(L, L - n + wg_last / G + 1));
-  const int wg_free = L - n + (int)first / G + 1, w_free = L - n + min(r0, (int)rows - 1) / G + 1;
+  const int wg_free = L - n + first / G + 1, w_free = L - n + min(r0, (int)rows - 1) / G + 1;
 
   // queries: the factor's sign goes into them, so that it leaves maxima maxima
   bf16x8 q[KS];

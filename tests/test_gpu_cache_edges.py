@@ -80,6 +80,32 @@ def test_packed_many_row_blocks_and_key_steps_of_every_remainder(code, d, page, 
     check_rows(packed_call(dev, new, lens, table, q), oracle_rows(f64(q), rows, lens, new, d ** -0.5), d)
 
 
+@pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 130])
+def test_packed_every_row_of_any_number_of_prompts(n):
+    """Long, short, empty and out-of-bounds prompts: whatever the order in which
+    tiles are taken, each row is written once and rows behind the last stay."""
+    rng = np.random.default_rng(n)
+    d, page, g = 64, 64, 8
+    new = [int(x) for x in rng.choice([0, 1, 3, 31, 33, 70, 100], n)]
+    new[0] = 90
+    ctx = [int(x) for x in rng.choice([0, 0, 5, 250, 600, 1300, -40], n)]
+    lens = [max(0, a + b) for a, b in zip(new, ctx)]
+    ref, dev, table, rows = filled(rng, lens, 1, page, d, "int8")
+    q = bf(rng.standard_normal((sum(new), g, d))).to(DEV)
+    want = oracle_rows(f64(q), rows, lens, new, d ** -0.5)
+    out = packed_call(dev, new, lens, table, q)
+    check_rows(out, want, d)
+    bad = list(lens)
+    bad[n // 2], bad[0] = -3, table.shape[1] * page + 1
+    got, at = packed_call(dev, new, bad, table, q), 0
+    for i, x in enumerate(new):
+        if bad[i] != lens[i]:
+            assert torch.all(torch.isnan(got[at:at + x]))
+        else:
+            assert torch.equal(got[at:at + x].view(torch.int16), out[at:at + x].view(torch.int16))
+        at += x
+
+
 @pytest.mark.parametrize("code", ["e4m3", "int8"])
 def test_requests_that_share_the_pages_of_a_prefix(code):
     rng = np.random.default_rng(21)
