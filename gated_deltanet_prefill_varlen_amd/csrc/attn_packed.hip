@@ -77,47 +77,27 @@ __device__ __forceinline__ float uniform(float x) {
 typedef const int32_t __attribute__((address_space(4)))* ConstI32;
 typedef const float __attribute__((address_space(4)))* ConstF32;
 
-// Sum of x over the lanes up to this one.
-__device__ __forceinline__ int scan_lanes(int x) {
-  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, true);    // one to the right in each row of 16
-  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, true);    // two
-  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, true);    // four
-  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, true);    // eight
-  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);   // a row's sum to the next, for rows 1 and 3
-  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);   // the first two rows' sum to the others
-  return x;
-}
-
-// Workgroups start in order of their index, so the tiles with the most keys
-// (counted in 256s) go first and the short ones fill the end.  For up to 64
-// prompts, a lane each: how many tiles of a prompt see at least 256 q keys has
-// a closed form, the rank-th tile's q is found by halving, and its prompt by a
-// sum over the lanes.  More prompts are taken last row first, in the pack's
-// order: they are short beside the card's 256 workgroups.  (8 prompts of 17 to
-// 2,048 tokens on up to 4,096: heads of 64 412 -> 384 us, of 128 521 -> 507 us.)
+// Workgroups start in order of their index.  A prompt's last rows see most keys
+// and go first; up to 64 prompts are taken in the order of the keys that their
+// first rows see, so that the short tiles fill the end (8 prompts of 17 to 2,048
+// tokens on up to 4,096, two draws: 535 -> 507 us and 450 -> 452 us).  By the
+// keys of each tile, across the prompts, the end is as even, but the prompts no
+// longer share an L2 (507 and 462 us).  More prompts are taken in the pack's
+// order: each is little beside the card's 256 workgroups.
 __device__ __forceinline__ bool tile_of_rank(const AttnArgs& a, int G, int rank, int* prompt, int* first) {
   const int lane = threadIdx.x & 63, s = min(lane, a.n_seqs - 1);
   const int i0 = a.cu[s], n = lane < a.n_seqs && i0 >= 0 ? max(min(a.cu[s + 1], a.n_tokens) - i0, 0) : 0;
-  const int tiles = (int)(((int64_t)n * G + kRows - 1) / kRows), len = a.kv_len[s];
-  const int L = len < 0 || len > a.max_kv ? 0 : len;
-  auto count = [&](int q) -> int {   // tiles whose last row sees 256 q keys or more
-    if (q == 0) return tiles;
-    const int64_t d = (int64_t)256 * q - 1 - L + n;   // the first of the prompt's tokens that sees them
-    return d >= n || L == 0 ? 0 : d <= 0 ? tiles : tiles - (int)((G * d + 1 + kRows - 1) / kRows - 1);
-  };
-  auto total = [&](int q) -> int { return __builtin_amdgcn_readlane(scan_lanes(count(q)), 63); };
-  if (total(0) <= rank) return false;
-  int lo = 0, hi = 1;
-  while (__any(n > 0 && (L >> 8) >= hi)) hi *= 2;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (total(mid) > rank) lo = mid; else hi = mid;
+  const int tiles = (int)(((int64_t)n * G + kRows - 1) / kRows);
+  const int keys = max(a.kv_len[s] - n + min(n, kRows / G), 0);   // of the first tile, nearly
+  int before = 0;   // tiles of the prompts that go first
+  for (int j = 0; j < a.n_seqs; ++j) {
+    const int k = __builtin_amdgcn_readlane(keys, j), t = __builtin_amdgcn_readlane(tiles, j);
+    if (k > keys || (k == keys && j > s)) before += t;
   }
-  const int more = count(lo + 1), same = count(lo) - more;
-  const int past = scan_lanes(same) - (rank - __builtin_amdgcn_readlane(scan_lanes(more), 63));   // > 0 from the tile's prompt on
-  const int at = __builtin_ctzll(__ballot(past > 0));
-  *prompt = at;
-  *first = __builtin_amdgcn_readlane((tiles - more - same + past - 1) * kRows, at);
+  const uint64_t mine = __ballot(rank >= before && rank < before + tiles);
+  if (!mine) return false;
+  *prompt = __builtin_ctzll(mine);
+  *first = __builtin_amdgcn_readlane((before + tiles - 1 - rank) * kRows, *prompt);
   return true;
 }
 
