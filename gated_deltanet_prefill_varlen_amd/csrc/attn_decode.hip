@@ -25,6 +25,7 @@
 // (fp32 sums against the running maximum) are joined in a fixed order, so a
 // request's bits do not depend on its batch.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_device.h"
 
@@ -32,7 +33,6 @@ namespace gdn {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kTile = 64;
 
 // Keys per workgroup: by the head size alone, so that how a request's keys are
 // split never depends on its batch.  Fewer make more partial sums to write and
@@ -49,6 +49,12 @@ struct Partial {
 
 template <int D, bool I8, int NT>
 __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 ? 2 : 1) attn_decode_kernel(const AttnArgs a, const Partial part) {
+  // Keys of a tile: 64, so that a lane's values are whole vectors; 32 where that
+  // lets two waves into a SIMD (32 requests to 8,192 keys, 4 kv heads of 256:
+  // 67 us, with 64 a few registers spill and it takes 72).
+  constexpr int KT = D == 256 && NT == 1 ? 32 : 64;
+  constexpr int KG = KT / 4;    // keys of a lane group
+  constexpr int NS = KT / 16;   // score tiles
   constexpr int KL = D / 64;    // 16-byte loads of a key per lane
   constexpr int KS = D / 32;    // contraction steps of a score
   constexpr int OB = D / 16;    // 16-channel blocks of the output
@@ -63,13 +69,13 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
   const int hk = blockIdx.x / groups, r0 = (blockIdx.x % groups) * 16 * NT;
   const int shift = a.c.page_shift, pmask = (1 << shift) - 1;
   const int32_t* table = a.table + (int64_t)b * a.max_pages;
-  constexpr int kStep = kWaves * kTile, per = split_keys(D);
+  constexpr int kStep = kWaves * KT, per = split_keys(D);
   const int key0 = sp * per;
   // the first tile's entries do not wait for the length
-  int t0 = key0 + wave * kTile;
+  int t0 = key0 + wave * KT;
   auto entry_of = [&](int key) -> int { return a.max_pages > 0 ? table[min(key >> shift, a.max_pages - 1)] : -1; };
-  const int ek = entry_of(t0 + 16 * (c16 >> 2)), ev = entry_of(t0 + 16 * g);
-  const int ek1 = entry_of(t0 + kStep + 16 * (c16 >> 2)), ev1 = entry_of(t0 + kStep + 16 * g);
+  const int ek = entry_of(t0 + KG * (c16 >> 2)), ev = entry_of(t0 + KG * g);
+  const int ek1 = entry_of(t0 + kStep + KG * (c16 >> 2)), ev1 = entry_of(t0 + kStep + KG * g);
   const int L = a.kv_len[b];
   const bool bad = L < 0 || L > a.max_kv;
   const int splits = bad ? 1 : n_splits(L, D);
@@ -95,7 +101,11 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
   // registers are needed for the codes in flight.
   constexpr bool QL = NT * D >= 256;
   constexpr int QN = QL ? NT * KS / kWaves : NT * KS;
-  __shared__ __align__(16) bf16x8 ql[QL ? NT * KS : 1][64];
+  __shared__ union {
+    bf16x8 q[QL ? NT * KS : 1][64];
+    f32x4 o[kWaves][NT * OB][64];
+  } lds;
+  auto& ql = lds.q;
   bf16x8 q[QN];
 #pragma unroll
   for (int n = 0; n < QN; ++n) {
@@ -111,35 +121,37 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
   const int key1 = min(L, key0 + per);
   const float log_scale = a.scale * kLog2e;
 
-  // A tile's pages: of the 16 keys whose values (and scores) this lane has, and
+  // A tile's pages: of the keys whose values (and scores) this lane has, and
   // of the key whose codes it loads (-1: not held, read as page 0 and masked).
   auto page_of = [&](int entry, int key) -> int { return key < key1 && entry < a.c.n_pages ? entry : -1; };
-  uint4 kc[4][KL], vc[OB];
+  typedef std::conditional_t<KT == 64, uint4, uint2> Values;   // a lane's KG keys of a channel
+  uint4 kc[NS][KL];
+  Values vc[OB];
   float ks, vs;
   auto load_keys = [&](int t0, int pk, int pv) {
-    const int kk = t0 + 16 * (c16 >> 2);
+    const int kk = t0 + KG * (c16 >> 2);
     const uint8_t* kp = a.c.k + page_base(a.c, max(pk, 0), hk) + ((kk & pmask) + (c16 & 3)) * D + 16 * g;
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < NS; ++s)
 #pragma unroll
       for (int i = 0; i < KL; ++i) kc[s][i] = *reinterpret_cast<const uint4*>(kp + 4 * s * D + 64 * i);
     ks = a.c.ks[(int64_t)max(pv, 0) * a.c.Hkv + hk];
   };
   auto load_values = [&](int t0, int pv) {
-    const int kv = t0 + 16 * g;
-    const uint8_t* vp = a.c.v + page_base(a.c, max(pv, 0), hk) + ((kv & pmask) * D + c16 * 16);
+    const int kv = t0 + KG * g;
+    const uint8_t* vp = a.c.v + page_base(a.c, max(pv, 0), hk) + ((kv & pmask & ~15) * D + c16 * 16 + (kv & 15));
 #pragma unroll
-    for (int x = 0; x < OB; ++x) vc[x] = *reinterpret_cast<const uint4*>(vp + x * 256);
+    for (int x = 0; x < OB; ++x) vc[x] = *reinterpret_cast<const Values*>(vp + x * 256);
     vs = a.c.vs[(int64_t)max(pv, 0) * a.c.Hkv + hk];
   };
 
   // Loads run ahead: a tile's keys are asked for when the scores before them
   // are done, its values after the products before them, its pages a tile
   // earlier.
-  int pv = page_of(ev, t0 + 16 * g);
-  int pk1 = page_of(ek1, t0 + kStep + 16 * (c16 >> 2)), pv1 = page_of(ev1, t0 + kStep + 16 * g);
+  int pv = page_of(ev, t0 + KG * g);
+  int pk1 = page_of(ek1, t0 + kStep + KG * (c16 >> 2)), pv1 = page_of(ev1, t0 + kStep + KG * g);
   if (t0 < key1) {
-    load_keys(t0, page_of(ek, t0 + 16 * (c16 >> 2)), pv);
+    load_keys(t0, page_of(ek, t0 + KG * (c16 >> 2)), pv);
     load_values(t0, pv);
   }
   if constexpr (QL) {
@@ -159,16 +171,16 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
 
   for (; t0 < key1; t0 += kStep) {
     const bool more = t0 + kStep < key1;
-    const int kk2 = t0 + 2 * kStep + 16 * (c16 >> 2), kv2 = t0 + 2 * kStep + 16 * g;
+    const int kk2 = t0 + 2 * kStep + KG * (c16 >> 2), kv2 = t0 + 2 * kStep + KG * g;
     const int pk2 = page_of(table[min(kk2, key1 - 1) >> shift], kk2), pv2 = page_of(table[min(kv2, key1 - 1) >> shift], kv2);
-    const int kv = t0 + 16 * g;
+    const int kv = t0 + KG * g;
     const bool held = pv >= 0;
 
-    f32x4 s4[NT][4];
+    f32x4 s4[NT][NS];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int s = 0; s < 4; ++s) s4[t][s] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int s = 0; s < NS; ++s) s4[t][s] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < KL; ++i) {
       bf16x8 q0[NT], q1[NT];
@@ -178,7 +190,7 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
         q1[t] = query(t, 2 * i + 1);
       }
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
+      for (int s = 0; s < NS; ++s) {
         const bf16x8 k0 = codes_to_operand<I8>(kc[s][i].x, kc[s][i].y);
         const bf16x8 k1 = codes_to_operand<I8>(kc[s][i].z, kc[s][i].w);
 #pragma unroll
@@ -197,16 +209,18 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
     // among them, which a probability of 0 would not silence; so would a NaN
     // value that only some rows see: it becomes 0, and its key's score NaN for
     // the rows that see it
-    const bool whole = t0 + kTile <= key1 - (a.n_tok - 1);   // every row sees the tile
+    const bool whole = t0 + KT <= key1 - (a.n_tok - 1);   // every row sees the tile
     uint32_t nan = 0;
     if (!whole || __any(!held)) {
       const int left = held ? key1 - kv : 0;
 #pragma unroll
       for (int x = 0; x < OB; ++x) {
-        uint32_t w[4] = {vc[x].x, vc[x].y, vc[x].z, vc[x].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = without_nan<I8>(w[j] & first_bytes(left - 4 * j), 4 * j, &nan);
-        vc[x] = make_uint4(w[0], w[1], w[2], w[3]);
+        vc[x].x = without_nan<I8>(vc[x].x & first_bytes(left), 0, &nan);
+        vc[x].y = without_nan<I8>(vc[x].y & first_bytes(left - 4), 4, &nan);
+        if constexpr (KT == 64) {
+          vc[x].z = without_nan<I8>(vc[x].z & first_bytes(left - 8), 8, &nan);
+          vc[x].w = without_nan<I8>(vc[x].w & first_bytes(left - 12), 12, &nan);
+        }
       }
       if constexpr (!I8)
 #pragma unroll
@@ -215,12 +229,12 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
 
     // scores to probabilities; in units of log2
     const float vf = held ? vs : 0.f;
-    bf16x8 p[NT][2];
+    bf16x8 p[NT][NS / 2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float mx = -__builtin_inff();
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+      for (int s = 0; s < NS; ++s)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float x = s4[t][s][i] * kf;
@@ -240,9 +254,9 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
         for (int x = 0; x < OB; ++x) o[t][x] *= again;
         m[t] = m1;
       }
-      u32x4 w[2];
+      u32x4 w[NS / 2];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
+      for (int s = 0; s < NS; ++s) {
         float e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -253,17 +267,18 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
         w[s >> 1][2 * (s & 1)] = pack_bf16(e[0], e[1]);
         w[s >> 1][2 * (s & 1) + 1] = pack_bf16(e[2], e[3]);
       }
-      p[t][0] = __builtin_bit_cast(bf16x8, w[0]);
-      p[t][1] = __builtin_bit_cast(bf16x8, w[1]);
+#pragma unroll
+      for (int u = 0; u < NS / 2; ++u) p[t][u] = __builtin_bit_cast(bf16x8, w[u]);
     }
 #pragma unroll
     for (int x = 0; x < OB; ++x) {
       const bf16x8 v0 = codes_to_operand<I8>(vc[x].x, vc[x].y);
-      const bf16x8 v1 = codes_to_operand<I8>(vc[x].z, vc[x].w);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        o[t][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, p[t][0], o[t][x], 0, 0, 0);
-        o[t][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, p[t][1], o[t][x], 0, 0, 0);
+      for (int t = 0; t < NT; ++t) o[t][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, p[t][0], o[t][x], 0, 0, 0);
+      if constexpr (KT == 64) {
+        const bf16x8 v1 = codes_to_operand<I8>(vc[x].z, vc[x].w);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) o[t][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, p[t][1], o[t][x], 0, 0, 0);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -276,7 +291,6 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
   // The waves' sums meet in LDS, each against the common maximum; then each
   // wave adds up a quarter of the 16 x 16 blocks, in the waves' order.
   __shared__ float sm[kWaves][16 * NT], sl[kWaves][16 * NT];
-  __shared__ __align__(16) f32x4 so[kWaves][NT * OB][64];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     l[t] += __shfl_xor(l[t], 16);
@@ -294,15 +308,15 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
     for (int w = 0; w < kWaves; ++w) mt = fmaxf(mt, sm[w][16 * t + c16]);
     const float mine = m[t] == -__builtin_inff() ? 0.f : exp2_fast(m[t] - mt);
 #pragma unroll
-    for (int x = 0; x < OB; ++x) so[wave][t * OB + x][lane] = o[t][x] * mine;
+    for (int x = 0; x < OB; ++x) lds.o[wave][t * OB + x][lane] = o[t][x] * mine;
   }
   __syncthreads();
 #pragma unroll 1
   for (int n = wave; n < NT * OB; n += kWaves) {
     const int t = n / OB, c = 16 * (n % OB) + 4 * g, r = r0 + 16 * t + c16;
-    f32x4 y = so[0][n][lane];
+    f32x4 y = lds.o[0][n][lane];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) y += so[w][n][lane];
+    for (int w = 1; w < kWaves; ++w) y += lds.o[w][n][lane];
     float mt = -__builtin_inff(), lt = 0.f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) mt = fmaxf(mt, sm[w][16 * t + c16]);
