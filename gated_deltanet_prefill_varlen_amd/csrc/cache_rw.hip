@@ -7,7 +7,7 @@
 // maxima, settles the scales and stores the codes.  A query workgroup forms
 // the angles of its tokens once in LDS and turns every head with them.
 // Measured: 32 prompts of 1,024 tokens (32 query heads, 8 kv heads of 128)
-// 178 us, HBM bound (0.74 GB, 4.1 TB/s); a decode step of 64 tokens 10.4 us,
+// 160 us, HBM bound (0.74 GB, 4.6 TB/s); a decode step of 64 tokens 9.6 us,
 // the latency of the way from the prompts' offsets over slots and rows to the
 // scale and the codes.
 #include <algorithm>
@@ -17,7 +17,6 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256;
 
 // cos and sin of position * freq, to a little over half an ulp.  In 64 bits
 // the angle becomes quarter turns, of which the nearest whole number is taken
@@ -101,9 +100,10 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
 }
 
 // ---------------------------------------------------------------- queries --
+template <int T>
 __device__ __forceinline__ void rotate_q(const AppendArgs& a, int dim, int t0, int n, float2* cs) {
   const int half = a.rope.rot / 2;
-  for (int e = threadIdx.x; e < n * half; e += kThreads) {
+  for (int e = threadIdx.x; e < n * half; e += T) {
     const int t = e / half, i = e - t * half;
     float c, s;
     cos_sin(a.pos[a.rope.axis[i] * a.pos_stride + t0 + t], a.rope.freq[i], a.rope.scale, &c, &s);
@@ -111,7 +111,7 @@ __device__ __forceinline__ void rotate_q(const AppendArgs& a, int dim, int t0, i
   }
   __syncthreads();
   const int chunks = dim / 16, per = a.Hq * chunks;
-  for (int e = threadIdx.x; e < n * per; e += kThreads) {
+  for (int e = threadIdx.x; e < n * per; e += T) {
     const int t = e / per, hc = e - t * per, h = hc / chunks, c = hc - h * chunks;
     const Chunk ch(a.rope, c);
     const uint16_t* src = a.q + (t0 + t) * a.q_stride + (int64_t)h * dim;
@@ -133,32 +133,44 @@ __device__ __forceinline__ void rotate_q(const AppendArgs& a, int dim, int t0, i
 }
 
 // Largest value over the workgroup of x >= 0 and y >= 0.
+template <int T>
 __device__ __forceinline__ void block_max(float* x, float* y, float2* lds) {
 #pragma unroll
   for (int d = 32; d; d >>= 1) {
     *x = fmaxf(*x, __shfl_xor(*x, d));
     *y = fmaxf(*y, __shfl_xor(*y, d));
   }
+  if constexpr (T == 64) return;
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = make_float2(*x, *y);
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kThreads / 64; ++i) {
+  for (int i = 0; i < T / 64; ++i) {
     *x = fmaxf(*x, lds[i].x);
     *y = fmaxf(*y, lds[i].y);
   }
 }
 
-__device__ __forceinline__ float old_scale(const float* p) {
-  const float s = *p;
+__device__ __forceinline__ float old_scale(float s) {
   return s >= kMinScale && s < __builtin_inff() ? s : kMinScale;   // a page never written holds anything
 }
 
 // ---------------------------------------------------------- keys, values --
 // NV: value items (16 tokens x 2 channels) per thread; a key item (1 token x
 // 16 channels) is half as large, so there are 2 NV of them.
-template <int D, bool I8, int NV>
+template <int D, bool I8, int NV, int T>
 __device__ __forceinline__ void write_page(const AppendArgs& a, int unit, int h, uint8_t* valid, float2* red) {
   const int tid = threadIdx.x, shift = a.c.page_shift, P = 1 << shift;
+  // all of a thread's key items have the same channels: their frequencies and
+  // axes are under way before anything else is known
+  const int kc = tid % (D / 16);
+  const Chunk ch(a.rope, kc);
+  float freq[8];
+  uint64_t axes = 0;
+  if (ch.turned && tid / (D / 16) < P) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) freq[i] = a.rope.freq[8 * kc + i];
+    axes = *reinterpret_cast<const uint64_t*>(a.rope.axis + 8 * kc);
+  }
   // unit -> (prompt s, its j-th page of this call): prompt s has the units
   // cu[s] / P + 2 s on, more than its ceil(len / P) + 1 pages
   // (counted 64 prompts at a time: one round through memory, not log2 n)
@@ -176,11 +188,16 @@ __device__ __forceinline__ void write_page(const AppendArgs& a, int unit, int h,
   if (begin >= i1) return;
   const int tl = (int)begin, off = j == 0 ? off0 : 0;
   const int cnt = min(P - off, i1 - tl);
-  const int64_t lead = a.slot[tl];
+  // the page's slots in one trip, then its scales beside its rows
+  const bool inside = tid >= off && tid < off + cnt;
+  const int64_t lead = a.slot[tl], own = inside ? a.slot[tl + tid - off] : 0;
   if (lead < 0 || (lead & (P - 1)) != off || (lead >> shift) >= a.c.n_pages) return;
   const int64_t page = lead >> shift;
+  float* const ksp = a.c.ks + page * a.c.Hkv + h;
+  float* const vsp = a.c.vs + page * a.c.Hkv + h;
+  const float k_was = *ksp, v_was = *vsp;
 
-  if (tid < P) valid[tid] = tid >= off && tid < off + cnt && a.slot[tl + tid - off] == lead + (tid - off);
+  if (tid < P) valid[tid] = inside && own == lead + (tid - off);
   __syncthreads();
 
   uint32_t v[NV][16];
@@ -188,7 +205,7 @@ __device__ __forceinline__ void write_page(const AppendArgs& a, int unit, int h,
   const int tiles = P / 16;
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
-    const int item = tid + n * kThreads, u = item / (D / 2), c2 = item % (D / 2);
+    const int item = tid + n * T, u = item / (D / 2), c2 = item % (D / 2);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int o = u * 16 + i;
@@ -198,44 +215,49 @@ __device__ __forceinline__ void write_page(const AppendArgs& a, int unit, int h,
     }
   }
   uint4 k[2 * NV][2];
+  constexpr int AHEAD = NV <= 2 ? 2 * NV : 0;   // items whose positions are asked for with the keys (registers)
+  Positions pos[AHEAD + 1];
 #pragma unroll
   for (int n = 0; n < 2 * NV; ++n) {
-    const int item = tid + n * kThreads, o = item / (D / 16), c = item % (D / 16);
+    const int o = (tid + n * T) / (D / 16);
     k[n][0] = k[n][1] = make_uint4(0, 0, 0, 0);
     if (o < P && valid[o]) {
       const int t = tl + o - off;
-      const Chunk ch(a.rope, c);
       const uint16_t* src = a.k + t * a.k_stride + (int64_t)h * D;
       k[n][0] = *reinterpret_cast<const uint4*>(src + ch.e0);
       k[n][1] = *reinterpret_cast<const uint4*>(src + ch.e1);
-      float x[16];
+      if (n < AHEAD && ch.turned) pos[n].load(a, t);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < 2 * NV; ++n) {
+    const int o = (tid + n * T) / (D / 16);
+    if (o >= P || !valid[o]) continue;
+    float x[16];
+    unpack8(k[n][0], x);
+    unpack8(k[n][1], x + 8);
+    if (ch.turned) {
+      Positions& at = pos[n < AHEAD ? n : AHEAD];
+      if (n >= AHEAD) at.load(a, tl + o - off);
+      turn(x, a.rope.adjacent, [&](int i, float* co, float* si) {
+        cos_sin(at.at((int)(axes >> (8 * i) & 255)), freq[i], a.rope.scale, co, si);
+      });
+      k[n][0] = pack8(x);
+      k[n][1] = pack8(x + 8);
       unpack8(k[n][0], x);
       unpack8(k[n][1], x + 8);
-      if (ch.turned) {
-        Positions pos;
-        pos.load(a, t);
-        turn(x, a.rope.adjacent, [&](int i, float* co, float* si) {
-          cos_sin(pos.at(a.rope.axis[8 * c + i]), a.rope.freq[8 * c + i], a.rope.scale, co, si);
-        });
-        k[n][0] = pack8(x);
-        k[n][1] = pack8(x + 8);
-        unpack8(k[n][0], x);
-        unpack8(k[n][1], x + 8);
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) kmax = fmaxf(kmax, finite_abs(x[i]));
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) kmax = fmaxf(kmax, finite_abs(x[i]));
   }
 #pragma unroll
   for (int n = 0; n < NV; ++n)
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       vmax = fmaxf(vmax, fmaxf(finite_abs(lo_bf16(v[n][i])), finite_abs(hi_bf16(v[n][i]))));
-  block_max(&kmax, &vmax, red);
+  block_max<T>(&kmax, &vmax, red);
 
-  float* const ksp = a.c.ks + page * a.c.Hkv + h;
-  float* const vsp = a.c.vs + page * a.c.Hkv + h;
-  const float k_old = off ? old_scale(ksp) : kMinScale, v_old = off ? old_scale(vsp) : kMinScale;
+  const float k_old = off ? old_scale(k_was) : kMinScale, v_old = off ? old_scale(v_was) : kMinScale;
   const float k_new = fmaxf(k_old, scale_for<I8>(kmax)), v_new = fmaxf(v_old, scale_for<I8>(vmax));
   __syncthreads();   // every thread has the old scales
   if (tid == 0) {
@@ -250,9 +272,8 @@ __device__ __forceinline__ void write_page(const AppendArgs& a, int unit, int h,
   uint8_t* const kb = a.c.k + page_base(a.c, page, h);
 #pragma unroll
   for (int n = 0; n < 2 * NV; ++n) {
-    const int item = tid + n * kThreads, o = item / (D / 16), c = item % (D / 16);
+    const int o = (tid + n * T) / (D / 16);
     if (o >= P) continue;
-    const Chunk ch(a.rope, c);
     uint2* const d0 = reinterpret_cast<uint2*>(kb + o * D + ch.e0);
     uint2* const d1 = reinterpret_cast<uint2*>(kb + o * D + ch.e1);
     if (valid[o]) {
@@ -273,7 +294,7 @@ __device__ __forceinline__ void write_page(const AppendArgs& a, int unit, int h,
   uint8_t* const vb = a.c.v + page_base(a.c, page, h);
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
-    const int item = tid + n * kThreads, u = item / (D / 2), c2 = item % (D / 2);
+    const int item = tid + n * T, u = item / (D / 2), c2 = item % (D / 2);
     if (u >= tiles) continue;
     uint32_t mask[4];   // the bytes of this tile that are new
     bool any = false, all = true;
@@ -317,20 +338,23 @@ __device__ __forceinline__ void write_page(const AppendArgs& a, int unit, int h,
   }
 }
 
-constexpr int kQTokens = 4;
-
-template <int D, bool I8, int NV>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const AppendArgs a, const int64_t page_blocks) {
+// Workgroups of 256, or of one wave where a page and head have no more than
+// 2,048 codes to write: a wave has enough loads of those, and needs no barrier
+// for its maxima (16 prompts of 500 to 1,500 tokens, 4 kv heads of 64, pages of
+// 16, with their read: 51 us in workgroups of 256, 35 us).
+template <int D, bool I8, int NV, int T>
+__global__ void __launch_bounds__(T, NV == 4 ? 2 : 5 - NV) rope_append_kernel(const AppendArgs a, const int64_t page_blocks) {
+  constexpr int Q = T / 64;   // tokens of a query workgroup
   __shared__ union {
-    struct { uint8_t valid[128]; float2 red[kThreads / 64]; } w;
-    float2 cs[kQTokens * 128];
+    struct { uint8_t valid[128]; float2 red[T / 64]; } w;
+    float2 cs[Q * 128];
   } lds;
   const int64_t b = blockIdx.x;
   if (b < page_blocks) {
-    write_page<D, I8, NV>(a, (int)(b / a.c.Hkv), (int)(b % a.c.Hkv), lds.w.valid, lds.w.red);
+    write_page<D, I8, NV, T>(a, (int)(b / a.c.Hkv), (int)(b % a.c.Hkv), lds.w.valid, lds.w.red);
   } else {
-    const int t0 = (int)(b - page_blocks) * kQTokens;
-    rotate_q(a, D, t0, min(kQTokens, a.n_tokens - t0), lds.cs);
+    const int t0 = (int)(b - page_blocks) * Q;
+    rotate_q<T>(a, D, t0, min(Q, a.n_tokens - t0), lds.cs);
   }
 }
 
@@ -343,6 +367,8 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const AppendArgs 
 // heads of 128 take 31 us, 0.20 GB (6.4 TB/s with a part of it still cached,
 // 48 us from cold); a prefix of 1,000 rows takes 4 us.  16 rows a wave read
 // each vector once, but are no faster anywhere (49 and 5.4 us).
+constexpr int kThreads = 256;
+
 template <int D, bool I8>
 __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const GatherArgs a) {
   constexpr int C = D / 64;   // a lane's channels of the values
@@ -439,26 +465,34 @@ __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const GatherArgs
   }
 }
 
-template <int D, bool I8>
-hipError_t append_nv(const AppendArgs& a, dim3 grid, int64_t page_blocks, hipStream_t st) {
-  const int nv = std::max(1, (D << a.c.page_shift) / (32 * kThreads));
-  if (nv == 1) hipLaunchKernelGGL((rope_append_kernel<D, I8, 1>), grid, dim3(kThreads), 0, st, a, page_blocks);
-  else if (nv == 2) hipLaunchKernelGGL((rope_append_kernel<D, I8, 2>), grid, dim3(kThreads), 0, st, a, page_blocks);
-  else hipLaunchKernelGGL((rope_append_kernel<D, I8, 4>), grid, dim3(kThreads), 0, st, a, page_blocks);
+template <int D, bool I8, int NV, int T>
+hipError_t append(const AppendArgs& a, hipStream_t st) {
+  const int64_t units = (a.n_tokens >> a.c.page_shift) + 2 * (int64_t)a.n_seqs;
+  const int64_t page_blocks = units * a.c.Hkv;
+  const int64_t q_blocks = a.q ? ((int64_t)a.n_tokens + T / 64 - 1) / (T / 64) : 0;
+  hipLaunchKernelGGL((rope_append_kernel<D, I8, NV, T>), dim3((uint32_t)(page_blocks + q_blocks)), dim3(T), 0, st, a, page_blocks);
   return hipGetLastError();
+}
+
+template <int D, bool I8>
+hipError_t append_d(const AppendArgs& a, hipStream_t st) {
+  const int codes = D << a.c.page_shift;
+  if constexpr (D < 256)
+    if (codes <= 2048) return append<D, I8, 1, 64>(a, st);
+  if constexpr (D > 128)
+    if (codes > 16384) return append<D, I8, 4, 256>(a, st);
+  if constexpr (D > 64)
+    if (codes > 8192) return append<D, I8, 2, 256>(a, st);
+  return append<D, I8, 1, 256>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_rope_append(const AppendArgs& a, hipStream_t st) {
-  const int64_t units = (a.n_tokens >> a.c.page_shift) + 2 * (int64_t)a.n_seqs;
-  const int64_t page_blocks = units * a.c.Hkv;
-  const int64_t q_blocks = a.q ? (a.n_tokens + kQTokens - 1) / kQTokens : 0;
-  const dim3 grid((uint32_t)(page_blocks + q_blocks));
   switch (a.c.dim) {
-    case 64: return a.c.i8 ? append_nv<64, true>(a, grid, page_blocks, st) : append_nv<64, false>(a, grid, page_blocks, st);
-    case 128: return a.c.i8 ? append_nv<128, true>(a, grid, page_blocks, st) : append_nv<128, false>(a, grid, page_blocks, st);
-    default: return a.c.i8 ? append_nv<256, true>(a, grid, page_blocks, st) : append_nv<256, false>(a, grid, page_blocks, st);
+    case 64: return a.c.i8 ? append_d<64, true>(a, st) : append_d<64, false>(a, st);
+    case 128: return a.c.i8 ? append_d<128, true>(a, st) : append_d<128, false>(a, st);
+    default: return a.c.i8 ? append_d<256, true>(a, st) : append_d<256, false>(a, st);
   }
 }
 
