@@ -2,8 +2,8 @@
 // whole cache read once, so HBM bounds it.
 //
 // The rows of a request that share a kv head (n_tok tokens x Hq / Hkv heads)
-// are packed into tiles of 16.  A wave takes 64 keys at a time straight from
-// the pages into registers, with no LDS between:
+// are packed into tiles of 16.  A wave takes 64 keys at a time (or 32, with 8 a
+// lane group below) straight from the pages into registers, with no LDS between:
 //   S^T = K Q^T   (16x16x32 products, rows = keys, columns = query rows)
 //   O^T += V^T P^T  (rows = channels, columns = query rows).
 // A product's result holds in lane group g (16 lanes) the rows 4g .. 4g + 3 of
@@ -21,7 +21,7 @@
 // overlap its waits.
 //
 // Keys are split over workgroups in runs of fixed length (split_keys), the
-// four waves of a workgroup take 64-key tiles in turn, and partial results
+// four waves of a workgroup take tiles in turn, and partial results
 // (fp32 sums against the running maximum) are joined in a fixed order, so a
 // request's bits do not depend on its batch.
 #include <algorithm>
