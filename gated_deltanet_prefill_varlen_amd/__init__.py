@@ -221,6 +221,8 @@ def _rows(t: torch.Tensor, rows: int, heads: Optional[int], d: int, dev: int, wh
     st = t.stride()
     if st[2] != 1 or (h > 1 and st[1] != d):
         raise ValueError(f"{what}: the heads of a token must be dense")
+    if n > 1 and st[0] < h * d:   # (0 would mean dense rows)
+        raise ValueError(f"{what}: the rows overlap")
     return t.data_ptr(), (st[0] if n > 1 else h * d), h
 
 
@@ -230,6 +232,8 @@ def _where(stream):
     if not torch.cuda.is_initialized():
         return -2, None
     dev = torch.cuda.current_device()
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise ValueError("the stream is not on the current device")
     return dev, (torch._C._cuda_getCurrentRawStream(dev) or None) if stream is None else _stream(stream)
 
 

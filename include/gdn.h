@@ -476,7 +476,9 @@ GDN_API gdn_status gdn_cache_gather(const gdn_cache* cache, int32_t n_tokens, co
  * Query head h reads kv head h / (Hq / Hkv).  A row that sees no key
  * (kv_len < n_s) is 0.  A prompt whose kv_len is negative or over max_pages *
  * page gets NaN rows.  A block-table entry outside [0, n_pages) below kv_len
- * is a page that is not held: its tokens are not seen.
+ * is a page that is not held: its tokens are not seen.  Codes behind the last
+ * token may be anything; an e4m3 NaN makes the rows that see its token NaN (a
+ * value's, at least its channel), and no other.
  *   num_q_heads:    Hq, a multiple of Hkv, Hq / Hkv <= 64.
  *   scale:          finite; d^-1/2 as a rule.
  *   kv_len:         device int32 [n_seqs];  block_table: [n_seqs, max_pages].

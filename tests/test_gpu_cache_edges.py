@@ -126,6 +126,27 @@ def test_requests_that_share_the_pages_of_a_prefix(code):
     np.testing.assert_array_equal(f64(k_out), np.concatenate([rows[0][0][60:90]] * 2))
 
 
+def test_rows_that_overlap_are_refused():
+    """A broadcast token has a stride of 0, which the C call takes for dense
+    rows: the binding must not pass it on."""
+    rng = np.random.default_rng(2)
+    ref, dev, table, rows = filled(rng, [20, 20], 1, 16, 64, "int8")
+    one = bf(rng.standard_normal((1, 2, 64))).to(DEV)
+    wide, out = one.expand(2, 2, 64), torch.empty(2, 2, 64, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="overlap"):
+        gdn.gdn_attn_decode(dev.handle, 1, i32([20, 20]), i32(table), wide, out)
+    with pytest.raises(ValueError, match="overlap"):
+        gdn.gdn_attn_packed(dev.handle, i32([0, 1, 2]), [0, 1, 2], i32([20, 20]), i32(table), wide, out)
+    kv = out[:, :1].contiguous()
+    slots, cu = i64([0, 1]), i32([0, 2])
+    for args in ((wide, kv, kv, out), (out, one[:, :1].expand(2, 1, 64), kv, out), (out, kv, kv, wide)):
+        with pytest.raises(ValueError, match="overlap"):
+            gdn.gdn_rope_append(gdn.make_rope([]), dev.handle, cu, [0, 2], args[0], args[1], args[2], None, slots, args[3])
+    got = torch.empty_like(out[:1])                                    # a single row may have any stride
+    gdn.gdn_attn_decode(dev.handle, 1, i32([20]), i32(table[:1]), one.expand(2, 2, 64)[:1], got)
+    check_rows(got, oracle_rows(f64(one), rows[:1], [20], [1], 64 ** -0.5), 64)
+
+
 @pytest.mark.parametrize("n", [63, 64, 65, 1000, 1023, 1024])
 def test_plan_at_the_block_size(n):
     """Growing, shrinking and ending requests with a stack too short for all:
