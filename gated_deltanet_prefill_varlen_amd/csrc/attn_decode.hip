@@ -47,7 +47,7 @@ struct Partial {
   int splits;
 };
 
-template <int D, bool I8, int NT>
+template <int D, bool I8, int NT, bool PACKED>
 __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 ? 2 : 1) attn_decode_kernel(const AttnArgs a, const Partial part) {
   // Keys of a tile: 64, so that a lane's values are whole vectors; 32 where that
   // lets two waves into a SIMD (32 requests to 8,192 keys, 4 kv heads of 256:
@@ -62,15 +62,22 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
   // splits, and the requests one further on with every split, so that neither
   // the first splits nor a long request's all go to one of them (16 requests of
   // 4,096 to 32,768 keys, 2 kv heads of 256: 114 us, without the turn 155).
-  const int sp = blockIdx.z, b = (int)((blockIdx.y + blockIdx.z) % gridDim.y);
-  const int G = a.Hq / a.c.Hkv, R = a.n_tok * G;
-  const int groups = (R + 16 * NT - 1) / (16 * NT);
+  // In a pack (z: more prompts) a workgroup takes all keys of its rows.
+  const int sp = PACKED ? 0 : blockIdx.z;
+  const int b = PACKED ? (int)(blockIdx.y + blockIdx.z * gridDim.y) : (int)((blockIdx.y + blockIdx.z) % gridDim.y);
+  if (PACKED && b >= a.n_seqs) return;
+  const int G = a.Hq / a.c.Hkv;
+  const int tok0 = PACKED ? a.cu[b] : b * a.n_tok, n_tok = PACKED ? min(a.cu[b + 1], a.n_tokens) - tok0 : a.n_tok;
+  if (PACKED && (tok0 < 0 || n_tok < 1 || n_tok > few_rows(D) / G)) return;
+  const int R = n_tok * G;
+  const int groups = ((PACKED ? a.few * G : R) + 16 * NT - 1) / (16 * NT);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c16 = lane & 15, g = lane >> 4;
   const int hk = blockIdx.x / groups, r0 = (blockIdx.x % groups) * 16 * NT;
+  if (PACKED && r0 >= R) return;
   const int shift = a.c.page_shift, pmask = (1 << shift) - 1;
   const int32_t* table = a.table + (int64_t)b * a.max_pages;
-  constexpr int kStep = kWaves * KT, per = split_keys(D);
-  const int key0 = sp * per;
+  constexpr int kStep = kWaves * KT;
+  const int key0 = sp * split_keys(D);
   // the first tile's entries do not wait for the length
   int t0 = key0 + wave * KT;
   auto entry_of = [&](int key) -> int { return a.max_pages > 0 ? table[min(key >> shift, a.max_pages - 1)] : -1; };
@@ -78,20 +85,20 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
   const int ek1 = entry_of(t0 + kStep + KG * (c16 >> 2)), ev1 = entry_of(t0 + kStep + KG * g);
   const int L = a.kv_len[b];
   const bool bad = L < 0 || L > a.max_kv;
-  const int splits = bad ? 1 : n_splits(L, D);
+  const int splits = bad || PACKED ? 1 : n_splits(L, D);
   if (sp >= splits) return;
 
   // this lane's column: its query row per tile, and the last key that it sees
   auto row_of = [&](int t) -> int { return min(r0 + 16 * t + c16, R - 1); };
   int last[NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) last[t] = L - a.n_tok + row_of(t) / G;
+  for (int t = 0; t < NT; ++t) last[t] = L - n_tok + row_of(t) / G;
   if (bad || L == 0) {
     for (int e = tid; e < 16 * NT * D; e += 64 * kWaves) {
       const int r = r0 + e / D;
       if (r < R) {
         const int i = r / G;
-        a.out[(((int64_t)b * a.n_tok + i) * a.Hq + hk * G + (r - i * G)) * D + e % D] = bad ? 0x7FC0 : 0;
+        a.out[((int64_t)(tok0 + i) * a.Hq + hk * G + (r - i * G)) * D + e % D] = bad ? 0x7FC0 : 0;
       }
     }
     return;
@@ -110,7 +117,7 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
 #pragma unroll
   for (int n = 0; n < QN; ++n) {
     const int e = QL ? n * kWaves + wave : n, t = e / KS, k = e % KS, r = row_of(t), i = r / G;
-    const uint16_t* p = a.q + ((int64_t)b * a.n_tok + i) * a.q_stride + (hk * G + (r - i * G)) * D + 16 * g;
+    const uint16_t* p = a.q + (tok0 + i) * a.q_stride + (hk * G + (r - i * G)) * D + 16 * g;
     q[n] = *reinterpret_cast<const bf16x8*>(p + 64 * (k >> 1) + 8 * (k & 1));
   }
   auto query = [&](int t, int k) -> bf16x8 {
@@ -118,7 +125,7 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
     else return q[t * KS + k];
   };
 
-  const int key1 = min(L, key0 + per);
+  const int key1 = PACKED ? L : min(L, key0 + split_keys(D));
   const float log_scale = a.scale * kLog2e;
 
   // A tile's pages: of the keys whose values (and scores) this lane has, and
@@ -209,7 +216,7 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
     // among them, which a probability of 0 would not silence; so would a NaN
     // value that only some rows see: it becomes 0, and its key's score NaN for
     // the rows that see it
-    const bool whole = t0 + KT <= key1 - (a.n_tok - 1);   // every row sees the tile
+    const bool whole = t0 + KT <= key1 - (n_tok - 1);   // every row sees the tile
     uint32_t nan = 0;
     if (!whole || __any(!held)) {
       const int left = held ? key1 - kv : 0;
@@ -325,7 +332,7 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
     for (int w = 0; w < kWaves; ++w) lt += sl[w][16 * t + c16] * exp2_fast(sm[w][16 * t + c16] - base);
     if (r >= R) continue;
     const int i = r / G;
-    const int64_t row = ((int64_t)b * a.n_tok + i) * a.Hq + hk * G + (r - i * G);
+    const int64_t row = (int64_t)(tok0 + i) * a.Hq + hk * G + (r - i * G);
     if (splits == 1) {
       const float inv = mt == -__builtin_inff() ? 0.f : 1.f / lt;
       *reinterpret_cast<uint2*>(a.out + row * D + c) = make_uint2(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv));
@@ -388,15 +395,36 @@ hipError_t launch_d(const AttnArgs& a, const Partial& part, hipStream_t st) {
   // which loses more than it saves (64 rows of 128: 83 us, with four 113).
   const int nt = R <= 16 ? 1 : 2;
   const dim3 grid(a.c.Hkv * ((R + 16 * nt - 1) / (16 * nt)), a.n_seqs, part.splits), block(64 * kWaves);
-  if (nt == 1) hipLaunchKernelGGL((attn_decode_kernel<D, I8, 1>), grid, block, 0, st, a, part);
-  else hipLaunchKernelGGL((attn_decode_kernel<D, I8, 2>), grid, block, 0, st, a, part);
+  if (nt == 1) hipLaunchKernelGGL((attn_decode_kernel<D, I8, 1, false>), grid, block, 0, st, a, part);
+  else hipLaunchKernelGGL((attn_decode_kernel<D, I8, 2, false>), grid, block, 0, st, a, part);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || part.splits == 1) return e;
   hipLaunchKernelGGL((attn_join_kernel<D>), dim3((uint32_t)(a.n_seqs * a.n_tok * a.Hq)), dim3(64), 0, st, a, part);
   return hipGetLastError();
 }
 
+template <int D, bool I8>
+hipError_t launch_few_d(const AttnArgs& a, hipStream_t st) {
+  // (heads of 256: one tile a wave for all, as the steps differ in length, and
+  // with them the bits)
+  const int R = a.few * (a.Hq / a.c.Hkv), nt = R <= 16 || D == 256 ? 1 : 2;
+  const int y = std::min(a.n_seqs, 32768);
+  const dim3 grid(a.c.Hkv * ((R + 16 * nt - 1) / (16 * nt)), y, (a.n_seqs + y - 1) / y), block(64 * kWaves);
+  const Partial none{};
+  if (nt == 1) hipLaunchKernelGGL((attn_decode_kernel<D, I8, 1, true>), grid, block, 0, st, a, none);
+  else if constexpr (D < 256) hipLaunchKernelGGL((attn_decode_kernel<D, I8, 2, true>), grid, block, 0, st, a, none);
+  return hipGetLastError();
+}
+
 }  // namespace
+
+hipError_t launch_attn_few(const AttnArgs& a, hipStream_t st) {
+  switch (a.c.dim) {
+    case 64: return a.c.i8 ? launch_few_d<64, true>(a, st) : launch_few_d<64, false>(a, st);
+    case 128: return a.c.i8 ? launch_few_d<128, true>(a, st) : launch_few_d<128, false>(a, st);
+    default: return a.c.i8 ? launch_few_d<256, true>(a, st) : launch_few_d<256, false>(a, st);
+  }
+}
 
 int attn_decode_splits(int dim, int max_kv) { return n_splits(max_kv, dim); }
 

@@ -1,5 +1,6 @@
 // Causal attention of packed prompts over the paged 8-bit cache: many rows per
-// prompt, so the matrix cores bound it.
+// prompt, so the matrix cores bound it.  (Prompts of few rows are left to the
+// kernel of the decoding requests.)
 //
 // The rows of a prompt that share a kv head (tokens x Hq / Hkv heads) are
 // packed and dealt out to workgroups of eight waves, 32 rows a wave.  Every
@@ -87,7 +88,7 @@ typedef const float __attribute__((address_space(4)))* ConstF32;
 __device__ __forceinline__ bool tile_of_rank(const AttnArgs& a, int G, int rank, int* prompt, int* first) {
   const int lane = threadIdx.x & 63, s = min(lane, a.n_seqs - 1);
   const int i0 = a.cu[s], n = lane < a.n_seqs && i0 >= 0 ? max(min(a.cu[s + 1], a.n_tokens) - i0, 0) : 0;
-  const int tiles = (int)(((int64_t)n * G + kRows - 1) / kRows);
+  const int tiles = n <= few_rows(a.c.dim) / G ? 0 : (int)(((int64_t)n * G + kRows - 1) / kRows);
   const int keys = max(a.kv_len[s] - n + min(n, kRows / G), 0);   // of the first tile, nearly
   int before = 0;   // tiles of the prompts that go first
   for (int j = 0; j < a.n_seqs; ++j) {
@@ -132,7 +133,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
       if ((int)((int64_t)cu[mid] * G / kRows) + mid <= unit) s = mid; else hi = mid;
     }
     const int64_t at = (int64_t)(unit - (int)((int64_t)cu[s] * G / kRows) - s) * kRows;
-    if (cu[s] < 0 || at < 0 || at >= (int64_t)(min(cu[s + 1], a.n_tokens) - cu[s]) * G) return;
+    const int n = min(cu[s + 1], a.n_tokens) - cu[s];
+    if (cu[s] < 0 || at < 0 || at >= (int64_t)n * G || n <= few_rows(D) / G) return;
     first = (int)at;
   }
   const int i0 = cu[s], n = min(cu[s + 1], a.n_tokens) - i0;
@@ -489,6 +491,10 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_attn_packed(const AttnArgs& a, hipStream_t st) {
+  if (a.few) {
+    const hipError_t e = launch_attn_few(a, st);
+    if (e != hipSuccess || !a.many) return e;
+  }
   switch (a.c.dim) {
     case 64: return a.c.i8 ? launch_d<64, true>(a, st) : launch_d<64, false>(a, st);
     case 128: return a.c.i8 ? launch_d<128, true>(a, st) : launch_d<128, false>(a, st);

@@ -65,10 +65,20 @@ struct GatherArgs {
   uint16_t* v_out;
 };
 
+// A packed prompt with no more rows than this (tokens x Hq / Hkv) is computed
+// as a decoding request is, four waves sharing its keys.  The rule goes by the
+// prompt's own rows, so its bits do not depend on the pack.  Measured, heads of
+// 128 (of 256), with the rule and without it: a prompt of 16 rows on 4,096 keys
+// 39 and 109 us (62 and 265), 8 of 128 rows 64 and 116 us (160 and 292), 32 of
+// 64 rows on 3,000 68 and 112 us (226 and 267), 64 of 128 rows on 2,000, which
+// fill the card, 170 and 156 us (594 and 378).
+constexpr int few_rows(int dim) { return dim == 256 ? 64 : 128; }
+
 struct AttnArgs {
   CacheRef c;
   int32_t Hq, n_seqs, n_tokens;
   int32_t n_tok;           // rows per request (decode), 0 = rows by cu
+  int32_t few, many;       // packed: tokens of the longest prompt of up to few_rows() rows; prompts with more
   float scale;
   const int32_t* cu;
   const int32_t* kv_len;   // [n_seqs]
@@ -84,6 +94,7 @@ hipError_t launch_plan_pages(const PlanArgs& a, hipStream_t stream);
 hipError_t launch_rope_append(const AppendArgs& a, hipStream_t stream);
 hipError_t launch_cache_gather(const GatherArgs& a, hipStream_t stream);
 hipError_t launch_attn_packed(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attn_few(const AttnArgs& a, hipStream_t stream);   // the packed prompts of few rows
 int attn_decode_splits(int dim, int max_kv);   // workgroups that share a request's keys
 int64_t attn_decode_bytes(int dim, int Hq, int batch, int n_tok, int max_kv);
 hipError_t launch_attn_decode(const AttnArgs& a, void* workspace, hipStream_t stream);

@@ -127,6 +127,7 @@ gdn_status check_attn(const gdn_cache* cache, int32_t Hq, float scale, int32_t n
   gdn_status st = check_cache(cache, true, &a->c);
   if (st != GDN_OK) return st;
   if (Hq < 1 || max_pages < 0 || !std::isfinite(scale)) return GDN_ERR_SHAPE;
+  if ((int64_t)max_pages << a->c.page_shift > 1 << 30) return GDN_ERR_SHAPE;   // positions and steps past them in 32 bits
   if (Hq % a->c.Hkv != 0 || Hq / a->c.Hkv > 64) return GDN_ERR_UNSUPPORTED;
   if (rows * Hq > INT32_MAX) return GDN_ERR_SHAPE;
   if (n_seqs > 0 && (!kv_len || (max_pages > 0 && !table))) return GDN_ERR_NULL;
@@ -142,7 +143,7 @@ gdn_status check_attn(const gdn_cache* cache, int32_t Hq, float scale, int32_t n
   }
   a->Hq = Hq; a->n_seqs = n_seqs; a->n_tokens = (int32_t)rows; a->scale = scale;
   a->kv_len = kv_len; a->table = table; a->max_pages = max_pages;
-  a->max_kv = (int32_t)std::min<int64_t>((int64_t)max_pages << a->c.page_shift, INT32_MAX);
+  a->max_kv = max_pages << a->c.page_shift;
   a->q = static_cast<const uint16_t*>(q); a->out = static_cast<uint16_t*>(const_cast<void*>(out));
   return GDN_OK;
 }
@@ -548,6 +549,11 @@ gdn_status gdn_attn_packed(const gdn_cache* cache, int32_t num_q_heads, float sc
   // a workgroup of 512 per 256 rows of a prompt and kv head
   if (!fits_grid(((int64_t)n_tokens * (num_q_heads / a.c.Hkv) / 256 + n_seqs) * a.c.Hkv, 512)) return GDN_ERR_SHAPE;
   if (n_tokens == 0) return GDN_OK;
+  for (int32_t i = 0; i < n_seqs; ++i) {
+    const int32_t n = cu_seqlens_host[i + 1] - cu_seqlens_host[i];
+    if (n > gdn::few_rows(a.c.dim) / (num_q_heads / a.c.Hkv)) ++a.many;
+    else a.few = std::max(a.few, n);
+  }
   a.cu = cu_seqlens;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return finish_launch(gdn::launch_attn_packed(a, s), s);

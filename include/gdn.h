@@ -481,7 +481,8 @@ GDN_API gdn_status gdn_cache_gather(const gdn_cache* cache, int32_t n_tokens, co
  * value's, at least its channel), and no other.
  *   num_q_heads:    Hq, a multiple of Hkv, Hq / Hkv <= 64.
  *   scale:          finite; d^-1/2 as a rule.
- *   kv_len:         device int32 [n_seqs];  block_table: [n_seqs, max_pages].
+ *   kv_len:         device int32 [n_seqs];  block_table: [n_seqs, max_pages],
+ *                   max_pages * page at most 2^30.
  *   q:              device bf16 [n_tokens, Hq, d], token stride q_tok_stride.
  *   out:            device bf16 [n_tokens, Hq, d] (dense), not overlapping q.
  * Rows of out behind the last prompt are not written.

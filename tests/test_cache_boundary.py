@@ -159,6 +159,7 @@ def test_sizes_that_no_launch_holds_are_refused():
     assert decode(most=65535 * 1024, **far) == HIP and decode(most=65535 * 1024 + 1, **far) == SHAPE
     assert decode(most=2 ** 30, **far) == SHAPE
     assert decode(b=65535, n_tok=256, most=64, **far) == HIP and decode(b=65535, n_tok=257, most=64, **far) == SHAPE
+    assert decode(m=(1 << 24) + 1, most=64) == SHAPE and packed(m=(1 << 24) + 1) == SHAPE
     n = ctypes.c_int64()
     big = cache(page=128)
     assert gdn.load().gdn_attn_decode_workspace(ref(big), 4, 1, 1, 2 ** 31 - 1, ctypes.byref(n)) == 0

@@ -126,6 +126,24 @@ def test_requests_that_share_the_pages_of_a_prefix(code):
     np.testing.assert_array_equal(f64(k_out), np.concatenate([rows[0][0][60:90]] * 2))
 
 
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("d,g", [(64, 4), (128, 4), (128, 1), (256, 4), (256, 16)])
+def test_packed_bits_do_not_depend_on_the_pack(code, d, g):
+    """Prompts of few and of many rows, on both sides of every limit: alone, two
+    together and all in one pack."""
+    rng = np.random.default_rng(d + g)
+    new = [1, 4, 5, 16, 17, 32, 33, 2, 64, 65, 129, 0]
+    lens = [int(x) + int(y) for x, y in zip(new, rng.choice([0, 7, 300, 700], len(new)))]
+    ref, dev, table, rows = filled(rng, lens, 1, 32, d, code)
+    q = bf(rng.standard_normal((sum(new), g, d))).to(DEV)
+    whole = packed_call(dev, new, lens, table, q)
+    check_rows(whole, oracle_rows(f64(q), rows, lens, new, d ** -0.5), d)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    for a, b in [(i, i + 1) for i in range(len(new))] + [(i, i + 2) for i in range(0, len(new) - 1, 2)]:
+        part = packed_call(dev, new[a:b], lens[a:b], table[a:b], q[cu[a]:cu[b]].contiguous())
+        assert torch.equal(part.view(torch.int16), whole[cu[a]:cu[b]].view(torch.int16)), (a, b)
+
+
 def test_rows_that_overlap_are_refused():
     """A broadcast token has a stride of 0, which the C call takes for dense
     rows: the binding must not pass it on."""
