@@ -37,6 +37,17 @@ constexpr int kWaves = 8;
 constexpr int kRows = 32 * kWaves;   // of a workgroup
 constexpr float kLazy = 16.f;  // the running maximum follows once it lags by this many powers of two
 
+// Value scales from 2^-100 to 2^122 meet probabilities in one fp32 product.
+// A key whose scale is over 2^kLarge counts for the running maximum with what
+// its scale is over: a softmax is the same against any measure, and against
+// that one no probability times scale passes 2^(kLarge + kLazy), which leaves
+// the sums of 2^30 keys room.  The measure is then up to 2^58 above the largest
+// score, but only where that key outweighs all others in the output.  The sum
+// of the probabilities is formed from their products with the scales, divided
+// by the scale again; below 2^kTiny the products could lose what the sum needs
+// (2^-58 of the measure, 2^-26 of a probability), and it is formed apart.
+constexpr float kLarge = 64.f, kTiny = -40.f;
+
 __device__ __forceinline__ uint2 both_halves(float x) {
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   const uint32_t u = __float_as_uint(x);
@@ -232,16 +243,16 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
     }
   };
   // The scales as the steps use them: the scores' factor (at least 2^-126: its
-  // product with a masked score stays -inf), the values' as a power of two and
-  // the inverse of that, which is 0 for a piece that is not held.  Values are
-  // measured in units of the first page's scale, within limits that keep zero
-  // pages and huge ones from pushing the others out of range.
-  float unit_log = 0.f;
+  // product with a masked score stays -inf); the values' as a power of two; the
+  // inverse of that, or 0 where the piece is not held or its probabilities are
+  // summed apart; and the power of two by which the values' is over 2^kLarge,
+  // or -1 where the piece is not held.
   auto put_scales = [&](int tile) {
-    const float lv = __builtin_amdgcn_logf(page < 0 ? 1.f : fmaxf(vs, kMinScale)) - unit_log;
+    const float lv = __builtin_amdgcn_logf(page < 0 ? 1.f : fmaxf(vs, kMinScale));
     if (lane == 0 && part == 0)
-      pieces[tile & 3][piece] = page < 0 ? make_float4(1.f, 0.f, 0.f, 0.f)
-                                         : make_float4(fmaxf(ks * log_scale, 0x1p-126f), lv, exp2_fast(-lv), 0.f);
+      pieces[tile & 3][piece] = page < 0 ? make_float4(1.f, 0.f, 0.f, -1.f)
+                                         : make_float4(fmaxf(ks * log_scale, 0x1p-126f), lv,
+                                                       lv < kTiny ? 0.f : fmaxf(exp2_fast(-lv), 0x1p-126f), fmaxf(lv - kLarge, 0.f));
   };
   // LDS addresses of a lane's units of a tile: 8 channels of a key, 8 keys of a channel
   // (of two units: in chunks that differ in their last bit)
@@ -341,15 +352,16 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
     fetch_values();        // of tile t + 2
     look_up(tile + 3);
     fetch(a.c.k, kr);
-    float held = pc[0].z;
+    float least = pc[0].z;
 #pragma unroll
-    for (int u = 1; u < NP; ++u) held = fminf(held, pc[u].z);
-    if (key0 + KT > w_free || __any(held == 0.f)) {
+    for (int u = 1; u < NP; ++u) least = fminf(least, pc[u].z);
+    const bool odd = __any(least == 0.f);   // pieces not held, or summed apart
+    if (key0 + KT > w_free || odd) {
 #pragma unroll
       for (int b = 0; b < KB; ++b)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (pc[2 * b + (e >> 3)].z == 0.f || key0 + 32 * b + 16 * (e >> 3) + 8 * h + (e & 7) > last) sc[b][e] = -__builtin_inff();
+          if (pc[2 * b + (e >> 3)].w < 0.f || key0 + 32 * b + 16 * (e >> 3) + 8 * h + (e & 7) > last) sc[b][e] = -__builtin_inff();
       if constexpr (!I8) {
         if (key0 + KT > wg_free) {
           uint32_t nan[NP], any = 0;
@@ -377,7 +389,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
       float y = sc[u >> 1][8 * (u & 1)];
 #pragma unroll
       for (int e = 1; e < 8; ++e) y = fmaxf(y, sc[u >> 1][8 * (u & 1) + e]);
-      mx = fmaxf(mx, y * pc[u].x);
+      mx = fmaxf(mx, fmaf(y, pc[u].x, pc[u].w));
     }
     mx = max_halves(mx);
     const bool grow = mx > m + kLazy;
@@ -391,6 +403,16 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
       m = m1;
     }
     const float less = m == -__builtin_inff() ? 0.f : m;
+    if (odd) {
+#pragma unroll
+      for (int u = 0; u < NP; ++u)
+        if (pc[u].z == 0.f && pc[u].w >= 0.f) {
+#pragma unroll
+          for (int i = 0; i < 8; i += 2)
+            l = add_pair(pack_bf16(exp2_fast(fmaf(sc[u >> 1][8 * (u & 1) + i], pc[u].x, -less)),
+                                   exp2_fast(fmaf(sc[u >> 1][8 * (u & 1) + i + 1], pc[u].x, -less))), l);
+        }
+    }
     // p times its value's scale, a power of two, rounded to bf16 once; the sum
     // is of the rounded ones, so a row that one key takes is that key's value
     // exactly
@@ -420,10 +442,6 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
 #pragma unroll
   for (int u = 0; u < NP; ++u) p[u] = bf16x8{};
   if (steps > 0) {
-    const int p0 = table[0];
-    const bool held = p0 >= 0 && p0 < a.c.n_pages;
-    const float v0 = ((ConstF32)a.c.vs)[(int64_t)(held ? p0 : 0) * a.c.Hkv + hk];
-    unit_log = uniform(fminf(fmaxf(__builtin_amdgcn_logf(held ? fmaxf(v0, kMinScale) : 1.f), -30.f), 60.f));
     entry = entry_of(0);
     look_up(0);
     fetch(a.c.k, kr);
@@ -470,7 +488,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
   const int r1 = r0 + (lane1 & 31), i1 = r1 / G;
   if (r1 >= rows) return;
   const float sum = add_halves(l);
-  const float inv = bad ? __builtin_nanf("") : m == -__builtin_inff() ? 0.f : exp2_fast(unit_log) / sum;
+  const float inv = bad ? __builtin_nanf("") : m == -__builtin_inff() ? 0.f : 1.f / sum;
   uint16_t* out = a.out + ((int64_t)(i0 + i1) * a.Hq + hk * G + (r1 - i1 * G)) * D + 4 * (lane1 >> 5);
 #pragma unroll
   for (int x = 0; x < OB; ++x)

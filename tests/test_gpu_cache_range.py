@@ -1,0 +1,57 @@
+"""Attention over values of every size that bf16 holds: pages whose scales lie
+far apart, and sums that would pass fp32."""
+import numpy as np
+import pytest
+
+from cache_util import DEV, bf, f64, filled
+from oracle import cache_oracle as C
+from packed_util import few_rows, many_rows_call
+from test_gpu_cache import check_rows, oracle_rows
+
+pytestmark = pytest.mark.gpu
+
+# sizes of the values in turn, each over a few pages
+RISING, FALLING = [0.0, 1e-30, 1.0, 1e12, 1e30], [1e30, 1e12, 1.0, 1e-30, 0.0]
+ORDERS = {"rising": RISING, "falling": FALLING, "mixed": [1.0, 0.0, 1e30, 1e-30, 1e12], "zeros first": [0.0, 1e37, 0.0, 1e37, 1e-20],
+          "far below the first": [1e11, 0.0, 0.0, 0.0, 0.0], "at the border": [1e21, 1e-12, 1e23, 1e-10, 1e19],
+          "near the largest": [3e37] * 5}
+
+
+def sized(sizes, L, run):
+    """[L, 1, 1]: the size of each token's values, `run` tokens each in turn."""
+    return np.array([sizes[t // run % len(sizes)] for t in range(L)])[:, None, None]
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("d,page,g", [(64, 16, 2), (128, 32, 2), (256, 16, 1)])
+@pytest.mark.parametrize("order", list(ORDERS))
+def test_packed_pages_of_values_far_apart(order, d, page, g, code):
+    """Every row of a whole prompt, so that its first ones see the first sizes
+    alone; heads whose queries are zero weigh all keys alike, so a page that
+    dropped out of the sum shows."""
+    rng = np.random.default_rng(d)
+    L = max(170, 2 * few_rows(d))
+    ref, dev, table, rows = filled(rng, [L], 1, page, d, code, 1.0, sized(ORDERS[order], L, 32))
+    q = rng.standard_normal((L, g, d))
+    q[::3] = 0.0
+    q = bf(q).to(DEV)
+    check_rows(many_rows_call(dev, [L], [L], table, q), oracle_rows(f64(q), rows, [L], [L], d ** -0.5), d, order)
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("low", [0, 2, 4])
+def test_packed_sizes_apart_and_scores_apart(low, code):
+    """One size's keys score hundreds below the others: huge values that no row
+    weighs leave the tiny ones as they are."""
+    rng = np.random.default_rng(low)
+    d, page, run, L = 128, 16, 48, 240
+    ref, dev, table, rows = filled(rng, [L], 1, page, d, code, 1.0, sized(RISING, L, run))
+    k, v = ref.read([int(table[0, p // page]) * page + p % page for p in range(L)])
+    k[:, :, 0] = np.where(np.arange(L) // run % 5 == low, 20.0, -20.0)[:, None]
+    ref.append([0, L], [int(table[0, p // page]) * page + p % page for p in range(L)], C.round_bf16(k), C.round_bf16(v))
+    dev.load(ref, [(int(table[0, p // page]), p % page) for p in range(L)])
+    rows = [ref.read([int(table[0, p // page]) * page + p % page for p in range(L)])]
+    q = 0.1 * rng.standard_normal((L, 2, d))
+    q[:, 0, 0], q[:, 1, 0] = 20.0, -20.0
+    q = bf(q).to(DEV)
+    check_rows(many_rows_call(dev, [L], [L], table, q, 1.0), oracle_rows(f64(q), rows, [L], [L], 1.0), d, low)
