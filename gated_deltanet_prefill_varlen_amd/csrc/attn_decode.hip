@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
     }
 
     // scores to probabilities; in units of log2
-    const float vf = held ? vs : 0.f;
+    const float vf = held ? vs : 0.f, over = fmaxf(__builtin_amdgcn_logf(vf) - kLarge, 0.f);
     bf16x8 p[NT][NS / 2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
           s4[t][s][i] = x;
           mx = fmaxf(mx, x);
         }
+      mx += over;
       mx = fmaxf(mx, __shfl_xor(mx, 16));
       mx = fmaxf(mx, __shfl_xor(mx, 32));
       const float m1 = fmaxf(m[t], mx);

@@ -55,4 +55,13 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w, int at, uint32_t* fo
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// Value scales from 2^-100 to 2^122 meet probabilities in one fp32 product.
+// A key whose scale is over 2^kLarge counts for the running maximum with what
+// its scale is over: a softmax is the same against any measure, and against
+// that one no probability times scale passes 2^kLarge (2^80 where the maximum
+// may lag), which leaves the sums of 2^30 keys room.  The measure is then up to
+// 2^58 above the largest score, but only where that key outweighs all others in
+// the output.
+constexpr float kLarge = 64.f;
+
 }  // namespace gdn

@@ -37,16 +37,11 @@ constexpr int kWaves = 8;
 constexpr int kRows = 32 * kWaves;   // of a workgroup
 constexpr float kLazy = 16.f;  // the running maximum follows once it lags by this many powers of two
 
-// Value scales from 2^-100 to 2^122 meet probabilities in one fp32 product.
-// A key whose scale is over 2^kLarge counts for the running maximum with what
-// its scale is over: a softmax is the same against any measure, and against
-// that one no probability times scale passes 2^(kLarge + kLazy), which leaves
-// the sums of 2^30 keys room.  The measure is then up to 2^58 above the largest
-// score, but only where that key outweighs all others in the output.  The sum
-// of the probabilities is formed from their products with the scales, divided
-// by the scale again; below 2^kTiny the products could lose what the sum needs
-// (2^-58 of the measure, 2^-26 of a probability), and it is formed apart.
-constexpr float kLarge = 64.f, kTiny = -40.f;
+// The sum of the probabilities is formed from their products with the values'
+// scales, divided by the scale again; below 2^kTiny the products could lose
+// what the sum needs (2^-58 of the measure, 2^-26 of a probability), and it is
+// formed apart.
+constexpr float kTiny = -40.f;
 
 __device__ __forceinline__ uint2 both_halves(float x) {
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));

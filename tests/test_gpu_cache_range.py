@@ -5,8 +5,8 @@ import pytest
 
 from cache_util import DEV, bf, f64, filled
 from oracle import cache_oracle as C
-from packed_util import few_rows, many_rows_call
-from test_gpu_cache import check_rows, oracle_rows
+from packed_util import few_rows, many_rows_call, packed_call
+from test_gpu_cache import check_rows, decode_call, oracle_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +55,30 @@ def test_packed_sizes_apart_and_scores_apart(low, code):
     q[:, 0, 0], q[:, 1, 0] = 20.0, -20.0
     q = bf(q).to(DEV)
     check_rows(many_rows_call(dev, [L], [L], table, q, 1.0), oracle_rows(f64(q), rows, [L], [L], 1.0), d, low)
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("d,page,g,n_tok", [(64, 32, 2, 1), (128, 64, 4, 3), (128, 16, 20, 1), (256, 32, 2, 1), (256, 64, 6, 4)])
+def test_decode_sums_of_values_near_the_largest(d, page, g, n_tok, code):
+    """Thousands of values of one sign near bf16's largest: their mean is a
+    number, their sum is none in fp32.  Alone, after pages of zeros and of ones,
+    and as prompts of few rows."""
+    rng = np.random.default_rng(d + g)
+    lens = [4200, 3500, 700]
+    assert n_tok * g <= few_rows(d)
+    ref, dev, table, rows = filled(rng, lens, 1, page, d, code, 0.1, 1.0)
+    # in place of the codes' scales: huge ones on all pages of the first request, and on some of the others'
+    for i, every in enumerate((1, 3, 5)):
+        ids = table[i, :-(-lens[i] // page)]
+        ref.v[ids] = np.abs(ref.v[ids])
+        ref.vs[ids[::every]] = 2.0 ** (119 if code == "e4m3" else 120)
+        if every == 5:
+            ref.vs[ids[1::5]] = 2.0 ** -100
+    top = {"e4m3": 224.0, "int8": 100.0}[code]
+    ref.v[:] = np.minimum(ref.v, top)
+    dev.load(ref, [(int(table[i, p // page]), p % page) for i, n in enumerate(lens) for p in range(n)])
+    rows = [ref.read([int(table[i, p // page]) * page + p % page for p in range(n)]) for i, n in enumerate(lens)]
+    q = bf(rng.standard_normal((3 * n_tok, g, d))).to(DEV)
+    want = oracle_rows(f64(q), rows, lens, [n_tok] * 3, d ** -0.5)
+    check_rows(decode_call(dev, n_tok, lens, table, q), want, d, "decode")
+    check_rows(packed_call(dev, [n_tok] * 3, lens, table, q), want, d, "few rows")
