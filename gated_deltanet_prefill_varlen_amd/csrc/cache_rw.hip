@@ -69,6 +69,10 @@ struct Chunk {
   }
 };
 
+__device__ __forceinline__ float at_most_largest(float x) {
+  return __builtin_amdgcn_fmed3f(x, -0x1.fffffep127f, 0x1.fffffep127f);
+}
+
 // Turns the 8 pairs of a chunk (x: 16 channels, e0's 8 then e1's 8).
 template <typename CosSin>
 __device__ __forceinline__ void turn(float* x, int adjacent, CosSin cs) {
@@ -79,9 +83,11 @@ __device__ __forceinline__ void turn(float* x, int adjacent, CosSin cs) {
     float& a = adjacent ? x[2 * i] : x[i];
     float& b = adjacent ? x[2 * i + 1] : x[8 + i];
     // the second product's rounding error goes back in, so that fewer results
-    // land on the other side of a bf16 step
+    // land on the other side of a bf16 step; an infinite product's is taken
+    // against the largest number, so that it is infinite too and not NaN
     const float bs = b * s, bc = b * c;
-    const float ra = fmaf(a, c, -bs) - fmaf(b, s, -bs), rb = fmaf(a, s, bc) + fmaf(b, c, -bc);
+    const float es = fmaf(b, s, -at_most_largest(bs)), ec = fmaf(b, c, -at_most_largest(bc));
+    const float ra = fmaf(a, c, -bs) - es, rb = fmaf(a, s, bc) + ec;
     a = ra;
     b = rb;
   }
