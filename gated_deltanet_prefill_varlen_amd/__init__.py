@@ -111,8 +111,9 @@ def make_cache(k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
 
 def make_rope(freq: Sequence[float], axis: Optional[Sequence[int]] = None, n_axes: int = 1,
               adjacent: bool = False, scale: float = 1.0) -> gdn_rope:
-    """Rotary plan: freq in radians per position of each of rot_dim / 2 pairs,
-    axis the position row (below n_axes) that turns each pair (default 0)."""
+    """Rotary plan: freq in radians per position (up to 65,536 in size) of each
+    of rot_dim / 2 pairs, axis the position row (below n_axes) that turns each
+    pair (default 0)."""
     freq = [float(f) for f in freq]
     axis = [0] * len(freq) if axis is None else [int(i) for i in axis]
     if len(freq) > 128 or len(axis) != len(freq) or any(not 0 <= i < n_axes for i in axis):

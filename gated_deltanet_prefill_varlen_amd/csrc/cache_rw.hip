@@ -18,16 +18,19 @@ namespace gdn {
 namespace {
 
 
-// cos and sin of position * freq, to a little over half an ulp.  In 64 bits
-// the angle becomes quarter turns, of which the nearest whole number is taken
-// off; what is left is x + x_lo in [-pi/4, pi/4], where the Taylor sums through
-// x^9 and x^10 leave 2e-9 and 3e-11.  Each sum's last addition is the only
-// rounding at the result's size: the lower part of x, of x^2 and of 1 - x^2/2
-// goes into the small terms.
+// cos and sin of position * freq, to 0.86 ulp at any size that the call takes
+// (|freq| <= 2^16, so angles up to 2^47).  The angle, a product of
+// 31 and 24 bits, is held in two doubles, and 2 / pi in two: the nearest whole
+// number of quarter turns comes off exactly, and what is left of the angle is
+// right to 2^-54 turns.  It is x + x_lo, at most 0.8, where the Taylor sums
+// through x^9 and x^10 leave 2e-9 and 1.4e-10.  Each sum's last addition is the
+// only rounding at the result's size: the lower part of x, of x^2 and of
+// 1 - x^2/2 goes into the small terms.
 __device__ __forceinline__ void cos_sin(int pos, float freq, float scale, float* c, float* s) {
-  const double quarters = (double)pos * (double)freq * 0.63661977236758134308;   // 2 / pi
-  const double n = rint(quarters);
-  const double xd = (quarters - n) * 1.57079632679489661923;                     // pi / 2
+  constexpr double kQuarters = 0.63661977236758134308, kQuartersLow = -3.935735335036497e-17;   // 2 / pi
+  const double angle = (double)pos * (double)freq, angle_lo = fma((double)pos, (double)freq, -angle);
+  const double n = rint(angle * kQuarters);
+  const double xd = (fma(angle, kQuarters, -n) + fma(angle, kQuartersLow, angle_lo * kQuarters)) * 1.57079632679489661923;   // pi / 2
   const float x = (float)xd, x_lo = (float)(xd - (double)x);
   const float y = x * x, y_lo = fmaf(2.f * x, x_lo, fmaf(x, x, -y));
   float sn = fmaf(y, 2.7557319e-6f, -1.9841270e-4f);

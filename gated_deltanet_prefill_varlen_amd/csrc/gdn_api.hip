@@ -488,7 +488,7 @@ gdn_status gdn_rope_append(const gdn_rope* rope, const gdn_cache* cache, int32_t
   if (rope->n_axes < 1 || rope->n_axes > 4 || (rope->adjacent != 0 && rope->adjacent != 1)) return GDN_ERR_UNSUPPORTED;
   if (!std::isfinite(rope->scale) || pos_axis_stride < 0) return GDN_ERR_SHAPE;
   for (int32_t i = 0; i < rope->rot_dim / 2; ++i)
-    if (!std::isfinite(rope->freq[i]) || rope->axis[i] >= rope->n_axes) return GDN_ERR_SHAPE;
+    if (!(std::fabs(rope->freq[i]) <= 65536.f) || rope->axis[i] >= rope->n_axes) return GDN_ERR_SHAPE;
   st = check_seqlens(cu_seqlens_host, n_seqs, n_tokens);
   if (st != GDN_OK) return st;
   if (!q != !q_out) return GDN_ERR_NULL;

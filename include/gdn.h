@@ -381,8 +381,8 @@ typedef struct gdn_cache {
  *   rot_dim:   a multiple of 16 in [0, min(d, 256)].   n_axes: 1 .. 4.
  *   adjacent:  0: pair i is channels (i, i + rot_dim/2); 1: (2i, 2i + 1).
  *   scale:     factor on cos and sin (1.0 for none).
- *   freq:      radians per position, finite.   axis: each below n_axes (in
- *              sections, or dealt out in turn). */
+ *   freq:      radians per position, -65,536 .. 65,536.   axis: each below
+ *              n_axes (in sections, or dealt out in turn). */
 typedef struct gdn_rope {
   int32_t rot_dim;
   int32_t n_axes;

@@ -49,3 +49,27 @@ def test_infinite_channels_turn_as_the_formula_says(d, rot, code, adjacent):
         inf = np.isinf(y)
         np.testing.assert_array_equal(x[inf], np.copysign(C.TOP[code], y[inf]))
         assert np.all(x[np.isnan(y)] == 0) or code == "e4m3"
+
+
+@pytest.mark.parametrize("top", [1.0, 300.0, 65536.0])
+def test_angles_of_every_size(top):
+    """Frequencies up to the largest that the call takes at positions up to
+    2^31, negative ones too: the rotation by the angle itself, in 80 bits (the
+    products of 24 and 31 bits are exact there).  Error: the bf16
+    result by 2^-8 of itself; 2^-20 of the pair covers cos and sin (2^-24) and the
+    fp32 work."""
+    if np.finfo(np.longdouble).nmant < 63:
+        pytest.skip("no 80-bit numbers here")
+    rng = np.random.default_rng(int(top))
+    d, T = 128, 64
+    freq = [float(np.float32(top * x)) for x in np.concatenate([[1.0, -1.0], rng.uniform(0.3, 1.0, 62)])]
+    pos = np.concatenate([[0, 1, -1, 2 ** 31 - 1, -2 ** 31], rng.integers(-2 ** 31, 2 ** 31, T - 5)]).astype(np.int32)
+    x = bf(rng.standard_normal((T, 4, d))).to(DEV)
+    kv, out = torch.zeros(T, 1, d, dtype=torch.bfloat16, device=DEV), torch.empty_like(x)
+    dev = DevCache(1, 1, 16, d, "int8")
+    gdn.gdn_rope_append(gdn.make_rope(freq), dev.handle, i32([0, T]), [0, T], x, kv, kv, i32(pos), i64([-1] * T), out)
+    angle = pos.astype(np.longdouble)[:, None, None] * np.array(freq, np.longdouble)
+    c, s = np.cos(angle).astype(np.float64), np.sin(angle).astype(np.float64)
+    a, b = f64(x)[..., :64], f64(x)[..., 64:]
+    want = np.concatenate([a * c - b * s, a * s + b * c], -1)
+    assert np.all(np.abs(f64(out) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -20 * 2 * np.abs(f64(x)).max())
