@@ -406,9 +406,7 @@ hipError_t launch_d(const AttnArgs& a, const Partial& part, hipStream_t st) {
 
 template <int D, bool I8>
 hipError_t launch_few_d(const AttnArgs& a, hipStream_t st) {
-  // (heads of 256: one tile a wave for all, as the steps differ in length, and
-  // with them the bits)
-  const int R = a.few * (a.Hq / a.c.Hkv), nt = R <= 16 || D == 256 ? 1 : 2;
+  const int R = a.few * (a.Hq / a.c.Hkv), nt = few_tiles(D, R);
   const int y = std::min(a.n_seqs, 32768);
   const dim3 grid(a.c.Hkv * ((R + 16 * nt - 1) / (16 * nt)), y, (a.n_seqs + y - 1) / y), block(64 * kWaves);
   const Partial none{};

@@ -74,6 +74,10 @@ struct GatherArgs {
 // fill the card, 170 and 156 us (594 and 378).
 constexpr int few_rows(int dim) { return dim == 256 ? 64 : 128; }
 
+// 16-row tiles of a wave there, for `rows` rows of the longest of them (heads
+// of 256: one for all, as the steps differ in length, and with them the bits).
+constexpr int few_tiles(int dim, int rows) { return rows <= 16 || dim == 256 ? 1 : 2; }
+
 struct AttnArgs {
   CacheRef c;
   int32_t Hq, n_seqs, n_tokens;

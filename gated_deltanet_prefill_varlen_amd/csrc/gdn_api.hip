@@ -554,6 +554,9 @@ gdn_status gdn_attn_packed(const gdn_cache* cache, int32_t num_q_heads, float sc
     if (n > gdn::few_rows(a.c.dim) / (num_q_heads / a.c.Hkv)) ++a.many;
     else a.few = std::max(a.few, n);
   }
+  // one of 256 per few 16-row tiles of the longest prompt of few rows and kv head
+  const int64_t few = (int64_t)a.few * (num_q_heads / a.c.Hkv), tile = 16 * gdn::few_tiles(a.c.dim, (int)few);
+  if (!fits_grid((few + tile - 1) / tile * a.c.Hkv, 256)) return GDN_ERR_SHAPE;
   a.cu = cu_seqlens;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return finish_launch(gdn::launch_attn_packed(a, s), s);
