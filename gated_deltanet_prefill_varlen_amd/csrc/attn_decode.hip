@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(64 * kWaves, D == 64 ? 5 - NT : NT * D <= 256 
         }
       }
     }
-    const float kf = ks * log_scale;
+    const float kf = __builtin_amdgcn_fmed3f(ks * log_scale, -kMostFactor, kMostFactor);
     __builtin_amdgcn_sched_barrier(0);
     if (more) load_keys(t0 + kStep, pk1, pv1);
     __builtin_amdgcn_sched_barrier(0);

@@ -64,4 +64,8 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // the output.
 constexpr float kLarge = 64.f;
 
+// A page's factor of its scores.  Past fp32 it is the largest number: a score
+// of 0 stays 0.
+constexpr float kMostFactor = 0x1.fffffep127f;
+
 }  // namespace gdn

@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
       if (lane == 0) nan_keys[tile & 3][wave] = found;
     }
   };
-  // The scales as the steps use them: the scores' factor (at least 2^-126: its
-  // product with a masked score stays -inf); the values' as a power of two; the
+  // The scales as the steps use them: the scores' factor (a number, at least
+  // 2^-126: its product with a masked score stays -inf); the values' as a power of two; the
   // inverse of that, or 0 where the piece is not held or its probabilities are
   // summed apart; and the power of two by which the values' is over 2^kLarge,
   // or -1 where the piece is not held.
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
     const float lv = __builtin_amdgcn_logf(page < 0 ? 1.f : fmaxf(vs, kMinScale));
     if (lane == 0 && part == 0)
       pieces[tile & 3][piece] = page < 0 ? make_float4(1.f, 0.f, 0.f, -1.f)
-                                         : make_float4(fmaxf(ks * log_scale, 0x1p-126f), lv,
+                                         : make_float4(__builtin_amdgcn_fmed3f(ks * log_scale, 0x1p-126f, kMostFactor), lv,
                                                        lv < kTiny ? 0.f : fmaxf(exp2_fast(-lv), 0x1p-126f), fmaxf(lv - kLarge, 0.f));
   };
   // LDS addresses of a lane's units of a tile: 8 channels of a key, 8 keys of a channel

@@ -1,7 +1,9 @@
 """Attention over values of every size that bf16 holds: pages whose scales lie
-far apart, and sums that would pass fp32."""
+far apart, sums that would pass fp32, and keys whose scale times the call's
+passes it."""
 import numpy as np
 import pytest
+import torch
 
 from cache_util import DEV, bf, f64, filled
 from oracle import cache_oracle as C
@@ -82,3 +84,17 @@ def test_decode_sums_of_values_near_the_largest(d, page, g, n_tok, code):
     want = oracle_rows(f64(q), rows, lens, [n_tok] * 3, d ** -0.5)
     check_rows(decode_call(dev, n_tok, lens, table, q), want, d, "decode")
     check_rows(packed_call(dev, [n_tok] * 3, lens, table, q), want, d, "few rows")
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_keys_whose_scale_times_the_calls_passes_fp32(d, code):
+    """Scores of 0 stay 0 however large the factor: the mean of the values."""
+    rng = np.random.default_rng(d)
+    L = 2 * few_rows(d) + 5
+    ref, dev, table, rows = filled(rng, [L], 1, 32, d, code, 2e37, 1.0)
+    q = torch.zeros(L, 1, d, dtype=torch.bfloat16, device=DEV)
+    for scale in (5000.0, -5000.0):
+        want = oracle_rows(f64(q), rows, [L], [L], scale)
+        check_rows(many_rows_call(dev, [L], [L], table, q, scale), want, d, "packed")
+        check_rows(decode_call(dev, 1, [L], table, q[:1], scale=scale), want[-1:], d, "decode")
