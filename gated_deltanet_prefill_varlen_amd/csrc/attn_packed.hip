@@ -351,7 +351,9 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
 #pragma unroll
     for (int u = 1; u < NP; ++u) least = fminf(least, pc[u].z);
     const bool odd = __any(least == 0.f);   // pieces not held, or summed apart
-    if (key0 + KT > w_free || odd) {
+    // (e4m3: for every wave of the tiles that were cleaned, also where its rows
+    // all see them: the marks stand for the NaN values taken out)
+    if (key0 + KT > (I8 ? w_free : wg_free) || odd) {
 #pragma unroll
       for (int b = 0; b < KB; ++b)
 #pragma unroll
