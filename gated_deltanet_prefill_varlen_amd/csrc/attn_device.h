@@ -58,11 +58,10 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // Value scales from 2^-100 to 2^122 meet probabilities in one fp32 product.
 // A key whose scale is over 2^kLarge counts for the running maximum with what
 // its scale is over: a softmax is the same against any measure, and against
-// that one no probability times scale passes 2^kLarge (2^80 where the maximum
-// may lag), which leaves the sums of 2^30 keys room.  The measure is then up to
-// 2^58 above the largest score, but only where that key outweighs all others in
-// the output.
-constexpr float kLarge = 64.f;
+// that one no probability times scale passes 2^kLarge, which leaves the sums of
+// 2^30 keys with codes up to 448 room.  The measure is then above the largest
+// score, but only where that key outweighs all others in the output.
+constexpr float kLarge = 88.f;
 
 // A page's factor of its scores.  Past fp32 it is the largest number: a score
 // of 0 stays 0.

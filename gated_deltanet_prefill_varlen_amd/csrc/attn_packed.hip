@@ -37,11 +37,13 @@ constexpr int kWaves = 8;
 constexpr int kRows = 32 * kWaves;   // of a workgroup
 constexpr float kLazy = 16.f;  // the running maximum follows once it lags by this many powers of two
 
-// The sum of the probabilities is formed from their products with the values'
-// scales, divided by the scale again; below 2^kTiny the products could lose
-// what the sum needs (2^-58 of the measure, 2^-26 of a probability), and it is
-// formed apart.
-constexpr float kTiny = -40.f;
+// Values are measured in units of 2^-kUnit, so that a page of the smallest scale
+// (2^-100) keeps probabilities down to 2^-50.  The sum of the probabilities is
+// formed from their products with the scales, divided by the scale again.
+// Beyond these limits the products could lose what the sum needs (they are down
+// to 2^-74 by the measure and 2^-26 by a probability), or fp32 does not hold
+// the inverse, and it is formed apart.
+constexpr float kUnit = 24.f, kTiny = -26.f, kHuge = 126.f;
 
 __device__ __forceinline__ uint2 both_halves(float x) {
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -238,16 +240,17 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
     }
   };
   // The scales as the steps use them: the scores' factor (a number, at least
-  // 2^-126: its product with a masked score stays -inf); the values' as a power of two; the
-  // inverse of that, or 0 where the piece is not held or its probabilities are
-  // summed apart; and the power of two by which the values' is over 2^kLarge,
-  // or -1 where the piece is not held.
+  // 2^-126: its product with a masked score stays -inf); the values' as a power
+  // of two; the inverse of that, or 0 where the piece is not held or its
+  // probabilities are summed apart; and the power of two by which the values'
+  // is too large, or -1 where the piece is not held.
   auto put_scales = [&](int tile) {
-    const float lv = __builtin_amdgcn_logf(page < 0 ? 1.f : fmaxf(vs, kMinScale));
+    const float lv = __builtin_amdgcn_logf(page < 0 ? 1.f : fmaxf(vs, kMinScale)) + kUnit;
     if (lane == 0 && part == 0)
       pieces[tile & 3][piece] = page < 0 ? make_float4(1.f, 0.f, 0.f, -1.f)
                                          : make_float4(__builtin_amdgcn_fmed3f(ks * log_scale, 0x1p-126f, kMostFactor), lv,
-                                                       lv < kTiny ? 0.f : fmaxf(exp2_fast(-lv), 0x1p-126f), fmaxf(lv - kLarge, 0.f));
+                                                       lv < kTiny || lv > kHuge ? 0.f : exp2_fast(-lv),
+                                                       fmaxf(lv - (kLarge - kLazy), 0.f));
   };
   // LDS addresses of a lane's units of a tile: 8 channels of a key, 8 keys of a channel
   // (of two units: in chunks that differ in their last bit)
@@ -485,7 +488,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_packed_kernel(const AttnA
   const int r1 = r0 + (lane1 & 31), i1 = r1 / G;
   if (r1 >= rows) return;
   const float sum = add_halves(l);
-  const float inv = bad ? __builtin_nanf("") : m == -__builtin_inff() ? 0.f : 1.f / sum;
+  const float inv = bad ? __builtin_nanf("") : m == -__builtin_inff() ? 0.f : exp2_fast(-kUnit) / sum;
   uint16_t* out = a.out + ((int64_t)(i0 + i1) * a.Hq + hk * G + (r1 - i1 * G)) * D + 4 * (lane1 >> 5);
 #pragma unroll
   for (int x = 0; x < OB; ++x)

@@ -41,6 +41,18 @@ def test_packed_pages_of_values_far_apart(order, d, page, g, code):
 
 
 @pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("size", [1e-30, 1e-27, 1e20, 1e30])
+def test_packed_small_probabilities_of_tiny_and_huge_values(size, code):
+    """Scores spread over a hundred: channels whose likeliest keys hold codes of
+    0 consist of probabilities far below 2^-26."""
+    rng = np.random.default_rng(3)
+    d, L = 128, 3 * few_rows(128)
+    ref, dev, table, rows = filled(rng, [L], 1, 32, d, code, 1.0, size)
+    q = bf(rng.standard_normal((L, 1, d))).to(DEV)
+    check_rows(many_rows_call(dev, [L], [L], table, q, 1.0), oracle_rows(f64(q), rows, [L], [L], 1.0), d, size)
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
 @pytest.mark.parametrize("low", [0, 2, 4])
 def test_packed_sizes_apart_and_scores_apart(low, code):
     """One size's keys score hundreds below the others: huge values that no row
