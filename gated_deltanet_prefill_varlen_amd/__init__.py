@@ -403,7 +403,8 @@ def _cache(cache: gdn_cache, dev: int) -> int:
 def gdn_plan_pages(page: int, want_len, kv_len, kv_len_out, block_table, free_pages, free_count,
                    free_count_out, cu_seqlens, slot_map, positions, status, stream=None) -> None:
     """Block tables, the pack of new tokens and its slot map, from the lengths
-    that the requests hold (kv_len) and want; all on the device."""
+    that the requests hold (kv_len) and want; all on the device.  No two rows of
+    block_table may share a page: it is free again when its request ends."""
     i32 = torch.int32
     dev, st = _where(stream)
     n, (rows, max_pages) = want_len.numel(), block_table.shape

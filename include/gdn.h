@@ -409,7 +409,11 @@ typedef struct gdn_rope {
  *   want_len, kv_len: device int32 [n_seqs].   kv_len_out: int32 [n_seqs], the
  *                     lengths after the call; may equal kv_len.
  *   block_table:      device int32 [n_seqs, max_pages], in place: entries of
- *                     held pages are read, of taken pages written.
+ *                     held pages are read, of taken pages written.  A page is
+ *                     held by one request alone: it goes back on the stack with
+ *                     its request, and users are not counted.  (Attention and
+ *                     read back may share pages of a prefix between rows: those
+ *                     tables are then not this call's.)
  *   free_pages:       device int32 [n_pages], a stack: the first *free_count
  *                     are free.   free_count, free_count_out: device int32 [1];
  *                     may be equal.
