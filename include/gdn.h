@@ -344,7 +344,8 @@ GDN_API gdn_status gdn_snapshot_copy(const void* ckpt_buf, int32_t n, int64_t by
  * is exact, so a stored value is off by at most half a step of its code plus,
  * per growth, half a step of the smaller scales before (together under one
  * int8 step; e4m3 codes only lose what falls below the subnormals).
- * code * scale is exact in bf16.
+ * code * scale is exact in bf16, but for values from 1.9375 * 2^127 on, which
+ * may be rounded up to 2^128, infinity there.
  *
  *   num_kv_heads:  Hkv >= 1.      head_dim: d, one of 64, 128, 256.
  *   page:          tokens per page, one of 16, 32, 64, 128.
@@ -492,9 +493,12 @@ GDN_API gdn_status gdn_cache_gather(const gdn_cache* cache, int32_t n_tokens, co
  * Rows of out behind the last prompt are not written.
  * Arithmetic: products of bf16 queries and the codes (exact in bf16) sum in
  * fp32 on the matrix cores; the softmax runs in fp32 with a running maximum;
- * its probabilities times the values' scale are rounded to bf16 once.
- * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_UNSUPPORTED, GDN_ERR_SEQLENS,
- * GDN_ERR_HIP. */
+ * its probabilities times the values' scale are rounded to bf16 once.  Pages of
+ * any scales may meet in a row, and their sums stay numbers; a key's term is
+ * lost where its probability, or that times its scale, falls below fp32.  A row
+ * whose scores are all -infinity (infinite queries) is 0.
+ * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE (also for sizes that no launch holds, 2^32
+ * threads), GDN_ERR_UNSUPPORTED, GDN_ERR_SEQLENS, GDN_ERR_HIP. */
 GDN_API gdn_status gdn_attn_packed(const gdn_cache* cache, int32_t num_q_heads, float scale,
                                    const int32_t* cu_seqlens, const int32_t* cu_seqlens_host,
                                    int32_t n_seqs, int32_t n_tokens, const int32_t* kv_len,
@@ -512,7 +516,10 @@ GDN_API gdn_status gdn_attn_packed(const gdn_cache* cache, int32_t num_q_heads, 
  *                   q or out; its contents mean nothing before or after the
  *                   call, and calls that may run at the same time need one each.
  * How a request's keys are split depends on its own length alone.
- * Errors: as gdn_attn_packed; GDN_ERR_CAPACITY (workspace too small). */
+ * Errors: as gdn_attn_packed; GDN_ERR_CAPACITY (workspace too small);
+ * GDN_ERR_SHAPE also for more than 65,535 requests, for max_kv_len over 65,535
+ * splits (of 1,024 keys; heads of 256: 1,536), and for more than 65,535 blocks
+ * of 16 rows (n_tok * Hq / Hkv of them a kv head) over the kv heads. */
 GDN_API gdn_status gdn_attn_decode(const gdn_cache* cache, int32_t num_q_heads, float scale,
                                    int32_t batch, int32_t n_tok, const int32_t* kv_len,
                                    const int32_t* block_table, int32_t max_pages, int32_t max_kv_len,

@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 import torch
 
-from cache_util import DEV, bf, f64, filled
+import gated_deltanet_prefill_varlen_amd as gdn
+from cache_util import DEV, DevCache, bf, f64, filled, i32, i64
 from oracle import cache_oracle as C
 from packed_util import few_rows, many_rows_call, packed_call
 from test_gpu_cache import check_rows, decode_call, oracle_rows
@@ -110,3 +111,22 @@ def test_keys_whose_scale_times_the_calls_passes_fp32(d, code):
         want = oracle_rows(f64(q), rows, [L], [L], scale)
         check_rows(many_rows_call(dev, [L], [L], table, q, scale), want, d, "packed")
         check_rows(decode_call(dev, 1, [L], table, q[:1], scale=scale), want[-1:], d, "decode")
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_the_largest_values_read_back_as_rounded(code):
+    """bf16's last values round up to 2^128, which it holds as infinity; those
+    below 1.9375 * 2^127 read back as numbers."""
+    top = np.array([255.0, 254.0, 252.0, 249.0, 248.0, 247.0, 240.0, 130.0, 1.0] + [0.0] * 7) * 2.0 ** 120
+    for x in (top, top[4:], top[5:]):                  # the largest sets the page's scale
+        rows = np.zeros((16, 1, 64))
+        rows[:, 0, :len(x)] = x
+        ref, dev = C.PagedCache(1, 1, 16, 64, code), DevCache(1, 1, 16, 64, code)
+        t, slots = bf(rows).to(DEV), list(range(16))
+        gdn.gdn_rope_append(gdn.make_rope([]), dev.handle, i32([0, 16]), [0, 16], None, t, -t, None, i64(slots), None)
+        ref.append([0, 16], slots, f64(t), f64(-t))
+        k, v = torch.empty_like(t), torch.empty_like(t)
+        gdn.gdn_cache_gather(dev.handle, i64(slots), k, v)
+        for got, want in zip((k, v), ref.read(slots)):
+            np.testing.assert_array_equal(f64(got), np.where(np.abs(want) >= 2.0 ** 128, np.copysign(np.inf, want), want))
+            assert np.all(np.isfinite(f64(got)[np.abs(f64(t)) < 1.9375 * 2.0 ** 127]))
