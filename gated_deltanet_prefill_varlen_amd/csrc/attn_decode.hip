@@ -15,10 +15,14 @@
 // probabilities go from one product into the next without leaving their lane.
 //
 // Measured: 32 requests of 17 to 8,192 keys, 8 kv heads of 128, e4m3: 64 us,
-// 4.1 TB/s of codes (a plain sum reads 4.0 TB/s); 16 of 4,096 to 32,768 keys with
-// 4 tokens each, 2 kv heads of 256, int8: 104 us, 2.9 TB/s.  There 32 rows of
-// sums leave one wave a SIMD, whose conversions (45 % of its cycles) do not
-// overlap its waits.
+// 4.1 TB/s of codes (a large copy moves 4.9 TB/s); 16 of 4,096 to 32,768 keys
+// with 4 tokens each, 2 kv heads of 256, int8: 104 us, 2.9 TB/s.  There 32 rows
+// of sums leave one wave a SIMD, whose conversions (45 % of its cycles) do not
+// overlap its waits; partial sums of up to 22 splits are written and read again,
+// 9 us of it in the join's own launch.  Workgroups of splits that a request does
+// not have leave once they know its length: a bound of 4 times the lengths costs
+// nothing measurable, one of 16 times 22 us of the 55 (the first batch) and 9 of
+// the 103 (the second).
 //
 // Keys are split over workgroups in runs of fixed length (split_keys), the
 // four waves of a workgroup take tiles in turn, and partial results
@@ -36,8 +40,16 @@ constexpr int kWaves = 4;
 
 // Keys per workgroup: by the head size alone, so that how a request's keys are
 // split never depends on its batch.  Fewer make more partial sums to write and
-// join, more leave the last workgroups to run alone (16 requests of 4,096 to
-// 32,768 keys, 2 kv heads of 256: 1,024 keys 120 us, 1,536 105, 2,048 120).
+// join, more leave the last workgroups to run alone, or a short request to few
+// workgroups: no length is best for all.  Measured, 2 kv heads of 256 (512, 768,
+// 1,024, 1,536, 2,048 keys, in us):
+//   16 requests of 4,096 to 32,768 keys, 4 tokens  138  130  118  102  119
+//   the same, 1 token                               84   77   79   64   78
+//   32 requests of 17 to 8,192                      42   35   39   48   45
+//   one of 8,192                                    23   26   29   37   44
+// 4 kv heads of 256: the long batch of 1 token 150, 134, 130, 129 and 146, the
+// batch to 8,192 60, 58, 62, 56 and 63.  8 of 128 (512, 768, 1,024, 2,048): 149,
+// 130, 131 and 127, 60, 58, 55 and 60, one of 8,192 keys 17, 18, 19 and 26.
 __host__ __device__ constexpr int split_keys(int dim) { return dim == 256 ? 1536 : 1024; }
 __host__ __device__ inline int n_splits(int L, int dim) { return L <= 0 ? 1 : (L - 1) / split_keys(dim) + 1; }
 

@@ -1,5 +1,5 @@
 // Causal attention of packed prompts over the paged 8-bit cache: many rows per
-// prompt, so the matrix cores bound it.  (Prompts of few rows are left to the
+// prompt, work for the matrix cores.  (Prompts of few rows are left to the
 // kernel of the decoding requests.)
 //
 // The rows of a prompt that share a kv head (tokens x Hq / Hkv heads) are
@@ -17,11 +17,13 @@
 // then one 16-key piece of a page: its scales are the same for every lane.
 //
 // Measured: 4 prompts of 8,192 tokens, 16 query heads on 4 kv heads of 128,
-// int8: 1.12 ms, 980 TFLOP/s (a bf16 library product of 8,192^3 reaches 1,270).
-// The reads of the operands from LDS bound it: a workgroup reads 256 KB for 64
-// keys, 1.8 of the 2.1 us at the 142 bytes a ns that a CU's LDS gives.  Heads of
-// 64: 540 TFLOP/s, bound by the exponentials; heads of 256: 850 (int8) and 700
-// (e4m3, whose NaN handling leaves a few registers to spill).
+// int8: 1.13 ms, 976 TFLOP/s (a bf16 library product of 8,192^3 reaches 1,270 to
+// 1,390).  Prompts of 4,096: heads of 64 570 TFLOP/s, of 128 785, of 256 825
+// (int8) and 770 (e4m3); both spill a few registers.  No unit is near its
+// limit there: of a SIMD's or CU's cycles, matrix cores are busy in 27, 41 and
+// 40 % (heads of 64, 128, 256, int8), vector units in 52, 48 and 33 %, LDS in
+// 26, 35 and 32 %.  Half steps (below) end at barriers, where each side waits
+// for the slower one.
 //
 // LDS rows are permuted in 16-byte chunks, so that the reads of sixteen lanes
 // at one chunk of sixteen rows touch all banks.

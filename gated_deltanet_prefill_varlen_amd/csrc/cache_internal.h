@@ -67,11 +67,16 @@ struct GatherArgs {
 
 // A packed prompt with no more rows than this (tokens x Hq / Hkv) is computed
 // as a decoding request is, four waves sharing its keys.  The rule goes by the
-// prompt's own rows, so its bits do not depend on the pack.  Measured, heads of
-// 128 (of 256), with the rule and without it: a prompt of 16 rows on 4,096 keys
-// 39 and 109 us (62 and 265), 8 of 128 rows 64 and 116 us (160 and 292), 32 of
-// 64 rows on 3,000 68 and 112 us (226 and 267), 64 of 128 rows on 2,000, which
-// fill the card, 170 and 156 us (594 and 378).
+// prompt's own rows, so its bits do not depend on the pack.  Measured with it
+// and without it, 4 kv heads of 64, 128 and 256, int8, in us:
+//   1 prompt of 16 rows on 4,096 keys    32 and  92   40 and 115   72 and 237
+//   8 of 64 rows on 3,000                36 and  71   47 and  88   65 and 180
+//   64 of 64 rows on 2,000               37 and  65   54 and  82  154 and 158
+//   8 of 128 rows on 3,000               38 and  71   49 and  90   70 and 184 *
+//   64 of 128 rows on 2,000              62 and  66   98 and  86  295 and 169 *
+// (* with a limit of 128, which heads of 256 do not have.)  64 prompts fill the
+// card: there 128 rows of 128 cost a seventh more with the rule, against the
+// half that it saves where they are few.
 constexpr int few_rows(int dim) { return dim == 256 ? 64 : 128; }
 
 // 16-row tiles of a wave there, for `rows` rows of the longest of them (heads

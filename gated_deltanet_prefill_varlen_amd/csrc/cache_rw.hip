@@ -9,7 +9,9 @@
 // Measured: 32 prompts of 1,024 tokens (32 query heads, 8 kv heads of 128)
 // 160 us, HBM bound (0.74 GB, 4.6 TB/s); a decode step of 64 tokens 9.6 us,
 // the latency of the way from the prompts' offsets over slots and rows to the
-// scale and the codes.
+// scale and the codes.  Pages of 128 tokens with heads of 256 (keys and values
+// of 256 registers, two waves a SIMD): 16 prompts of 500 to 1,500 tokens, 4 kv
+// heads, with their read 138 us, 3.3 TB/s, where heads of 128 reach 4.4.
 #include <algorithm>
 
 #include "cache_device.h"
