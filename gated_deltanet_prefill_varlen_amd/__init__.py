@@ -1,6 +1,7 @@
 """Python binding of libgdn (packed gated-delta-rule prefill, checkpoints,
-decode, short conv and checkpoint copy, and the paged 8-bit key/value cache of
-the softmax-attention layers with the attention over it, on MI355X / gfx950).
+decode, short conv and checkpoint copy; the paged 8-bit key/value cache of the
+softmax-attention layers with the attention over it; the scan and decode step of
+state space layers; and the norm around these layers, on MI355X / gfx950).
 
 Argument marshalling only: every function here passes torch tensor data
 pointers, sizes and the current HIP stream to the C entry point of the same
@@ -29,17 +30,22 @@ __all__ = [
     "gdn_cache", "gdn_rope", "make_cache", "make_rope", "GDN_E4M3", "GDN_I8",
     "gdn_plan_pages", "gdn_rope_append", "gdn_cache_gather", "gdn_attn_packed", "gdn_attn_decode",
     "gdn_attn_decode_workspace",
+    "gdn_ssm_shape", "gdn_norm_shape", "make_ssm", "make_norm", "gdn_ssm_prefill_workspace",
+    "gdn_ssm_prefill_packed", "gdn_ssm_decode", "gdn_rms_norm",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgdn.so")
 GDN_BF16, GDN_F32, GDN_E4M3, GDN_I8 = 0, 1, 2, 3
 GDN_QK_L2NORM = 1
+GDN_SSM_SOFTPLUS = 1
+GDN_NORM_GATE_FIRST = 1
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_UNSUPPORTED",
           4: "GDN_ERR_SEQLENS", 5: "GDN_ERR_CKPT", 6: "GDN_ERR_CAPACITY", 7: "GDN_ERR_HIP"}
 EXPORTED = ("gdn_status_string", "gdn_plan_checkpoints", "gdn_conv1d_silu_packed",
             "gdn_prefill_packed", "gdn_prefill_conv_packed", "gdn_decode_step",
             "gdn_decode_tokens", "gdn_snapshot_copy", "gdn_plan_pages", "gdn_rope_append",
-            "gdn_cache_gather", "gdn_attn_packed", "gdn_attn_decode", "gdn_attn_decode_workspace")
+            "gdn_cache_gather", "gdn_attn_packed", "gdn_attn_decode", "gdn_attn_decode_workspace",
+            "gdn_ssm_prefill_workspace", "gdn_ssm_prefill_packed", "gdn_ssm_decode", "gdn_rms_norm")
 
 
 class GdnError(RuntimeError):
@@ -81,6 +87,35 @@ class gdn_rope(ctypes.Structure):
         ("rot_dim", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("adjacent", ctypes.c_int32),
         ("scale", ctypes.c_float), ("freq", ctypes.c_float * 128), ("axis", ctypes.c_uint8 * 128),
     ]
+
+
+class gdn_ssm_shape(ctypes.Structure):
+    _fields_ = [
+        ("num_heads", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("state_dim", ctypes.c_int32), ("flags", ctypes.c_uint32), ("dt_min", ctypes.c_float),
+        ("dt_max", ctypes.c_float), ("reserved", ctypes.c_int32),
+    ]
+
+
+def make_ssm(H: int, G: int, P: int, N: int, softplus: bool = True, dt_min: float = 0.0,
+             dt_max: float = float("inf")) -> gdn_ssm_shape:
+    """A state space layer of H heads of P channels, G groups of B and C, N state columns."""
+    return gdn_ssm_shape(H, G, P, N, GDN_SSM_SOFTPLUS if softplus else 0, dt_min, dt_max, 0)
+
+
+class gdn_norm_shape(ctypes.Structure):
+    _fields_ = [
+        ("dim", ctypes.c_int32), ("groups", ctypes.c_int32), ("weight_dim", ctypes.c_int32),
+        ("scale_block", ctypes.c_int32), ("flags", ctypes.c_uint32), ("eps", ctypes.c_float),
+        ("weight_offset", ctypes.c_float), ("reserved", ctypes.c_int32),
+    ]
+
+
+def make_norm(dim: int, groups: int = 1, eps: float = 1e-6, gate_first: bool = False, scale_block: int = 0,
+              weight_offset: float = 0.0, shared_weight: bool = False) -> gdn_norm_shape:
+    """A norm over dim channels in groups; shared_weight: one weight of dim / groups for all groups."""
+    return gdn_norm_shape(dim, groups, dim // groups if shared_weight and groups > 0 else dim, scale_block,
+                          GDN_NORM_GATE_FIRST if gate_first else 0, eps, weight_offset, 0)
 
 
 _CODES = {torch.float8_e4m3fn: GDN_E4M3, torch.int8: GDN_I8}
@@ -174,6 +209,16 @@ def load() -> ctypes.CDLL:
                                     _I64, _P, _P, _I64, _P]
     lib.gdn_attn_decode_workspace.restype = _I32
     lib.gdn_attn_decode_workspace.argtypes = [_P, _I32, _I32, _I32, _I32, _P]
+    lib.gdn_ssm_prefill_workspace.restype = _I32
+    lib.gdn_ssm_prefill_workspace.argtypes = [_P, _P, _I32, _I32, _P]
+    lib.gdn_ssm_prefill_packed.restype = _I32
+    lib.gdn_ssm_prefill_packed.argtypes = [_P, _P, _P, _I32, _I32, _P, _I64, _P, _P, _P, _P, _I32, _P, _I64, _P, _P, _P,
+                                           _P, _P, _P, _I32, _P, _P, _P, _P, _P, _I64, _P]
+    lib.gdn_ssm_decode.restype = _I32
+    lib.gdn_ssm_decode.argtypes = [_P, _I32, _I32, _P, _I64, _P, _P, _P, _I32, _P, _I64, _P, _P, _P, _P, _I64, _P, _P,
+                                   _P, _P, _P]
+    lib.gdn_rms_norm.restype = _I32
+    lib.gdn_rms_norm.argtypes = [_P, _I32, _I32, _P, _I64, _I32, _P, _I64, _P, _P, _I64, _P, _P, _I32, _P, _P, _P]
     _lib = lib
     return lib
 
@@ -520,3 +565,145 @@ def gdn_attn_decode(cache: gdn_cache, n_tok: int, kv_len, block_table, q, out,
         min(max_pages * cache.page, 2**31 - 1) if max_kv_len is None else max_kv_len, qp, qs,
         _buf(out, torch.bfloat16, dev, "out"), _buf(workspace, torch.uint8, dev, "workspace"),
         0 if workspace is None else workspace.numel(), st), "gdn_attn_decode")
+
+
+# ------------------------------------------------- state space layers, norm --
+
+_IO = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
+
+
+def _row_stride(t: torch.Tensor, rows: int, width: int, dev: int, what: str, dtype=None, exact: bool = False):
+    """Pointer and row stride of rows [>= rows, width] (exact: [rows, width])
+    with dense channels (columns of a wider row will do); 0 rows: no pointer."""
+    if t.get_device() != dev or (t.dtype not in _IO if dtype is None else t.dtype is not dtype):
+        _refuse(t, torch.bfloat16 if dtype is None else dtype, what)
+    if t.dim() != 2 or t.shape[1] != width or (t.shape[0] != rows if exact else t.shape[0] < rows):
+        raise ValueError(f"{what} must be [{rows}, {width}], got {tuple(t.shape)}")
+    st = t.stride()
+    if width > 1 and st[1] != 1:
+        raise ValueError(f"{what}: the channels of a row must be dense")
+    if t.shape[0] > 1 and st[0] < width:
+        raise ValueError(f"{what}: the rows overlap")
+    return (t.data_ptr() if rows else None), (st[0] if t.shape[0] > 1 else 0)
+
+
+def _sized(t, dtype, dev: int, shape, what: str) -> Optional[int]:
+    """Pointer of a dense tensor of one type and shape (None passes NULL)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {list(shape)}, got {tuple(t.shape)}")
+    return _buf(t, dtype, dev, what)
+
+
+def _ssm_dims(shape: gdn_ssm_shape):
+    return shape.num_heads, shape.head_dim, shape.state_dim, (shape.num_heads * shape.head_dim +
+                                                              2 * shape.num_groups * shape.state_dim)
+
+
+def _ssm_dt(dt: torch.Tensor, rows: int, H: int, dev: int):
+    p, st = _row_stride(dt, rows, H, dev, "dt")
+    return _IO[dt.dtype], p, st
+
+
+def gdn_ssm_prefill_workspace(shape: gdn_ssm_shape, cu_seqlens_host) -> int:
+    """Bytes of workspace of gdn_ssm_prefill_packed for a pack."""
+    cu_h = _host_i32(cu_seqlens_host)
+    n = ctypes.c_int64(0)
+    _check(load().gdn_ssm_prefill_workspace(ctypes.addressof(shape), cu_h.ctypes.data, len(cu_h) - 1, int(cu_h[-1]),
+                                            ctypes.byref(n)), "gdn_ssm_prefill_workspace")
+    return n.value
+
+
+def gdn_ssm_prefill_packed(shape: gdn_ssm_shape, cu_seqlens, cu_seqlens_host, x, dt, A, out, dt_bias=None, D=None,
+                           init_state=None, final_state=None, ckpt_positions=None, ckpt_positions_host=None,
+                           ckpt_buf=None, conv_weight=None, conv_bias=None, conv_state_in=None, conv_state_out=None,
+                           conv_ckpt=None, workspace=None, stream=None) -> None:
+    """The packed scan of a state space layer: x [T, conv_dim] bf16 (columns
+    [x | B | C], before the short convolution where conv_weight is given), dt
+    [T, H] raw steps in bf16 or fp32, both columns of a wider row if need be;
+    out [T, H, P] bf16.  workspace: a uint8 tensor of
+    gdn_ssm_prefill_workspace() bytes."""
+    dev, st = _where(stream)
+    f32, bf16 = torch.float32, torch.bfloat16
+    cu_h, ck_h = _host_i32(cu_seqlens_host), _host_i32(ckpt_positions_host)
+    n, T, k = len(cu_h) - 1, int(cu_h[-1]), 0 if ck_h is None else len(ck_h)
+    H, P, N, C = _ssm_dims(shape)
+    xp, xs = _row_stride(x, T, C, dev, "x", bf16)
+    dtt, dtp, dts = _ssm_dt(dt, T, H, dev)
+    if tuple(out.shape[1:]) != (H, P) or out.shape[0] < T:
+        raise ValueError("out must be [T, H, P]")
+    if cu_seqlens.numel() < n + 1 or (k and ckpt_positions is not None and ckpt_positions.numel() < k):
+        raise ValueError("cu_seqlens or ckpt_positions is shorter than its host mirror")
+    _check(load().gdn_ssm_prefill_packed(
+        ctypes.addressof(shape), _buf(cu_seqlens, torch.int32, dev, "cu_seqlens"), cu_h.ctypes.data, n, T, xp, xs,
+        _sized(conv_weight, f32, dev, (C, 4), "conv_weight"), _sized(conv_bias, f32, dev, (C,), "conv_bias"),
+        _sized(conv_state_in, bf16, dev, (n, 3, C), "conv_state_in"),
+        _sized(conv_state_out, bf16, dev, (n, 3, C), "conv_state_out"), dtt, dtp, dts,
+        _sized(A, f32, dev, (H,), "A"), _sized(dt_bias, f32, dev, (H,), "dt_bias"), _sized(D, f32, dev, (H,), "D"),
+        _sized(init_state, f32, dev, (n, H, P, N), "init_state"),
+        _buf(ckpt_positions, torch.int32, dev, "ckpt_positions"), _hp(ck_h), k,
+        _sized(conv_ckpt, bf16, dev, (k, 3, C), "conv_ckpt"), _buf(out, bf16, dev, "out"),
+        _sized(final_state, f32, dev, (n, H, P, N), "final_state"),
+        _sized(ckpt_buf, f32, dev, (k, H, P, N), "ckpt_buf"), _buf(workspace, torch.uint8, dev, "workspace"),
+        0 if workspace is None else workspace.numel(), st), "gdn_ssm_prefill_packed")
+
+
+def gdn_ssm_decode(shape: gdn_ssm_shape, n_tok: int, x, dt, A, state, out, dt_bias=None, D=None, conv_weight=None,
+                   conv_bias=None, conv_state=None, slot=None, slot_host=None, snapshots=None, stream=None) -> None:
+    """n_tok tokens per sequence (rows b * n_tok + i of x [batch * n_tok,
+    conv_dim] and dt [batch * n_tok, H]) in place on the pools state
+    [slots, H, P, N] and conv_state [slots, 3, conv_dim]."""
+    dev, st = _where(stream)
+    f32, bf16 = torch.float32, torch.bfloat16
+    H, P, N, C = _ssm_dims(shape)
+    rows, n_tok = x.shape[0], int(n_tok)
+    if n_tok < 1 or rows % n_tok != 0:
+        raise ValueError("x must have n_tok rows per sequence")
+    B, pool = rows // n_tok, state.shape[0]
+    sl_h = _host_i32(slot_host)
+    if slot is not None and (slot.numel() < B or (sl_h is not None and len(sl_h) < B)):
+        raise ValueError("slot is shorter than the batch")
+    xp, xs = _row_stride(x, rows, C, dev, "x", bf16, exact=True)
+    dtt, dtp, dts = _ssm_dt(dt, rows, H, dev)
+    _check(load().gdn_ssm_decode(
+        ctypes.addressof(shape), B, n_tok, xp, xs, _sized(conv_weight, f32, dev, (C, 4), "conv_weight"),
+        _sized(conv_bias, f32, dev, (C,), "conv_bias"), _sized(conv_state, bf16, dev, (pool, 3, C), "conv_state"),
+        dtt, dtp, dts, _sized(A, f32, dev, (H,), "A"), _sized(dt_bias, f32, dev, (H,), "dt_bias"),
+        _sized(D, f32, dev, (H,), "D"), _sized(state, f32, dev, (pool, H, P, N), "state"), pool,
+        _buf(slot, torch.int32, dev, "slot"), _hp(sl_h), _sized(out, bf16, dev, (rows, H, P), "out"),
+        _sized(snapshots, f32, dev, (B, n_tok, H, P, N), "snapshots"), st), "gdn_ssm_decode")
+
+
+def gdn_rms_norm(shape: gdn_norm_shape, x, weight=None, out=None, residual=None, residual_out=None, gate=None,
+                 codes=None, scales=None, stream=None) -> None:
+    """Root-mean-square norm of x [rows, dim] (bf16 or fp32), after the addition
+    of a residual (its sum to residual_out), gated by silu(gate); to out (x's
+    type) and / or to codes (float8_e4m3fn or int8) with fp32 scales [rows, 1]
+    or [rows, dim / scale_block]."""
+    dev, st = _where(stream)
+    rows, d = x.shape[0], shape.dim
+    xp, xs = _row_stride(x, rows, d, dev, "x", exact=True)
+    rp = rs = zp = zs = rop = ros = None
+    rt = ct = 0
+    if residual is not None:
+        rp, rs = _row_stride(residual, rows, d, dev, "residual", exact=True)
+        rt = _IO[residual.dtype]
+    if residual_out is not None:
+        if residual is None:
+            raise ValueError("residual_out needs a residual")
+        rop, ros = _row_stride(residual_out, rows, d, dev, "residual_out", residual.dtype, exact=True)
+        if ros != rs:
+            raise ValueError("residual_out must have residual's row stride")
+    if gate is not None:
+        zp, zs = _row_stride(gate, rows, d, dev, "gate", x.dtype, exact=True)
+    if codes is not None:
+        if codes.dtype not in _CODES:
+            raise TypeError("codes must be float8_e4m3fn or int8")
+        ct = _CODES[codes.dtype]
+    n_sc = d // shape.scale_block if shape.scale_block > 0 else 1
+    _check(load().gdn_rms_norm(
+        ctypes.addressof(shape), rows, _IO[x.dtype], xp, xs, rt, rp, rs or 0, rop, zp, zs or 0,
+        _sized(weight, torch.float32, dev, (shape.weight_dim,), "weight"), _sized(out, x.dtype, dev, (rows, d), "out"),
+        ct, None if codes is None else _sized(codes, codes.dtype, dev, (rows, d), "codes"),
+        _sized(scales, torch.float32, dev, (rows, n_sc), "scales"), st), "gdn_rms_norm")

@@ -10,6 +10,7 @@
 #include "cache_internal.h"
 #include "gdn.h"
 #include "gdn_internal.h"
+#include "ssm_internal.h"
 
 namespace {
 
@@ -117,6 +118,12 @@ gdn_status bf16_stride(int64_t given, int64_t dense, int64_t* out) {
   return GDN_OK;
 }
 
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const char* x = static_cast<const char*>(a);
+  const char* y = static_cast<const char*>(b);
+  return x && y && x < y + b_bytes && y < x + a_bytes;
+}
+
 // A launch holds fewer than 2^32 threads along its first axis.
 bool fits_grid(int64_t groups, int64_t threads) { return groups * threads <= UINT32_MAX; }
 
@@ -145,6 +152,42 @@ gdn_status check_attn(const gdn_cache* cache, int32_t Hq, float scale, int32_t n
   a->kv_len = kv_len; a->table = table; a->max_pages = max_pages;
   a->max_kv = max_pages << a->c.page_shift;
   a->q = static_cast<const uint16_t*>(q); a->out = static_cast<uint16_t*>(const_cast<void*>(out));
+  return GDN_OK;
+}
+
+// Checks of a state space layer and what it reads; the kernels' form of it.
+gdn_status check_ssm(const gdn_ssm_shape* s, gdn::SsmLayer* l) {
+  if (!s) return GDN_ERR_NULL;
+  if (s->num_heads < 1 || s->num_groups < 1) return GDN_ERR_SHAPE;
+  if (s->num_heads % s->num_groups != 0) return GDN_ERR_UNSUPPORTED;
+  if (!supported_dim(s->head_dim) || !supported_dim(s->state_dim)) return GDN_ERR_UNSUPPORTED;
+  if (s->flags & ~GDN_SSM_SOFTPLUS) return GDN_ERR_UNSUPPORTED;
+  if (!(s->dt_min <= s->dt_max)) return GDN_ERR_SHAPE;   // also NaN
+  const int64_t dim = (int64_t)s->num_heads * s->head_dim + 2 * (int64_t)s->num_groups * s->state_dim;
+  if (s->num_heads > 65535 || dim >= (1 << 23)) return GDN_ERR_SHAPE;
+  l->H = s->num_heads; l->G = s->num_groups; l->P = s->head_dim; l->N = s->state_dim; l->conv_dim = (int32_t)dim;
+  l->softplus = (s->flags & GDN_SSM_SOFTPLUS) != 0;
+  l->dt_min = s->dt_min; l->dt_max = s->dt_max;
+  return GDN_OK;
+}
+
+// The strides of a state space call's rows and its constants.
+gdn_status check_ssm_rows(int64_t rows, int64_t x_given, const void* x, int32_t dt_dtype, int64_t dt_given,
+                          const void* dt, const float* A, const float* dt_bias, const float* D, const float* conv_w,
+                          const float* conv_b, const void* out, gdn::SsmLayer* l, int64_t* xs, int64_t* dts) {
+  if (dt_dtype != GDN_BF16 && dt_dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
+  if (conv_b && !conv_w) return GDN_ERR_NULL;
+  gdn_status st = bf16_stride(x_given, l->conv_dim, xs);
+  if (st != GDN_OK) return st;
+  *dts = dt_given == 0 ? l->H : dt_given;
+  if (*dts < l->H || *dts > INT32_MAX || *xs >= (1 << 23)) return GDN_ERR_SHAPE;
+  if ((x && !aligned16(x)) || (conv_w && !aligned16(conv_w)) || (conv_b && !aligned16(conv_b)) || (out && !aligned16(out))) return GDN_ERR_SHAPE;
+  if (rows > 0) {
+    if (!x || !dt || !A || !out) return GDN_ERR_NULL;
+    if (overlap(x, ((rows - 1) * *xs + l->conv_dim) * 2, out, rows * l->H * l->P * 2)) return GDN_ERR_SHAPE;
+  }
+  l->dt_f32 = dt_dtype == GDN_F32;
+  l->A = A; l->dt_bias = dt_bias; l->D = D; l->conv_w = conv_w; l->conv_bias = conv_b;
   return GDN_OK;
 }
 
@@ -604,6 +647,144 @@ gdn_status gdn_attn_decode(const gdn_cache* cache, int32_t num_q_heads, float sc
   if (batch > 65535 || a.c.Hkv * (((int64_t)n_tok * (num_q_heads / a.c.Hkv) + 15) / 16) > 65535) return GDN_ERR_SHAPE;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return finish_launch(gdn::launch_attn_decode(a, workspace, s), s);
+}
+
+gdn_status gdn_ssm_prefill_workspace(const gdn_ssm_shape* shape, const int32_t* cu_seqlens_host, int32_t n_seqs,
+                                     int32_t n_tokens, int64_t* bytes) {
+  gdn::SsmLayer l{};
+  if (!bytes) return GDN_ERR_NULL;
+  gdn_status st = check_ssm(shape, &l);
+  if (st != GDN_OK) return st;
+  if ((st = check_seqlens(cu_seqlens_host, n_seqs, n_tokens)) != GDN_OK) return st;
+  *bytes = gdn::ssm_scan_bytes(l, n_seqs, cu_seqlens_host);
+  return GDN_OK;
+}
+
+gdn_status gdn_ssm_prefill_packed(
+    const gdn_ssm_shape* shape, const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, int32_t n_seqs,
+    int32_t n_tokens, const void* x, int64_t x_tok_stride, const float* conv_weight, const float* conv_bias,
+    const void* conv_state_in, void* conv_state_out, int32_t dt_dtype, const void* dt, int64_t dt_tok_stride,
+    const float* A, const float* dt_bias, const float* D, const float* init_state, const int32_t* ckpt_positions,
+    const int32_t* ckpt_positions_host, int32_t n_ckpt, void* conv_ckpt, void* out, float* final_state,
+    float* ckpt_buf, void* workspace, int64_t workspace_bytes, void* stream) {
+  gdn::SsmScanArgs a{};
+  gdn_status st = check_ssm(shape, &a.l);
+  if (st != GDN_OK) return st;
+  if ((st = check_seqlens(cu_seqlens_host, n_seqs, n_tokens)) != GDN_OK) return st;
+  if (n_seqs > 0 && !cu_seqlens) return GDN_ERR_NULL;
+  if (n_ckpt < 0) return GDN_ERR_SHAPE;
+  if (n_ckpt > 0 && (!ckpt_positions || !ckpt_positions_host || !ckpt_buf)) return GDN_ERR_NULL;
+  if ((st = check_ckpts(cu_seqlens_host, n_seqs, ckpt_positions_host, n_ckpt)) != GDN_OK) return st;
+  if (!conv_weight && (conv_state_in || conv_state_out || conv_ckpt)) return GDN_ERR_NULL;
+  st = check_ssm_rows(n_tokens, x_tok_stride, x, dt_dtype, dt_tok_stride, dt, A, dt_bias, D, conv_weight, conv_bias,
+                      out, &a.l, &a.x_stride, &a.dt_stride);
+  if (st != GDN_OK) return st;
+  const void* ptrs[] = {conv_state_in, conv_state_out, conv_ckpt, init_state, final_state, ckpt_buf, workspace};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return GDN_ERR_SHAPE;
+  const int64_t windows = (int64_t)n_seqs * 3 * a.l.conv_dim * 2;
+  if (conv_state_in != conv_state_out && overlap(conv_state_in, windows, conv_state_out, windows)) return GDN_ERR_SHAPE;
+  const int64_t need = gdn::ssm_scan_bytes(a.l, n_seqs, cu_seqlens_host);
+  if (need > 0 && !workspace) return GDN_ERR_NULL;
+  if (workspace_bytes < need) return GDN_ERR_CAPACITY;
+  if (n_tokens > 0 && (overlap(workspace, need, x, ((n_tokens - 1) * a.x_stride + a.l.conv_dim) * 2) ||
+                       overlap(workspace, need, out, (int64_t)n_tokens * a.l.H * a.l.P * 2))) return GDN_ERR_SHAPE;
+  if (n_seqs == 0) return GDN_OK;
+  a.cu = cu_seqlens; a.n_seqs = n_seqs; a.n_tokens = n_tokens;
+  a.x = static_cast<const uint16_t*>(x); a.dt = dt;
+  a.init = init_state; a.final_state = final_state;
+  a.ckpt = ckpt_positions; a.n_ckpt = n_ckpt; a.ckpt_buf = ckpt_buf;
+  a.out = static_cast<uint16_t*>(out);
+  a.conv_in = static_cast<const uint16_t*>(conv_state_in);
+  a.conv_out = static_cast<uint16_t*>(conv_state_out);
+  a.conv_ckpt = static_cast<uint16_t*>(conv_ckpt);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  return finish_launch(gdn::launch_ssm_scan(a, workspace, s), s);
+}
+
+gdn_status gdn_ssm_decode(const gdn_ssm_shape* shape, int32_t batch, int32_t n_tok, const void* x,
+                          int64_t x_tok_stride, const float* conv_weight, const float* conv_bias, void* conv_state,
+                          int32_t dt_dtype, const void* dt, int64_t dt_tok_stride, const float* A,
+                          const float* dt_bias, const float* D, float* state, int64_t pool_slots,
+                          const int32_t* slot, const int32_t* slot_host, void* out, float* snapshots, void* stream) {
+  gdn::SsmDecodeArgs a{};
+  gdn_status st = check_ssm(shape, &a.l);
+  if (st != GDN_OK) return st;
+  if (batch < 0 || pool_slots < 0 || n_tok < 1) return GDN_ERR_SHAPE;
+  if ((int64_t)batch * n_tok > INT32_MAX) return GDN_ERR_SHAPE;
+  if (!conv_weight != !conv_state) return GDN_ERR_NULL;   // the conv needs both
+  st = check_ssm_rows((int64_t)batch * n_tok, x_tok_stride, x, dt_dtype, dt_tok_stride, dt, A, dt_bias, D, conv_weight,
+                      conv_bias, out, &a.l, &a.x_stride, &a.dt_stride);
+  if (st != GDN_OK) return st;
+  const void* ptrs[] = {state, snapshots, conv_state};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return GDN_ERR_SHAPE;
+  if (batch == 0) return GDN_OK;
+  if (!state) return GDN_ERR_NULL;
+  if (slot) {
+    if (!slot_host) return GDN_ERR_NULL;
+    if ((st = check_slots(slot_host, batch, pool_slots)) != GDN_OK) return st;
+  } else if (batch > pool_slots) {
+    return GDN_ERR_CAPACITY;
+  }
+  a.batch = batch; a.n_tok = n_tok;
+  a.x = static_cast<const uint16_t*>(x); a.dt = dt; a.state = state; a.slot = slot;
+  a.out = static_cast<uint16_t*>(out); a.snap = snapshots;
+  a.conv_state = static_cast<uint16_t*>(conv_state);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  return finish_launch(gdn::launch_ssm_decode(a, s), s);
+}
+
+gdn_status gdn_rms_norm(const gdn_norm_shape* shape, int32_t n_rows, int32_t x_dtype, const void* x,
+                        int64_t x_row_stride, int32_t res_dtype, const void* residual, int64_t res_row_stride,
+                        void* residual_out, const void* gate, int64_t gate_row_stride, const float* weight, void* out,
+                        int32_t code_dtype, void* codes, float* scales, void* stream) {
+  if (!shape) return GDN_ERR_NULL;
+  const int64_t d = shape->dim, rows = n_rows;
+  if (d < 1 || shape->groups < 1 || d % shape->groups != 0 || n_rows < 0) return GDN_ERR_SHAPE;
+  if (!(shape->eps >= 0.f) || !std::isfinite(shape->eps) || !std::isfinite(shape->weight_offset)) return GDN_ERR_SHAPE;
+  const int64_t gd = d / shape->groups;
+  if (d > 32768 || (shape->flags & ~GDN_NORM_GATE_FIRST)) return GDN_ERR_UNSUPPORTED;
+  if (shape->groups > 1 && gd % 512 != 0 && (gd < 8 || gd > 512 || (gd & (gd - 1)) != 0)) return GDN_ERR_UNSUPPORTED;
+  if (shape->weight_dim != d && shape->weight_dim != gd) return GDN_ERR_SHAPE;
+  if (shape->scale_block != 0 && (shape->scale_block != 128 || d % 128 != 0)) return GDN_ERR_UNSUPPORTED;
+  if (x_dtype != GDN_BF16 && x_dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
+  if (residual && res_dtype != GDN_BF16 && res_dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
+  if (codes && code_dtype != GDN_E4M3 && code_dtype != GDN_I8) return GDN_ERR_UNSUPPORTED;
+  const int64_t xs = x_row_stride == 0 ? d : x_row_stride, rs = res_row_stride == 0 ? d : res_row_stride;
+  const int64_t zs = gate_row_stride == 0 ? d : gate_row_stride;
+  if (xs < d || rs < d || zs < d || xs > INT32_MAX || rs > INT32_MAX || zs > INT32_MAX) return GDN_ERR_SHAPE;
+  if (n_rows == 0) return GDN_OK;
+  if (!x || !codes != !scales || (residual_out && !residual)) return GDN_ERR_NULL;
+  if (!out && !codes && !residual_out) return GDN_ERR_NULL;
+  if ((shape->flags & GDN_NORM_GATE_FIRST) && !gate) return GDN_ERR_NULL;
+  const int64_t xb = x_dtype == GDN_BF16 ? 2 : 4, rb = res_dtype == GDN_BF16 ? 2 : 4;
+  const uintptr_t odd = (uintptr_t)x | (uintptr_t)gate | (uintptr_t)out, rodd = (uintptr_t)residual | (uintptr_t)residual_out;
+  if (odd % xb != 0 || rodd % rb != 0 || ((uintptr_t)weight | (uintptr_t)scales) % 4 != 0) return GDN_ERR_SHAPE;
+  // what is written overlaps nothing, but residual_out may be residual and out a dense x
+  struct Span { const void* p; int64_t bytes; };
+  const int64_t scale_n = shape->scale_block ? d / 128 : 1;
+  const Span in[] = {{x, ((rows - 1) * xs + d) * xb}, {residual, ((rows - 1) * rs + d) * rb},
+                     {gate, ((rows - 1) * zs + d) * xb}, {weight, shape->weight_dim * 4}};
+  const Span to[] = {{out, rows * d * xb}, {residual_out, ((rows - 1) * rs + d) * rb}, {codes, rows * d}, {scales, rows * scale_n * 4}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 4; ++j) {
+      if ((i == 0 && j == 0 && out == x && xs == d) || (i == 1 && j == 1 && residual_out == residual)) continue;
+      if (overlap(to[i].p, to[i].bytes, in[j].p, in[j].bytes)) return GDN_ERR_SHAPE;
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(to[i].p, to[i].bytes, to[j].p, to[j].bytes)) return GDN_ERR_SHAPE;
+  }
+  if (!fits_grid(rows, d <= 512 ? 64 : d <= 8192 ? 256 : 1024)) return GDN_ERR_SHAPE;
+  gdn::NormArgs a{};
+  a.dim = (int32_t)d; a.groups = shape->groups; a.group_dim = (int32_t)gd; a.scale_block = shape->scale_block;
+  a.n_rows = n_rows; a.x_f32 = x_dtype == GDN_F32; a.res_f32 = res_dtype == GDN_F32;
+  a.gate_first = (shape->flags & GDN_NORM_GATE_FIRST) != 0; a.codes_i8 = code_dtype == GDN_I8;
+  a.eps = shape->eps; a.weight_offset = shape->weight_offset; a.weight_dim = shape->weight_dim;
+  a.x = x; a.res = residual; a.gate = gate; a.x_stride = xs; a.res_stride = rs; a.gate_stride = zs;
+  a.w = weight; a.out = out; a.res_out = residual_out; a.codes = static_cast<uint8_t*>(codes); a.scales = scales;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  return finish_launch(gdn::launch_rms_norm(a, s), s);
 }
 
 }  // extern "C"

@@ -530,6 +530,148 @@ GDN_API gdn_status gdn_attn_decode(const gdn_cache* cache, int32_t num_q_heads, 
 GDN_API gdn_status gdn_attn_decode_workspace(const gdn_cache* cache, int32_t num_q_heads, int32_t batch,
                                              int32_t n_tok, int32_t max_kv_len, int64_t* bytes);
 
+/* ------------------------------------------------- state space layers --
+ * The selective state space layers of hybrid models: per head h (group
+ * j = h / (H / G)) and token t, from S = the initial state (zeros when none),
+ *     dt_t = clamp(softplus(raw_t + dt_bias[h]), dt_min, dt_max)
+ *     S   <- exp(A[h] dt_t) S + dt_t x_t B_t^T
+ *     y_t  = S C_t + D[h] x_t
+ * with S [P, N], x_t the P channels of the head, B_t and C_t the N channels of
+ * its group (Dao & Gu, "Transformers are SSMs", ICML 2024).  x, B and C are the
+ * columns [x | B | C] of one row of conv_dim = H P + 2 G N channels, which the
+ * calls pass through the layer's short convolution first,
+ *     u_t = silu(bias + sum_{k=0..3} w[k] raw_{t-3+k}),
+ * never reading across a prompt's start, where the prompt's own window of
+ * three inputs (or zeros) stands.  The convolution's result is not rounded:
+ * states carry fp32's precision from the bf16 inputs on.
+ *
+ *   num_heads, num_groups: H and G, H a multiple of G.
+ *   head_dim, state_dim:   P and N, each one of 32, 64, 128.
+ *   flags:                 GDN_SSM_SOFTPLUS (without it dt_t is the clamped
+ *                          raw_t + dt_bias).
+ *   dt_min, dt_max:        0 and infinity for no clamp.
+ * A is below 0 in a trained layer; steps of A dt below -138 (2^-200) count as
+ * that. */
+#define GDN_SSM_SOFTPLUS 1u
+typedef struct gdn_ssm_shape {
+  int32_t num_heads;
+  int32_t num_groups;
+  int32_t head_dim;
+  int32_t state_dim;
+  uint32_t flags;
+  float dt_min;
+  float dt_max;
+  int32_t reserved;
+} gdn_ssm_shape;
+
+/* Bytes of workspace of gdn_ssm_prefill_packed for a pack. */
+GDN_API gdn_status gdn_ssm_prefill_workspace(const gdn_ssm_shape* shape, const int32_t* cu_seqlens_host,
+                                             int32_t n_seqs, int32_t n_tokens, int64_t* bytes);
+
+/* Packed scan with the short convolution: outputs, the state and the
+ * convolution's window at every checkpoint, final states and windows.
+ *   cu_seqlens(_host), ckpt_positions(_host), n_ckpt, init_state, final_state,
+ *   ckpt_buf:         as in gdn_prefill_packed, states [.., H, P, N] fp32.
+ *   x:                device bf16 [n_tokens, conv_dim], token stride
+ *                     x_tok_stride (0 = conv_dim; a multiple of 8), 16-byte
+ *                     aligned: columns of a wider projected row will do.
+ *   conv_weight:      device fp32 [conv_dim, 4], tap 3 on the current token, or
+ *                     NULL: the rows are convolved already, and conv_bias and
+ *                     the windows are NULL too.
+ *   conv_bias:        device fp32 [conv_dim] or NULL.
+ *   conv_state_in/out, conv_ckpt: as in gdn_prefill_conv_packed (out may equal
+ *                     in; windows bf16 [.., 3, conv_dim], oldest first).
+ *   dt_dtype, dt:     GDN_BF16 or GDN_F32; device [n_tokens, H], token stride
+ *                     dt_tok_stride (0 = H).
+ *   A, dt_bias, D:    device fp32 [H]; dt_bias and D may be NULL (0).
+ *   out:              device bf16 [n_tokens, H, P]; must not overlap x.
+ *   workspace:        device memory, 16-byte aligned, of at least
+ *                     gdn_ssm_prefill_workspace bytes; may be NULL where that
+ *                     is 0.  Its contents need no preparation and mean nothing
+ *                     afterwards; calls that may run at the same time need one
+ *                     each.
+ * A prompt's bits do not depend on the pack.  A prompt continued from a
+ * checkpoint agrees with the unbroken one to fp32's rounding.
+ * Errors: as gdn_prefill_packed; GDN_ERR_CAPACITY (workspace too short). */
+GDN_API gdn_status gdn_ssm_prefill_packed(
+    const gdn_ssm_shape* shape, const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, int32_t n_seqs,
+    int32_t n_tokens, const void* x, int64_t x_tok_stride, const float* conv_weight, const float* conv_bias,
+    const void* conv_state_in, void* conv_state_out, int32_t dt_dtype, const void* dt, int64_t dt_tok_stride,
+    const float* A, const float* dt_bias, const float* D, const float* init_state, const int32_t* ckpt_positions,
+    const int32_t* ckpt_positions_host, int32_t n_ckpt, void* conv_ckpt, void* out, float* final_state,
+    float* ckpt_buf, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* n_tok tokens for each of `batch` decoding sequences, in place on a pool of
+ * states and of convolution windows (as gdn_decode_tokens).
+ *   x, dt:       rows b * n_tok + i: token i of sequence b; otherwise as above.
+ *   state:       device fp32 [pool_slots, H, P, N]; the addressed slots end at
+ *                the state after the sequence's last token, others stay.
+ *   slot, slot_host, pool_slots: as in gdn_decode_step.
+ *   conv_weight, conv_bias: as above; with conv_weight, conv_state: device
+ *                bf16 [pool_slots, 3, conv_dim], which moves on by n_tok inputs.
+ *   out:         device bf16 [batch * n_tok, H, P].
+ *   snapshots:   device fp32 [batch, n_tok, H, P, N] or NULL.
+ * Errors: as gdn_decode_tokens. */
+GDN_API gdn_status gdn_ssm_decode(const gdn_ssm_shape* shape, int32_t batch, int32_t n_tok, const void* x,
+                                  int64_t x_tok_stride, const float* conv_weight, const float* conv_bias,
+                                  void* conv_state, int32_t dt_dtype, const void* dt, int64_t dt_tok_stride,
+                                  const float* A, const float* dt_bias, const float* D, float* state,
+                                  int64_t pool_slots, const int32_t* slot, const int32_t* slot_host, void* out,
+                                  float* snapshots, void* stream);
+
+/* Root-mean-square norm of rows, with the residual's addition, a gate and
+ * 8-bit codes: the norm ahead of a layer's projections, and the gated one that
+ * ends the linear-attention and state space layers.  Per row
+ *     r = x + residual
+ *     v = r silu(gate) with GDN_NORM_GATE_FIRST, else r
+ *     y = v / sqrt(mean over the group of v^2 + eps) * (weight + weight_offset)
+ *         * silu(gate) without GDN_NORM_GATE_FIRST
+ *   dim:           channels of a row, 1 to 32,768.
+ *   groups:        the mean is over dim / groups channels; more than one group:
+ *                  dim / groups a power of two from 8 to 512 or a multiple of
+ *                  512.
+ *   weight_dim:    dim, or dim / groups (the groups share their weights).
+ *   scale_block:   channels per scale of the codes: 0 = the whole row, or 128
+ *                  (dim a multiple of it).
+ * r is formed in fp32, and its fp32 value is normed; residual_out gets it
+ * rounded to the residual's type.  A row's mean square must lie inside fp32's
+ * range. */
+#define GDN_NORM_GATE_FIRST 1u
+typedef struct gdn_norm_shape {
+  int32_t dim;
+  int32_t groups;
+  int32_t weight_dim;
+  int32_t scale_block;
+  uint32_t flags;
+  float eps;
+  float weight_offset;
+  int32_t reserved;
+} gdn_norm_shape;
+
+/*   x_dtype:       GDN_BF16 or GDN_F32, of x, gate and out.
+ *   x, gate:       device [n_rows, dim], row strides in elements (0 = dim; no
+ *                  alignment beyond the element's); gate may be NULL.
+ *   res_dtype, residual, residual_out: GDN_BF16 or GDN_F32 rows of one stride;
+ *                  either may be NULL (residual_out needs residual); they may
+ *                  be the same.
+ *   weight:        device fp32 [weight_dim] or NULL (1, without the offset).
+ *   out:           device [n_rows, dim] dense, or NULL; may be x where x is
+ *                  dense.
+ *   code_dtype, codes, scales: GDN_E4M3 or GDN_I8 [n_rows, dim] with fp32
+ *                  scales [n_rows, 1 or dim / 128], or both NULL.  A scale is
+ *                  the block's largest finite |y| over 448 or 127 (at least
+ *                  2^-100), so that code * scale stands for y; codes are
+ *                  rounded to nearest, ties to even, infinities saturate, NaN
+ *                  is e4m3's NaN and 0 in int8.
+ * Other overlaps of outputs with inputs or each other are not allowed.
+ * Errors: GDN_ERR_NULL (also: nothing to write), GDN_ERR_SHAPE,
+ * GDN_ERR_UNSUPPORTED, GDN_ERR_HIP. */
+GDN_API gdn_status gdn_rms_norm(const gdn_norm_shape* shape, int32_t n_rows, int32_t x_dtype, const void* x,
+                                int64_t x_row_stride, int32_t res_dtype, const void* residual,
+                                int64_t res_row_stride, void* residual_out, const void* gate,
+                                int64_t gate_row_stride, const float* weight, void* out, int32_t code_dtype,
+                                void* codes, float* scales, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
