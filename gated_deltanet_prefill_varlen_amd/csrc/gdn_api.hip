@@ -164,7 +164,8 @@ gdn_status check_ssm(const gdn_ssm_shape* s, gdn::SsmLayer* l) {
   if (s->flags & ~GDN_SSM_SOFTPLUS) return GDN_ERR_UNSUPPORTED;
   if (!(s->dt_min <= s->dt_max)) return GDN_ERR_SHAPE;   // also NaN
   const int64_t dim = (int64_t)s->num_heads * s->head_dim + 2 * (int64_t)s->num_groups * s->state_dim;
-  if (s->num_heads > 65535 || dim >= (1 << 23)) return GDN_ERR_SHAPE;
+  // the kernels' grids take a head, or a group and four heads, along their second axis
+  if (s->num_heads > 65535 || s->num_groups + (s->num_heads + 3) / 4 > 65535 || dim >= (1 << 23)) return GDN_ERR_SHAPE;
   l->H = s->num_heads; l->G = s->num_groups; l->P = s->head_dim; l->N = s->state_dim; l->conv_dim = (int32_t)dim;
   l->softplus = (s->flags & GDN_SSM_SOFTPLUS) != 0;
   l->dt_min = s->dt_min; l->dt_max = s->dt_max;
@@ -682,6 +683,7 @@ gdn_status gdn_ssm_prefill_packed(
   const void* ptrs[] = {conv_state_in, conv_state_out, conv_ckpt, init_state, final_state, ckpt_buf, workspace};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return GDN_ERR_SHAPE;
+  if (!fits_grid(gdn::ssm_scan_groups(a.l, n_seqs, n_tokens), 256)) return GDN_ERR_SHAPE;
   const int64_t windows = (int64_t)n_seqs * 3 * a.l.conv_dim * 2;
   if (conv_state_in != conv_state_out && overlap(conv_state_in, windows, conv_state_out, windows)) return GDN_ERR_SHAPE;
   const int64_t need = gdn::ssm_scan_bytes(a.l, n_seqs, cu_seqlens_host);
@@ -699,7 +701,7 @@ gdn_status gdn_ssm_prefill_packed(
   a.conv_out = static_cast<uint16_t*>(conv_state_out);
   a.conv_ckpt = static_cast<uint16_t*>(conv_ckpt);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  return finish_launch(gdn::launch_ssm_scan(a, workspace, s), s);
+  return finish_launch(gdn::launch_ssm_scan(a, cu_seqlens_host, workspace, s), s);
 }
 
 gdn_status gdn_ssm_decode(const gdn_ssm_shape* shape, int32_t batch, int32_t n_tok, const void* x,
@@ -711,7 +713,7 @@ gdn_status gdn_ssm_decode(const gdn_ssm_shape* shape, int32_t batch, int32_t n_t
   gdn_status st = check_ssm(shape, &a.l);
   if (st != GDN_OK) return st;
   if (batch < 0 || pool_slots < 0 || n_tok < 1) return GDN_ERR_SHAPE;
-  if ((int64_t)batch * n_tok > INT32_MAX) return GDN_ERR_SHAPE;
+  if ((int64_t)batch * n_tok > INT32_MAX || !fits_grid(batch, 256)) return GDN_ERR_SHAPE;
   if (!conv_weight != !conv_state) return GDN_ERR_NULL;   // the conv needs both
   st = check_ssm_rows((int64_t)batch * n_tok, x_tok_stride, x, dt_dtype, dt_tok_stride, dt, A, dt_bias, D, conv_weight,
                       conv_bias, out, &a.l, &a.x_stride, &a.dt_stride);

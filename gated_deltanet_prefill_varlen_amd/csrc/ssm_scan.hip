@@ -1,74 +1,779 @@
-// Packed scan of the state space layers, token by token: a workgroup owns 32
-// rows of one (prompt, head), as the decode step does.
+// Packed scan of the state space layers on the matrix cores, in chunks of 64
+// tokens.  With cum_t = sum of A dt up to token t of a chunk, S0 the state
+// that enters it, L its last token:
+//
+//   y_t = exp(cum_t) S0 C_t + sum_{s <= t} M_ts x_s + D x_t,
+//         M_ts = exp(cum_t - cum_s) dt_s (C_t . B_s)
+//   S   = exp(cum_L) S0 + sum_s w_s x_s B_s^T,  w_s = exp(cum_L - cum_s) dt_s
+//
+// Three launches (the second only where a prompt is cut into segments):
+//  1. prepare: per chunk and group the convolved B and C as fp16 operands laid
+//     out as the products read them, and the products C . B; per chunk and
+//     head the steps, their running sums and the weights w.
+//  2. segments: long prompts on few heads would leave most of the chip idle
+//     behind the chain of their chunks, so their chunks are dealt to segments
+//     by a rule on the prompt's own length; each segment's state from zero,
+//     then the states that enter the segments, one after the other.
+//  3. scan: a workgroup walks the chunks of a segment for 128 / P heads of one
+//     group, one wave per 32 channels of a head, S^T in accumulators.
+//
+// Precision.  States come back in fp32 and are held to it: x w and B enter
+// their product as fp16 pairs hi + lo (hi hi + hi lo + lo hi: 2^-21).  What only
+// ends in the bf16 outputs (M, x, C, S as operands) is fp16 once, 2^-11 of the
+// value.  fp16's range is met by powers of two: B and C per chunk and group, x
+// per chunk and channel, S per channel by a bound of its largest entry that is
+// carried along.  A channel's x, as an operand, and its state, as an
+// accumulator, lie in the same lanes, so a channel's scale never leaves them
+// but for the outputs.
+#include <algorithm>
 #include <climits>
 
+#include "cache_device.h"
 #include "ssm_device.h"
 
 namespace gdn {
 namespace {
 
-constexpr int kRows = 32;
+constexpr int kChunk = 64;
+constexpr int kTab = 256;                 // floats of a (chunk, head)'s table: dt, cum, w, scalars
+// Powers of two that the largest values are brought to: B^T in the update of the
+// state (and S, where 64 products of x w and B fill it), B and C in C . B (whose
+// sums over N, times a step's share, fit fp16).
+constexpr int kTopBt = 14, kTopS = 30, kTopS16 = 14, kTopB = 4, kTopC = 4;
+constexpr float kLog2e = 1.44269504088896341f;
 
-// Input of channel c at position p of prompt s (t0 = its first row; p < 0: its history).
-__device__ __forceinline__ uint16_t raw_at(const SsmScanArgs& a, int s, int t0, int p, int c) {
-  if (p >= 0) return a.x[(size_t)(t0 + p) * a.x_stride + c];
-  return a.conv_in ? a.conv_in[((size_t)s * 3 + 3 + p) * a.l.conv_dim + c] : 0;
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ f32x4 mma(f16x8 a, f16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+
+__device__ __forceinline__ f16x2 pack_f16(float a, float b) { return __builtin_convertvector(f32x2{a, b}, f16x2); }
+
+// x < 2^pow2_above(x) for finite x >= 0, within -100 .. 110.
+__device__ __forceinline__ int pow2_above(float x) { return min(max((int)(__float_as_uint(x) >> 23) - 126, -100), 110); }
+
+template <typename Op>
+__device__ __forceinline__ float over_wave(float x, Op op) {
+  x = op(x, dpp_f32<0xB1>(x));
+  x = op(x, dpp_f32<0x4E>(x));
+  x = op(x, dpp_f32<0x141>(x));
+  x = op(x, dpp_f32<0x140>(x));
+  x = op(x, __shfl_xor(x, 16));
+  return op(x, __shfl_xor(x, 32));
+}
+struct MaxOp { __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); } };
+// The largest over the lane groups: of the lanes that hold the same channels.
+__device__ __forceinline__ float over_groups(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16));
+  return fmaxf(x, __shfl_xor(x, 32));
+}
+struct AddOp { __device__ __forceinline__ float operator()(float a, float b) const { return a + b; } };
+
+// ------------------------------------------------------------ the layout --
+// Chunk c of prompt s has slot cu[s] / 64 + s + c: no two chunks share one,
+// and none passes n_tokens / 64 + n_seqs.  Segments alike, by 256 tokens.
+struct Ws {
+  char* bc;              // [slots][G]: C operands, B^T hi, B^T lo (64 N halves each)
+  float* gt;             // [slots][G][10][64][4]: the tiles of C . B on and below the diagonal
+  int2* k;               // [slots][G]: powers of two on B and C
+  float* tab;            // [slots][H][kTab]
+  float* seg;            // [segment slots][H][P][N]
+  float* seg_sum;        // [segment slots][H]: log2 of the segment's decay
+  int32_t slots, seg_slots;
+  int64_t bytes;
+};
+
+constexpr int kSegUnit = 4;               // chunks a segment has at least
+
+// Chunks of a segment for a prompt of nc chunks whose chunk row takes hb
+// workgroups.
+__host__ __device__ inline int seg_chunks(int nc, int hb) {
+  if (nc < 4 * kSegUnit) return nc > 0 ? nc : 1;
+  const int want = (512 + hb - 1) / hb, most = nc / kSegUnit, n = want < most ? want : most;
+  return (nc + n - 1) / n;
+}
+
+inline int64_t up(int64_t x) { return (x + 255) / 256 * 256; }
+
+inline Ws layout(const SsmLayer& l, int32_t n_seqs, int64_t n_tokens, bool split, void* base) {
+  Ws w{};
+  w.slots = (int32_t)(n_tokens / kChunk + n_seqs);
+  w.seg_slots = split ? (int32_t)(n_tokens / (kChunk * kSegUnit) + n_seqs) : 0;
+  char* p = static_cast<char*>(base);
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) { const int64_t here = at; at += up(bytes); return p + here; };
+  const int64_t sg = (int64_t)w.slots * l.G;
+  w.bc = take(sg * 3 * kChunk * l.N * 2);
+  w.gt = reinterpret_cast<float*>(take(sg * 10 * 256 * 4));
+  w.k = reinterpret_cast<int2*>(take(sg * 8));
+  w.tab = reinterpret_cast<float*>(take((int64_t)w.slots * l.H * kTab * 4));
+  w.seg = reinterpret_cast<float*>(take((int64_t)w.seg_slots * l.H * l.P * l.N * 4));
+  w.seg_sum = reinterpret_cast<float*>(take((int64_t)w.seg_slots * l.H * 4));
+  w.bytes = at;
+  return w;
+}
+
+// Heads of a workgroup: 128 / P, or the largest power of two below it that
+// divides a group's heads.
+inline int heads_per_group(const SsmLayer& l) { return l.H / l.G; }
+inline int heads_per_wg(const SsmLayer& l) {
+  int n = 128 / l.P;
+  while (heads_per_group(l) % n != 0) n /= 2;
+  return n;
+}
+
+inline int max_segments(const SsmLayer& l, int32_t n_seqs, const int32_t* cu) {
+  const int hb = l.H / heads_per_wg(l);
+  int most = 1;
+  for (int s = 0; s < n_seqs; ++s) {
+    const int nc = (cu[s + 1] - cu[s] + kChunk - 1) / kChunk, per = seg_chunks(nc, hb);
+    most = std::max(most, (nc + per - 1) / per);
+  }
+  return most;
+}
+
+// The prompt s that owns slot b where prompt s begins at cu[s] / unit + s.
+__device__ __forceinline__ int owner(const int32_t* cu_ptr, int n_seqs, int unit, int b) {
+  typedef const int32_t __attribute__((address_space(4)))* ConstI32;
+  const ConstI32 cu = (ConstI32)cu_ptr;
+  int lo = 0, hi = n_seqs;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] / unit + mid <= b) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Token of element j (0 .. 7) of lane group g in step ks of a product over 64
+// tokens (columns of a product over N alike): the rows that two accumulator
+// tiles of 16 hold in the lane group, so that an accumulator is an operand.
+__device__ __forceinline__ constexpr int slot_of(int ks, int g, int j) { return 32 * ks + 16 * (j / 4) + 4 * g + j % 4; }
+
+// --------------------------------------------------------------- prepare --
+template <int N>
+__device__ __forceinline__ void prepare_bc(const SsmScanArgs& a, const Ws& w, int s, int c, int grp, char* smem) {
+  constexpr int PITCH = 2 * N + 8, ROW = N + 8, NT = N / 16, KN = N / 32, TILES = N / 32;
+  uint16_t* raw = reinterpret_cast<uint16_t*>(smem);                       // [67][PITCH]
+  _Float16* rb = reinterpret_cast<_Float16*>(smem + 67 * PITCH * 2);       // [64][ROW]
+  _Float16* rc = rb + kChunk * ROW;
+  float* red = reinterpret_cast<float*>(rc + kChunk * ROW);                // [2][4]
+  const SsmLayer& l = a.l;
+  const int tid = threadIdx.x, wave = tid / 64, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int t0 = a.cu[s], len = a.cu[s + 1] - t0, inner = l.H * l.P;
+  const int col_b = inner + grp * N, col_c = inner + (l.G + grp) * N;
+  for (int i = tid; i < 67 * (N / 4); i += 256) {
+    const int row = i / (N / 4), k = 8 * (i % (N / 4)), p = c * kChunk - 3 + row;
+    const int col = k < N ? col_b + k : col_c + k - N;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (p >= 0) {
+      if (p < len) v = *reinterpret_cast<const uint4*>(a.x + (int64_t)(t0 + p) * a.x_stride + col);
+    } else if (a.conv_in) {
+      v = *reinterpret_cast<const uint4*>(a.conv_in + ((int64_t)s * 3 + 3 + p) * l.conv_dim + col);
+    }
+    *reinterpret_cast<uint4*>(raw + row * PITCH + k) = v;
+  }
+  __syncthreads();
+  const int left = len - c * kChunk;    // tokens from the chunk's first on
+  float v[TILES][2][8];
+  float m[2] = {0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < TILES; ++k) {
+    const int ct = wave + 4 * k, col = 16 * ct + r, ch = ct < NT ? col_b + col : col_c + col - N;
+    float w0 = 0.f, w1 = 0.f, w2 = 0.f, w3 = 0.f, b = 0.f;
+    if (l.conv_w) {
+      const float4 q = reinterpret_cast<const float4*>(l.conv_w)[ch];
+      w0 = conv_tap(q.x); w1 = conv_tap(q.y); w2 = conv_tap(q.z); w3 = conv_tap(q.w);
+      if (l.conv_bias) b = conv_tap(l.conv_bias[ch]);
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int base = 32 * ks + 16 * hf + 4 * g;
+        float x[7];
+#pragma unroll
+        for (int i = 0; i < 7; ++i) x[i] = bf16_to_f32(raw[(base + i) * PITCH + col]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float u = l.conv_w ? conv4_bias_silu(b, w0, w1, w2, w3, x[i], x[i + 1], x[i + 2], x[i + 3]) : x[i + 3];
+          if (base + i >= left) u = 0.f;
+          v[k][ks][4 * hf + i] = u;
+          m[ct >= NT] = fmaxf(m[ct >= NT], finite_abs(u));
+        }
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    m[i] = over_wave(m[i], MaxOp{});
+    if (lane == 0) red[4 * i + wave] = m[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) m[i] = fmaxf(fmaxf(red[4 * i], red[4 * i + 1]), fmaxf(red[4 * i + 2], red[4 * i + 3]));
+  const int kb = kTopBt - pow2_above(m[0]), kc = kTopC - pow2_above(m[1]);
+  const int64_t sg = (int64_t)(t0 / kChunk + s + c) * l.G + grp;
+  if (tid == 0) w.k[sg] = make_int2(kb, kc);
+  f16x8* ops = reinterpret_cast<f16x8*>(w.bc + sg * 3 * kChunk * N * 2);
+#pragma unroll
+  for (int k = 0; k < TILES; ++k) {
+    const int ct = wave + 4 * k;
+    const bool is_c = ct >= NT;
+    const float f = ldexpf(1.f, is_c ? kc : kb);
+    _Float16* rows = is_c ? rc : rb;
+    const int n = 16 * (is_c ? ct - NT : ct) + r;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      f16x8 hi, lo;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float u = v[k][ks][j] * f;
+        hi[j] = (_Float16)u;
+        lo[j] = (_Float16)(u - (float)hi[j]);
+        rows[slot_of(ks, g, j) * ROW + n] = is_c ? hi[j] : (_Float16)ldexpf(u, kTopB - kTopBt);
+      }
+      if (!is_c) {
+        f16x8* bt = ops + kChunk * N / 8;
+        bt[(ct * 2 + ks) * 64 + lane] = hi;
+        bt[kChunk * N / 8 + (ct * 2 + ks) * 64 + lane] = lo;
+      }
+    }
+  }
+  __syncthreads();
+  auto row_frag = [&](const _Float16* rows, int t, int ks) __attribute__((always_inline)) {
+    const f16x4 x = *reinterpret_cast<const f16x4*>(rows + t * ROW + 32 * ks + 4 * g);
+    const f16x4 y = *reinterpret_cast<const f16x4*>(rows + t * ROW + 32 * ks + 16 + 4 * g);
+    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  f16x8 cf[KN];
+#pragma unroll
+  for (int ks = 0; ks < KN; ++ks) {
+    cf[ks] = row_frag(rc, 16 * wave + r, ks);
+    ops[(wave * KN + ks) * 64 + lane] = cf[ks];
+  }
+  f32x4* gt = reinterpret_cast<f32x4*>(w.gt + sg * 10 * 256);
+  for (int st = 0; st <= wave; ++st) {
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < KN; ++ks) acc = mma(row_frag(rb, 16 * st + r, ks), cf[ks], acc);
+    gt[(wave * (wave + 1) / 2 + st) * 64 + lane] = acc;
+  }
+}
+
+// The steps of one (chunk, head): a wave, a lane per token.
+__device__ __forceinline__ void prepare_steps(const SsmScanArgs& a, const Ws& w, int s, int c, int h) {
+  const int lane = threadIdx.x & 63, t0 = a.cu[s], len = a.cu[s + 1] - t0, p = c * kChunk + lane;
+  const float A = a.l.A[h];
+  const float dt = p < len ? ssm_step(a.l, a.dt, (int64_t)(t0 + p) * a.dt_stride + h, h) : 0.f;
+  // log2 of the token's decay; one of 2^-200 leaves nothing of a state, and
+  // longer ones would only take precision from the sums
+  float al = A * dt * kLog2e;
+  if (al < -200.f) al = -200.f;
+  if (p >= len) al = 0.f;
+  float cum = al, after = al;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const float x = __shfl_up(cum, d), y = __shfl_down(after, d);
+    if (lane >= d) cum += x;
+    if (lane + d < 64) after += y;
+  }
+  const float total = __shfl(cum, 63);
+  // sum of the later tokens' decays, from the end: near tokens keep their
+  // precision behind a long sum
+  after = __shfl_down(after, 1);
+  if (lane == 63) after = 0.f;
+  const float wt = __builtin_amdgcn_exp2f(after) * dt;
+  const float grow = over_wave(fmaxf(al, 0.f), AddOp{});
+  const float wmax = over_wave(finite_abs(wt), MaxOp{});
+  const float dmax = over_wave(finite_abs(dt), MaxOp{}) * __builtin_amdgcn_exp2f(fminf(grow, 60.f));
+  float* tab = w.tab + ((int64_t)(t0 / kChunk + s + c) * a.l.H + h) * kTab;
+  tab[lane] = dt;
+  tab[64 + lane] = cum;
+  tab[128 + lane] = wt;
+  if (lane < 4) tab[192 + lane] = lane == 0 ? total : lane == 1 ? wmax : lane == 2 ? dmax : __builtin_amdgcn_exp2f(total);
 }
 
 template <int N>
-__global__ void __launch_bounds__(kRows * (N / 16)) ssm_scan_kernel(const SsmScanArgs a) {
-  constexpr int LPR = N / 16, THREADS = kRows * LPR, NCH = kRows + 2 * N;
+__global__ void __launch_bounds__(256) ssm_prepare_kernel(const SsmScanArgs a, const Ws w) {
+  __shared__ __align__(16) char smem[67 * (2 * N + 8) * 2 + 2 * kChunk * (N + 8) * 2 + 64];
+  const int b = blockIdx.x, s = owner(a.cu, a.n_seqs, kChunk, b), c = b - (a.cu[s] / kChunk + s);
+  if (c * kChunk >= a.cu[s + 1] - a.cu[s]) return;
+  if ((int)blockIdx.y < a.l.G) {
+    prepare_bc<N>(a, w, s, c, blockIdx.y, smem);
+  } else {
+    const int h = (blockIdx.y - a.l.G) * 4 + threadIdx.x / 64;
+    if (h < a.l.H) prepare_steps(a, w, s, c, h);
+  }
+}
+
+// ------------------------------------------------------------------ scan --
+// Copies 16 bytes a lane from global memory to LDS, at the wave's base.
+__device__ __forceinline__ void to_lds(const void* g, void* base) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g, (__attribute__((address_space(3))) void*)base,
+                                   16, 0, 0);
+}
+
+// What a wave keeps of a prompt's inputs: the two channels 2 r, 2 r + 1 of its
+// 32 in one dword, at the tokens of its lane group and the three before each
+// run of four.
+struct RawX { uint32_t v[4][7]; };
+
+template <int P, int N, bool OUT>
+__global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, const Ws w, int hpw, int split, int grouped) {
+  constexpr int WPH = P / 32, NT = N / 16, KN = N / 32, OPS = kChunk * N * 2;   // bytes of one operand
+  constexpr int HMAX = 4 / WPH;
+  __shared__ __align__(16) char ops[3 * OPS];
+  __shared__ __align__(16) f16x8 fm[OUT ? HMAX : 1][6][64];
+  __shared__ __align__(16) float tabs[HMAX][kTab];
   const SsmLayer& l = a.l;
-  const int s = blockIdx.x, h = blockIdx.y, P = l.P, row0 = blockIdx.z * kRows;
-  const int tid = threadIdx.x, rg = tid / LPR, jl = tid % LPR;
-  const int grp = h / (l.H / l.G), inner = l.H * P;
-  const int t0 = a.cu[s], len = a.cu[s + 1] - t0;
-  float S[16];
-  const size_t at = ((size_t)h * P + row0 + rg) * N + 4 * jl, all = (size_t)l.H * P * N;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int nw = hpw * WPH, hl = wave / WPH, half = wave % WPH;
+  const int hb = l.H / hpw, per_group = hb / l.G;
+  int unit, b;
+  if (grouped) {   // the workgroups that read the same B and C go to one XCD
+    const int q = blockIdx.x / (8 * per_group), rem = blockIdx.x % (8 * per_group), cell = 8 * q + rem % 8;
+    unit = cell / l.G;
+    b = cell % l.G * per_group + rem / 8;
+  } else {
+    unit = blockIdx.x / hb;
+    b = blockIdx.x % hb;
+  }
+  const int units = split ? w.seg_slots : a.n_seqs;
+  if (unit >= units) return;
+  const int s = split ? owner(a.cu, a.n_seqs, kChunk * kSegUnit, unit) : unit;
+  const int t0 = a.cu[s], len = a.cu[s + 1] - t0, nc = (len + kChunk - 1) / kChunk;
+  const int per = split ? seg_chunks(nc, hb) : max(nc, 1), k = split ? unit - (t0 / (kChunk * kSegUnit) + s) : 0;
+  const int n_seg = max(1, (nc + per - 1) / per);
+  if (k >= n_seg || (!OUT && k + 1 >= n_seg)) return;
+  const int c_first = k * per, c_end = min(nc, c_first + per);
+
+  const int h = b * hpw + hl, grp = h / (l.H / l.G), ch0 = h * P + 32 * half + 2 * r;
+  const int64_t hpn = (int64_t)l.P * l.N, slot0 = t0 / kChunk + s;
+  const int64_t st_at = (int64_t)(32 * half + 2 * r) * N + 4 * g;       // this lane's entries of a head's state
+  float w0[2], w1[2], w2[2], w3[2], wb[2] = {0.f, 0.f};
+  if (l.conv_w) {
 #pragma unroll
-  for (int k = 0; k < 16; ++k) S[k] = a.init ? a.init[s * all + at + 4 * LPR * (k / 4) + k % 4] : 0.f;
-  int ci = lower_bound_i32(a.ckpt, a.n_ckpt, t0 + 1);
-  int next = ci < a.n_ckpt ? a.ckpt[ci] : INT_MAX;
-  __shared__ float u[NCH];
-  const float A = l.A[h], D = l.D ? l.D[h] : 0.f;
-  auto store = [&](float* q) __attribute__((always_inline)) {
+    for (int e = 0; e < 2; ++e) {
+      const float4 q = reinterpret_cast<const float4*>(l.conv_w)[ch0 + e];
+      w0[e] = conv_tap(q.x); w1[e] = conv_tap(q.y); w2[e] = conv_tap(q.z); w3[e] = conv_tap(q.w);
+      if (l.conv_bias) wb[e] = conv_tap(l.conv_bias[ch0 + e]);
+    }
+  }
+  const float D = OUT && l.D ? l.D[h] : 0.f;
+
+  RawX x;
+  auto load_x = [&](int c) __attribute__((always_inline)) {
+    const int left = len - c * kChunk;
+    const uint16_t* base = a.x + (int64_t)(t0 + c * kChunk) * a.x_stride + ch0;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) q[at + 4 * LPR * (k / 4) + k % 4] = S[k];
+    for (int run = 0; run < 4; ++run)
+#pragma unroll
+      for (int i = 0; i < 7; ++i) {
+        if (i < 3 && !l.conv_w) continue;
+        const int p = 16 * run + 4 * g - 3 + i;
+        if (i < 3 && run == 0 && c == 0 && p < 0) {
+          x.v[run][i] = a.conv_in ? *reinterpret_cast<const uint32_t*>(a.conv_in + ((int64_t)s * 3 + 3 + p) * l.conv_dim + ch0) : 0u;
+        } else {
+          x.v[run][i] = *reinterpret_cast<const uint32_t*>(base + (int64_t)min(p, left - 1) * a.x_stride);
+        }
+      }
   };
-  for (int p = 0; p < len; ++p) {
-    const size_t t = t0 + p;
-    __syncthreads();
-    for (int e = tid; e < NCH; e += THREADS) {
-      const int c = e < kRows ? h * P + row0 + e
-                  : e < kRows + N ? inner + grp * N + e - kRows : inner + (l.G + grp) * N + e - kRows - N;
-      if (l.conv_w) {
-        const float4 w = reinterpret_cast<const float4*>(l.conv_w)[c];
-        u[e] = conv4_bias_silu(l.conv_bias ? conv_tap(l.conv_bias[c]) : 0.f, conv_tap(w.x), conv_tap(w.y), conv_tap(w.z),
-                               conv_tap(w.w), bf16_to_f32(raw_at(a, s, t0, p - 3, c)), bf16_to_f32(raw_at(a, s, t0, p - 2, c)),
-                               bf16_to_f32(raw_at(a, s, t0, p - 1, c)), bf16_to_f32(raw_at(a, s, t0, p, c)));
-      } else {
-        u[e] = bf16_to_f32(raw_at(a, s, t0, p, c));
+
+  // the state that enters, S^T in tiles [16 n][16 p], scaled by 2^e
+  f32x4 S[NT][2];
+  int e[2] = {0, 0};
+  float bound[2] = {0.f, 0.f};
+  const float* from = !OUT ? nullptr
+                      : k > 0 ? w.seg + (((int64_t)unit - 1) * l.H + h) * hpn
+                      : a.init ? a.init + ((int64_t)s * l.H + h) * hpn : nullptr;
+  if (c_first < c_end) load_x(c_first);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      S[nt][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (from) S[nt][q] = *reinterpret_cast<const f32x4*>(from + st_at + q * N + 16 * nt);
+    }
+  if (from) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bound[q] = fmaxf(bound[q], finite_abs(S[nt][q][i]));
+      bound[q] = over_groups(bound[q]);
+      e[q] = kTopS - pow2_above(bound[q]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[nt][q][i] = ldexpf(S[nt][q][i], e[q]);
+    }
+  }
+  auto store_state = [&](float* to) __attribute__((always_inline)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        f32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = ldexpf(S[nt][q][i], -e[q]);
+        *reinterpret_cast<f32x4*>(to + st_at + q * N + 16 * nt) = v;
+      }
+  };
+  int ci = 0, next = INT_MAX;
+  if (OUT) {
+    ci = lower_bound_i32(a.ckpt, a.n_ckpt, t0 + c_first * kChunk + 1);
+    if (ci < a.n_ckpt) next = a.ckpt[ci];
+  }
+  float seg_sum = 0.f;
+
+  for (int c = c_first; c < c_end; ++c) {
+    const int64_t sg = (slot0 + c) * l.G + grp;
+    const int left = min(kChunk, len - c * kChunk);
+    __syncthreads();   // the last chunk's operands have been read
+    {
+      const char* src = w.bc + sg * 3 * OPS;
+      for (int i = (OUT ? 0 : OPS / 1024) + wave; i < 3 * OPS / 1024; i += nw) to_lds(src + 1024 * i + 16 * lane, ops + 1024 * i);
+      if (half == 0) to_lds(w.tab + ((slot0 + c) * l.H + h) * kTab + 4 * lane, tabs[hl]);
+    }
+    const int2 kk = w.k[sg];
+    const int kbt = kk.x, kb = kbt - kTopBt + kTopB, kc = kk.y;
+    // the tiles of C . B that this wave weighs
+    f32x4 gv[(6 + WPH - 1) / WPH][2];
+    if (OUT) {
+      const f32x4* gt = reinterpret_cast<const f32x4*>(w.gt + sg * 10 * 256) + lane;
+#pragma unroll
+      for (int i = 0; i < (6 + WPH - 1) / WPH; ++i) {
+        const int f = half + WPH * i;
+        if (f < 6) {
+          const int tt = f < 2 ? f : (f + 2) / 2, ks = f < 2 ? 0 : f % 2;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) gv[i][q] = gt[(tt * (tt + 1) / 2 + min(2 * ks + q, tt)) * 64];
+        }
       }
     }
-    const float dt = ssm_step(l, a.dt, t * a.dt_stride + h, h), alpha = expf(A * dt);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    const float x = u[rg], dx = dt * x;
-    float y = 0.f;
+    const float* tab = tabs[hl];
+    const float alpha = tab[195], wmax = tab[193], dmax = tab[194];
+
+    // x through the convolution: x2[q][run][i] = channel 2 r + q at token 16 run + 4 g + i
+    float xv[2][4][4];
+    float xmax[2] = {0.f, 0.f}, odd = 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int n = 4 * LPR * (k / 4) + 4 * jl + k % 4;
-      S[k] = fmaf(alpha, S[k], dx * u[kRows + n]);
-      y = fmaf(S[k], u[kRows + N + n], y);
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int run = 0; run < 4; ++run) {
+        float in[7];
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+          if (i >= 3 || l.conv_w) in[i] = q ? hi_bf16(x.v[run][i]) : lo_bf16(x.v[run][i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float u = l.conv_w ? conv4_bias_silu(wb[q], w0[q], w1[q], w2[q], w3[q], in[i], in[i + 1], in[i + 2], in[i + 3]) : in[i + 3];
+          xv[q][run][i] = u;
+          xmax[q] = fmaxf(xmax[q], fabsf(u));
+          odd = fmaf(u, 0.f, odd);     // NaN once a value is not finite
+        }
+      }
+    if (c + 1 < c_end) load_x(c + 1);
+    const bool bad = __ballot(odd != odd) != 0;
+    if (bad) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        xmax[q] = 0.f;
+#pragma unroll
+        for (int run = 0; run < 4; ++run)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) xmax[q] = fmaxf(xmax[q], finite_abs(xv[q][run][i]));
+      }
     }
-    y = group_sum<LPR>(y);
-    if (jl == 0) a.out[(t * l.H + h) * P + row0 + rg] = (uint16_t)f32_to_bf16(fmaf(D, x, y));
-    if (t + 1 == (size_t)next) {
-      store(a.ckpt_buf + (size_t)ci * all);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) xmax[q] = over_groups(xmax[q]);
+
+    // the weights inside the chunk, as operands: element (t = column, s) of M^T
+    int m = 0;
+    if (OUT) {
+      const int ad = min(-pow2_above(dmax), 14 - pow2_above(fabsf(D)) - (kb + kc));
+      m = kb + kc + ad;
+      const float dm = ldexpf(D, m);
+#pragma unroll
+      for (int i = 0; i < (6 + WPH - 1) / WPH; ++i) {
+        const int f = half + WPH * i;
+        if (f < 6) {
+          const int tt = f < 2 ? f : (f + 2) / 2, ks = f < 2 ? 0 : f % 2;
+          const float ct = tab[64 + 16 * tt + r];
+          f16x8 o;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int st = 2 * ks + q;
+            const f32x4 cs = *reinterpret_cast<const f32x4*>(tab + 64 + 16 * min(st, tt) + 4 * g);
+            const f32x4 ds = *reinterpret_cast<const f32x4*>(tab + 16 * min(st, tt) + 4 * g);
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[j] = gv[i][q][j] * (ldexpf(ds[j], ad) * __builtin_amdgcn_exp2f(ct - cs[j]));
+              if (st == tt) v[j] = 4 * g + j < r ? v[j] : 4 * g + j == r ? v[j] + dm : 0.f;
+              if (st > tt) v[j] = 0.f;
+            }
+            const f16x2 p0 = pack_f16(v[0], v[1]), p1 = pack_f16(v[2], v[3]);
+            o[4 * q] = p0[0]; o[4 * q + 1] = p0[1]; o[4 * q + 2] = p1[0]; o[4 * q + 3] = p1[1];
+          }
+          fm[hl][f][lane] = o;
+        }
+      }
+    }
+
+    // operands of x, for the outputs (x 2^kx) and for the state (x w, in pairs)
+    f16x8 xo[OUT ? 2 : 1][2], xh[2][2], xl[2][2];
+    int kx[2], e_new[2];
+    float fx[2], grown[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      kx[q] = xmax[q] >= 0.125f && xmax[q] < 32768.f ? 0 : 14 - pow2_above(xmax[q]);
+      fx[q] = ldexpf(1.f, kx[q]);
+      grown[q] = fmaf(alpha, bound[q], ldexpf(64.f * wmax * xmax[q], kTopBt - kbt));
+      e_new[q] = kTopS - pow2_above(grown[q]);
+    }
+    const bool plain = __ballot((kx[0] | kx[1]) != 0) == 0;
+#pragma unroll
+    for (int run = 0; run < 4; ++run) {
+      const f32x4 wv = *reinterpret_cast<const f32x4*>(tab + 128 + 16 * run + 4 * g);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float u0 = xv[q][run][i], u1 = xv[q][run][i + 1];
+          if (OUT) {
+            const f16x2 o = plain ? pack_f16(u0, u1) : pack_f16(u0 * fx[q], u1 * fx[q]);
+            xo[q][run / 2][4 * (run % 2) + i] = o[0];
+            xo[q][run / 2][4 * (run % 2) + i + 1] = o[1];
+          }
+          const float v0 = u0 * ldexpf(wv[i], e_new[q] - kbt), v1 = u1 * ldexpf(wv[i + 1], e_new[q] - kbt);
+          const f16x2 hi = pack_f16(v0, v1), lo = pack_f16(fmaf((float)hi[0], -1.f, v0), fmaf((float)hi[1], -1.f, v1));
+          xh[q][run / 2][4 * (run % 2) + i] = hi[0];
+          xh[q][run / 2][4 * (run % 2) + i + 1] = hi[1];
+          xl[q][run / 2][4 * (run % 2) + i] = lo[0];
+          xl[q][run / 2][4 * (run % 2) + i + 1] = lo[1];
+        }
+    }
+
+    if (OUT) {
+      int first_bad[2] = {INT_MAX, INT_MAX};    // first token of channels 2 r, 2 r + 1 that is not finite
+      if (bad) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+          for (int run = 3; run >= 0; --run)
+#pragma unroll
+            for (int i = 3; i >= 0; --i)
+              if (!(fabsf(xv[q][run][i]) < __builtin_inff())) {
+                first_bad[q] = 16 * run + 4 * g + i;
+                xo[q][run / 2][4 * (run % 2) + i] = (_Float16)0.f;
+              }
+          first_bad[q] = min(first_bad[q], __shfl_xor(first_bad[q], 16));
+          first_bad[q] = min(first_bad[q], __shfl_xor(first_bad[q], 32));
+        }
+      }
+      f16x8 so[2][KN];   // the entering state as an operand
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int ks = 0; ks < KN; ++ks)
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            constexpr float down = 1.f / (1 << (kTopS - kTopS16));
+            const f16x2 v = pack_f16(S[2 * ks + j / 4][q][j % 4] * down, S[2 * ks + j / 4][q][j % 4 + 1] * down);
+            so[q][ks][j] = v[0];
+            so[q][ks][j + 1] = v[1];
+          }
+      __syncthreads();   // M is whole
+      // scales of the rows that the accumulators of the outputs hold
+      float f1[4][2], f2[4][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          f1[i][q] = ldexpf(1.f, max(-126, min(126, kTopS - kTopS16 - (__shfl(e[q], 4 * g + i) + kc))));
+          f2[i][q] = ldexpf(1.f, max(-126, min(126, -(m + __shfl(kx[q], 4 * g + i)))));
+        }
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        f32x4 y1[2], y2[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) y1[q] = y2[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < KN; ++ks) {
+          const f16x8 cf = reinterpret_cast<const f16x8*>(ops)[(tt * KN + ks) * 64 + lane];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) y1[q] = mma(so[q][ks], cf, y1[q]);
+        }
+#pragma unroll
+        for (int ks = 0; ks <= tt / 2; ++ks) {
+          const f16x8 mf = fm[hl][tt < 2 ? tt : 2 * tt - 2 + ks][lane];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) y2[q] = mma(xo[q][ks], mf, y2[q]);
+        }
+        const int t = 16 * tt + r;
+        const float ec = __builtin_amdgcn_exp2f(tab[64 + t]);
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) y[2 * i + q] = fmaf(y2[q][i], f2[i][q], y1[q][i] * (f1[i][q] * ec));
+        if (bad) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              if (t >= __shfl(first_bad[q], 4 * g + i)) y[2 * i + q] = __builtin_nanf("");
+        }
+        if (t < left) {
+          uint4 o;
+          o.x = pack_bf16(y[0], y[1]); o.y = pack_bf16(y[2], y[3]); o.z = pack_bf16(y[4], y[5]); o.w = pack_bf16(y[6], y[7]);
+          *reinterpret_cast<uint4*>(a.out + ((int64_t)(t0 + c * kChunk + t) * l.H + h) * P + 32 * half + 8 * g) = o;
+        }
+      }
+    }
+
+    const f16x8* bh = reinterpret_cast<const f16x8*>(ops + OPS) + lane;
+    const f16x8* bl = reinterpret_cast<const f16x8*>(ops + 2 * OPS) + lane;
+    // checkpoints inside the chunk: the entering state and the tokens up to there
+    if (OUT) {
+      while (next < t0 + c * kChunk + left) {
+        const int last = next - (t0 + c * kChunk) - 1;      // its last token in the chunk
+        const float upto = tab[64 + last], al = __builtin_amdgcn_exp2f(upto);
+        int ec[2];
+        float mul[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          ec[q] = min(kbt + 14 - pow2_above(dmax * xmax[q]), 100 - pow2_above(al * bound[q]));
+          mul[q] = ldexpf(al, ec[q] - e[q]);
+        }
+        f16x8 ch[2][2], cl[2][2];
+        uint4 keep[2];                                       // of each operand of B, the tokens up to there
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          uint32_t mask[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int t = slot_of(ks, g, j);
+            const bool in = t <= last;
+            if (in) mask[j / 2] |= 0xFFFFu << (16 * (j % 2));
+            const float wt = tab[t] * __builtin_amdgcn_exp2f(upto - tab[64 + t]);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float v = in ? xv[q][2 * ks + j / 4][j % 4] * ldexpf(wt, ec[q] - kbt) : 0.f;
+              ch[q][ks][j] = (_Float16)v;
+              cl[q][ks][j] = (_Float16)(v - (float)ch[q][ks][j]);
+            }
+          }
+          keep[ks] = make_uint4(mask[0], mask[1], mask[2], mask[3]);
+        }
+        float* to = a.ckpt_buf + ((int64_t)ci * l.H + h) * hpn + st_at;
+#pragma unroll 1
+        for (int nt = 0; nt < NT; ++nt) {
+          f32x4 acc[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+#pragma unroll
+            for (int z = 0; z < NT; ++z)
+              if (z == nt) acc[q] = S[z][q];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[q][i] *= mul[q];
+          }
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            uint4 u = __builtin_bit_cast(uint4, bh[(nt * 2 + ks) * 64]), v = __builtin_bit_cast(uint4, bl[(nt * 2 + ks) * 64]);
+            u.x &= keep[ks].x; u.y &= keep[ks].y; u.z &= keep[ks].z; u.w &= keep[ks].w;
+            v.x &= keep[ks].x; v.y &= keep[ks].y; v.z &= keep[ks].z; v.w &= keep[ks].w;
+            const f16x8 fh = __builtin_bit_cast(f16x8, u), fl = __builtin_bit_cast(f16x8, v);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              acc[q] = mma(fh, ch[q][ks], acc[q]);
+              acc[q] = mma(fl, ch[q][ks], acc[q]);
+              acc[q] = mma(fh, cl[q][ks], acc[q]);
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[q][i] = ldexpf(acc[q][i], -ec[q]);
+            *reinterpret_cast<f32x4*>(to + q * N + 16 * nt) = acc[q];
+          }
+        }
+        ++ci;
+        next = ci < a.n_ckpt ? a.ckpt[ci] : INT_MAX;
+      }
+    }
+
+    // the state: S^T[n, p] += B^T[n, s] (x w)^T[s, p]
+    float mul[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      mul[q] = ldexpf(alpha, e_new[q] - e[q]);
+      e[q] = e_new[q];
+      bound[q] = grown[q];
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[nt][q][i] *= mul[q];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const f16x8 fh = bh[(nt * 2 + ks) * 64], fl = bl[(nt * 2 + ks) * 64];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          S[nt][q] = mma(fh, xh[q][ks], S[nt][q]);
+          S[nt][q] = mma(fl, xh[q][ks], S[nt][q]);
+          S[nt][q] = mma(fh, xl[q][ks], S[nt][q]);
+        }
+      }
+    }
+    if (!OUT) seg_sum += tab[192];
+    if (OUT && next == t0 + c * kChunk + left) {
+      store_state(a.ckpt_buf + ((int64_t)ci * l.H + h) * hpn);
       ++ci;
       next = ci < a.n_ckpt ? a.ckpt[ci] : INT_MAX;
     }
   }
-  if (a.final_state) store(a.final_state + s * all);
+  if (!OUT) {
+    store_state(w.seg + ((int64_t)unit * l.H + h) * hpn);
+    if (lane == 0 && half == 0) w.seg_sum[(int64_t)unit * l.H + h] = seg_sum;
+  } else if (a.final_state && k + 1 == n_seg) {
+    store_state(a.final_state + ((int64_t)s * l.H + h) * hpn);
+  }
+}
+
+// The states that enter a prompt's segments: segment k's slot, which holds its
+// state from zero, gets the state behind it (the one that enters k + 1).
+__global__ void __launch_bounds__(256) ssm_pass_kernel(const SsmScanArgs a, const Ws w, int hb) {
+  const SsmLayer& l = a.l;
+  const int s = blockIdx.x, h = blockIdx.y, i = (blockIdx.z * 256 + threadIdx.x) * 4;
+  const int64_t hpn = (int64_t)l.P * l.N;
+  const int t0 = a.cu[s], nc = (a.cu[s + 1] - t0 + kChunk - 1) / kChunk, per = seg_chunks(nc, hb), n_seg = (nc + per - 1) / per;
+  if (n_seg < 2 || i >= hpn) return;
+  const int64_t first = t0 / (kChunk * kSegUnit) + s;
+  f32x4 S = {0.f, 0.f, 0.f, 0.f};
+  if (a.init) S = *reinterpret_cast<const f32x4*>(a.init + ((int64_t)s * l.H + h) * hpn + i);
+  for (int k = 0; k + 1 < n_seg; ++k) {
+    f32x4* p = reinterpret_cast<f32x4*>(w.seg + ((first + k) * l.H + h) * hpn + i);
+    const float al = __builtin_amdgcn_exp2f(w.seg_sum[(first + k) * l.H + h]);
+    const f32x4 own = *p;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) S[j] = fmaf(al, S[j], own[j]);
+    *p = S;
+  }
+}
+
+// Input of channel c at position p of prompt s (t0 = its first row; p < 0: its history).
+__device__ __forceinline__ uint16_t raw_at(const SsmScanArgs& a, int s, int t0, int p, int c) {
+  if (p >= 0) return a.x[(int64_t)(t0 + p) * a.x_stride + c];
+  return a.conv_in ? a.conv_in[((int64_t)s * 3 + 3 + p) * a.l.conv_dim + c] : 0;
 }
 
 // The three inputs before each checkpoint (blockIdx.x < n_ck), or each
@@ -79,24 +784,57 @@ __global__ void __launch_bounds__(256) ssm_scan_window_kernel(const SsmScanArgs 
   const int i = blockIdx.x;
   const int s = i < n_ck ? seq_of_token(a.cu, a.n_seqs, a.ckpt[i] - 1) : i - n_ck;
   const int t0 = a.cu[s], p = (i < n_ck ? a.ckpt[i] : a.cu[s + 1]) - t0;
-  uint16_t* to = (i < n_ck ? a.conv_ckpt + (size_t)i * 3 * dim : a.conv_out + (size_t)s * 3 * dim) + c;
+  uint16_t* to = (i < n_ck ? a.conv_ckpt + (int64_t)i * 3 * dim : a.conv_out + (int64_t)s * 3 * dim) + c;
   uint16_t v[3];
 #pragma unroll
   for (int j = 0; j < 3; ++j) v[j] = raw_at(a, s, t0, p - 3 + j, c);
 #pragma unroll
-  for (int j = 0; j < 3; ++j) to[(size_t)j * dim] = v[j];
+  for (int j = 0; j < 3; ++j) to[(int64_t)j * dim] = v[j];
+}
+
+template <int P, int N>
+hipError_t launch(const SsmScanArgs& a, const Ws& w, int segs, hipStream_t st) {
+  const SsmLayer& l = a.l;
+  hipError_t e = hipSuccess;
+  if (a.n_tokens > 0) {
+    hipLaunchKernelGGL((ssm_prepare_kernel<N>), dim3(w.slots, l.G + (l.H + 3) / 4), dim3(256), 0, st, a, w);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  const int hpw = heads_per_wg(l), hb = l.H / hpw, split = segs > 1;
+  const int64_t units = split ? w.seg_slots : a.n_seqs, cells = units * l.G;
+  const int grouped = cells >= 32;
+  const dim3 grid((uint32_t)(grouped ? (cells + 7) / 8 * 8 * (hb / l.G) : units * hb)), blk(64 * hpw * (P / 32));
+  if (split) {
+    hipLaunchKernelGGL((ssm_chunk_kernel<P, N, false>), grid, blk, 0, st, a, w, hpw, split, grouped);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL(ssm_pass_kernel, dim3(a.n_seqs, l.H, (P * N + 1023) / 1024), dim3(256), 0, st, a, w, hb);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((ssm_chunk_kernel<P, N, true>), grid, blk, 0, st, a, w, hpw, split, grouped);
+  return hipGetLastError();
+}
+
+template <int P>
+hipError_t launch_p(const SsmScanArgs& a, const Ws& w, int segs, hipStream_t st) {
+  return a.l.N == 32 ? launch<P, 32>(a, w, segs, st) : a.l.N == 64 ? launch<P, 64>(a, w, segs, st) : launch<P, 128>(a, w, segs, st);
 }
 
 }  // namespace
 
-int64_t ssm_scan_bytes(const SsmLayer&, int32_t, const int32_t*) { return 0; }
+int64_t ssm_scan_bytes(const SsmLayer& l, int32_t n_seqs, const int32_t* cu) {
+  if (n_seqs == 0 || cu[n_seqs] == 0) return 0;
+  return layout(l, n_seqs, cu[n_seqs], max_segments(l, n_seqs, cu) > 1, nullptr).bytes;
+}
 
-hipError_t launch_ssm_scan(const SsmScanArgs& a, void*, hipStream_t st) {
-  const dim3 grid(a.n_seqs, a.l.H, a.l.P / kRows), blk(kRows * (a.l.N / 16));
-  if (a.l.N == 32) hipLaunchKernelGGL((ssm_scan_kernel<32>), grid, blk, 0, st, a);
-  else if (a.l.N == 64) hipLaunchKernelGGL((ssm_scan_kernel<64>), grid, blk, 0, st, a);
-  else hipLaunchKernelGGL((ssm_scan_kernel<128>), grid, blk, 0, st, a);
-  hipError_t e = hipGetLastError();
+int64_t ssm_scan_groups(const SsmLayer& l, int32_t n_seqs, int64_t n_tokens) {
+  const int64_t hb = l.H / heads_per_wg(l), units = n_tokens / (kChunk * kSegUnit) + n_seqs;
+  return std::max((units * l.G + 8) * (hb / l.G), n_tokens / kChunk + n_seqs);
+}
+
+hipError_t launch_ssm_scan(const SsmScanArgs& a, const int32_t* cu_host, void* workspace, hipStream_t st) {
+  const int segs = max_segments(a.l, a.n_seqs, cu_host);
+  const Ws w = layout(a.l, a.n_seqs, a.n_tokens, segs > 1, workspace);
+  hipError_t e = a.l.P == 32 ? launch_p<32>(a, w, segs, st) : a.l.P == 64 ? launch_p<64>(a, w, segs, st) : launch_p<128>(a, w, segs, st);
   const int gy = (a.l.conv_dim + 255) / 256;
   // the checkpoints' windows read conv_in, which the prompts' own may overwrite: before them
   if (e == hipSuccess && a.conv_ckpt && a.n_ckpt > 0) {
