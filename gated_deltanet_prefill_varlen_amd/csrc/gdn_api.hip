@@ -701,7 +701,7 @@ gdn_status gdn_ssm_prefill_packed(
   a.conv_out = static_cast<uint16_t*>(conv_state_out);
   a.conv_ckpt = static_cast<uint16_t*>(conv_ckpt);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  return finish_launch(gdn::launch_ssm_scan(a, cu_seqlens_host, workspace, s), s);
+  return finish_launch(gdn::launch_ssm_scan(a, cu_seqlens_host, ckpt_positions_host, workspace, s), s);
 }
 
 gdn_status gdn_ssm_decode(const gdn_ssm_shape* shape, int32_t batch, int32_t n_tok, const void* x,

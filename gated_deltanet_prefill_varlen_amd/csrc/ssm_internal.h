@@ -70,7 +70,8 @@ struct NormArgs {
   float* scales;           // [n_rows, dim / scale_block or 1]
 };
 
-hipError_t launch_ssm_scan(const SsmScanArgs& a, const int32_t* cu_host, void* workspace, hipStream_t stream);
+hipError_t launch_ssm_scan(const SsmScanArgs& a, const int32_t* cu_host, const int32_t* ckpt_host, void* workspace,
+                           hipStream_t stream);
 int64_t ssm_scan_bytes(const SsmLayer& l, int32_t n_seqs, const int32_t* cu_host);
 int64_t ssm_scan_groups(const SsmLayer& l, int32_t n_seqs, int64_t n_tokens);   // workgroups of its largest launch, at most
 hipError_t launch_ssm_decode(const SsmDecodeArgs& a, hipStream_t stream);

@@ -55,6 +55,16 @@ __device__ __forceinline__ f16x2 pack_f16(float a, float b) { return __builtin_c
 // x < 2^pow2_above(x) for finite x >= 0, within -100 .. 110.
 __device__ __forceinline__ int pow2_above(float x) { return min(max((int)(__float_as_uint(x) >> 23) - 126, -100), 110); }
 
+// x of another lane.
+__device__ __forceinline__ int from_lane(int x, int src) { return __builtin_amdgcn_ds_bpermute(src << 2, x); }
+__device__ __forceinline__ float from_lane(float x, int src) { return __int_as_float(from_lane(__float_as_int(x), src)); }
+// A value that the compiler takes for a new one: what is computed from it in a
+// rare path stays there, instead of in registers over the whole loop.
+__device__ __forceinline__ int anew(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 template <typename Op>
 __device__ __forceinline__ float over_wave(float x, Op op) {
   x = op(x, dpp_f32<0xB1>(x));
@@ -66,9 +76,16 @@ __device__ __forceinline__ float over_wave(float x, Op op) {
 }
 struct MaxOp { __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); } };
 // The largest over the lane groups: of the lanes that hold the same channels.
-__device__ __forceinline__ float over_groups(float x) {
-  x = fmaxf(x, __shfl_xor(x, 16));
-  return fmaxf(x, __shfl_xor(x, 32));
+__device__ __forceinline__ float over_groups(float x, int lane) {
+  x = fmaxf(x, from_lane(x, lane ^ 16));
+  return fmaxf(x, from_lane(x, lane ^ 32));
+}
+// The largest over a wave of what is the same in its lane groups.
+__device__ __forceinline__ float over_wave16(float x) {
+  x = fmaxf(x, dpp_f32<0xB1>(x));
+  x = fmaxf(x, dpp_f32<0x4E>(x));
+  x = fmaxf(x, dpp_f32<0x141>(x));
+  return fmaxf(x, dpp_f32<0x140>(x));
 }
 struct AddOp { __device__ __forceinline__ float operator()(float a, float b) const { return a + b; } };
 
@@ -91,8 +108,8 @@ constexpr int kSegUnit = 4;               // chunks a segment has at least
 // Chunks of a segment for a prompt of nc chunks whose chunk row takes hb
 // workgroups.
 __host__ __device__ inline int seg_chunks(int nc, int hb) {
-  if (nc < 4 * kSegUnit) return nc > 0 ? nc : 1;
-  const int want = (512 + hb - 1) / hb, most = nc / kSegUnit, n = want < most ? want : most;
+  if (nc <= 16) return nc > 0 ? nc : 1;
+  const int want = (256 + hb - 1) / hb, most = nc / kSegUnit, n = want < most ? want : most;
   return (nc + n - 1) / n;
 }
 
@@ -291,8 +308,10 @@ __device__ __forceinline__ void prepare_steps(const SsmScanArgs& a, const Ws& w,
   float* tab = w.tab + ((int64_t)(t0 / kChunk + s + c) * a.l.H + h) * kTab;
   tab[lane] = dt;
   tab[64 + lane] = cum;
-  tab[128 + lane] = wt;
-  if (lane < 4) tab[192 + lane] = lane == 0 ? total : lane == 1 ? wmax : lane == 2 ? dmax : __builtin_amdgcn_exp2f(total);
+  const int kw = 10 - pow2_above(wmax);
+  tab[128 + lane] = ldexpf(wt, kw);
+  if (lane < 5)
+    tab[192 + lane] = lane == 0 ? total : lane == 1 ? wmax : lane == 2 ? dmax : lane == 3 ? __builtin_amdgcn_exp2f(total) : __int_as_float(kw);
 }
 
 template <int N>
@@ -309,24 +328,108 @@ __global__ void __launch_bounds__(256) ssm_prepare_kernel(const SsmScanArgs a, c
 }
 
 // ------------------------------------------------------------------ scan --
-// Copies 16 bytes a lane from global memory to LDS, at the wave's base.
-__device__ __forceinline__ void to_lds(const void* g, void* base) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g, (__attribute__((address_space(3))) void*)base,
-                                   16, 0, 0);
+// Copies 16 bytes a lane from global memory to LDS, from the wave's base on.
+// The compiler does not see it and so waits for none before other reads of
+// LDS: an s_waitcnt vmcnt(0) and a barrier stand between it and its readers.
+__device__ __forceinline__ void to_lds(const void* g, const void* base) {
+  const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)base;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(g) : "memory", "m0");
 }
+__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// What a wave keeps of a prompt's inputs: the two channels 2 r, 2 r + 1 of its
-// 32 in one dword, at the tokens of its lane group and the three before each
-// run of four.
+// What a wave keeps of a chunk's inputs: the two channels 2 r, 2 r + 1 of its 32
+// in one dword, at the tokens of its lane group (runs of four: 16 run + 4 g ..)
+// and the three before each run.
 struct RawX { uint32_t v[4][7]; };
 
-template <int P, int N, bool OUT>
+// Where a wave's inputs lie.
+struct XRef {
+  const uint16_t* x;       // the prompt's first row
+  const uint16_t* hist;    // the prompt's window [3][conv_dim], or nullptr
+  int64_t stride;
+  int conv_dim, len, ch0;  // ch0: this lane's first channel
+};
+
+// Rows past the prompt's end read as 0 by the buffer's range check, as do the
+// ones before its start, whose place the window takes.
+template <bool CONV>
+__device__ __forceinline__ void load_x(const XRef& f, int c, int g, RawX& x) {
+  uint32_t row = (uint32_t)f.stride * 2;
+  asm volatile("" : "+s"(row));   // (offsets kept over the chunks would take 28 registers)
+  const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint16_t*>(f.x + (int64_t)(c * kChunk - 3) * f.stride), 0, (min(f.len - c * kChunk, kChunk) + 3) * row, 0x00020000);
+  const bool before = c == 0 && g == 0;
+#pragma unroll
+  for (int i = CONV ? 0 : 3; i < 7; ++i) {
+    const uint32_t at = (4 * g + i) * row + 2 * f.ch0;
+    x.v[0][i] = __builtin_amdgcn_raw_buffer_load_b32(buf, i < 3 && before ? 0xFFFFFFF0u : at, 0, 0);
+#pragma unroll
+    for (int run = 1; run < 4; ++run) x.v[run][i] = __builtin_amdgcn_raw_buffer_load_b32(buf, at + 16 * run * row, 0, 0);
+  }
+  if (CONV && c == 0 && f.hist) {
+    const uint16_t* p = f.hist + anew(f.ch0);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (g == 0) x.v[0][i] = *reinterpret_cast<const uint32_t*>(p + (int64_t)i * f.conv_dim);
+  }
+}
+
+// The convolution of a channel pair; v[q][run][i]: channel 2 r + q at token
+// 16 run + 4 g + i.
+struct ConvW { float w0[2], w1[2], w2[2], w3[2], b[2]; };
+template <bool CONV>
+__device__ __forceinline__ void conv_x(const RawX& x, const ConvW& k, float (&v)[2][4][4]) {
+#pragma unroll
+  for (int run = 0; run < 4; ++run) {
+    float in[2][7];
+#pragma unroll
+    for (int i = CONV ? 0 : 3; i < 7; ++i) { in[0][i] = lo_bf16(x.v[run][i]); in[1][i] = hi_bf16(x.v[run][i]); }
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[q][run][i] = CONV ? conv4_bias_silu(k.b[q], k.w0[q], k.w1[q], k.w2[q], k.w3[q], in[q][i], in[q][i + 1], in[q][i + 2], in[q][i + 3])
+                            : in[q][i + 3];
+  }
+}
+
+__device__ __forceinline__ f16x8 join(f16x2 a, f16x2 b, f16x2 c, f16x2 d) { return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]}; }
+
+// One (16 t, 32 s) operand of M^T: tiles st = 2 KS and 2 KS + 1 of the tile row TT.
+template <int TT, int KS>
+__device__ __forceinline__ f16x8 weigh(const f32x4* gt, const float* tab, int lane, int ad, float dm) {
+  const int r = lane & 15, g = lane >> 4;
+  const float ct = tab[64 + 16 * TT + r] + (float)ad;
+  f16x2 o[4];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int st = 2 * KS + q;
+    if (st > TT) { o[2 * q] = o[2 * q + 1] = f16x2{0, 0}; continue; }
+    const f32x4 gv = gt[(TT * (TT + 1) / 2 + st) * 64 + lane];
+    const f32x4 cs = *reinterpret_cast<const f32x4*>(tab + 64 + 16 * st + 4 * g);
+    const f32x4 ds = *reinterpret_cast<const f32x4*>(tab + 16 * st + 4 * g);
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = gv[j] * (ds[j] * __builtin_amdgcn_exp2f(ct - cs[j]));
+      if (st == TT) v[j] = 4 * g + j < r ? v[j] : 4 * g + j == r ? v[j] + dm : 0.f;
+    }
+    o[2 * q] = pack_f16(v[0], v[1]);
+    o[2 * q + 1] = pack_f16(v[2], v[3]);
+  }
+  return join(o[0], o[1], o[2], o[3]);
+}
+
+template <int P, int N, bool OUT, bool CONV>
 __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, const Ws w, int hpw, int split, int grouped) {
   constexpr int WPH = P / 32, NT = N / 16, KN = N / 32, OPS = kChunk * N * 2;   // bytes of one operand
-  constexpr int HMAX = 4 / WPH;
-  __shared__ __align__(16) char ops[3 * OPS];
+  constexpr int HMAX = 4 / WPH, GT = 10 * 1024;
+  // C, B^T hi, B^T lo (without the convolution B is exact in fp16: no lo)
+  constexpr int FIRST = OUT ? 0 : OPS, LAST = CONV ? 3 * OPS : 2 * OPS;
+  __shared__ __align__(16) char ops[LAST - FIRST];
+  __shared__ __align__(16) char gts[OUT ? GT : 16];
   __shared__ __align__(16) f16x8 fm[OUT ? HMAX : 1][6][64];
-  __shared__ __align__(16) float tabs[HMAX][kTab];
+  __shared__ __align__(16) float tabs[2][HMAX][kTab];
   const SsmLayer& l = a.l;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int nw = hpw * WPH, hl = wave / WPH, half = wave % WPH;
@@ -351,44 +454,43 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
 
   const int h = b * hpw + hl, grp = h / (l.H / l.G), ch0 = h * P + 32 * half + 2 * r;
   const int64_t hpn = (int64_t)l.P * l.N, slot0 = t0 / kChunk + s;
-  const int64_t st_at = (int64_t)(32 * half + 2 * r) * N + 4 * g;       // this lane's entries of a head's state
-  float w0[2], w1[2], w2[2], w3[2], wb[2] = {0.f, 0.f};
-  if (l.conv_w) {
+  const int st_at = (32 * half + 2 * r) * N + 4 * g;       // this lane's entries of a head's state
+  const XRef xref{a.x + (int64_t)t0 * a.x_stride, a.conv_in ? a.conv_in + (int64_t)s * 3 * l.conv_dim : nullptr, a.x_stride, l.conv_dim, len, ch0};
+  // The operands of a chunk are fetched while the one before is worked on:
+  // B^T, C . B and the tables once the update of the state is through, C once
+  // the outputs are.
+  auto fetch = [&](int c) __attribute__((always_inline)) {
+    const int64_t sg = (slot0 + c) * l.G + grp;
+    const char* src = w.bc + sg * 3 * OPS;
+    for (int i = OPS / 1024 + wave; i < LAST / 1024; i += nw) to_lds(src + 1024 * i + 16 * lane, ops + 1024 * i - FIRST);
+    if (OUT)
+      for (int i = wave; i < GT / 1024; i += nw) to_lds(reinterpret_cast<const char*>(w.gt) + sg * GT + 1024 * i + 16 * lane, gts + 1024 * i);
+    if (half == 0) to_lds(w.tab + ((slot0 + c) * l.H + h) * kTab + 4 * lane, tabs[c & 1][hl]);
+  };
+  RawX x;
+  if (c_first < c_end) {
+    fetch(c_first);
+    load_x<CONV>(xref, c_first, g, x);
+  }
+  ConvW cw;
+  if (CONV) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float4 q = reinterpret_cast<const float4*>(l.conv_w)[ch0 + e];
-      w0[e] = conv_tap(q.x); w1[e] = conv_tap(q.y); w2[e] = conv_tap(q.z); w3[e] = conv_tap(q.w);
-      if (l.conv_bias) wb[e] = conv_tap(l.conv_bias[ch0 + e]);
+    for (int q = 0; q < 2; ++q) {
+      const float4 t = reinterpret_cast<const float4*>(l.conv_w)[ch0 + q];
+      cw.w0[q] = conv_tap(t.x); cw.w1[q] = conv_tap(t.y); cw.w2[q] = conv_tap(t.z); cw.w3[q] = conv_tap(t.w);
+      cw.b[q] = l.conv_bias ? conv_tap(l.conv_bias[ch0 + q]) : 0.f;
     }
   }
   const float D = OUT && l.D ? l.D[h] : 0.f;
 
-  RawX x;
-  auto load_x = [&](int c) __attribute__((always_inline)) {
-    const int left = len - c * kChunk;
-    const uint16_t* base = a.x + (int64_t)(t0 + c * kChunk) * a.x_stride + ch0;
-#pragma unroll
-    for (int run = 0; run < 4; ++run)
-#pragma unroll
-      for (int i = 0; i < 7; ++i) {
-        if (i < 3 && !l.conv_w) continue;
-        const int p = 16 * run + 4 * g - 3 + i;
-        if (i < 3 && run == 0 && c == 0 && p < 0) {
-          x.v[run][i] = a.conv_in ? *reinterpret_cast<const uint32_t*>(a.conv_in + ((int64_t)s * 3 + 3 + p) * l.conv_dim + ch0) : 0u;
-        } else {
-          x.v[run][i] = *reinterpret_cast<const uint32_t*>(base + (int64_t)min(p, left - 1) * a.x_stride);
-        }
-      }
-  };
-
-  // the state that enters, S^T in tiles [16 n][16 p], scaled by 2^e
+  // the state that enters, S^T in tiles [16 n][16 p], scaled by 2^e; `bound`:
+  // no entry of the channel is larger
   f32x4 S[NT][2];
   int e[2] = {0, 0};
   float bound[2] = {0.f, 0.f};
   const float* from = !OUT ? nullptr
                       : k > 0 ? w.seg + (((int64_t)unit - 1) * l.H + h) * hpn
                       : a.init ? a.init + ((int64_t)s * l.H + h) * hpn : nullptr;
-  if (c_first < c_end) load_x(c_first);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -403,15 +505,18 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) bound[q] = fmaxf(bound[q], finite_abs(S[nt][q][i]));
-      bound[q] = over_groups(bound[q]);
+      bound[q] = over_groups(bound[q], lane);
       e[q] = kTopS - pow2_above(bound[q]);
+      const float f = ldexpf(1.f, e[q]);     // (e is within -80 .. 130: past 127 by parts)
+      const float f0 = e[q] > 126 ? 0x1p100f : f, f1 = e[q] > 126 ? ldexpf(1.f, e[q] - 100) : 1.f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) S[nt][q][i] = ldexpf(S[nt][q][i], e[q]);
+        for (int i = 0; i < 4; ++i) S[nt][q][i] = S[nt][q][i] * f0 * f1;
     }
   }
-  auto store_state = [&](float* to) __attribute__((always_inline)) {
+  auto store_state = [&](float* head) __attribute__((always_inline)) {
+    float* to = head + anew(st_at);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -419,79 +524,62 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
         f32x4 v;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = ldexpf(S[nt][q][i], -e[q]);
-        *reinterpret_cast<f32x4*>(to + st_at + q * N + 16 * nt) = v;
+        *reinterpret_cast<f32x4*>(to + q * N + 16 * nt) = v;
       }
   };
   int ci = 0, next = INT_MAX;
   if (OUT) {
     ci = lower_bound_i32(a.ckpt, a.n_ckpt, t0 + c_first * kChunk + 1);
     if (ci < a.n_ckpt) next = a.ckpt[ci];
+    ci = __builtin_amdgcn_readfirstlane(ci);
+    next = __builtin_amdgcn_readfirstlane(next);
   }
+  auto keep_until = [&](int end) __attribute__((always_inline)) {
+    while (next < end) {
+      store_state(a.ckpt_buf + ((int64_t)ci * l.H + h) * hpn);
+      ++ci;
+      next = __builtin_amdgcn_readfirstlane(ci < a.n_ckpt ? a.ckpt[ci] : INT_MAX);
+    }
+  };
   float seg_sum = 0.f;
+  const f16x8* fc = reinterpret_cast<const f16x8*>(ops) + lane;
+  const f16x8* bh = reinterpret_cast<const f16x8*>(ops + OPS - FIRST) + lane;
+  const f16x8* bl = reinterpret_cast<const f16x8*>(ops + (CONV ? 2 * OPS : OPS) - FIRST) + lane;
 
   for (int c = c_first; c < c_end; ++c) {
     const int64_t sg = (slot0 + c) * l.G + grp;
     const int left = min(kChunk, len - c * kChunk);
-    __syncthreads();   // the last chunk's operands have been read
-    {
-      const char* src = w.bc + sg * 3 * OPS;
-      for (int i = (OUT ? 0 : OPS / 1024) + wave; i < 3 * OPS / 1024; i += nw) to_lds(src + 1024 * i + 16 * lane, ops + 1024 * i);
-      if (half == 0) to_lds(w.tab + ((slot0 + c) * l.H + h) * kTab + 4 * lane, tabs[hl]);
-    }
+    // a checkpoint at the chunk's start gets the state that enters it, and so
+    // does one inside, to which a launch behind this one adds the tokens
+    if (OUT) keep_until(t0 + c * kChunk + left);
     const int2 kk = w.k[sg];
     const int kbt = kk.x, kb = kbt - kTopBt + kTopB, kc = kk.y;
-    // the tiles of C . B that this wave weighs
-    f32x4 gv[(6 + WPH - 1) / WPH][2];
-    if (OUT) {
-      const f32x4* gt = reinterpret_cast<const f32x4*>(w.gt + sg * 10 * 256) + lane;
-#pragma unroll
-      for (int i = 0; i < (6 + WPH - 1) / WPH; ++i) {
-        const int f = half + WPH * i;
-        if (f < 6) {
-          const int tt = f < 2 ? f : (f + 2) / 2, ks = f < 2 ? 0 : f % 2;
-#pragma unroll
-          for (int q = 0; q < 2; ++q) gv[i][q] = gt[(tt * (tt + 1) / 2 + min(2 * ks + q, tt)) * 64];
-        }
-      }
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    const float* tab = tabs[hl];
-    const float alpha = tab[195], wmax = tab[193], dmax = tab[194];
-
-    // x through the convolution: x2[q][run][i] = channel 2 r + q at token 16 run + 4 g + i
     float xv[2][4][4];
-    float xmax[2] = {0.f, 0.f}, odd = 0.f;
+    conv_x<CONV>(x, cw, xv);
+    float xmax[2] = {0.f, 0.f};
 #pragma unroll
     for (int q = 0; q < 2; ++q)
 #pragma unroll
-      for (int run = 0; run < 4; ++run) {
-        float in[7];
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-          if (i >= 3 || l.conv_w) in[i] = q ? hi_bf16(x.v[run][i]) : lo_bf16(x.v[run][i]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float u = l.conv_w ? conv4_bias_silu(wb[q], w0[q], w1[q], w2[q], w3[q], in[i], in[i + 1], in[i + 2], in[i + 3]) : in[i + 3];
-          xv[q][run][i] = u;
-          xmax[q] = fmaxf(xmax[q], fabsf(u));
-          odd = fmaf(u, 0.f, odd);     // NaN once a value is not finite
-        }
-      }
-    if (c + 1 < c_end) load_x(c + 1);
-    const bool bad = __ballot(odd != odd) != 0;
-    if (bad) {
+      for (int i = 0; i < 16; ++i) xmax[q] = fmaxf(xmax[q], fabsf(xv[q][i / 4][i % 4]));   // (NaN is passed over)
+    if (__ballot(!(fmaxf(xmax[0], xmax[1]) < __builtin_inff()))) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         xmax[q] = 0.f;
 #pragma unroll
-        for (int run = 0; run < 4; ++run)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) xmax[q] = fmaxf(xmax[q], finite_abs(xv[q][run][i]));
+        for (int i = 0; i < 16; ++i) xmax[q] = fmaxf(xmax[q], finite_abs(xv[q][i / 4][i % 4]));
       }
     }
 #pragma unroll
-    for (int q = 0; q < 2; ++q) xmax[q] = over_groups(xmax[q]);
+    for (int q = 0; q < 2; ++q) xmax[q] = over_groups(xmax[q], lane);
+    arrived();
+    __syncthreads();   // B^T, C . B and the tables are whole; the last outputs are through with C and M
+    if (OUT) {
+      const char* src = w.bc + sg * 3 * OPS;
+      for (int i = wave; i < OPS / 1024; i += nw) to_lds(src + 1024 * i + 16 * lane, ops + 1024 * i);
+    }
+    const float* tab = tabs[c & 1][hl];
+    const float alpha = tab[195], wmax = tab[193], dmax = tab[194];
+    const int kw = __float_as_int(tab[196]);
 
     // the weights inside the chunk, as operands: element (t = column, s) of M^T
     int m = 0;
@@ -499,213 +587,81 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
       const int ad = min(-pow2_above(dmax), 14 - pow2_above(fabsf(D)) - (kb + kc));
       m = kb + kc + ad;
       const float dm = ldexpf(D, m);
-#pragma unroll
-      for (int i = 0; i < (6 + WPH - 1) / WPH; ++i) {
-        const int f = half + WPH * i;
-        if (f < 6) {
-          const int tt = f < 2 ? f : (f + 2) / 2, ks = f < 2 ? 0 : f % 2;
-          const float ct = tab[64 + 16 * tt + r];
-          f16x8 o;
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int st = 2 * ks + q;
-            const f32x4 cs = *reinterpret_cast<const f32x4*>(tab + 64 + 16 * min(st, tt) + 4 * g);
-            const f32x4 ds = *reinterpret_cast<const f32x4*>(tab + 16 * min(st, tt) + 4 * g);
-            float v[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              v[j] = gv[i][q][j] * (ldexpf(ds[j], ad) * __builtin_amdgcn_exp2f(ct - cs[j]));
-              if (st == tt) v[j] = 4 * g + j < r ? v[j] : 4 * g + j == r ? v[j] + dm : 0.f;
-              if (st > tt) v[j] = 0.f;
-            }
-            const f16x2 p0 = pack_f16(v[0], v[1]), p1 = pack_f16(v[2], v[3]);
-            o[4 * q] = p0[0]; o[4 * q + 1] = p0[1]; o[4 * q + 2] = p1[0]; o[4 * q + 3] = p1[1];
-          }
-          fm[hl][f][lane] = o;
-        }
-      }
+      const f32x4* gt = reinterpret_cast<const f32x4*>(gts);
+      if (0 % WPH == half) fm[hl][0][lane] = weigh<0, 0>(gt, tab, lane, ad, dm);
+      if (1 % WPH == half) fm[hl][1][lane] = weigh<1, 0>(gt, tab, lane, ad, dm);
+      if (2 % WPH == half) fm[hl][2][lane] = weigh<2, 0>(gt, tab, lane, ad, dm);
+      if (3 % WPH == half) fm[hl][3][lane] = weigh<2, 1>(gt, tab, lane, ad, dm);
+      if (4 % WPH == half) fm[hl][4][lane] = weigh<3, 0>(gt, tab, lane, ad, dm);
+      if (5 % WPH == half) fm[hl][5][lane] = weigh<3, 1>(gt, tab, lane, ad, dm);
     }
+    __builtin_amdgcn_sched_barrier(0);
 
-    // operands of x, for the outputs (x 2^kx) and for the state (x w, in pairs)
-    f16x8 xo[OUT ? 2 : 1][2], xh[2][2], xl[2][2];
-    int kx[2], e_new[2];
-    float fx[2], grown[2];
+    // x as operand of the outputs: times 2^kx, one power for the wave; x w of
+    // the state, in pairs: times 2^(kw + ks), one power for the channel
+    const float xw = OUT ? over_wave16(fmaxf(xmax[0], xmax[1])) : 0.f;
+    const int kx = !OUT || (xw >= 0.125f && xw < 32768.f) ? 0 : 14 - pow2_above(xw);
+    int ks[2], e_new[2];
+    float grown[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      kx[q] = xmax[q] >= 0.125f && xmax[q] < 32768.f ? 0 : 14 - pow2_above(xmax[q]);
-      fx[q] = ldexpf(1.f, kx[q]);
       grown[q] = fmaf(alpha, bound[q], ldexpf(64.f * wmax * xmax[q], kTopBt - kbt));
-      e_new[q] = kTopS - pow2_above(grown[q]);
+      ks[q] = xmax[q] >= 0x1p-6f && xmax[q] < 16.f ? 0 : 4 - pow2_above(xmax[q]);
+      ks[q] = min(ks[q], 90 - pow2_above(grown[q]) - kbt - kw);     // the state stays inside fp32
+      e_new[q] = kbt + kw + ks[q];
     }
-    const bool plain = __ballot((kx[0] | kx[1]) != 0) == 0;
+    const bool plain = __ballot((kx | ks[0] | ks[1]) != 0) == 0;
+    f16x8 xo[2][2], xh[2][2], xl[2][2], so[2][KN];
+    if (OUT) {
+      if (!plain) {
+        const float f = ldexpf(1.f, kx);
 #pragma unroll
-    for (int run = 0; run < 4; ++run) {
-      const f32x4 wv = *reinterpret_cast<const f32x4*>(tab + 128 + 16 * run + 4 * g);
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) xv[q][i / 4][i % 4] *= f;
+      }
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          const float u0 = xv[q][run][i], u1 = xv[q][run][i + 1];
-          if (OUT) {
-            const f16x2 o = plain ? pack_f16(u0, u1) : pack_f16(u0 * fx[q], u1 * fx[q]);
-            xo[q][run / 2][4 * (run % 2) + i] = o[0];
-            xo[q][run / 2][4 * (run % 2) + i + 1] = o[1];
-          }
-          const float v0 = u0 * ldexpf(wv[i], e_new[q] - kbt), v1 = u1 * ldexpf(wv[i + 1], e_new[q] - kbt);
-          const f16x2 hi = pack_f16(v0, v1), lo = pack_f16(fmaf((float)hi[0], -1.f, v0), fmaf((float)hi[1], -1.f, v1));
-          xh[q][run / 2][4 * (run % 2) + i] = hi[0];
-          xh[q][run / 2][4 * (run % 2) + i + 1] = hi[1];
-          xl[q][run / 2][4 * (run % 2) + i] = lo[0];
-          xl[q][run / 2][4 * (run % 2) + i + 1] = lo[1];
-        }
+        for (int z = 0; z < 2; ++z)
+          xo[q][z] = join(pack_f16(xv[q][2 * z][0], xv[q][2 * z][1]), pack_f16(xv[q][2 * z][2], xv[q][2 * z][3]),
+                          pack_f16(xv[q][2 * z + 1][0], xv[q][2 * z + 1][1]), pack_f16(xv[q][2 * z + 1][2], xv[q][2 * z + 1][3]));
     }
-
-    if (OUT) {
-      int first_bad[2] = {INT_MAX, INT_MAX};    // first token of channels 2 r, 2 r + 1 that is not finite
-      if (bad) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-#pragma unroll
-          for (int run = 3; run >= 0; --run)
-#pragma unroll
-            for (int i = 3; i >= 0; --i)
-              if (!(fabsf(xv[q][run][i]) < __builtin_inff())) {
-                first_bad[q] = 16 * run + 4 * g + i;
-                xo[q][run / 2][4 * (run % 2) + i] = (_Float16)0.f;
-              }
-          first_bad[q] = min(first_bad[q], __shfl_xor(first_bad[q], 16));
-          first_bad[q] = min(first_bad[q], __shfl_xor(first_bad[q], 32));
-        }
-      }
-      f16x8 so[2][KN];   // the entering state as an operand
+    if (!plain) {
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int ks = 0; ks < KN; ++ks)
+        for (int i = 0; i < 16; ++i) xv[q][i / 4][i % 4] = ldexpf(xv[q][i / 4][i % 4], ks[q] - kx);
+    }
 #pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            constexpr float down = 1.f / (1 << (kTopS - kTopS16));
-            const f16x2 v = pack_f16(S[2 * ks + j / 4][q][j % 4] * down, S[2 * ks + j / 4][q][j % 4 + 1] * down);
-            so[q][ks][j] = v[0];
-            so[q][ks][j + 1] = v[1];
-          }
-      __syncthreads();   // M is whole
-      // scales of the rows that the accumulators of the outputs hold
-      float f1[4][2], f2[4][2];
+    for (int z = 0; z < 2; ++z) {
+      const f32x4 wa = *reinterpret_cast<const f32x4*>(tab + 128 + 32 * z + 4 * g), wb = *reinterpret_cast<const f32x4*>(tab + 144 + 32 * z + 4 * g);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int q = 0; q < 2; ++q) {
+        f16x2 hi[4], lo[4];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          f1[i][q] = ldexpf(1.f, max(-126, min(126, kTopS - kTopS16 - (__shfl(e[q], 4 * g + i) + kc))));
-          f2[i][q] = ldexpf(1.f, max(-126, min(126, -(m + __shfl(kx[q], 4 * g + i)))));
+        for (int i = 0; i < 4; ++i) {
+          const f32x4& wt = i < 2 ? wa : wb;
+          const float v0 = xv[q][2 * z + i / 2][2 * (i % 2)] * wt[2 * (i % 2)], v1 = xv[q][2 * z + i / 2][2 * (i % 2) + 1] * wt[2 * (i % 2) + 1];
+          hi[i] = pack_f16(v0, v1);
+          lo[i] = pack_f16(fmaf((float)hi[i][0], -1.f, v0), fmaf((float)hi[i][1], -1.f, v1));
         }
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        f32x4 y1[2], y2[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) y1[q] = y2[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ks = 0; ks < KN; ++ks) {
-          const f16x8 cf = reinterpret_cast<const f16x8*>(ops)[(tt * KN + ks) * 64 + lane];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) y1[q] = mma(so[q][ks], cf, y1[q]);
-        }
-#pragma unroll
-        for (int ks = 0; ks <= tt / 2; ++ks) {
-          const f16x8 mf = fm[hl][tt < 2 ? tt : 2 * tt - 2 + ks][lane];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) y2[q] = mma(xo[q][ks], mf, y2[q]);
-        }
-        const int t = 16 * tt + r;
-        const float ec = __builtin_amdgcn_exp2f(tab[64 + t]);
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int q = 0; q < 2; ++q) y[2 * i + q] = fmaf(y2[q][i], f2[i][q], y1[q][i] * (f1[i][q] * ec));
-        if (bad) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-              if (t >= __shfl(first_bad[q], 4 * g + i)) y[2 * i + q] = __builtin_nanf("");
-        }
-        if (t < left) {
-          uint4 o;
-          o.x = pack_bf16(y[0], y[1]); o.y = pack_bf16(y[2], y[3]); o.z = pack_bf16(y[4], y[5]); o.w = pack_bf16(y[6], y[7]);
-          *reinterpret_cast<uint4*>(a.out + ((int64_t)(t0 + c * kChunk + t) * l.H + h) * P + 32 * half + 8 * g) = o;
-        }
+        xh[q][z] = join(hi[0], hi[1], hi[2], hi[3]);
+        xl[q][z] = join(lo[0], lo[1], lo[2], lo[3]);
       }
     }
-
-    const f16x8* bh = reinterpret_cast<const f16x8*>(ops + OPS) + lane;
-    const f16x8* bl = reinterpret_cast<const f16x8*>(ops + 2 * OPS) + lane;
-    // checkpoints inside the chunk: the entering state and the tokens up to there
+    float f1 = 0.f;
     if (OUT) {
-      while (next < t0 + c * kChunk + left) {
-        const int last = next - (t0 + c * kChunk) - 1;      // its last token in the chunk
-        const float upto = tab[64 + last], al = __builtin_amdgcn_exp2f(upto);
-        int ec[2];
-        float mul[2];
+      // the entering state as an operand: times 2^es, one power for the wave
+      const int es = kTopS16 - pow2_above(over_wave16(fmaxf(bound[0], bound[1])));
+      f1 = ldexpf(1.f, max(-126, min(126, -(es + kc))));
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          ec[q] = min(kbt + 14 - pow2_above(dmax * xmax[q]), 100 - pow2_above(al * bound[q]));
-          mul[q] = ldexpf(al, ec[q] - e[q]);
-        }
-        f16x8 ch[2][2], cl[2][2];
-        uint4 keep[2];                                       // of each operand of B, the tokens up to there
+      for (int q = 0; q < 2; ++q) {
+        const float down = ldexpf(1.f, es - e[q]);
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          uint32_t mask[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int t = slot_of(ks, g, j);
-            const bool in = t <= last;
-            if (in) mask[j / 2] |= 0xFFFFu << (16 * (j % 2));
-            const float wt = tab[t] * __builtin_amdgcn_exp2f(upto - tab[64 + t]);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const float v = in ? xv[q][2 * ks + j / 4][j % 4] * ldexpf(wt, ec[q] - kbt) : 0.f;
-              ch[q][ks][j] = (_Float16)v;
-              cl[q][ks][j] = (_Float16)(v - (float)ch[q][ks][j]);
-            }
-          }
-          keep[ks] = make_uint4(mask[0], mask[1], mask[2], mask[3]);
-        }
-        float* to = a.ckpt_buf + ((int64_t)ci * l.H + h) * hpn + st_at;
-#pragma unroll 1
-        for (int nt = 0; nt < NT; ++nt) {
-          f32x4 acc[2];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-#pragma unroll
-            for (int z = 0; z < NT; ++z)
-              if (z == nt) acc[q] = S[z][q];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[q][i] *= mul[q];
-          }
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            uint4 u = __builtin_bit_cast(uint4, bh[(nt * 2 + ks) * 64]), v = __builtin_bit_cast(uint4, bl[(nt * 2 + ks) * 64]);
-            u.x &= keep[ks].x; u.y &= keep[ks].y; u.z &= keep[ks].z; u.w &= keep[ks].w;
-            v.x &= keep[ks].x; v.y &= keep[ks].y; v.z &= keep[ks].z; v.w &= keep[ks].w;
-            const f16x8 fh = __builtin_bit_cast(f16x8, u), fl = __builtin_bit_cast(f16x8, v);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              acc[q] = mma(fh, ch[q][ks], acc[q]);
-              acc[q] = mma(fl, ch[q][ks], acc[q]);
-              acc[q] = mma(fh, cl[q][ks], acc[q]);
-            }
-          }
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[q][i] = ldexpf(acc[q][i], -ec[q]);
-            *reinterpret_cast<f32x4*>(to + q * N + 16 * nt) = acc[q];
-          }
-        }
-        ++ci;
-        next = ci < a.n_ckpt ? a.ckpt[ci] : INT_MAX;
+        for (int z = 0; z < KN; ++z)
+          so[q][z] = join(pack_f16(S[2 * z][q][0] * down, S[2 * z][q][1] * down), pack_f16(S[2 * z][q][2] * down, S[2 * z][q][3] * down),
+                          pack_f16(S[2 * z + 1][q][0] * down, S[2 * z + 1][q][1] * down), pack_f16(S[2 * z + 1][q][2] * down, S[2 * z + 1][q][3] * down));
       }
     }
 
@@ -719,34 +675,162 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      if (nt % 2 == 0) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int i = 0; i < 4; ++i) S[nt][q][i] *= mul[q];
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const f16x8 fh = bh[(nt * 2 + ks) * 64], fl = bl[(nt * 2 + ks) * 64];
+      for (int z = 0; z < 2; ++z) {
+        const f16x8 fh = bh[(nt * 2 + z) * 64];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          S[nt][q] = mma(fh, xh[q][ks], S[nt][q]);
-          S[nt][q] = mma(fl, xh[q][ks], S[nt][q]);
-          S[nt][q] = mma(fh, xl[q][ks], S[nt][q]);
+          S[nt][q] = mma(fh, xh[q][z], S[nt][q]);
+          S[nt][q] = mma(fh, xl[q][z], S[nt][q]);
+        }
+        if (CONV) {
+          const f16x8 fl = bl[(nt * 2 + z) * 64];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) S[nt][q] = mma(fl, xh[q][z], S[nt][q]);
         }
       }
     }
-    if (!OUT) seg_sum += tab[192];
-    if (OUT && next == t0 + c * kChunk + left) {
-      store_state(a.ckpt_buf + ((int64_t)ci * l.H + h) * hpn);
-      ++ci;
-      next = ci < a.n_ckpt ? a.ckpt[ci] : INT_MAX;
+    __builtin_amdgcn_sched_barrier(0);
+    if (!OUT) {
+      seg_sum += tab[192];
+      __syncthreads();   // the update is through with B^T
+      if (c + 1 < c_end) {
+        fetch(c + 1);
+        load_x<CONV>(xref, c + 1, g, x);
+      }
+      continue;
+    }
+
+    // a value of x that is not finite has left none of its channel's state
+    // finite; in the products inside the chunk it would reach the tokens
+    // before it, at weights of 0
+    int first_bad[2] = {INT_MAX, INT_MAX};
+    const bool bad = __ballot(!(fabsf(S[0][0][0]) + fabsf(S[0][1][0]) < __builtin_inff())) != 0;
+    if (bad) {
+      const int g2 = anew(g), lane2 = anew(lane);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+#pragma unroll
+        for (int j = 15; j >= 0; --j) {
+          if (!(fabsf((float)xo[q][j / 8][j % 8]) < __builtin_inff())) {
+            first_bad[q] = slot_of(j / 8, g2, j % 8);
+            xo[q][j / 8][j % 8] = (_Float16)0.f;
+          }
+        }
+        first_bad[q] = min(first_bad[q], from_lane(first_bad[q], lane2 ^ 16));
+        first_bad[q] = min(first_bad[q], from_lane(first_bad[q], lane2 ^ 32));
+      }
+    }
+    arrived();
+    __syncthreads();   // C and M are whole; the update is through with B^T
+    if (c + 1 < c_end) {
+      fetch(c + 1);
+      load_x<CONV>(xref, c + 1, g, x);
+    }
+    const float f2 = ldexpf(1.f, max(-126, min(126, -(m + kx))));
+    uint16_t* to = a.out + ((int64_t)(t0 + c * kChunk) * l.H + h) * P + 32 * half;
+    const uint32_t out_at = (uint32_t)(r * l.H * P + 8 * g);
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+      __builtin_amdgcn_sched_barrier(0);
+      // a tile of 16 tokens: with the entering state, and inside the chunk
+      f32x4 y1[2], y2[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) y1[q] = y2[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int z = 0; z < KN; ++z) {
+        const f16x8 cf = fc[(tt * KN + z) * 64];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) y1[q] = mma(so[q][z], cf, y1[q]);
+      }
+#pragma unroll
+      for (int z = 0; z <= tt / 2; ++z) {
+        const f16x8 mf = fm[hl][tt < 2 ? tt : 2 * tt - 2 + z][lane];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) y2[q] = mma(xo[q][z], mf, y2[q]);
+      }
+      const int t = 16 * tt + r;
+      const float fe = f1 * __builtin_amdgcn_exp2f(tab[64 + t]);
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) y[2 * i + q] = fmaf(y2[q][i], f2, y1[q][i] * fe);
+      if (bad) {
+        const int row = anew(4 * g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            if (t >= from_lane(first_bad[q], row + i)) y[2 * i + q] = __builtin_nanf("");
+      }
+      if (t < left) {
+        uint4 o;
+        o.x = pack_bf16(y[0], y[1]); o.y = pack_bf16(y[2], y[3]); o.z = pack_bf16(y[4], y[5]); o.w = pack_bf16(y[6], y[7]);
+        *reinterpret_cast<uint4*>(to + (int64_t)16 * tt * l.H * P + out_at) = o;
+      }
     }
   }
   if (!OUT) {
     store_state(w.seg + ((int64_t)unit * l.H + h) * hpn);
     if (lane == 0 && half == 0) w.seg_sum[(int64_t)unit * l.H + h] = seg_sum;
-  } else if (a.final_state && k + 1 == n_seg) {
-    store_state(a.final_state + ((int64_t)s * l.H + h) * hpn);
+  } else {
+    keep_until(min(t0 + len, t0 + c_end * kChunk) + 1);
+    if (a.final_state && k + 1 == n_seg) store_state(a.final_state + ((int64_t)s * l.H + h) * hpn);
   }
+}
+
+// Input of channel c at position p of prompt s (t0 = its first row; p < 0: its history).
+__device__ __forceinline__ uint16_t raw_at(const SsmScanArgs& a, int s, int t0, int p, int c) {
+  if (p >= 0) return a.x[(int64_t)(t0 + p) * a.x_stride + c];
+  return a.conv_in ? a.conv_in[((int64_t)s * 3 + 3 + p) * a.l.conv_dim + c] : 0;
+}
+
+// The state at a checkpoint inside a chunk, from the one that enters the chunk,
+// token by token (63 at most): a workgroup per 32 channels of a head, whose N
+// columns lie on N / 16 lanes.
+template <int N>
+__global__ void __launch_bounds__(2 * N) ssm_ckpt_kernel(const SsmScanArgs a) {
+  constexpr int LPR = N / 16, NCH = 32 + N;
+  const SsmLayer& l = a.l;
+  const int i = blockIdx.x, h = blockIdx.y, row0 = blockIdx.z * 32, pos = a.ckpt[i], s = seq_of_token(a.cu, a.n_seqs, pos - 1);
+  const int t0 = a.cu[s], upto = pos - t0, first = (upto - 1) / kChunk * kChunk;
+  if (upto == first + kChunk || pos == a.cu[s + 1]) return;      // the chunk's end: it is there already
+  const int tid = threadIdx.x, rg = tid / LPR, jl = tid % LPR, grp = h / (l.H / l.G), inner = l.H * l.P;
+  float* p = a.ckpt_buf + (((int64_t)i * l.H + h) * l.P + row0 + rg) * N + 4 * jl;
+  float S[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) S[k] = p[4 * LPR * (k / 4) + k % 4];
+  __shared__ float u[NCH];
+  const float A = l.A[h];
+  for (int t = first; t < upto; ++t) {
+    __syncthreads();
+    for (int e = tid; e < NCH; e += 2 * N) {
+      const int c = e < 32 ? h * l.P + row0 + e : inner + grp * N + e - 32;
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j == 3 || l.conv_w) x[j] = bf16_to_f32(raw_at(a, s, t0, t - 3 + j, c));
+      if (l.conv_w) {
+        const float4 k = reinterpret_cast<const float4*>(l.conv_w)[c];
+        x[3] = conv4_bias_silu(l.conv_bias ? conv_tap(l.conv_bias[c]) : 0.f, conv_tap(k.x), conv_tap(k.y), conv_tap(k.z),
+                               conv_tap(k.w), x[0], x[1], x[2], x[3]);
+      }
+      u[e] = x[3];
+    }
+    const float dt = ssm_step(l, a.dt, (int64_t)(t0 + t) * a.dt_stride + h, h), alpha = expf(A * dt);
+    __syncthreads();
+    const float dx = dt * u[rg];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) S[k] = fmaf(alpha, S[k], dx * u[32 + 4 * LPR * (k / 4) + 4 * jl + k % 4]);
+  }
+#pragma unroll
+  for (int k = 0; k < 16; ++k) p[4 * LPR * (k / 4) + k % 4] = S[k];
 }
 
 // The states that enter a prompt's segments: segment k's slot, which holds its
@@ -770,12 +854,6 @@ __global__ void __launch_bounds__(256) ssm_pass_kernel(const SsmScanArgs a, cons
   }
 }
 
-// Input of channel c at position p of prompt s (t0 = its first row; p < 0: its history).
-__device__ __forceinline__ uint16_t raw_at(const SsmScanArgs& a, int s, int t0, int p, int c) {
-  if (p >= 0) return a.x[(int64_t)(t0 + p) * a.x_stride + c];
-  return a.conv_in ? a.conv_in[((int64_t)s * 3 + 3 + p) * a.l.conv_dim + c] : 0;
-}
-
 // The three inputs before each checkpoint (blockIdx.x < n_ck), or each
 // prompt's last three; all reads before all writes of a thread's channels.
 __global__ void __launch_bounds__(256) ssm_scan_window_kernel(const SsmScanArgs a, int n_ck) {
@@ -793,7 +871,7 @@ __global__ void __launch_bounds__(256) ssm_scan_window_kernel(const SsmScanArgs 
 }
 
 template <int P, int N>
-hipError_t launch(const SsmScanArgs& a, const Ws& w, int segs, hipStream_t st) {
+hipError_t launch(const SsmScanArgs& a, const Ws& w, int segs, bool inside, hipStream_t st) {
   const SsmLayer& l = a.l;
   hipError_t e = hipSuccess;
   if (a.n_tokens > 0) {
@@ -805,18 +883,22 @@ hipError_t launch(const SsmScanArgs& a, const Ws& w, int segs, hipStream_t st) {
   const int grouped = cells >= 32;
   const dim3 grid((uint32_t)(grouped ? (cells + 7) / 8 * 8 * (hb / l.G) : units * hb)), blk(64 * hpw * (P / 32));
   if (split) {
-    hipLaunchKernelGGL((ssm_chunk_kernel<P, N, false>), grid, blk, 0, st, a, w, hpw, split, grouped);
+    if (l.conv_w) hipLaunchKernelGGL((ssm_chunk_kernel<P, N, false, true>), grid, blk, 0, st, a, w, hpw, split, grouped);
+    else hipLaunchKernelGGL((ssm_chunk_kernel<P, N, false, false>), grid, blk, 0, st, a, w, hpw, split, grouped);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     hipLaunchKernelGGL(ssm_pass_kernel, dim3(a.n_seqs, l.H, (P * N + 1023) / 1024), dim3(256), 0, st, a, w, hb);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((ssm_chunk_kernel<P, N, true>), grid, blk, 0, st, a, w, hpw, split, grouped);
+  if (l.conv_w) hipLaunchKernelGGL((ssm_chunk_kernel<P, N, true, true>), grid, blk, 0, st, a, w, hpw, split, grouped);
+  else hipLaunchKernelGGL((ssm_chunk_kernel<P, N, true, false>), grid, blk, 0, st, a, w, hpw, split, grouped);
+  if ((e = hipGetLastError()) != hipSuccess || !inside) return e;
+  hipLaunchKernelGGL((ssm_ckpt_kernel<N>), dim3(a.n_ckpt, l.H, P / 32), dim3(2 * N), 0, st, a);
   return hipGetLastError();
 }
 
 template <int P>
-hipError_t launch_p(const SsmScanArgs& a, const Ws& w, int segs, hipStream_t st) {
-  return a.l.N == 32 ? launch<P, 32>(a, w, segs, st) : a.l.N == 64 ? launch<P, 64>(a, w, segs, st) : launch<P, 128>(a, w, segs, st);
+hipError_t launch_p(const SsmScanArgs& a, const Ws& w, int segs, bool inside, hipStream_t st) {
+  return a.l.N == 32 ? launch<P, 32>(a, w, segs, inside, st) : a.l.N == 64 ? launch<P, 64>(a, w, segs, inside, st) : launch<P, 128>(a, w, segs, inside, st);
 }
 
 }  // namespace
@@ -831,10 +913,22 @@ int64_t ssm_scan_groups(const SsmLayer& l, int32_t n_seqs, int64_t n_tokens) {
   return std::max((units * l.G + 8) * (hb / l.G), n_tokens / kChunk + n_seqs);
 }
 
-hipError_t launch_ssm_scan(const SsmScanArgs& a, const int32_t* cu_host, void* workspace, hipStream_t st) {
+// Whether a checkpoint lies inside a chunk.
+static bool ckpt_inside(const SsmScanArgs& a, const int32_t* cu, const int32_t* ckpt) {
+  int s = 0;
+  for (int i = 0; i < a.n_ckpt; ++i) {
+    while (cu[s + 1] < ckpt[i]) ++s;
+    if ((ckpt[i] - cu[s]) % kChunk != 0 && ckpt[i] != cu[s + 1]) return true;
+  }
+  return false;
+}
+
+hipError_t launch_ssm_scan(const SsmScanArgs& a, const int32_t* cu_host, const int32_t* ckpt_host, void* workspace,
+                           hipStream_t st) {
+  const bool inside = ckpt_inside(a, cu_host, ckpt_host);
   const int segs = max_segments(a.l, a.n_seqs, cu_host);
   const Ws w = layout(a.l, a.n_seqs, a.n_tokens, segs > 1, workspace);
-  hipError_t e = a.l.P == 32 ? launch_p<32>(a, w, segs, st) : a.l.P == 64 ? launch_p<64>(a, w, segs, st) : launch_p<128>(a, w, segs, st);
+  hipError_t e = a.l.P == 32 ? launch_p<32>(a, w, segs, inside, st) : a.l.P == 64 ? launch_p<64>(a, w, segs, inside, st) : launch_p<128>(a, w, segs, inside, st);
   const int gy = (a.l.conv_dim + 255) / 256;
   // the checkpoints' windows read conv_in, which the prompts' own may overwrite: before them
   if (e == hipSuccess && a.conv_ckpt && a.n_ckpt > 0) {
