@@ -94,7 +94,7 @@ struct AddOp { __device__ __forceinline__ float operator()(float a, float b) con
 // and none passes n_tokens / 64 + n_seqs.  Segments alike, by 256 tokens.
 struct Ws {
   char* bc;              // [slots][G]: C operands, B^T hi, B^T lo (64 N halves each)
-  float* gt;             // [slots][G][10][64][4]: the tiles of C . B on and below the diagonal
+  _Float16* gt;          // [slots][G][10][64][4]: the tiles of C . B on and below the diagonal
   int2* k;               // [slots][G]: powers of two on B and C
   float* tab;            // [slots][H][kTab]
   float* seg;            // [segment slots][H][P][N]
@@ -124,7 +124,7 @@ inline Ws layout(const SsmLayer& l, int32_t n_seqs, int64_t n_tokens, bool split
   auto take = [&](int64_t bytes) { const int64_t here = at; at += up(bytes); return p + here; };
   const int64_t sg = (int64_t)w.slots * l.G;
   w.bc = take(sg * 3 * kChunk * l.N * 2);
-  w.gt = reinterpret_cast<float*>(take(sg * 10 * 256 * 4));
+  w.gt = reinterpret_cast<_Float16*>(take(sg * 10 * 256 * 2));
   w.k = reinterpret_cast<int2*>(take(sg * 8));
   w.tab = reinterpret_cast<float*>(take((int64_t)w.slots * l.H * kTab * 4));
   w.seg = reinterpret_cast<float*>(take((int64_t)w.seg_slots * l.H * l.P * l.N * 4));
@@ -164,179 +164,15 @@ __device__ __forceinline__ int owner(const int32_t* cu_ptr, int n_seqs, int unit
   return lo;
 }
 
-// Token of element j (0 .. 7) of lane group g in step ks of a product over 64
-// tokens (columns of a product over N alike): the rows that two accumulator
-// tiles of 16 hold in the lane group, so that an accumulator is an operand.
+// The order of sums.  A product of 32 takes 8 elements from each lane group g.
+// Over tokens, element j of step ks is token slot_of(ks, g, j): the rows that
+// two accumulator tiles of 16 hold in the lane group.  Over N, it is column
+// 32 ks + 8 g + j, where row r of the tile 2 ks + q of S^T is column 32 ks + 2 r +
+// q: element j lies in tile j % 2, so an accumulator of S^T is an operand too,
+// rows of C are read as they lie, and a lane's entries of S are 8 in a row.
 __device__ __forceinline__ constexpr int slot_of(int ks, int g, int j) { return 32 * ks + 16 * (j / 4) + 4 * g + j % 4; }
 
-// --------------------------------------------------------------- prepare --
-template <int N>
-__device__ __forceinline__ void prepare_bc(const SsmScanArgs& a, const Ws& w, int s, int c, int grp, char* smem) {
-  constexpr int PITCH = 2 * N + 8, ROW = N + 8, NT = N / 16, KN = N / 32, TILES = N / 32;
-  uint16_t* raw = reinterpret_cast<uint16_t*>(smem);                       // [67][PITCH]
-  _Float16* rb = reinterpret_cast<_Float16*>(smem + 67 * PITCH * 2);       // [64][ROW]
-  _Float16* rc = rb + kChunk * ROW;
-  float* red = reinterpret_cast<float*>(rc + kChunk * ROW);                // [2][4]
-  const SsmLayer& l = a.l;
-  const int tid = threadIdx.x, wave = tid / 64, lane = tid & 63, r = lane & 15, g = lane >> 4;
-  const int t0 = a.cu[s], len = a.cu[s + 1] - t0, inner = l.H * l.P;
-  const int col_b = inner + grp * N, col_c = inner + (l.G + grp) * N;
-  for (int i = tid; i < 67 * (N / 4); i += 256) {
-    const int row = i / (N / 4), k = 8 * (i % (N / 4)), p = c * kChunk - 3 + row;
-    const int col = k < N ? col_b + k : col_c + k - N;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (p >= 0) {
-      if (p < len) v = *reinterpret_cast<const uint4*>(a.x + (int64_t)(t0 + p) * a.x_stride + col);
-    } else if (a.conv_in) {
-      v = *reinterpret_cast<const uint4*>(a.conv_in + ((int64_t)s * 3 + 3 + p) * l.conv_dim + col);
-    }
-    *reinterpret_cast<uint4*>(raw + row * PITCH + k) = v;
-  }
-  __syncthreads();
-  const int left = len - c * kChunk;    // tokens from the chunk's first on
-  float v[TILES][2][8];
-  float m[2] = {0.f, 0.f};
-#pragma unroll
-  for (int k = 0; k < TILES; ++k) {
-    const int ct = wave + 4 * k, col = 16 * ct + r, ch = ct < NT ? col_b + col : col_c + col - N;
-    float w0 = 0.f, w1 = 0.f, w2 = 0.f, w3 = 0.f, b = 0.f;
-    if (l.conv_w) {
-      const float4 q = reinterpret_cast<const float4*>(l.conv_w)[ch];
-      w0 = conv_tap(q.x); w1 = conv_tap(q.y); w2 = conv_tap(q.z); w3 = conv_tap(q.w);
-      if (l.conv_bias) b = conv_tap(l.conv_bias[ch]);
-    }
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int base = 32 * ks + 16 * hf + 4 * g;
-        float x[7];
-#pragma unroll
-        for (int i = 0; i < 7; ++i) x[i] = bf16_to_f32(raw[(base + i) * PITCH + col]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float u = l.conv_w ? conv4_bias_silu(b, w0, w1, w2, w3, x[i], x[i + 1], x[i + 2], x[i + 3]) : x[i + 3];
-          if (base + i >= left) u = 0.f;
-          v[k][ks][4 * hf + i] = u;
-          m[ct >= NT] = fmaxf(m[ct >= NT], finite_abs(u));
-        }
-      }
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    m[i] = over_wave(m[i], MaxOp{});
-    if (lane == 0) red[4 * i + wave] = m[i];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 2; ++i) m[i] = fmaxf(fmaxf(red[4 * i], red[4 * i + 1]), fmaxf(red[4 * i + 2], red[4 * i + 3]));
-  const int kb = kTopBt - pow2_above(m[0]), kc = kTopC - pow2_above(m[1]);
-  const int64_t sg = (int64_t)(t0 / kChunk + s + c) * l.G + grp;
-  if (tid == 0) w.k[sg] = make_int2(kb, kc);
-  f16x8* ops = reinterpret_cast<f16x8*>(w.bc + sg * 3 * kChunk * N * 2);
-#pragma unroll
-  for (int k = 0; k < TILES; ++k) {
-    const int ct = wave + 4 * k;
-    const bool is_c = ct >= NT;
-    const float f = ldexpf(1.f, is_c ? kc : kb);
-    _Float16* rows = is_c ? rc : rb;
-    const int n = 16 * (is_c ? ct - NT : ct) + r;
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      f16x8 hi, lo;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float u = v[k][ks][j] * f;
-        hi[j] = (_Float16)u;
-        lo[j] = (_Float16)(u - (float)hi[j]);
-        rows[slot_of(ks, g, j) * ROW + n] = is_c ? hi[j] : (_Float16)ldexpf(u, kTopB - kTopBt);
-      }
-      if (!is_c) {
-        f16x8* bt = ops + kChunk * N / 8;
-        bt[(ct * 2 + ks) * 64 + lane] = hi;
-        bt[kChunk * N / 8 + (ct * 2 + ks) * 64 + lane] = lo;
-      }
-    }
-  }
-  __syncthreads();
-  auto row_frag = [&](const _Float16* rows, int t, int ks) __attribute__((always_inline)) {
-    const f16x4 x = *reinterpret_cast<const f16x4*>(rows + t * ROW + 32 * ks + 4 * g);
-    const f16x4 y = *reinterpret_cast<const f16x4*>(rows + t * ROW + 32 * ks + 16 + 4 * g);
-    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-  };
-  f16x8 cf[KN];
-#pragma unroll
-  for (int ks = 0; ks < KN; ++ks) {
-    cf[ks] = row_frag(rc, 16 * wave + r, ks);
-    ops[(wave * KN + ks) * 64 + lane] = cf[ks];
-  }
-  f32x4* gt = reinterpret_cast<f32x4*>(w.gt + sg * 10 * 256);
-  for (int st = 0; st <= wave; ++st) {
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int ks = 0; ks < KN; ++ks) acc = mma(row_frag(rb, 16 * st + r, ks), cf[ks], acc);
-    gt[(wave * (wave + 1) / 2 + st) * 64 + lane] = acc;
-  }
-}
-
-// The steps of one (chunk, head): a wave, a lane per token.
-__device__ __forceinline__ void prepare_steps(const SsmScanArgs& a, const Ws& w, int s, int c, int h) {
-  const int lane = threadIdx.x & 63, t0 = a.cu[s], len = a.cu[s + 1] - t0, p = c * kChunk + lane;
-  const float A = a.l.A[h];
-  const float dt = p < len ? ssm_step(a.l, a.dt, (int64_t)(t0 + p) * a.dt_stride + h, h) : 0.f;
-  // log2 of the token's decay; one of 2^-200 leaves nothing of a state, and
-  // longer ones would only take precision from the sums
-  float al = A * dt * kLog2e;
-  if (al < -200.f) al = -200.f;
-  if (p >= len) al = 0.f;
-  float cum = al, after = al;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const float x = __shfl_up(cum, d), y = __shfl_down(after, d);
-    if (lane >= d) cum += x;
-    if (lane + d < 64) after += y;
-  }
-  const float total = __shfl(cum, 63);
-  // sum of the later tokens' decays, from the end: near tokens keep their
-  // precision behind a long sum
-  after = __shfl_down(after, 1);
-  if (lane == 63) after = 0.f;
-  const float wt = __builtin_amdgcn_exp2f(after) * dt;
-  const float grow = over_wave(fmaxf(al, 0.f), AddOp{});
-  const float wmax = over_wave(finite_abs(wt), MaxOp{});
-  const float dmax = over_wave(finite_abs(dt), MaxOp{}) * __builtin_amdgcn_exp2f(fminf(grow, 60.f));
-  float* tab = w.tab + ((int64_t)(t0 / kChunk + s + c) * a.l.H + h) * kTab;
-  tab[lane] = dt;
-  tab[64 + lane] = cum;
-  const int kw = 10 - pow2_above(wmax);
-  tab[128 + lane] = ldexpf(wt, kw);
-  if (lane < 5)
-    tab[192 + lane] = lane == 0 ? total : lane == 1 ? wmax : lane == 2 ? dmax : lane == 3 ? __builtin_amdgcn_exp2f(total) : __int_as_float(kw);
-}
-
-template <int N>
-__global__ void __launch_bounds__(256) ssm_prepare_kernel(const SsmScanArgs a, const Ws w) {
-  __shared__ __align__(16) char smem[67 * (2 * N + 8) * 2 + 2 * kChunk * (N + 8) * 2 + 64];
-  const int b = blockIdx.x, s = owner(a.cu, a.n_seqs, kChunk, b), c = b - (a.cu[s] / kChunk + s);
-  if (c * kChunk >= a.cu[s + 1] - a.cu[s]) return;
-  if ((int)blockIdx.y < a.l.G) {
-    prepare_bc<N>(a, w, s, c, blockIdx.y, smem);
-  } else {
-    const int h = (blockIdx.y - a.l.G) * 4 + threadIdx.x / 64;
-    if (h < a.l.H) prepare_steps(a, w, s, c, h);
-  }
-}
-
-// ------------------------------------------------------------------ scan --
-// Copies 16 bytes a lane from global memory to LDS, from the wave's base on.
-// The compiler does not see it and so waits for none before other reads of
-// LDS: an s_waitcnt vmcnt(0) and a barrier stand between it and its readers.
-__device__ __forceinline__ void to_lds(const void* g, const void* base) {
-  const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)base;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(g) : "memory", "m0");
-}
-__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
+// ---------------------------------------------------------------- inputs --
 // What a wave keeps of a chunk's inputs: the two channels 2 r, 2 r + 1 of its 32
 // in one dword, at the tokens of its lane group (runs of four: 16 run + 4 g ..)
 // and the three before each run.
@@ -393,11 +229,181 @@ __device__ __forceinline__ void conv_x(const RawX& x, const ConvW& k, float (&v)
   }
 }
 
+__device__ __forceinline__ void load_conv(const SsmLayer& l, int ch, ConvW& k) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const float4 t = reinterpret_cast<const float4*>(l.conv_w)[ch + q];
+    k.w0[q] = conv_tap(t.x); k.w1[q] = conv_tap(t.y); k.w2[q] = conv_tap(t.z); k.w3[q] = conv_tap(t.w);
+    k.b[q] = l.conv_bias ? conv_tap(l.conv_bias[ch + q]) : 0.f;
+  }
+}
+
 __device__ __forceinline__ f16x8 join(f16x2 a, f16x2 b, f16x2 c, f16x2 d) { return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]}; }
+
+// --------------------------------------------------------------- prepare --
+template <int N, bool CONV>
+__device__ __forceinline__ void prepare_bc(const SsmScanArgs& a, const Ws& w, int s, int c, int grp, _Float16* rows, float* red) {
+  constexpr int ROW = N + 8, PAIRS = N / 32, KN = N / 32, TILES = (2 * PAIRS + 3) / 4;   // tiles of 32 channels a wave
+  const SsmLayer& l = a.l;
+  const int tid = threadIdx.x, wave = tid / 64, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int t0 = a.cu[s], len = a.cu[s + 1] - t0, inner = l.H * l.P, left = len - c * kChunk;
+  const int64_t sg = (int64_t)(t0 / kChunk + s + c) * l.G + grp;
+  float v[TILES][2][4][4];
+  float m[2] = {0.f, 0.f};
+  RawX x[TILES];
+  auto tile_of = [&](int k) { return wave + 4 * k; };     // below PAIRS: of B, then of C
+  auto col_of = [&](int t) { return t < PAIRS ? inner + grp * N + 32 * t : inner + (l.G + grp) * N + 32 * (t - PAIRS); };
+#pragma unroll
+  for (int k = 0; k < TILES; ++k) {
+    if (tile_of(k) >= 2 * PAIRS) continue;
+    const XRef f{a.x + (int64_t)t0 * a.x_stride, a.conv_in ? a.conv_in + (int64_t)s * 3 * l.conv_dim : nullptr, a.x_stride, l.conv_dim, len,
+                 col_of(tile_of(k)) + 2 * r};
+    load_x<CONV>(f, c, g, x[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < TILES; ++k) {
+    if (tile_of(k) >= 2 * PAIRS) continue;
+    ConvW cw;
+    if (CONV) load_conv(l, col_of(tile_of(k)) + 2 * r, cw);
+    conv_x<CONV>(x[k], cw, v[k]);
+    float top = 0.f;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float& u = v[k][q][i / 4][i % 4];
+        if (16 * (i / 4) + 4 * g + i % 4 >= left) u = 0.f;
+        top = fmaxf(top, finite_abs(u));
+      }
+    m[tile_of(k) >= PAIRS] = fmaxf(m[tile_of(k) >= PAIRS], top);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    m[i] = over_wave(m[i], MaxOp{});
+    if (lane == 0) red[4 * i + wave] = m[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) m[i] = fmaxf(fmaxf(red[4 * i], red[4 * i + 1]), fmaxf(red[4 * i + 2], red[4 * i + 3]));
+  const int kb = kTopBt - pow2_above(m[0]), kc = kTopC - pow2_above(m[1]);
+  if (tid == 0) w.k[sg] = make_int2(kb, kc);
+  f16x8* ops = reinterpret_cast<f16x8*>(w.bc + sg * 3 * kChunk * N * 2);
+#pragma unroll
+  for (int k = 0; k < TILES; ++k) {
+    const int t = tile_of(k);
+    if (t >= 2 * PAIRS) continue;
+    const bool is_c = t >= PAIRS;
+    const float f = ldexpf(1.f, is_c ? kc : kb);
+    _Float16* to = rows + (is_c ? kChunk * ROW + 32 * (t - PAIRS) : 32 * t) + 2 * r;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[k][q][i / 4][i % 4] *= f;
+    const float down = is_c ? 1.f : 1.f / (1 << (kTopBt - kTopB));
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      *reinterpret_cast<f16x2*>(to + (16 * (i / 4) + 4 * g + i % 4) * ROW) = pack_f16(v[k][0][i / 4][i % 4] * down, v[k][1][i / 4][i % 4] * down);
+    if (!is_c) {
+      f16x8* bt = ops + kChunk * N / 8;
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          f16x2 hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float v0 = v[k][q][2 * z + i / 2][2 * (i % 2)], v1 = v[k][q][2 * z + i / 2][2 * (i % 2) + 1];
+            hi[i] = pack_f16(v0, v1);
+            lo[i] = pack_f16(fmaf((float)hi[i][0], -1.f, v0), fmaf((float)hi[i][1], -1.f, v1));
+          }
+          bt[((2 * t + q) * 2 + z) * 64 + lane] = join(hi[0], hi[1], hi[2], hi[3]);
+          if (CONV) bt[kChunk * N / 8 + ((2 * t + q) * 2 + z) * 64 + lane] = join(lo[0], lo[1], lo[2], lo[3]);
+        }
+    }
+  }
+  __syncthreads();
+  const _Float16* rc = rows + kChunk * ROW + (16 * wave + r) * ROW + 8 * g;
+  f16x8 cf[KN];
+#pragma unroll
+  for (int ks = 0; ks < KN; ++ks) {
+    cf[ks] = *reinterpret_cast<const f16x8*>(rc + 32 * ks);
+    ops[(wave * KN + ks) * 64 + lane] = cf[ks];
+  }
+  f16x4* gt = reinterpret_cast<f16x4*>(w.gt + sg * 10 * 256);
+  for (int st = 0; st <= wave; ++st) {
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < KN; ++ks)
+      acc = mma(*reinterpret_cast<const f16x8*>(rows + (16 * st + r) * ROW + 8 * g + 32 * ks), cf[ks], acc);
+    const f16x2 p0 = pack_f16(acc[0], acc[1]), p1 = pack_f16(acc[2], acc[3]);
+    gt[(wave * (wave + 1) / 2 + st) * 64 + lane] = f16x4{p0[0], p0[1], p1[0], p1[1]};
+  }
+}
+
+// The steps of one (chunk, head): a wave, a lane per token.
+__device__ __forceinline__ void prepare_steps(const SsmScanArgs& a, const Ws& w, int s, int c, int h) {
+  const int lane = threadIdx.x & 63, t0 = a.cu[s], len = a.cu[s + 1] - t0, p = c * kChunk + lane;
+  const float A = a.l.A[h];
+  const float dt = p < len ? ssm_step(a.l, a.dt, (int64_t)(t0 + p) * a.dt_stride + h, h) : 0.f;
+  // log2 of the token's decay; one of 2^-200 leaves nothing of a state, and
+  // longer ones would only take precision from the sums
+  float al = A * dt * kLog2e;
+  if (al < -200.f) al = -200.f;
+  if (p >= len) al = 0.f;
+  float cum = al, after = al;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const float x = __shfl_up(cum, d), y = __shfl_down(after, d);
+    if (lane >= d) cum += x;
+    if (lane + d < 64) after += y;
+  }
+  const float total = __shfl(cum, 63);
+  // sum of the later tokens' decays, from the end: near tokens keep their
+  // precision behind a long sum
+  after = __shfl_down(after, 1);
+  if (lane == 63) after = 0.f;
+  const float wt = __builtin_amdgcn_exp2f(after) * dt;
+  const float grow = over_wave(fmaxf(al, 0.f), AddOp{});
+  const float wmax = over_wave(finite_abs(wt), MaxOp{});
+  const float dmax = over_wave(finite_abs(dt), MaxOp{}) * __builtin_amdgcn_exp2f(fminf(grow, 60.f));
+  float* tab = w.tab + ((int64_t)(t0 / kChunk + s + c) * a.l.H + h) * kTab;
+  tab[lane] = dt;
+  tab[64 + lane] = cum;
+  const int kw = 10 - pow2_above(wmax);
+  tab[128 + lane] = ldexpf(wt, kw);
+  if (lane < 5)
+    tab[192 + lane] = lane == 0 ? total : lane == 1 ? wmax : lane == 2 ? dmax : lane == 3 ? __builtin_amdgcn_exp2f(total) : __int_as_float(kw);
+}
+
+template <int N, bool CONV>
+__global__ void __launch_bounds__(256) ssm_prepare_kernel(const SsmScanArgs a, const Ws w) {
+  __shared__ __align__(16) _Float16 rows[2 * kChunk * (N + 8)];
+  __shared__ float red[8];
+  const int b = blockIdx.x, s = owner(a.cu, a.n_seqs, kChunk, b), c = b - (a.cu[s] / kChunk + s);
+  if (c * kChunk >= a.cu[s + 1] - a.cu[s]) return;
+  if ((int)blockIdx.y < a.l.G) {
+    prepare_bc<N, CONV>(a, w, s, c, blockIdx.y, rows, red);
+  } else {
+    const int h = (blockIdx.y - a.l.G) * 4 + threadIdx.x / 64;
+    if (h < a.l.H) prepare_steps(a, w, s, c, h);
+  }
+}
+
+// ------------------------------------------------------------------ scan --
+// Copies 16 bytes a lane from global memory to LDS, from the wave's base on.
+// The compiler does not see it and so waits for none before other reads of
+// LDS: an s_waitcnt vmcnt(0) and a barrier stand between it and its readers.
+__device__ __forceinline__ void to_lds(const void* g, const void* base) {
+  const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)base;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(g) : "memory", "m0");
+}
+// Waits until all but the N latest accesses to memory are done.
+template <int N>
+__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 
 // One (16 t, 32 s) operand of M^T: tiles st = 2 KS and 2 KS + 1 of the tile row TT.
 template <int TT, int KS>
-__device__ __forceinline__ f16x8 weigh(const f32x4* gt, const float* tab, int lane, int ad, float dm) {
+__device__ __forceinline__ f16x8 weigh(const f16x4* gt, const float* tab, int lane, int ad, float dm) {
   const int r = lane & 15, g = lane >> 4;
   const float ct = tab[64 + 16 * TT + r] + (float)ad;
   f16x2 o[4];
@@ -405,13 +411,13 @@ __device__ __forceinline__ f16x8 weigh(const f32x4* gt, const float* tab, int la
   for (int q = 0; q < 2; ++q) {
     const int st = 2 * KS + q;
     if (st > TT) { o[2 * q] = o[2 * q + 1] = f16x2{0, 0}; continue; }
-    const f32x4 gv = gt[(TT * (TT + 1) / 2 + st) * 64 + lane];
+    const f16x4 gv = gt[(TT * (TT + 1) / 2 + st) * 64 + lane];
     const f32x4 cs = *reinterpret_cast<const f32x4*>(tab + 64 + 16 * st + 4 * g);
     const f32x4 ds = *reinterpret_cast<const f32x4*>(tab + 16 * st + 4 * g);
     float v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[j] = gv[j] * (ds[j] * __builtin_amdgcn_exp2f(ct - cs[j]));
+      v[j] = (float)gv[j] * (ds[j] * __builtin_amdgcn_exp2f(ct - cs[j]));
       if (st == TT) v[j] = 4 * g + j < r ? v[j] : 4 * g + j == r ? v[j] + dm : 0.f;
     }
     o[2 * q] = pack_f16(v[0], v[1]);
@@ -423,7 +429,7 @@ __device__ __forceinline__ f16x8 weigh(const f32x4* gt, const float* tab, int la
 template <int P, int N, bool OUT, bool CONV>
 __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, const Ws w, int hpw, int split, int grouped) {
   constexpr int WPH = P / 32, NT = N / 16, KN = N / 32, OPS = kChunk * N * 2;   // bytes of one operand
-  constexpr int HMAX = 4 / WPH, GT = 10 * 1024;
+  constexpr int HMAX = 4 / WPH, GT = 10 * 512;
   // C, B^T hi, B^T lo (without the convolution B is exact in fp16: no lo)
   constexpr int FIRST = OUT ? 0 : OPS, LAST = CONV ? 3 * OPS : 2 * OPS;
   __shared__ __align__(16) char ops[LAST - FIRST];
@@ -454,7 +460,7 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
 
   const int h = b * hpw + hl, grp = h / (l.H / l.G), ch0 = h * P + 32 * half + 2 * r;
   const int64_t hpn = (int64_t)l.P * l.N, slot0 = t0 / kChunk + s;
-  const int st_at = (32 * half + 2 * r) * N + 4 * g;       // this lane's entries of a head's state
+  const int st_at = (32 * half + 2 * r) * N + 8 * g;       // this lane's entries of a head's state
   const XRef xref{a.x + (int64_t)t0 * a.x_stride, a.conv_in ? a.conv_in + (int64_t)s * 3 * l.conv_dim : nullptr, a.x_stride, l.conv_dim, len, ch0};
   // The operands of a chunk are fetched while the one before is worked on:
   // B^T, C . B and the tables once the update of the state is through, C once
@@ -473,17 +479,11 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
     load_x<CONV>(xref, c_first, g, x);
   }
   ConvW cw;
-  if (CONV) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const float4 t = reinterpret_cast<const float4*>(l.conv_w)[ch0 + q];
-      cw.w0[q] = conv_tap(t.x); cw.w1[q] = conv_tap(t.y); cw.w2[q] = conv_tap(t.z); cw.w3[q] = conv_tap(t.w);
-      cw.b[q] = l.conv_bias ? conv_tap(l.conv_bias[ch0 + q]) : 0.f;
-    }
-  }
+  if (CONV) load_conv(l, ch0, cw);
   const float D = OUT && l.D ? l.D[h] : 0.f;
 
-  // the state that enters, S^T in tiles [16 n][16 p], scaled by 2^e; `bound`:
+  // the state that enters, S^T in tiles [16 n][16 p] (columns of N in the order
+  // of the sums), scaled by 2^e; `bound`:
   // no entry of the channel is larger
   f32x4 S[NT][2];
   int e[2] = {0, 0};
@@ -492,11 +492,16 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
                       : k > 0 ? w.seg + (((int64_t)unit - 1) * l.H + h) * hpn
                       : a.init ? a.init + ((int64_t)s * l.H + h) * hpn : nullptr;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int z = 0; z < KN; ++z)
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      S[nt][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (from) S[nt][q] = *reinterpret_cast<const f32x4*>(from + st_at + q * N + 16 * nt);
+      f32x4 v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
+      if (from) {
+        v0 = *reinterpret_cast<const f32x4*>(from + st_at + q * N + 32 * z);
+        v1 = *reinterpret_cast<const f32x4*>(from + st_at + q * N + 32 * z + 4);
+      }
+      S[2 * z][q] = f32x4{v0[0], v0[2], v1[0], v1[2]};
+      S[2 * z + 1][q] = f32x4{v0[1], v0[3], v1[1], v1[3]};
     }
   if (from) {
 #pragma unroll
@@ -518,14 +523,14 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
   auto store_state = [&](float* head) __attribute__((always_inline)) {
     float* to = head + anew(st_at);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int z = 0; z < KN; ++z)
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        f32x4 v;
+      for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = ldexpf(S[nt][q][i], -e[q]);
-        *reinterpret_cast<f32x4*>(to + q * N + 16 * nt) = v;
-      }
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<f32x4*>(to + q * N + 32 * z + 4 * i) =
+              f32x4{ldexpf(S[2 * z][q][2 * i], -e[q]), ldexpf(S[2 * z + 1][q][2 * i], -e[q]), ldexpf(S[2 * z][q][2 * i + 1], -e[q]),
+                    ldexpf(S[2 * z + 1][q][2 * i + 1], -e[q])};
   };
   int ci = 0, next = INT_MAX;
   if (OUT) {
@@ -571,12 +576,14 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
     }
 #pragma unroll
     for (int q = 0; q < 2; ++q) xmax[q] = over_groups(xmax[q], lane);
-    arrived();
+    arrived<0>();
     __syncthreads();   // B^T, C . B and the tables are whole; the last outputs are through with C and M
     if (OUT) {
       const char* src = w.bc + sg * 3 * OPS;
       for (int i = wave; i < OPS / 1024; i += nw) to_lds(src + 1024 * i + 16 * lane, ops + 1024 * i);
     }
+    if (c + 1 < c_end) load_x<CONV>(xref, c + 1, g, x);
+    __builtin_amdgcn_sched_barrier(0);
     const float* tab = tabs[c & 1][hl];
     const float alpha = tab[195], wmax = tab[193], dmax = tab[194];
     const int kw = __float_as_int(tab[196]);
@@ -587,7 +594,7 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
       const int ad = min(-pow2_above(dmax), 14 - pow2_above(fabsf(D)) - (kb + kc));
       m = kb + kc + ad;
       const float dm = ldexpf(D, m);
-      const f32x4* gt = reinterpret_cast<const f32x4*>(gts);
+      const f16x4* gt = reinterpret_cast<const f16x4*>(gts);
       if (0 % WPH == half) fm[hl][0][lane] = weigh<0, 0>(gt, tab, lane, ad, dm);
       if (1 % WPH == half) fm[hl][1][lane] = weigh<1, 0>(gt, tab, lane, ad, dm);
       if (2 % WPH == half) fm[hl][2][lane] = weigh<2, 0>(gt, tab, lane, ad, dm);
@@ -660,8 +667,8 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
         const float down = ldexpf(1.f, es - e[q]);
 #pragma unroll
         for (int z = 0; z < KN; ++z)
-          so[q][z] = join(pack_f16(S[2 * z][q][0] * down, S[2 * z][q][1] * down), pack_f16(S[2 * z][q][2] * down, S[2 * z][q][3] * down),
-                          pack_f16(S[2 * z + 1][q][0] * down, S[2 * z + 1][q][1] * down), pack_f16(S[2 * z + 1][q][2] * down, S[2 * z + 1][q][3] * down));
+          so[q][z] = join(pack_f16(S[2 * z][q][0] * down, S[2 * z + 1][q][0] * down), pack_f16(S[2 * z][q][1] * down, S[2 * z + 1][q][1] * down),
+                          pack_f16(S[2 * z][q][2] * down, S[2 * z + 1][q][2] * down), pack_f16(S[2 * z][q][3] * down, S[2 * z + 1][q][3] * down));
       }
     }
 
@@ -699,10 +706,7 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
     if (!OUT) {
       seg_sum += tab[192];
       __syncthreads();   // the update is through with B^T
-      if (c + 1 < c_end) {
-        fetch(c + 1);
-        load_x<CONV>(xref, c + 1, g, x);
-      }
+      if (c + 1 < c_end) fetch(c + 1);
       continue;
     }
 
@@ -726,12 +730,10 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
         first_bad[q] = min(first_bad[q], from_lane(first_bad[q], lane2 ^ 32));
       }
     }
-    arrived();
+    if (c + 1 < c_end) arrived<CONV ? 28 : 16>();   // all but the next inputs
+    else arrived<0>();
     __syncthreads();   // C and M are whole; the update is through with B^T
-    if (c + 1 < c_end) {
-      fetch(c + 1);
-      load_x<CONV>(xref, c + 1, g, x);
-    }
+    if (c + 1 < c_end) fetch(c + 1);
     const float f2 = ldexpf(1.f, max(-126, min(126, -(m + kx))));
     uint16_t* to = a.out + ((int64_t)(t0 + c * kChunk) * l.H + h) * P + 32 * half;
     const uint32_t out_at = (uint32_t)(r * l.H * P + 8 * g);
@@ -875,7 +877,9 @@ hipError_t launch(const SsmScanArgs& a, const Ws& w, int segs, bool inside, hipS
   const SsmLayer& l = a.l;
   hipError_t e = hipSuccess;
   if (a.n_tokens > 0) {
-    hipLaunchKernelGGL((ssm_prepare_kernel<N>), dim3(w.slots, l.G + (l.H + 3) / 4), dim3(256), 0, st, a, w);
+    const dim3 prep(w.slots, l.G + (l.H + 3) / 4);
+    if (l.conv_w) hipLaunchKernelGGL((ssm_prepare_kernel<N, true>), prep, dim3(256), 0, st, a, w);
+    else hipLaunchKernelGGL((ssm_prepare_kernel<N, false>), prep, dim3(256), 0, st, a, w);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   const int hpw = heads_per_wg(l), hb = l.H / hpw, split = segs > 1;
