@@ -1,4 +1,4 @@
-// Packed scan of the state space layers on the matrix cores, in chunks of 64
+// Packed scan of the state space layers on the matrix cores, in chunks of 32
 // tokens.  With cum_t = sum of A dt up to token t of a chunk, S0 the state
 // that enters it, L its last token:
 //
@@ -27,6 +27,7 @@
 // but for the outputs.
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "cache_device.h"
 #include "ssm_device.h"
@@ -34,10 +35,11 @@
 namespace gdn {
 namespace {
 
-constexpr int kChunk = 64;
-constexpr int kTab = 256;                 // floats of a (chunk, head)'s table: dt, cum, w, scalars
+constexpr int kChunk = 32;
+constexpr int kTab = 128;                 // floats of a (chunk, head)'s table: dt, cum, w, scalars
+constexpr int kTiles = 3;                 // 16 x 16 tiles of C . B on and below the diagonal
 // Powers of two that the largest values are brought to: B^T in the update of the
-// state (and S, where 64 products of x w and B fill it), B and C in C . B (whose
+// state (and S, where a chunk's products of x w and B fill it), B and C in C . B (whose
 // sums over N, times a step's share, fit fp16).
 constexpr int kTopBt = 14, kTopS = 30, kTopS16 = 14, kTopB = 4, kTopC = 4;
 constexpr float kLog2e = 1.44269504088896341f;
@@ -74,6 +76,14 @@ __device__ __forceinline__ float over_wave(float x, Op op) {
   x = op(x, __shfl_xor(x, 16));
   return op(x, __shfl_xor(x, 32));
 }
+template <typename Op>
+__device__ __forceinline__ float over_half(float x, Op op) {
+  x = op(x, dpp_f32<0xB1>(x));
+  x = op(x, dpp_f32<0x4E>(x));
+  x = op(x, dpp_f32<0x141>(x));
+  x = op(x, dpp_f32<0x140>(x));
+  return op(x, __shfl_xor(x, 16));
+}
 struct MaxOp { __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); } };
 // The largest over the lane groups: of the lanes that hold the same channels.
 __device__ __forceinline__ float over_groups(float x, int lane) {
@@ -90,11 +100,11 @@ __device__ __forceinline__ float over_wave16(float x) {
 struct AddOp { __device__ __forceinline__ float operator()(float a, float b) const { return a + b; } };
 
 // ------------------------------------------------------------ the layout --
-// Chunk c of prompt s has slot cu[s] / 64 + s + c: no two chunks share one,
-// and none passes n_tokens / 64 + n_seqs.  Segments alike, by 256 tokens.
+// Chunk c of prompt s has slot cu[s] / 32 + s + c: no two chunks share one,
+// and none passes n_tokens / 32 + n_seqs.  Segments alike, by 256 tokens.
 struct Ws {
-  char* bc;              // [slots][G]: C operands, B^T hi, B^T lo (64 N halves each)
-  _Float16* gt;          // [slots][G][10][64][4]: the tiles of C . B on and below the diagonal
+  char* bc;              // [slots][G]: C operands, B^T hi, B^T lo (32 N halves each)
+  _Float16* gt;          // [slots][G][4][64][4]: the tiles of C . B on and below the diagonal (and one unused)
   int2* k;               // [slots][G]: powers of two on B and C
   float* tab;            // [slots][H][kTab]
   float* seg;            // [segment slots][H][P][N]
@@ -103,12 +113,12 @@ struct Ws {
   int64_t bytes;
 };
 
-constexpr int kSegUnit = 4;               // chunks a segment has at least
+constexpr int kSegUnit = 8;               // chunks a segment has at least
 
 // Chunks of a segment for a prompt of nc chunks whose chunk row takes hb
 // workgroups.
 __host__ __device__ inline int seg_chunks(int nc, int hb) {
-  if (nc <= 16) return nc > 0 ? nc : 1;
+  if (nc <= 32) return nc > 0 ? nc : 1;
   const int want = (256 + hb - 1) / hb, most = nc / kSegUnit, n = want < most ? want : most;
   return (nc + n - 1) / n;
 }
@@ -124,17 +134,17 @@ inline Ws layout(const SsmLayer& l, int32_t n_seqs, int64_t n_tokens, bool split
   auto take = [&](int64_t bytes) { const int64_t here = at; at += up(bytes); return p + here; };
   const int64_t sg = (int64_t)w.slots * l.G;
   w.bc = take(sg * 3 * kChunk * l.N * 2);
-  w.gt = reinterpret_cast<_Float16*>(take(sg * 10 * 256 * 2));
+  w.gt = reinterpret_cast<_Float16*>(take(sg * 4 * 256 * 2));
   w.k = reinterpret_cast<int2*>(take(sg * 8));
-  w.tab = reinterpret_cast<float*>(take((int64_t)w.slots * l.H * kTab * 4));
+  w.tab = reinterpret_cast<float*>(take((int64_t)w.slots * l.H * kTab * 4 + 512));
   w.seg = reinterpret_cast<float*>(take((int64_t)w.seg_slots * l.H * l.P * l.N * 4));
   w.seg_sum = reinterpret_cast<float*>(take((int64_t)w.seg_slots * l.H * 4));
   w.bytes = at;
   return w;
 }
 
-// Heads of a workgroup: 128 / P, or the largest power of two below it that
-// divides a group's heads.
+// Heads of a workgroup: 128 / P (four waves), or the largest power of two below
+// it that divides a group's heads.
 inline int heads_per_group(const SsmLayer& l) { return l.H / l.G; }
 inline int heads_per_wg(const SsmLayer& l) {
   int n = 128 / l.P;
@@ -165,18 +175,18 @@ __device__ __forceinline__ int owner(const int32_t* cu_ptr, int n_seqs, int unit
 }
 
 // The order of sums.  A product of 32 takes 8 elements from each lane group g.
-// Over tokens, element j of step ks is token slot_of(ks, g, j): the rows that
-// two accumulator tiles of 16 hold in the lane group.  Over N, it is column
+// Over a chunk's tokens, element j is token slot_of(g, j): the rows that the two
+// accumulator tiles of 16 hold in the lane group.  Over N, it is column
 // 32 ks + 8 g + j, where row r of the tile 2 ks + q of S^T is column 32 ks + 2 r +
 // q: element j lies in tile j % 2, so an accumulator of S^T is an operand too,
 // rows of C are read as they lie, and a lane's entries of S are 8 in a row.
-__device__ __forceinline__ constexpr int slot_of(int ks, int g, int j) { return 32 * ks + 16 * (j / 4) + 4 * g + j % 4; }
+__device__ __forceinline__ constexpr int slot_of(int g, int j) { return 16 * (j / 4) + 4 * g + j % 4; }
 
 // ---------------------------------------------------------------- inputs --
 // What a wave keeps of a chunk's inputs: the two channels 2 r, 2 r + 1 of its 32
 // in one dword, at the tokens of its lane group (runs of four: 16 run + 4 g ..)
 // and the three before each run.
-struct RawX { uint32_t v[4][7]; };
+struct RawX { uint32_t v[2][7]; };
 
 // Where a wave's inputs lie.
 struct XRef {
@@ -200,7 +210,7 @@ __device__ __forceinline__ void load_x(const XRef& f, int c, int g, RawX& x) {
     const uint32_t at = (4 * g + i) * row + 2 * f.ch0;
     x.v[0][i] = __builtin_amdgcn_raw_buffer_load_b32(buf, i < 3 && before ? 0xFFFFFFF0u : at, 0, 0);
 #pragma unroll
-    for (int run = 1; run < 4; ++run) x.v[run][i] = __builtin_amdgcn_raw_buffer_load_b32(buf, at + 16 * run * row, 0, 0);
+    for (int run = 1; run < 2; ++run) x.v[run][i] = __builtin_amdgcn_raw_buffer_load_b32(buf, at + 16 * run * row, 0, 0);
   }
   if (CONV && c == 0 && f.hist) {
     const uint16_t* p = f.hist + anew(f.ch0);
@@ -214,19 +224,16 @@ __device__ __forceinline__ void load_x(const XRef& f, int c, int g, RawX& x) {
 // 16 run + 4 g + i.
 struct ConvW { float w0[2], w1[2], w2[2], w3[2], b[2]; };
 template <bool CONV>
-__device__ __forceinline__ void conv_x(const RawX& x, const ConvW& k, float (&v)[2][4][4]) {
+__device__ __forceinline__ void conv_run(const uint32_t (&x)[7], const ConvW& k, float (&v0)[4], float (&v1)[4]) {
+  float in[2][7];
 #pragma unroll
-  for (int run = 0; run < 4; ++run) {
-    float in[2][7];
+  for (int i = CONV ? 0 : 3; i < 7; ++i) { in[0][i] = lo_bf16(x[i]); in[1][i] = hi_bf16(x[i]); }
 #pragma unroll
-    for (int i = CONV ? 0 : 3; i < 7; ++i) { in[0][i] = lo_bf16(x.v[run][i]); in[1][i] = hi_bf16(x.v[run][i]); }
+  for (int q = 0; q < 2; ++q)
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[q][run][i] = CONV ? conv4_bias_silu(k.b[q], k.w0[q], k.w1[q], k.w2[q], k.w3[q], in[q][i], in[q][i + 1], in[q][i + 2], in[q][i + 3])
-                            : in[q][i + 3];
-  }
+    for (int i = 0; i < 4; ++i)
+      (q ? v1 : v0)[i] = CONV ? conv4_bias_silu(k.b[q], k.w0[q], k.w1[q], k.w2[q], k.w3[q], in[q][i], in[q][i + 1], in[q][i + 2], in[q][i + 3])
+                              : in[q][i + 3];
 }
 
 __device__ __forceinline__ void load_conv(const SsmLayer& l, int ch, ConvW& k) {
@@ -248,7 +255,7 @@ __device__ __forceinline__ void prepare_bc(const SsmScanArgs& a, const Ws& w, in
   const int tid = threadIdx.x, wave = tid / 64, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int t0 = a.cu[s], len = a.cu[s + 1] - t0, inner = l.H * l.P, left = len - c * kChunk;
   const int64_t sg = (int64_t)(t0 / kChunk + s + c) * l.G + grp;
-  float v[TILES][2][4][4];
+  float v[TILES][2][2][4];
   float m[2] = {0.f, 0.f};
   RawX x[TILES];
   auto tile_of = [&](int k) { return wave + 4 * k; };     // below PAIRS: of B, then of C
@@ -265,16 +272,19 @@ __device__ __forceinline__ void prepare_bc(const SsmScanArgs& a, const Ws& w, in
     if (tile_of(k) >= 2 * PAIRS) continue;
     ConvW cw;
     if (CONV) load_conv(l, col_of(tile_of(k)) + 2 * r, cw);
-    conv_x<CONV>(x[k], cw, v[k]);
     float top = 0.f;
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+    for (int run = 0; run < 2; ++run) {
+      conv_run<CONV>(x[k].v[run], cw, v[k][0][run], v[k][1][run]);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float& u = v[k][q][i / 4][i % 4];
-        if (16 * (i / 4) + 4 * g + i % 4 >= left) u = 0.f;
-        top = fmaxf(top, finite_abs(u));
-      }
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float& u = v[k][q][run][i];
+          if (16 * run + 4 * g + i >= left) u = 0.f;
+          top = fmaxf(top, finite_abs(u));
+        }
+    }
     m[tile_of(k) >= PAIRS] = fmaxf(m[tile_of(k) >= PAIRS], top);
   }
 #pragma unroll
@@ -293,56 +303,52 @@ __device__ __forceinline__ void prepare_bc(const SsmScanArgs& a, const Ws& w, in
     const int t = tile_of(k);
     if (t >= 2 * PAIRS) continue;
     const bool is_c = t >= PAIRS;
-    const float f = ldexpf(1.f, is_c ? kc : kb);
+    const float f = ldexpf(1.f, is_c ? kc : kb), down = is_c ? 1.f : 1.f / (1 << (kTopBt - kTopB));
     _Float16* to = rows + (is_c ? kChunk * ROW + 32 * (t - PAIRS) : 32 * t) + 2 * r;
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+    for (int run = 0; run < 2; ++run)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[k][q][i / 4][i % 4] *= f;
-    const float down = is_c ? 1.f : 1.f / (1 << (kTopBt - kTopB));
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      *reinterpret_cast<f16x2*>(to + (16 * (i / 4) + 4 * g + i % 4) * ROW) = pack_f16(v[k][0][i / 4][i % 4] * down, v[k][1][i / 4][i % 4] * down);
+      for (int i = 0; i < 4; ++i) {
+        v[k][0][run][i] *= f;
+        v[k][1][run][i] *= f;
+        *reinterpret_cast<f16x2*>(to + (16 * run + 4 * g + i) * ROW) = pack_f16(v[k][0][run][i] * down, v[k][1][run][i] * down);
+      }
     if (!is_c) {
       f16x8* bt = ops + kChunk * N / 8;
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int q = 0; q < 2; ++q) {
+        f16x2 hi[4], lo[4];
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          f16x2 hi[4], lo[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float v0 = v[k][q][2 * z + i / 2][2 * (i % 2)], v1 = v[k][q][2 * z + i / 2][2 * (i % 2) + 1];
-            hi[i] = pack_f16(v0, v1);
-            lo[i] = pack_f16(fmaf((float)hi[i][0], -1.f, v0), fmaf((float)hi[i][1], -1.f, v1));
-          }
-          bt[((2 * t + q) * 2 + z) * 64 + lane] = join(hi[0], hi[1], hi[2], hi[3]);
-          if (CONV) bt[kChunk * N / 8 + ((2 * t + q) * 2 + z) * 64 + lane] = join(lo[0], lo[1], lo[2], lo[3]);
+        for (int i = 0; i < 4; ++i) {
+          const float v0 = v[k][q][i / 2][2 * (i % 2)], v1 = v[k][q][i / 2][2 * (i % 2) + 1];
+          hi[i] = pack_f16(v0, v1);
+          lo[i] = pack_f16(fmaf((float)hi[i][0], -1.f, v0), fmaf((float)hi[i][1], -1.f, v1));
         }
+        bt[(2 * t + q) * 64 + lane] = join(hi[0], hi[1], hi[2], hi[3]);
+        if (CONV) bt[kChunk * N / 8 + (2 * t + q) * 64 + lane] = join(lo[0], lo[1], lo[2], lo[3]);
+      }
     }
   }
   __syncthreads();
-  const _Float16* rc = rows + kChunk * ROW + (16 * wave + r) * ROW + 8 * g;
-  f16x8 cf[KN];
-#pragma unroll
-  for (int ks = 0; ks < KN; ++ks) {
-    cf[ks] = *reinterpret_cast<const f16x8*>(rc + 32 * ks);
-    ops[(wave * KN + ks) * 64 + lane] = cf[ks];
-  }
-  f16x4* gt = reinterpret_cast<f16x4*>(w.gt + sg * 10 * 256);
-  for (int st = 0; st <= wave; ++st) {
+  // rows of C as operands, two tiles of 16 by two waves each; the three tiles of C . B by a wave each
+  const _Float16* rc = rows + kChunk * ROW + r * ROW + 8 * g;
+  for (int ks = wave / 2; ks < KN; ks += 2)
+    ops[((wave % 2) * KN + ks) * 64 + lane] = *reinterpret_cast<const f16x8*>(rc + 16 * (wave % 2) * ROW + 32 * ks);
+  if (wave < kTiles) {
+    const int tt = wave > 0, st = wave > 1;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int ks = 0; ks < KN; ++ks)
-      acc = mma(*reinterpret_cast<const f16x8*>(rows + (16 * st + r) * ROW + 8 * g + 32 * ks), cf[ks], acc);
+      acc = mma(*reinterpret_cast<const f16x8*>(rows + (16 * st + r) * ROW + 8 * g + 32 * ks),
+                *reinterpret_cast<const f16x8*>(rc + 16 * tt * ROW + 32 * ks), acc);
     const f16x2 p0 = pack_f16(acc[0], acc[1]), p1 = pack_f16(acc[2], acc[3]);
-    gt[(wave * (wave + 1) / 2 + st) * 64 + lane] = f16x4{p0[0], p0[1], p1[0], p1[1]};
+    reinterpret_cast<f16x4*>(w.gt + sg * 4 * 256)[wave * 64 + lane] = f16x4{p0[0], p0[1], p1[0], p1[1]};
   }
 }
 
-// The steps of one (chunk, head): a wave, a lane per token.
+// The steps of a chunk for two heads: half a wave each, a lane per token.
 __device__ __forceinline__ void prepare_steps(const SsmScanArgs& a, const Ws& w, int s, int c, int h) {
-  const int lane = threadIdx.x & 63, t0 = a.cu[s], len = a.cu[s + 1] - t0, p = c * kChunk + lane;
+  const int lane = threadIdx.x & 31, t0 = a.cu[s], len = a.cu[s + 1] - t0, p = c * kChunk + lane;
   const float A = a.l.A[h];
   const float dt = p < len ? ssm_step(a.l, a.dt, (int64_t)(t0 + p) * a.dt_stride + h, h) : 0.f;
   // log2 of the token's decay; one of 2^-200 leaves nothing of a state, and
@@ -352,27 +358,31 @@ __device__ __forceinline__ void prepare_steps(const SsmScanArgs& a, const Ws& w,
   if (p >= len) al = 0.f;
   float cum = al, after = al;
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const float x = __shfl_up(cum, d), y = __shfl_down(after, d);
+  for (int d = 1; d < 32; d *= 2) {
+    const float x = __shfl_up(cum, d, 32), y = __shfl_down(after, d, 32);
     if (lane >= d) cum += x;
-    if (lane + d < 64) after += y;
+    if (lane + d < 32) after += y;
   }
-  const float total = __shfl(cum, 63);
+  const float total = __shfl(cum, 31, 32);
   // sum of the later tokens' decays, from the end: near tokens keep their
   // precision behind a long sum
-  after = __shfl_down(after, 1);
-  if (lane == 63) after = 0.f;
+  after = __shfl_down(after, 1, 32);
+  if (lane == 31) after = 0.f;
   const float wt = __builtin_amdgcn_exp2f(after) * dt;
-  const float grow = over_wave(fmaxf(al, 0.f), AddOp{});
-  const float wmax = over_wave(finite_abs(wt), MaxOp{});
-  const float dmax = over_wave(finite_abs(dt), MaxOp{}) * __builtin_amdgcn_exp2f(fminf(grow, 60.f));
+  const float grow = over_half(fmaxf(al, 0.f), AddOp{});
+  const float wmax = over_half(finite_abs(wt), MaxOp{});
+  const float dmax = over_half(finite_abs(dt), MaxOp{}) * __builtin_amdgcn_exp2f(fminf(grow, 60.f));
   float* tab = w.tab + ((int64_t)(t0 / kChunk + s + c) * a.l.H + h) * kTab;
   tab[lane] = dt;
-  tab[64 + lane] = cum;
+  tab[32 + lane] = cum;
   const int kw = 10 - pow2_above(wmax);
-  tab[128 + lane] = ldexpf(wt, kw);
+  tab[64 + lane] = ldexpf(wt, kw);
   if (lane < 5)
-    tab[192 + lane] = lane == 0 ? total : lane == 1 ? wmax : lane == 2 ? dmax : lane == 3 ? __builtin_amdgcn_exp2f(total) : __int_as_float(kw);
+    tab[96 + lane] = lane == 0   ? total
+                     : lane == 1 ? wmax * kChunk
+                     : lane == 2 ? __int_as_float(pow2_above(dmax))
+                     : lane == 3 ? __builtin_amdgcn_exp2f(total)
+                                 : __int_as_float(kw);
 }
 
 template <int N, bool CONV>
@@ -384,7 +394,7 @@ __global__ void __launch_bounds__(256) ssm_prepare_kernel(const SsmScanArgs a, c
   if ((int)blockIdx.y < a.l.G) {
     prepare_bc<N, CONV>(a, w, s, c, blockIdx.y, rows, red);
   } else {
-    const int h = (blockIdx.y - a.l.G) * 4 + threadIdx.x / 64;
+    const int h = (blockIdx.y - a.l.G) * 8 + threadIdx.x / 32;
     if (h < a.l.H) prepare_steps(a, w, s, c, h);
   }
 }
@@ -392,27 +402,28 @@ __global__ void __launch_bounds__(256) ssm_prepare_kernel(const SsmScanArgs a, c
 // ------------------------------------------------------------------ scan --
 // Copies 16 bytes a lane from global memory to LDS, from the wave's base on.
 // The compiler does not see it and so waits for none before other reads of
-// LDS: an s_waitcnt vmcnt(0) and a barrier stand between it and its readers.
+// LDS: arrived() and a barrier stand between it and its readers.
 __device__ __forceinline__ void to_lds(const void* g, const void* base) {
   const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)base;
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(g) : "memory", "m0");
 }
-// Waits until all but the N latest accesses to memory are done.
-template <int N>
-__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+// Waits for the wave's accesses to memory, but the LATER newest of them (they
+// complete in order).
+template <int LATER>
+__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER) : "memory"); }
 
-// One (16 t, 32 s) operand of M^T: tiles st = 2 KS and 2 KS + 1 of the tile row TT.
-template <int TT, int KS>
+// The operand of M^T for 16 tokens t (tile row TT): both tiles of s.
+template <int TT>
 __device__ __forceinline__ f16x8 weigh(const f16x4* gt, const float* tab, int lane, int ad, float dm) {
   const int r = lane & 15, g = lane >> 4;
-  const float ct = tab[64 + 16 * TT + r] + (float)ad;
+  const float ct = tab[32 + 16 * TT + r] + (float)ad;
   f16x2 o[4];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int st = 2 * KS + q;
+    const int st = q;
     if (st > TT) { o[2 * q] = o[2 * q + 1] = f16x2{0, 0}; continue; }
-    const f16x4 gv = gt[(TT * (TT + 1) / 2 + st) * 64 + lane];
-    const f32x4 cs = *reinterpret_cast<const f32x4*>(tab + 64 + 16 * st + 4 * g);
+    const f16x4 gv = gt[(TT + st) * 64 + lane];
+    const f32x4 cs = *reinterpret_cast<const f32x4*>(tab + 32 + 16 * st + 4 * g);
     const f32x4 ds = *reinterpret_cast<const f32x4*>(tab + 16 * st + 4 * g);
     float v[4];
 #pragma unroll
@@ -426,19 +437,32 @@ __device__ __forceinline__ f16x8 weigh(const f16x4* gt, const float* tab, int la
   return join(o[0], o[1], o[2], o[3]);
 }
 
-template <int P, int N, bool OUT, bool CONV>
-__global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, const Ws w, int hpw, int split, int grouped) {
-  constexpr int WPH = P / 32, NT = N / 16, KN = N / 32, OPS = kChunk * N * 2;   // bytes of one operand
-  constexpr int HMAX = 4 / WPH, GT = 10 * 512;
-  // C, B^T hi, B^T lo (without the convolution B is exact in fp16: no lo)
-  constexpr int FIRST = OUT ? 0 : OPS, LAST = CONV ? 3 * OPS : 2 * OPS;
-  __shared__ __align__(16) char ops[LAST - FIRST];
-  __shared__ __align__(16) char gts[OUT ? GT : 16];
-  __shared__ __align__(16) f16x8 fm[OUT ? HMAX : 1][6][64];
-  __shared__ __align__(16) float tabs[2][HMAX][kTab];
+// LDS of a workgroup of NW waves: C, B^T hi, B^T lo (without the
+// convolution B is exact in fp16: no lo), C . B, x, M and the tables.
+template <int P, int N, int NW, bool OUT, bool CONV>
+struct ScanLds {
+  static constexpr int OPS = kChunk * N * 2;
+  static constexpr int FIRST = OUT ? 0 : OPS, LAST = CONV ? 3 * OPS : 2 * OPS;   // of the operands in a slot
+  static constexpr int GT = OUT ? 4 * 512 : 0, ROWS = CONV ? 35 : 32;
+  static constexpr int X = (ROWS * 64 * NW + 1023) / 1024 * 1024, HPW = NW / (P / 32);
+  static constexpr int TABS = HPW > 2 ? HPW * kTab * 4 : 1024;     // of a chunk, fetched by 1,024 bytes
+  static constexpr int BYTES = LAST - FIRST + GT + 2 * X + (OUT ? HPW * 2048 : 0) + 2 * TABS;
+};
+
+template <int P, int N, int NW, bool OUT, bool CONV>
+__global__ void __launch_bounds__(64 * NW, N == 128 ? 2 : 3) ssm_chunk_kernel(const SsmScanArgs a, const Ws w, int split, int grouped) {
+  using L = ScanLds<P, N, NW, OUT, CONV>;
+  constexpr int nw = NW, hpw = L::HPW;
+  constexpr int WPH = P / 32, NT = N / 16, KN = N / 32, OPS = L::OPS, FIRST = L::FIRST, LAST = L::LAST, GT = L::GT;
+  extern __shared__ __align__(16) char lds[];
   const SsmLayer& l = a.l;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid & 63, r = lane & 15, g = lane >> 4;
-  const int nw = hpw * WPH, hl = wave / WPH, half = wave % WPH;
+  const int hl = wave / WPH, half = wave % WPH;
+  char* const ops = lds;
+  char* const gts = ops + (LAST - FIRST);
+  char* const xs = gts + GT;
+  f16x8 (*const fm)[64] = reinterpret_cast<f16x8 (*)[64]>(xs + 2 * L::X + (OUT ? hl * 2048 : 0));   // this head's M
+  char* const tabs = xs + 2 * L::X + (OUT ? hpw * 2048 : 0);
   const int hb = l.H / hpw, per_group = hb / l.G;
   int unit, b;
   if (grouped) {   // the workgroups that read the same B and C go to one XCD
@@ -461,22 +485,42 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
   const int h = b * hpw + hl, grp = h / (l.H / l.G), ch0 = h * P + 32 * half + 2 * r;
   const int64_t hpn = (int64_t)l.P * l.N, slot0 = t0 / kChunk + s;
   const int st_at = (32 * half + 2 * r) * N + 8 * g;       // this lane's entries of a head's state
-  const XRef xref{a.x + (int64_t)t0 * a.x_stride, a.conv_in ? a.conv_in + (int64_t)s * 3 * l.conv_dim : nullptr, a.x_stride, l.conv_dim, len, ch0};
-  // The operands of a chunk are fetched while the one before is worked on:
-  // B^T, C . B and the tables once the update of the state is through, C once
-  // the outputs are.
+  // A chunk is fetched while others are worked on, to LDS directly, 16 bytes a
+  // lane: its operands once the ones before are through with the products, its
+  // x a chunk earlier.  Nothing waits for the outputs' way to memory: the waits
+  // leave the two newest accesses, the chunk's two stores, out (waiting for them
+  // cost 117 us of 364 at 32 x 1,024 tokens of 64 heads of 64 on 128).
   auto fetch = [&](int c) __attribute__((always_inline)) {
     const int64_t sg = (slot0 + c) * l.G + grp;
     const char* src = w.bc + sg * 3 * OPS;
-    for (int i = OPS / 1024 + wave; i < LAST / 1024; i += nw) to_lds(src + 1024 * i + 16 * lane, ops + 1024 * i - FIRST);
-    if (OUT)
-      for (int i = wave; i < GT / 1024; i += nw) to_lds(reinterpret_cast<const char*>(w.gt) + sg * GT + 1024 * i + 16 * lane, gts + 1024 * i);
-    if (half == 0) to_lds(w.tab + ((slot0 + c) * l.H + h) * kTab + 4 * lane, tabs[c & 1][hl]);
+    for (int i = FIRST / 1024 + wave; i < LAST / 1024; i += nw) to_lds(src + 1024 * i + 16 * lane, ops + 1024 * i - FIRST);
+    for (int i = wave; i < GT / 1024; i += nw) to_lds(reinterpret_cast<const char*>(w.gt) + sg * GT + 1024 * i + 16 * lane, gts + 1024 * i);
+    for (int i = wave; i < L::TABS / 1024; i += nw)
+      to_lds(w.tab + ((slot0 + c) * l.H + b * hpw) * kTab + 256 * i + 4 * lane, tabs + (c & 1) * L::TABS + 1024 * i);
   };
-  RawX x;
+  // Rows of x (from three before the chunk's first with the convolution; past
+  // the prompt's end its last) of the workgroup's channels, 64 bytes a wave.
+  // Row p keeps wave w's piece at piece w ^ (p / 4 % 2): rows 4 apart, which two
+  // lane groups read together, lie in different banks.
+  constexpr int XSWAP = NW > 1 ? 1 : 0;
+  auto fetch_x = [&](int c) __attribute__((always_inline)) {
+    const char* src = reinterpret_cast<const char*>(a.x + (int64_t)t0 * a.x_stride + b * hpw * P);
+    const int p0 = c * kChunk - (CONV ? 3 : 0);
+    for (int i = wave; i < L::X / 1024; i += nw) {
+      const int at = 64 * i + lane, p = at / (4 * nw), blk = (at % (4 * nw)) ^ (((p >> 2) & XSWAP) << 2);
+      to_lds(src + (int64_t)min(max(p0 + p, 0), len - 1) * a.x_stride * 2 + 16 * blk, xs + (c & 1) * L::X + 1024 * i);
+    }
+  };
+  uint32_t hist[3] = {0, 0, 0};     // this lane's inputs before the prompt
   if (c_first < c_end) {
     fetch(c_first);
-    load_x<CONV>(xref, c_first, g, x);
+    fetch_x(c_first);
+    if (c_first + 1 < c_end) fetch_x(c_first + 1);
+    if (CONV && c_first == 0 && a.conv_in) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        hist[i] = *reinterpret_cast<const uint32_t*>(a.conv_in + ((int64_t)s * 3 + i) * l.conv_dim + ch0);
+    }
   }
   ConvW cw;
   if (CONV) load_conv(l, ch0, cw);
@@ -547,9 +591,52 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
     }
   };
   float seg_sum = 0.f;
+  arrived<0>();
+  __syncthreads();   // the first chunk is whole
   const f16x8* fc = reinterpret_cast<const f16x8*>(ops) + lane;
   const f16x8* bh = reinterpret_cast<const f16x8*>(ops + OPS - FIRST) + lane;
   const f16x8* bl = reinterpret_cast<const f16x8*>(ops + (CONV ? 2 * OPS : OPS) - FIRST) + lane;
+
+  // A chunk's x through the convolution, and the largest of each channel.
+  float xv[2][2][4], xmax[2];
+  auto take_x = [&](int c) __attribute__((always_inline)) {
+    // row 16 run + 4 g + j of the tile, from one address for j below 4 and one beyond
+    const uint32_t* xr[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) xr[j] = reinterpret_cast<const uint32_t*>(xs + (c & 1) * L::X) + r + 16 * (4 * g * nw + (wave ^ ((g + j) & XSWAP)));
+#pragma unroll
+    for (int run = 0; run < 2; ++run) {
+      uint32_t x[7];
+#pragma unroll
+      for (int i = CONV ? 0 : 3; i < 7; ++i) {
+        const int j = i - (CONV ? 0 : 3);
+        x[i] = xr[j / 4][16 * nw * (16 * run + j)];
+      }
+      if (CONV && run == 0 && c == 0 && g == 0) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) x[i] = hist[i];
+      }
+      conv_run<CONV>(x, cw, xv[0][run], xv[1][run]);
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      xmax[q] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) xmax[q] = fmaxf(xmax[q], fabsf(xv[q][i / 4][i % 4]));   // (NaN is passed over)
+    }
+    if (__ballot(!(fmaxf(xmax[0], xmax[1]) < __builtin_inff()))) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        xmax[q] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) xmax[q] = fmaxf(xmax[q], finite_abs(xv[q][i / 4][i % 4]));
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) xmax[q] = over_groups(xmax[q], lane);
+  };
+  const int pd_max = 14 - pow2_above(fabsf(D));
+  if (c_first < c_end) take_x(c_first);
 
   for (int c = c_first; c < c_end; ++c) {
     const int64_t sg = (slot0 + c) * l.G + grp;
@@ -559,48 +646,45 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
     if (OUT) keep_until(t0 + c * kChunk + left);
     const int2 kk = w.k[sg];
     const int kbt = kk.x, kb = kbt - kTopBt + kTopB, kc = kk.y;
-    float xv[2][4][4];
-    conv_x<CONV>(x, cw, xv);
-    float xmax[2] = {0.f, 0.f};
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) xmax[q] = fmaxf(xmax[q], fabsf(xv[q][i / 4][i % 4]));   // (NaN is passed over)
-    if (__ballot(!(fmaxf(xmax[0], xmax[1]) < __builtin_inff()))) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        xmax[q] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) xmax[q] = fmaxf(xmax[q], finite_abs(xv[q][i / 4][i % 4]));
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < 2; ++q) xmax[q] = over_groups(xmax[q], lane);
-    arrived<0>();
-    __syncthreads();   // B^T, C . B and the tables are whole; the last outputs are through with C and M
-    if (OUT) {
-      const char* src = w.bc + sg * 3 * OPS;
-      for (int i = wave; i < OPS / 1024; i += nw) to_lds(src + 1024 * i + 16 * lane, ops + 1024 * i);
-    }
-    if (c + 1 < c_end) load_x<CONV>(xref, c + 1, g, x);
+    arrived<OUT ? 2 : 0>();
+    __syncthreads();   // the chunk's operands and the next x are whole; x is in registers; the last outputs are through with M
+    if (c + 2 < c_end) fetch_x(c + 2);
+    const float* tab = reinterpret_cast<const float*>(tabs + (c & 1) * L::TABS) + hl * kTab;
+    const float alpha = tab[99];
+    const int kw = __float_as_int(tab[100]), ad = min(-__float_as_int(tab[98]), pd_max - (kb + kc)), m = kb + kc + ad;
     __builtin_amdgcn_sched_barrier(0);
-    const float* tab = tabs[c & 1][hl];
-    const float alpha = tab[195], wmax = tab[193], dmax = tab[194];
-    const int kw = __float_as_int(tab[196]);
 
-    // the weights inside the chunk, as operands: element (t = column, s) of M^T
-    int m = 0;
+    // the entering state with C: S as an operand times 2^es, one power for the
+    // wave; y[tt][q]: channel 2 (4 g + i) + q at token 16 tt + r
+    f32x4 y[2][2];
+    float f1 = 0.f;
     if (OUT) {
-      const int ad = min(-pow2_above(dmax), 14 - pow2_above(fabsf(D)) - (kb + kc));
-      m = kb + kc + ad;
+      const int es = kTopS16 - pow2_above(over_wave16(fmaxf(bound[0], bound[1])));
+      f1 = ldexpf(1.f, max(-126, min(126, -(es + kc))));
+      const float down[2] = {ldexpf(1.f, es - e[0]), ldexpf(1.f, es - e[1])};
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) y[tt][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int z = 0; z < KN; ++z) {
+        const f16x8 c0 = fc[z * 64], c1 = fc[(KN + z) * 64];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const f16x8 so = join(pack_f16(S[2 * z][q][0] * down[q], S[2 * z + 1][q][0] * down[q]),
+                                pack_f16(S[2 * z][q][1] * down[q], S[2 * z + 1][q][1] * down[q]),
+                                pack_f16(S[2 * z][q][2] * down[q], S[2 * z + 1][q][2] * down[q]),
+                                pack_f16(S[2 * z][q][3] * down[q], S[2 * z + 1][q][3] * down[q]));
+          y[0][q] = mma(so, c0, y[0][q]);
+          y[1][q] = mma(so, c1, y[1][q]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      // the weights inside the chunk, as operands: element (t = column, s) of M^T
       const float dm = ldexpf(D, m);
       const f16x4* gt = reinterpret_cast<const f16x4*>(gts);
-      if (0 % WPH == half) fm[hl][0][lane] = weigh<0, 0>(gt, tab, lane, ad, dm);
-      if (1 % WPH == half) fm[hl][1][lane] = weigh<1, 0>(gt, tab, lane, ad, dm);
-      if (2 % WPH == half) fm[hl][2][lane] = weigh<2, 0>(gt, tab, lane, ad, dm);
-      if (3 % WPH == half) fm[hl][3][lane] = weigh<2, 1>(gt, tab, lane, ad, dm);
-      if (4 % WPH == half) fm[hl][4][lane] = weigh<3, 0>(gt, tab, lane, ad, dm);
-      if (5 % WPH == half) fm[hl][5][lane] = weigh<3, 1>(gt, tab, lane, ad, dm);
+      if (0 == half) fm[0][lane] = weigh<0>(gt, tab, lane, ad, dm);
+      if (1 % WPH == half) fm[1][lane] = weigh<1>(gt, tab, lane, ad, dm);
     }
     __builtin_amdgcn_sched_barrier(0);
 
@@ -610,65 +694,48 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
     const int kx = !OUT || (xw >= 0.125f && xw < 32768.f) ? 0 : 14 - pow2_above(xw);
     int ks[2], e_new[2];
     float grown[2];
+    const float wmax = ldexpf(tab[97], kTopBt - kbt);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      grown[q] = fmaf(alpha, bound[q], ldexpf(64.f * wmax * xmax[q], kTopBt - kbt));
+      grown[q] = fmaf(alpha, bound[q], wmax * xmax[q]);
       ks[q] = xmax[q] >= 0x1p-6f && xmax[q] < 16.f ? 0 : 4 - pow2_above(xmax[q]);
       ks[q] = min(ks[q], 90 - pow2_above(grown[q]) - kbt - kw);     // the state stays inside fp32
       e_new[q] = kbt + kw + ks[q];
     }
     const bool plain = __ballot((kx | ks[0] | ks[1]) != 0) == 0;
-    f16x8 xo[2][2], xh[2][2], xl[2][2], so[2][KN];
+    f16x8 xo[2], xh[2], xl[2];
     if (OUT) {
       if (!plain) {
         const float f = ldexpf(1.f, kx);
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) xv[q][i / 4][i % 4] *= f;
+          for (int i = 0; i < 8; ++i) xv[q][i / 4][i % 4] *= f;
       }
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int z = 0; z < 2; ++z)
-          xo[q][z] = join(pack_f16(xv[q][2 * z][0], xv[q][2 * z][1]), pack_f16(xv[q][2 * z][2], xv[q][2 * z][3]),
-                          pack_f16(xv[q][2 * z + 1][0], xv[q][2 * z + 1][1]), pack_f16(xv[q][2 * z + 1][2], xv[q][2 * z + 1][3]));
+        xo[q] = join(pack_f16(xv[q][0][0], xv[q][0][1]), pack_f16(xv[q][0][2], xv[q][0][3]), pack_f16(xv[q][1][0], xv[q][1][1]),
+                     pack_f16(xv[q][1][2], xv[q][1][3]));
     }
     if (!plain) {
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) xv[q][i / 4][i % 4] = ldexpf(xv[q][i / 4][i % 4], ks[q] - kx);
+        for (int i = 0; i < 8; ++i) xv[q][i / 4][i % 4] = ldexpf(xv[q][i / 4][i % 4], ks[q] - kx);
     }
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      const f32x4 wa = *reinterpret_cast<const f32x4*>(tab + 128 + 32 * z + 4 * g), wb = *reinterpret_cast<const f32x4*>(tab + 144 + 32 * z + 4 * g);
+    {
+      const f32x4 wt[2] = {*reinterpret_cast<const f32x4*>(tab + 64 + 4 * g), *reinterpret_cast<const f32x4*>(tab + 80 + 4 * g)};
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         f16x2 hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const f32x4& wt = i < 2 ? wa : wb;
-          const float v0 = xv[q][2 * z + i / 2][2 * (i % 2)] * wt[2 * (i % 2)], v1 = xv[q][2 * z + i / 2][2 * (i % 2) + 1] * wt[2 * (i % 2) + 1];
+          const float v0 = xv[q][i / 2][2 * (i % 2)] * wt[i / 2][2 * (i % 2)], v1 = xv[q][i / 2][2 * (i % 2) + 1] * wt[i / 2][2 * (i % 2) + 1];
           hi[i] = pack_f16(v0, v1);
           lo[i] = pack_f16(fmaf((float)hi[i][0], -1.f, v0), fmaf((float)hi[i][1], -1.f, v1));
         }
-        xh[q][z] = join(hi[0], hi[1], hi[2], hi[3]);
-        xl[q][z] = join(lo[0], lo[1], lo[2], lo[3]);
-      }
-    }
-    float f1 = 0.f;
-    if (OUT) {
-      // the entering state as an operand: times 2^es, one power for the wave
-      const int es = kTopS16 - pow2_above(over_wave16(fmaxf(bound[0], bound[1])));
-      f1 = ldexpf(1.f, max(-126, min(126, -(es + kc))));
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const float down = ldexpf(1.f, es - e[q]);
-#pragma unroll
-        for (int z = 0; z < KN; ++z)
-          so[q][z] = join(pack_f16(S[2 * z][q][0] * down, S[2 * z + 1][q][0] * down), pack_f16(S[2 * z][q][1] * down, S[2 * z + 1][q][1] * down),
-                          pack_f16(S[2 * z][q][2] * down, S[2 * z + 1][q][2] * down), pack_f16(S[2 * z][q][3] * down, S[2 * z + 1][q][3] * down));
+        xh[q] = join(hi[0], hi[1], hi[2], hi[3]);
+        xl[q] = join(lo[0], lo[1], lo[2], lo[3]);
       }
     }
 
@@ -682,101 +749,79 @@ __global__ void __launch_bounds__(256, 2) ssm_chunk_kernel(const SsmScanArgs a, 
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      if (nt % 2 == 0) __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) S[nt][q][i] *= mul[q];
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const f16x8 fh = bh[(nt * 2 + z) * 64];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          S[nt][q] = mma(fh, xh[q][z], S[nt][q]);
-          S[nt][q] = mma(fh, xl[q][z], S[nt][q]);
-        }
-        if (CONV) {
-          const f16x8 fl = bl[(nt * 2 + z) * 64];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) S[nt][q] = mma(fl, xh[q][z], S[nt][q]);
-        }
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    if (!OUT) {
-      seg_sum += tab[192];
-      __syncthreads();   // the update is through with B^T
-      if (c + 1 < c_end) fetch(c + 1);
-      continue;
-    }
-
-    // a value of x that is not finite has left none of its channel's state
-    // finite; in the products inside the chunk it would reach the tokens
-    // before it, at weights of 0
-    int first_bad[2] = {INT_MAX, INT_MAX};
-    const bool bad = __ballot(!(fabsf(S[0][0][0]) + fabsf(S[0][1][0]) < __builtin_inff())) != 0;
-    if (bad) {
-      const int g2 = anew(g), lane2 = anew(lane);
+      if (nt % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+      const f16x8 fh = bh[nt * 64];
+      f16x8 fl;
+      if (CONV) fl = bl[nt * 64];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
 #pragma unroll
-        for (int j = 15; j >= 0; --j) {
-          if (!(fabsf((float)xo[q][j / 8][j % 8]) < __builtin_inff())) {
-            first_bad[q] = slot_of(j / 8, g2, j % 8);
-            xo[q][j / 8][j % 8] = (_Float16)0.f;
-          }
-        }
-        first_bad[q] = min(first_bad[q], from_lane(first_bad[q], lane2 ^ 16));
-        first_bad[q] = min(first_bad[q], from_lane(first_bad[q], lane2 ^ 32));
+        for (int i = 0; i < 4; ++i) S[nt][q][i] *= mul[q];
+        S[nt][q] = mma(fh, xh[q], S[nt][q]);
+        S[nt][q] = mma(fh, xl[q], S[nt][q]);
+        if (CONV) S[nt][q] = mma(fl, xh[q], S[nt][q]);
       }
     }
-    if (c + 1 < c_end) arrived<CONV ? 28 : 16>();   // all but the next inputs
-    else arrived<0>();
-    __syncthreads();   // C and M are whole; the update is through with B^T
+    __builtin_amdgcn_sched_barrier(0);
+    if (!OUT) seg_sum += tab[96];
+    // the outputs' decays, before the tables may be fetched over: from the start of the chunk
+    float fe[2];
+    if (OUT) {
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt) fe[tt] = f1 * __builtin_amdgcn_exp2f(tab[32 + 16 * tt + r]);
+    }
+    __syncthreads();   // M is whole; the products are through with the operands
     if (c + 1 < c_end) fetch(c + 1);
-    const float f2 = ldexpf(1.f, max(-126, min(126, -(m + kx))));
-    uint16_t* to = a.out + ((int64_t)(t0 + c * kChunk) * l.H + h) * P + 32 * half;
-    const uint32_t out_at = (uint32_t)(r * l.H * P + 8 * g);
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-      __builtin_amdgcn_sched_barrier(0);
-      // a tile of 16 tokens: with the entering state, and inside the chunk
-      f32x4 y1[2], y2[2];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) y1[q] = y2[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int z = 0; z < KN; ++z) {
-        const f16x8 cf = fc[(tt * KN + z) * 64];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) y1[q] = mma(so[q][z], cf, y1[q]);
-      }
-#pragma unroll
-      for (int z = 0; z <= tt / 2; ++z) {
-        const f16x8 mf = fm[hl][tt < 2 ? tt : 2 * tt - 2 + z][lane];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) y2[q] = mma(xo[q][z], mf, y2[q]);
-      }
-      const int t = 16 * tt + r;
-      const float fe = f1 * __builtin_amdgcn_exp2f(tab[64 + t]);
-      float y[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) y[2 * i + q] = fmaf(y2[q][i], f2, y1[q][i] * fe);
+    if (OUT) {
+      // a value of x that is not finite has left none of its channel's state
+      // finite; in the products inside the chunk it would reach the tokens
+      // before it, at weights of 0
+      int first_bad[2] = {INT_MAX, INT_MAX};
+      const bool bad = __ballot(!(fabsf(S[0][0][0]) + fabsf(S[0][1][0]) < __builtin_inff())) != 0;
       if (bad) {
-        const int row = anew(4 * g);
+        const int g2 = anew(g), lane2 = anew(lane);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int q = 0; q < 2; ++q) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-            if (t >= from_lane(first_bad[q], row + i)) y[2 * i + q] = __builtin_nanf("");
+          for (int j = 7; j >= 0; --j) {
+            if (!(fabsf((float)xo[q][j]) < __builtin_inff())) {
+              first_bad[q] = slot_of(g2, j);
+              xo[q][j] = (_Float16)0.f;
+            }
+          }
+          first_bad[q] = min(first_bad[q], from_lane(first_bad[q], lane2 ^ 16));
+          first_bad[q] = min(first_bad[q], from_lane(first_bad[q], lane2 ^ 32));
+        }
       }
-      if (t < left) {
-        uint4 o;
-        o.x = pack_bf16(y[0], y[1]); o.y = pack_bf16(y[2], y[3]); o.z = pack_bf16(y[4], y[5]); o.w = pack_bf16(y[6], y[7]);
-        *reinterpret_cast<uint4*>(to + (int64_t)16 * tt * l.H * P + out_at) = o;
+      const float f2 = ldexpf(1.f, max(-126, min(126, -(m + kx))));
+      uint16_t* to = a.out + ((int64_t)(t0 + c * kChunk) * l.H + h) * P + 32 * half;
+      const uint32_t out_at = (uint32_t)(r * l.H * P + 8 * g);
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt) {
+        const f16x8 mf = fm[tt][lane];
+        float o[8];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const f32x4 y2 = mma(xo[q], mf, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[2 * i + q] = fmaf(y2[i], f2, y[tt][q][i] * fe[tt]);
+        }
+        const int t = 16 * tt + r;
+        if (bad) {
+          const int row = anew(4 * g);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              if (t >= from_lane(first_bad[q], row + i)) o[2 * i + q] = __builtin_nanf("");
+        }
+        if (t < left)
+          *reinterpret_cast<uint4*>(to + (int64_t)16 * tt * l.H * P + out_at) =
+              make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
+    if (c + 1 < c_end) take_x(c + 1);
   }
   if (!OUT) {
     store_state(w.seg + ((int64_t)unit * l.H + h) * hpn);
@@ -794,7 +839,7 @@ __device__ __forceinline__ uint16_t raw_at(const SsmScanArgs& a, int s, int t0, 
 }
 
 // The state at a checkpoint inside a chunk, from the one that enters the chunk,
-// token by token (63 at most): a workgroup per 32 channels of a head, whose N
+// token by token (31 at most): a workgroup per 32 channels of a head, whose N
 // columns lie on N / 16 lanes.
 template <int N>
 __global__ void __launch_bounds__(2 * N) ssm_ckpt_kernel(const SsmScanArgs a) {
@@ -872,37 +917,56 @@ __global__ void __launch_bounds__(256) ssm_scan_window_kernel(const SsmScanArgs 
   for (int j = 0; j < 3; ++j) to[(int64_t)j * dim] = v[j];
 }
 
-template <int P, int N>
+template <int P, int N, int NW>
 hipError_t launch(const SsmScanArgs& a, const Ws& w, int segs, bool inside, hipStream_t st) {
   const SsmLayer& l = a.l;
   hipError_t e = hipSuccess;
   if (a.n_tokens > 0) {
-    const dim3 prep(w.slots, l.G + (l.H + 3) / 4);
+    const dim3 prep(w.slots, l.G + (l.H + 7) / 8);
     if (l.conv_w) hipLaunchKernelGGL((ssm_prepare_kernel<N, true>), prep, dim3(256), 0, st, a, w);
     else hipLaunchKernelGGL((ssm_prepare_kernel<N, false>), prep, dim3(256), 0, st, a, w);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  const int hpw = heads_per_wg(l), hb = l.H / hpw, split = segs > 1;
+  const int hb = l.H / (NW / (P / 32)), split = segs > 1;
   const int64_t units = split ? w.seg_slots : a.n_seqs, cells = units * l.G;
   const int grouped = cells >= 32;
-  const dim3 grid((uint32_t)(grouped ? (cells + 7) / 8 * 8 * (hb / l.G) : units * hb)), blk(64 * hpw * (P / 32));
+  const dim3 grid((uint32_t)(grouped ? (cells + 7) / 8 * 8 * (hb / l.G) : units * hb));
+  auto scan = [&](auto out, auto conv) {
+    constexpr bool O = decltype(out)::value, C = decltype(conv)::value;
+    constexpr int bytes = ScanLds<P, N, NW, O, C>::BYTES;
+    static_assert(bytes <= 64 * 1024, "past what a launch has without asking");
+    hipLaunchKernelGGL((ssm_chunk_kernel<P, N, NW, O, C>), grid, dim3(64 * NW), bytes, st, a, w, split, grouped);
+    return hipGetLastError();
+  };
+  using T = std::true_type;
+  using F = std::false_type;
   if (split) {
-    if (l.conv_w) hipLaunchKernelGGL((ssm_chunk_kernel<P, N, false, true>), grid, blk, 0, st, a, w, hpw, split, grouped);
-    else hipLaunchKernelGGL((ssm_chunk_kernel<P, N, false, false>), grid, blk, 0, st, a, w, hpw, split, grouped);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if ((e = l.conv_w ? scan(F{}, T{}) : scan(F{}, F{})) != hipSuccess) return e;
     hipLaunchKernelGGL(ssm_pass_kernel, dim3(a.n_seqs, l.H, (P * N + 1023) / 1024), dim3(256), 0, st, a, w, hb);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  if (l.conv_w) hipLaunchKernelGGL((ssm_chunk_kernel<P, N, true, true>), grid, blk, 0, st, a, w, hpw, split, grouped);
-  else hipLaunchKernelGGL((ssm_chunk_kernel<P, N, true, false>), grid, blk, 0, st, a, w, hpw, split, grouped);
-  if ((e = hipGetLastError()) != hipSuccess || !inside) return e;
+  e = l.conv_w ? scan(T{}, T{}) : scan(T{}, F{});
+  if (e != hipSuccess || !inside) return e;
   hipLaunchKernelGGL((ssm_ckpt_kernel<N>), dim3(a.n_ckpt, l.H, P / 32), dim3(2 * N), 0, st, a);
   return hipGetLastError();
 }
 
+template <int P, int N>
+hipError_t launch_n(const SsmScanArgs& a, const Ws& w, int segs, bool inside, hipStream_t st) {
+  const int nw = heads_per_wg(a.l) * (P / 32);
+  if constexpr (P <= 64) {
+    if (nw == 2) return launch<P, N, 2>(a, w, segs, inside, st);
+  }
+  if constexpr (P == 32) {
+    if (nw == 1) return launch<P, N, 1>(a, w, segs, inside, st);
+  }
+  return launch<P, N, 4>(a, w, segs, inside, st);
+}
+
 template <int P>
 hipError_t launch_p(const SsmScanArgs& a, const Ws& w, int segs, bool inside, hipStream_t st) {
-  return a.l.N == 32 ? launch<P, 32>(a, w, segs, inside, st) : a.l.N == 64 ? launch<P, 64>(a, w, segs, inside, st) : launch<P, 128>(a, w, segs, inside, st);
+  return a.l.N == 32 ? launch_n<P, 32>(a, w, segs, inside, st) : a.l.N == 64 ? launch_n<P, 64>(a, w, segs, inside, st)
+                                                                             : launch_n<P, 128>(a, w, segs, inside, st);
 }
 
 }  // namespace
