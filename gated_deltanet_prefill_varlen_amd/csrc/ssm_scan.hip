@@ -104,8 +104,8 @@ struct AddOp { __device__ __forceinline__ float operator()(float a, float b) con
 // and none passes n_tokens / 32 + n_seqs.  Segments alike, by 256 tokens.
 struct Ws {
   char* bc;              // [slots][G]: C operands, B^T hi, B^T lo (32 N halves each)
-  _Float16* gt;          // [slots][G][4][64][4]: the tiles of C . B on and below the diagonal (and one unused)
-  int2* k;               // [slots][G]: powers of two on B and C
+  _Float16* gt;          // [slots][G][4][64][4]: the tiles of C . B on and below the diagonal; the powers of
+                         // two on B^T and C in the first 8 bytes of the fourth
   float* tab;            // [slots][H][kTab]
   float* seg;            // [segment slots][H][P][N]
   float* seg_sum;        // [segment slots][H]: log2 of the segment's decay
@@ -135,7 +135,6 @@ inline Ws layout(const SsmLayer& l, int32_t n_seqs, int64_t n_tokens, bool split
   const int64_t sg = (int64_t)w.slots * l.G;
   w.bc = take(sg * 3 * kChunk * l.N * 2);
   w.gt = reinterpret_cast<_Float16*>(take(sg * 4 * 256 * 2));
-  w.k = reinterpret_cast<int2*>(take(sg * 8));
   w.tab = reinterpret_cast<float*>(take((int64_t)w.slots * l.H * kTab * 4 + 512));
   w.seg = reinterpret_cast<float*>(take((int64_t)w.seg_slots * l.H * l.P * l.N * 4));
   w.seg_sum = reinterpret_cast<float*>(take((int64_t)w.seg_slots * l.H * 4));
@@ -296,7 +295,7 @@ __device__ __forceinline__ void prepare_bc(const SsmScanArgs& a, const Ws& w, in
 #pragma unroll
   for (int i = 0; i < 2; ++i) m[i] = fmaxf(fmaxf(red[4 * i], red[4 * i + 1]), fmaxf(red[4 * i + 2], red[4 * i + 3]));
   const int kb = kTopBt - pow2_above(m[0]), kc = kTopC - pow2_above(m[1]);
-  if (tid == 0) w.k[sg] = make_int2(kb, kc);
+  if (tid == 0) *reinterpret_cast<int2*>(w.gt + sg * 4 * 256 + 3 * 256) = make_int2(kb, kc);
   f16x8* ops = reinterpret_cast<f16x8*>(w.bc + sg * 3 * kChunk * N * 2);
 #pragma unroll
   for (int k = 0; k < TILES; ++k) {
@@ -443,14 +442,15 @@ template <int P, int N, int NW, bool OUT, bool CONV>
 struct ScanLds {
   static constexpr int OPS = kChunk * N * 2;
   static constexpr int FIRST = OUT ? 0 : OPS, LAST = CONV ? 3 * OPS : 2 * OPS;   // of the operands in a slot
-  static constexpr int GT = OUT ? 4 * 512 : 0, ROWS = CONV ? 35 : 32;
+  static constexpr int GT = OUT ? 2048 : 1024,   // (the states need the powers of two alone)
+                        ROWS = CONV ? 35 : 32;
   static constexpr int X = (ROWS * 64 * NW + 1023) / 1024 * 1024, HPW = NW / (P / 32);
   static constexpr int TABS = HPW > 2 ? HPW * kTab * 4 : 1024;     // of a chunk, fetched by 1,024 bytes
-  static constexpr int BYTES = LAST - FIRST + GT + 2 * X + (OUT ? HPW * 2048 : 0) + 2 * TABS;
+  static constexpr int BYTES = LAST - FIRST + GT + 2 * X + (OUT ? HPW * 2048 : 0) + 2 * TABS + (CONV ? 5 * 32 * NW * 4 : 0);
 };
 
 template <int P, int N, int NW, bool OUT, bool CONV>
-__global__ void __launch_bounds__(64 * NW, N == 128 ? 2 : 3) ssm_chunk_kernel(const SsmScanArgs a, const Ws w, int split, int grouped) {
+__global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs a, const Ws w, int split, int grouped) {
   using L = ScanLds<P, N, NW, OUT, CONV>;
   constexpr int nw = NW, hpw = L::HPW;
   constexpr int WPH = P / 32, NT = N / 16, KN = N / 32, OPS = L::OPS, FIRST = L::FIRST, LAST = L::LAST, GT = L::GT;
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(64 * NW, N == 128 ? 2 : 3) ssm_chunk_kernel(co
     const int64_t sg = (slot0 + c) * l.G + grp;
     const char* src = w.bc + sg * 3 * OPS;
     for (int i = FIRST / 1024 + wave; i < LAST / 1024; i += nw) to_lds(src + 1024 * i + 16 * lane, ops + 1024 * i - FIRST);
-    for (int i = wave; i < GT / 1024; i += nw) to_lds(reinterpret_cast<const char*>(w.gt) + sg * GT + 1024 * i + 16 * lane, gts + 1024 * i);
+    for (int i = wave; i < GT / 1024; i += nw) to_lds(reinterpret_cast<const char*>(w.gt) + sg * 2048 + 2048 - GT + 1024 * i + 16 * lane, gts + 1024 * i);
     for (int i = wave; i < L::TABS / 1024; i += nw)
       to_lds(w.tab + ((slot0 + c) * l.H + b * hpw) * kTab + 256 * i + 4 * lane, tabs + (c & 1) * L::TABS + 1024 * i);
   };
@@ -511,19 +511,24 @@ __global__ void __launch_bounds__(64 * NW, N == 128 ? 2 : 3) ssm_chunk_kernel(co
       to_lds(src + (int64_t)min(max(p0 + p, 0), len - 1) * a.x_stride * 2 + 16 * blk, xs + (c & 1) * L::X + 1024 * i);
     }
   };
-  uint32_t hist[3] = {0, 0, 0};     // this lane's inputs before the prompt
   if (c_first < c_end) {
     fetch(c_first);
     fetch_x(c_first);
     if (c_first + 1 < c_end) fetch_x(c_first + 1);
-    if (CONV && c_first == 0 && a.conv_in) {
+  }
+  // the taps of the workgroup's channels, in LDS: [5][32 NW]
+  float* const taps = reinterpret_cast<float*>(tabs + 2 * L::TABS) + 32 * wave + 2 * r;
+  if (CONV && g == 0) {
 #pragma unroll
-      for (int i = 0; i < 3; ++i)
-        hist[i] = *reinterpret_cast<const uint32_t*>(a.conv_in + ((int64_t)s * 3 + i) * l.conv_dim + ch0);
+    for (int q = 0; q < 2; ++q) {
+      const float4 t = reinterpret_cast<const float4*>(l.conv_w)[ch0 + q];
+      taps[q] = conv_tap(t.x);
+      taps[32 * nw + q] = conv_tap(t.y);
+      taps[64 * nw + q] = conv_tap(t.z);
+      taps[96 * nw + q] = conv_tap(t.w);
+      taps[128 * nw + q] = l.conv_bias ? conv_tap(l.conv_bias[ch0 + q]) : 0.f;
     }
   }
-  ConvW cw;
-  if (CONV) load_conv(l, ch0, cw);
   const float D = OUT && l.D ? l.D[h] : 0.f;
 
   // the state that enters, S^T in tiles [16 n][16 p] (columns of N in the order
@@ -593,6 +598,15 @@ __global__ void __launch_bounds__(64 * NW, N == 128 ? 2 : 3) ssm_chunk_kernel(co
   float seg_sum = 0.f;
   arrived<0>();
   __syncthreads();   // the first chunk is whole
+  if (CONV && c_first == 0 && c_end > 0) {
+    // the window takes the place of the three rows before the prompt (rows 0 to 2: not swapped)
+    if (lane < 48) {
+      const int i = lane / 16;
+      reinterpret_cast<uint32_t*>(xs)[16 * (i * nw + wave) + lane % 16] =
+          a.conv_in ? *reinterpret_cast<const uint32_t*>(a.conv_in + ((int64_t)s * 3 + i) * l.conv_dim + h * P + 32 * half + 2 * (lane % 16)) : 0u;
+    }
+    __syncthreads();
+  }
   const f16x8* fc = reinterpret_cast<const f16x8*>(ops) + lane;
   const f16x8* bh = reinterpret_cast<const f16x8*>(ops + OPS - FIRST) + lane;
   const f16x8* bl = reinterpret_cast<const f16x8*>(ops + (CONV ? 2 * OPS : OPS) - FIRST) + lane;
@@ -601,6 +615,16 @@ __global__ void __launch_bounds__(64 * NW, N == 128 ? 2 : 3) ssm_chunk_kernel(co
   float xv[2][2][4], xmax[2];
   auto take_x = [&](int c) __attribute__((always_inline)) {
     // row 16 run + 4 g + j of the tile, from one address for j below 4 and one beyond
+    ConvW cw;
+    if (CONV) {
+      typedef float f32x2a __attribute__((ext_vector_type(2)));
+      const float* tp = taps + anew(0);    // (read here: kept over the chunks, they would take 10 registers)
+      const f32x2a t0 = *reinterpret_cast<const f32x2a*>(tp), t1 = *reinterpret_cast<const f32x2a*>(tp + 32 * nw),
+                   t2 = *reinterpret_cast<const f32x2a*>(tp + 64 * nw), t3 = *reinterpret_cast<const f32x2a*>(tp + 96 * nw),
+                   tb = *reinterpret_cast<const f32x2a*>(tp + 128 * nw);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) { cw.w0[q] = t0[q]; cw.w1[q] = t1[q]; cw.w2[q] = t2[q]; cw.w3[q] = t3[q]; cw.b[q] = tb[q]; }
+    }
     const uint32_t* xr[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) xr[j] = reinterpret_cast<const uint32_t*>(xs + (c & 1) * L::X) + r + 16 * (4 * g * nw + (wave ^ ((g + j) & XSWAP)));
@@ -611,10 +635,6 @@ __global__ void __launch_bounds__(64 * NW, N == 128 ? 2 : 3) ssm_chunk_kernel(co
       for (int i = CONV ? 0 : 3; i < 7; ++i) {
         const int j = i - (CONV ? 0 : 3);
         x[i] = xr[j / 4][16 * nw * (16 * run + j)];
-      }
-      if (CONV && run == 0 && c == 0 && g == 0) {
-#pragma unroll
-        for (int i = 0; i < 3; ++i) x[i] = hist[i];
       }
       conv_run<CONV>(x, cw, xv[0][run], xv[1][run]);
     }
@@ -639,16 +659,15 @@ __global__ void __launch_bounds__(64 * NW, N == 128 ? 2 : 3) ssm_chunk_kernel(co
   if (c_first < c_end) take_x(c_first);
 
   for (int c = c_first; c < c_end; ++c) {
-    const int64_t sg = (slot0 + c) * l.G + grp;
     const int left = min(kChunk, len - c * kChunk);
     // a checkpoint at the chunk's start gets the state that enters it, and so
     // does one inside, to which a launch behind this one adds the tokens
     if (OUT) keep_until(t0 + c * kChunk + left);
-    const int2 kk = w.k[sg];
-    const int kbt = kk.x, kb = kbt - kTopBt + kTopB, kc = kk.y;
     arrived<OUT ? 2 : 0>();
     __syncthreads();   // the chunk's operands and the next x are whole; x is in registers; the last outputs are through with M
     if (c + 2 < c_end) fetch_x(c + 2);
+    const int2 kk = *reinterpret_cast<const int2*>(gts + GT - 512);
+    const int kbt = __builtin_amdgcn_readfirstlane(kk.x), kb = kbt - kTopBt + kTopB, kc = __builtin_amdgcn_readfirstlane(kk.y);
     const float* tab = reinterpret_cast<const float*>(tabs + (c & 1) * L::TABS) + hl * kTab;
     const float alpha = tab[99];
     const int kw = __float_as_int(tab[100]), ad = min(-__float_as_int(tab[98]), pd_max - (kb + kc)), m = kb + kc + ad;
@@ -749,7 +768,7 @@ __global__ void __launch_bounds__(64 * NW, N == 128 ? 2 : 3) ssm_chunk_kernel(co
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      if (nt % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+      if (nt % 2 == 0) __builtin_amdgcn_sched_barrier(0);
       const f16x8 fh = bh[nt * 64];
       f16x8 fl;
       if (CONV) fl = bl[nt * 64];
