@@ -4,38 +4,38 @@
 //   S <- exp(A dt) S + dt x B^T,   y = S C + D x
 //
 // What bounds it is the state: every (sequence, head) reads and writes P x N
-// fp32 once per call, whatever n_tok is.  A workgroup owns 32 RPT rows of one
+// fp32 once per call, whatever n_tok is.  A workgroup owns 32 rows of one
 // (sequence, head); a row's N columns lie on LPR = N / 16 lanes as four
 // float4 each, so a load instruction reads whole 128-byte (N = 128) pieces of
 // rows, and the sum S C of a row is a reduction over LPR lanes in a fixed
 // order.  The convolved x (this workgroup's rows), B and C go through LDS,
-// computed once per workgroup and token.
+// computed once per workgroup and token (for four tokens at once, 64 sequences
+// of one took 57.0 us for 46.5).  64 rows a workgroup took 47.0 us there, 6.5 us
+// for 6.0 with one sequence and 11.8 us for 10.5 with four tokens of one.
+// 64 sequences, 268 MB: 5.8 TB/s with the windows' launch.
 #include "ssm_device.h"
 
 namespace gdn {
 namespace {
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int kRows = 32;
 
-template <int N, int P, int RPT, bool CONV>
+template <int N, int P, bool CONV, bool ONCE>
 __global__ void __launch_bounds__(kRows * (N / 16)) ssm_decode_kernel(const SsmDecodeArgs a) {
-  constexpr int LPR = N / 16, THREADS = kRows * LPR, XR = kRows * RPT, NCH = XR + 2 * N;
+  constexpr int LPR = N / 16, THREADS = kRows * LPR, NCH = kRows + 2 * N;
   const SsmLayer& l = a.l;
-  const int b = blockIdx.x, h = blockIdx.y, row0 = blockIdx.z * XR;
+  const int b = blockIdx.x, h = blockIdx.y, row0 = blockIdx.z * kRows;
   const int tid = threadIdx.x, rg = tid / LPR, jl = tid % LPR;
   const int grp = h / (l.H / l.G), inner = l.H * P;
   const int r = a.slot ? a.slot[b] : b;
 
-  // the rows of the state are asked for before the token's inputs
-  float* sp = a.state + (((size_t)r * l.H + h) * P + row0 + rg) * N + 4 * jl;
-  float S[RPT][16];
+  // the row of the state is asked for before the token's inputs
+  f32x4* const sp = reinterpret_cast<f32x4*>(a.state + (((size_t)r * l.H + h) * P + row0 + rg) * N + 4 * jl);
+  f32x4 S[4];
 #pragma unroll
-  for (int i = 0; i < RPT; ++i)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float4 v = *reinterpret_cast<const float4*>(sp + (size_t)i * kRows * N + 4 * LPR * k);
-      S[i][4 * k] = v.x; S[i][4 * k + 1] = v.y; S[i][4 * k + 2] = v.z; S[i][4 * k + 3] = v.w;
-    }
+  for (int k = 0; k < 4; ++k) S[k] = ONCE ? __builtin_nontemporal_load(sp + LPR * k) : sp[LPR * k];
 
   __shared__ float u[NCH];   // the token's x of these rows, B, C
   const float A = l.A[h], D = l.D ? l.D[h] : 0.f;
@@ -43,8 +43,8 @@ __global__ void __launch_bounds__(kRows * (N / 16)) ssm_decode_kernel(const SsmD
     const size_t t = (size_t)b * a.n_tok + n;
     if (n > 0) __syncthreads();   // the previous token's values have been read
     for (int e = tid; e < NCH; e += THREADS) {
-      const int c = e < XR ? h * P + row0 + e
-                  : e < XR + N ? inner + grp * N + e - XR : inner + (l.G + grp) * N + e - XR - N;
+      const int c = e < kRows ? h * P + row0 + e
+                  : e < kRows + N ? inner + grp * N + e - kRows : inner + (l.G + grp) * N + e - kRows - N;
       if constexpr (CONV) {
         // inputs n - 3 .. n: the tokens' own, before them the slot's window
         float xw[4];
@@ -63,39 +63,30 @@ __global__ void __launch_bounds__(kRows * (N / 16)) ssm_decode_kernel(const SsmD
     }
     const float dt = ssm_step(l, a.dt, t * a.dt_stride + h, h), alpha = expf(A * dt);
     __syncthreads();
-    float bv[16], cv[16];
+    const float x = u[rg], dx = dt * x;
+    float y = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 4; ++k) {
+      const int at = 4 * LPR * k + 4 * jl;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        bv[4 * k + i] = u[XR + 4 * LPR * k + 4 * jl + i];
-        cv[4 * k + i] = u[XR + N + 4 * LPR * k + 4 * jl + i];
+        S[k][i] = fmaf(alpha, S[k][i], dx * u[kRows + at + i]);
+        y = fmaf(S[k][i], u[kRows + N + at + i], y);
       }
+    }
+    y = group_sum<LPR>(y);
+    if (jl == 0) a.out[(t * l.H + h) * P + row0 + rg] = (uint16_t)f32_to_bf16(fmaf(D, x, y));
+    if (a.snap) {
+      f32x4* q = reinterpret_cast<f32x4*>(a.snap + ((t * l.H + h) * P + row0 + rg) * N + 4 * jl);
 #pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-      const float x = u[kRows * i + rg], dx = dt * x;
-      float y = 0.f;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        S[i][k] = fmaf(alpha, S[i][k], dx * bv[k]);
-        y = fmaf(S[i][k], cv[k], y);
-      }
-      y = group_sum<LPR>(y);
-      if (jl == 0) a.out[(t * l.H + h) * P + row0 + kRows * i + rg] = (uint16_t)f32_to_bf16(fmaf(D, x, y));
-      if (a.snap) {
-        float* q = a.snap + ((t * l.H + h) * P + row0 + kRows * i + rg) * N + 4 * jl;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<float4*>(q + 4 * LPR * k) = make_float4(S[i][4 * k], S[i][4 * k + 1], S[i][4 * k + 2], S[i][4 * k + 3]);
-      }
+      for (int k = 0; k < 4; ++k) q[LPR * k] = S[k];
     }
   }
 #pragma unroll
-  for (int i = 0; i < RPT; ++i)
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      *reinterpret_cast<float4*>(sp + (size_t)i * kRows * N + 4 * LPR * k) =
-          make_float4(S[i][4 * k], S[i][4 * k + 1], S[i][4 * k + 2], S[i][4 * k + 3]);
+  for (int k = 0; k < 4; ++k) {
+    if (ONCE) __builtin_nontemporal_store(S[k], sp + LPR * k);
+    else sp[LPR * k] = S[k];
+  }
 }
 
 // Each slot's window moves on by n_tok inputs: a launch of its own, since
@@ -118,13 +109,18 @@ __global__ void __launch_bounds__(256) ssm_window_kernel(const SsmDecodeArgs a) 
 
 template <int N, int P>
 hipError_t launch(const SsmDecodeArgs& a, hipStream_t st) {
-  constexpr int RPT = P >= 64 ? 2 : 1;
-  const dim3 grid(a.batch, a.l.H, P / (kRows * RPT)), blk(kRows * (N / 16));
+  // States that the last cache (256 MB) cannot hold to the next call pass it by:
+  // 128 sequences of 64 heads of 64 on 128 take 92 us for 99, 256 take 184 for
+  // 214; 64, whose 134 MB it holds, would take 49 for 46.5.
+  const bool once = (int64_t)a.batch * a.l.H * P * N * 4 >= 256 << 20;
+  const dim3 grid(a.batch, a.l.H, P / kRows), blk(kRows * (N / 16));
   if (!a.l.conv_w) {
-    hipLaunchKernelGGL((ssm_decode_kernel<N, P, RPT, false>), grid, blk, 0, st, a);
+    if (once) hipLaunchKernelGGL((ssm_decode_kernel<N, P, false, true>), grid, blk, 0, st, a);
+    else hipLaunchKernelGGL((ssm_decode_kernel<N, P, false, false>), grid, blk, 0, st, a);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((ssm_decode_kernel<N, P, RPT, true>), grid, blk, 0, st, a);
+  if (once) hipLaunchKernelGGL((ssm_decode_kernel<N, P, true, true>), grid, blk, 0, st, a);
+  else hipLaunchKernelGGL((ssm_decode_kernel<N, P, true, false>), grid, blk, 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(ssm_window_kernel, dim3(a.batch, (a.l.conv_dim + 1023) / 1024), dim3(256), 0, st, a);

@@ -164,3 +164,19 @@ def test_prefill_then_decode_then_norm():
         assert np.all(np.abs(got - normed) <= (2.0 ** -4 + 2.0 ** -18) * np.abs(normed) + 2.0 ** -10 * f64(scales))
     close(state[slots], want["final"], 2 * state_tol(want["final_mass"], 200), "state")
     assert np.array_equal(f64(window)[slots], want["window"])
+
+
+def test_states_past_the_last_cache_as_within_it():
+    """256 MB of states take another way to memory: the same bits as in parts."""
+    H, G, P, N, B = 64, 4, 64, 128, 130
+    y = Layer(H, G, P, N, [B], seed=21)
+    state, window = pools(y, B + 2, 9)
+    slots = np.random.default_rng(3).permutation(B + 2)[:B].tolist()
+    s2, w2 = state.clone(), window.clone()
+    a, _ = step(y, 1, slots, B + 2, state, window, False)
+    x, dt = y.x, y.dt
+    for i in range(0, B, 50):
+        y.x, y.dt = x[i:i + 50], dt[i:i + 50]
+        b, _ = step(y, 1, slots[i:i + 50], B + 2, s2, w2, False)
+        assert torch.equal(b, a[i:i + 50])
+    assert torch.equal(state, s2) and torch.equal(window, w2)
