@@ -691,6 +691,11 @@ gdn_status gdn_ssm_prefill_packed(
   if (workspace_bytes < need) return GDN_ERR_CAPACITY;
   if (n_tokens > 0 && (overlap(workspace, need, x, ((n_tokens - 1) * a.x_stride + a.l.conv_dim) * 2) ||
                        overlap(workspace, need, out, (int64_t)n_tokens * a.l.H * a.l.P * 2))) return GDN_ERR_SHAPE;
+  const int64_t head = (int64_t)a.l.H * a.l.P * a.l.N * 4, states = n_seqs * head, kept = n_ckpt * head;
+  if (init_state != final_state && overlap(init_state, states, final_state, states)) return GDN_ERR_SHAPE;
+  if (overlap(ckpt_buf, kept, init_state, states) || overlap(ckpt_buf, kept, final_state, states)) return GDN_ERR_SHAPE;
+  if (overlap(workspace, need, init_state, states) || overlap(workspace, need, final_state, states) ||
+      overlap(workspace, need, ckpt_buf, kept)) return GDN_ERR_SHAPE;
   if (n_seqs == 0) return GDN_OK;
   a.cu = cu_seqlens; a.n_seqs = n_seqs; a.n_tokens = n_tokens;
   a.x = static_cast<const uint16_t*>(x); a.dt = dt;
@@ -777,7 +782,7 @@ gdn_status gdn_rms_norm(const gdn_norm_shape* shape, int32_t n_rows, int32_t x_d
     for (int j = 0; j < i; ++j)
       if (overlap(to[i].p, to[i].bytes, to[j].p, to[j].bytes)) return GDN_ERR_SHAPE;
   }
-  if (!fits_grid(rows, d <= 512 ? 64 : d <= 8192 ? 256 : 1024)) return GDN_ERR_SHAPE;
+  if (!fits_grid(rows, d <= 512 ? 64 : d <= 2048 ? 256 : d <= 4096 ? 512 : 1024)) return GDN_ERR_SHAPE;
   gdn::NormArgs a{};
   a.dim = (int32_t)d; a.groups = shape->groups; a.group_dim = (int32_t)gd; a.scale_block = shape->scale_block;
   a.n_rows = n_rows; a.x_f32 = x_dtype == GDN_F32; a.res_f32 = res_dtype == GDN_F32;

@@ -559,7 +559,9 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
   float bound[2] = {0.f, 0.f};
   const float* from = !OUT ? nullptr
                       : k > 0 ? w.seg + (((int64_t)unit - 1) * l.H + h) * hpn
-                      : a.init ? a.init + ((int64_t)s * l.H + h) * hpn : nullptr;
+                      : !a.init ? nullptr
+                      : n_seg > 1 && a.init == a.final_state ? w.seg + (((int64_t)unit + n_seg - 1) * l.H + h) * hpn
+                      : a.init + ((int64_t)s * l.H + h) * hpn;
 #pragma unroll
   for (int z = 0; z < KN; ++z)
 #pragma unroll
@@ -921,7 +923,9 @@ __global__ void __launch_bounds__(2 * N) ssm_ckpt_kernel(const SsmScanArgs a) {
 }
 
 // The states that enter a prompt's segments: segment k's slot, which holds its
-// state from zero, gets the state behind it (the one that enters k + 1).
+// state from zero, gets the state behind it (the one that enters k + 1).  Where
+// final_state is init_state, the prompt's last segment may write it before the
+// first reads it: the first then has its own from the last one's slot.
 __global__ void __launch_bounds__(256) ssm_pass_kernel(const SsmScanArgs a, const Ws w, int hb) {
   const SsmLayer& l = a.l;
   const int s = blockIdx.x, h = blockIdx.y, i = (blockIdx.z * 256 + threadIdx.x) * 4;
@@ -931,6 +935,7 @@ __global__ void __launch_bounds__(256) ssm_pass_kernel(const SsmScanArgs a, cons
   const int64_t first = t0 / (kChunk * kSegUnit) + s;
   f32x4 S = {0.f, 0.f, 0.f, 0.f};
   if (a.init) S = *reinterpret_cast<const f32x4*>(a.init + ((int64_t)s * l.H + h) * hpn + i);
+  if (a.init && a.init == a.final_state) *reinterpret_cast<f32x4*>(w.seg + ((first + n_seg - 1) * l.H + h) * hpn + i) = S;
   for (int k = 0; k + 1 < n_seg; ++k) {
     f32x4* p = reinterpret_cast<f32x4*>(w.seg + ((first + k) * l.H + h) * hpn + i);
     const float al = __builtin_amdgcn_exp2f(w.seg_sum[(first + k) * l.H + h]);

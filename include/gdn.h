@@ -5,7 +5,9 @@
  * and, for the softmax-attention layers of the same hybrid models, a paged
  * key/value cache held in 8 bits: its page planner, rotary positions with the
  * cache's write, its read back, and attention over it for packed prompts and
- * for decoding requests.
+ * for decoding requests; and, for the selective state space layers of such
+ * models, their packed scan and decode step, with the root-mean-square norm
+ * that stands around all of these layers.
  *
  * What the layer computes
  *   Per prompt s and value head h (qk head j = h / (Hv / Hqk)), starting from
@@ -591,7 +593,8 @@ GDN_API gdn_status gdn_ssm_prefill_workspace(const gdn_ssm_shape* shape, const i
  *                     afterwards; calls that may run at the same time need one
  *                     each.
  * A prompt's bits do not depend on the pack.  A prompt continued from a
- * checkpoint agrees with the unbroken one to fp32's rounding.
+ * checkpoint agrees with the unbroken one to fp32's rounding.  init_state may be
+ * final_state; other overlaps of what is written are not allowed.
  * Errors: as gdn_prefill_packed; GDN_ERR_CAPACITY (workspace too short). */
 GDN_API gdn_status gdn_ssm_prefill_packed(
     const gdn_ssm_shape* shape, const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, int32_t n_seqs,

@@ -194,3 +194,31 @@ def test_streams_and_graph():
         call()
         torch.cuda.synchronize()
         assert torch.equal(o, out) and torch.equal(f, final)
+
+
+@pytest.mark.parametrize("lens", [[5000, 60, 0, 3000], [40, 7]], ids=str)
+def test_states_in_place(lens):
+    """final_state may be init_state, where a prompt is cut into segments too."""
+    y = Layer(4, 2, 64, 64, lens, seed=31, init=True, window=True)
+    want = y.run()
+    for _ in range(3):
+        state = y.init.clone()
+        out = torch.empty_like(want["out"])
+        i32 = torch.from_numpy(y.cu).to(DEV)
+        gdn.gdn_ssm_prefill_packed(y.shape, i32, y.cu, y.x, y.dt, y.A, out, dt_bias=y.dt_bias, D=y.D, init_state=state, final_state=state,
+                                   conv_weight=y.w, conv_bias=y.b, conv_state_in=y.window, workspace=y.workspace)
+        T = int(y.cu[-1])
+        assert torch.equal(out[:T], want["out"][:T]) and torch.equal(state, want["final"])
+
+
+def test_windows_and_states_in_place_with_checkpoints():
+    """Checkpoints one and two tokens into a prompt, between chunks' ends and on
+    them, with the windows and states written over the ones read."""
+    lens = [70, 1, 2, 300, 33]
+    y = Layer(4, 1, 32, 64, lens, seed=32, init=True, window=True)
+    ck = [1, 2, 32, 35, 70, 71, 72, 73, 74, 75, 105, 373, 374, 406]
+    want, whole = y.oracle(ck), y.run(ck)
+    y.check(whole, want, ck)
+    again = y.run(ck, window_out="in place")
+    assert all(torch.equal(whole[k], again[k]) for k in ("out", "final", "kept", "window", "window_kept"))
+    assert torch.equal(y.run()["window"], y.run(window_out="in place")["window"])
