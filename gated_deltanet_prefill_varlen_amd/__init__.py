@@ -577,23 +577,28 @@ def _row_stride(t: torch.Tensor, rows: int, width: int, dev: int, what: str, dty
     with dense channels (columns of a wider row will do); 0 rows: no pointer."""
     if t.get_device() != dev or (t.dtype not in _IO if dtype is None else t.dtype is not dtype):
         _refuse(t, torch.bfloat16 if dtype is None else dtype, what)
-    if t.dim() != 2 or t.shape[1] != width or (t.shape[0] != rows if exact else t.shape[0] < rows):
+    n, w = t.shape if t.dim() == 2 else (-1, -1)
+    if w != width or (n != rows if exact else n < rows):
         raise ValueError(f"{what} must be [{rows}, {width}], got {tuple(t.shape)}")
-    st = t.stride()
-    if width > 1 and st[1] != 1:
+    row, one = t.stride()
+    if one != 1 and width > 1:
         raise ValueError(f"{what}: the channels of a row must be dense")
-    if t.shape[0] > 1 and st[0] < width:
+    if n < 2:
+        row = 0
+    elif row < width:
         raise ValueError(f"{what}: the rows overlap")
-    return (t.data_ptr() if rows else None), (st[0] if t.shape[0] > 1 else 0)
+    return (t.data_ptr() if rows else None), row
 
 
 def _sized(t, dtype, dev: int, shape, what: str) -> Optional[int]:
     """Pointer of a dense tensor of one type and shape (None passes NULL)."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} must be {list(shape)}, got {tuple(t.shape)}")
-    return _buf(t, dtype, dev, what)
+    if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(t, dtype, what)
+    return t.data_ptr()
 
 
 def _ssm_dims(shape: gdn_ssm_shape):
