@@ -576,7 +576,7 @@ def _row_stride(t: torch.Tensor, rows: int, width: int, dev: int, what: str, dty
     """Pointer and row stride of rows [>= rows, width] (exact: [rows, width])
     with dense channels (columns of a wider row will do); 0 rows: no pointer."""
     if t.get_device() != dev or (t.dtype not in _IO if dtype is None else t.dtype is not dtype):
-        _refuse(t, torch.bfloat16 if dtype is None else dtype, what)
+        _refuse(t, dtype or (t.dtype if t.dtype in _IO else torch.bfloat16), what)
     n, w = t.shape if t.dim() == 2 else (-1, -1)
     if w != width or (n != rows if exact else n < rows):
         raise ValueError(f"{what} must be [{rows}, {width}], got {tuple(t.shape)}")

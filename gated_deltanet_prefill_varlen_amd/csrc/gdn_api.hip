@@ -683,7 +683,7 @@ gdn_status gdn_ssm_prefill_packed(
   const void* ptrs[] = {conv_state_in, conv_state_out, conv_ckpt, init_state, final_state, ckpt_buf, workspace};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return GDN_ERR_SHAPE;
-  if (!fits_grid(gdn::ssm_scan_groups(a.l, n_seqs, n_tokens), 512)) return GDN_ERR_SHAPE;
+  if (!fits_grid(gdn::ssm_scan_groups(a.l, n_seqs, n_tokens), 512) || !fits_grid((int64_t)n_ckpt + n_seqs, 256)) return GDN_ERR_SHAPE;
   const int64_t windows = (int64_t)n_seqs * 3 * a.l.conv_dim * 2;
   if (conv_state_in != conv_state_out && overlap(conv_state_in, windows, conv_state_out, windows)) return GDN_ERR_SHAPE;
   const int64_t need = gdn::ssm_scan_bytes(a.l, n_seqs, cu_seqlens_host);
