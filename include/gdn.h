@@ -666,7 +666,8 @@ typedef struct gdn_norm_shape {
  *                  2^-100), so that code * scale stands for y; codes are
  *                  rounded to nearest, ties to even, infinities saturate, NaN
  *                  is e4m3's NaN and 0 in int8.
- * Other overlaps of outputs with inputs or each other are not allowed.
+ * Other overlaps of outputs with inputs or each other are not allowed, taken as
+ * whole spans from the first row to the last.
  * Errors: GDN_ERR_NULL (also: nothing to write), GDN_ERR_SHAPE,
  * GDN_ERR_UNSUPPORTED, GDN_ERR_HIP. */
 GDN_API gdn_status gdn_rms_norm(const gdn_norm_shape* shape, int32_t n_rows, int32_t x_dtype, const void* x,
