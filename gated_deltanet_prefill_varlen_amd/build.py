@@ -23,14 +23,10 @@ FLAGS = [
     "-I", os.path.join(ROOT, "include"), "-I", CSRC,
 ]
 
-# flags of single sources: pairs of scalar fp32 operations formed as vectors only cost registers where
-# packed fp32 is off, and this kernel has none to spare (81 spilled beside 117)
-EXTRA = {"ssm_scan.hip": ["-fno-slp-vectorize"]}
-
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-    cmd = [HIPCC, *FLAGS, *EXTRA.get(os.path.basename(src), []), "-c", src, "-o", obj]
+    cmd = [HIPCC, *FLAGS, "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{r.stderr}")

@@ -120,7 +120,12 @@ struct Ws {
 constexpr int kSegUnit = 8;               // chunks a segment has at least
 
 // Chunks of a segment for a prompt of nc chunks whose chunk row takes hb
-// workgroups.
+// workgroups: as many segments as make 256 workgroups of the prompt alone, from
+// 1,024 tokens on.  The rule looks at one prompt, so that its bits do not depend
+// on the pack, and stands between a lone prompt and several.  With 128 and 512 in
+// 256's place, 32 heads of 128 on 128: one prompt of 8,192 tokens takes 281 and
+// 144 us for 177, four take 484 and 547 for 508; one of 2,048 takes 86 and 64 for
+// 64, sixteen take 490 and 598 for 598.
 __host__ __device__ inline int seg_chunks(int nc, int hb) {
   if (nc <= 32) return nc > 0 ? nc : 1;
   const int want = (256 + hb - 1) / hb, most = nc / kSegUnit, n = want < most ? want : most;
@@ -410,10 +415,8 @@ __device__ __forceinline__ void to_lds(const void* g, const void* base) {
   const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)base;
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(g) : "memory", "m0");
 }
-// Waits for the wave's accesses to memory, but the LATER newest of them (they
-// complete in order).
-template <int LATER>
-__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER) : "memory"); }
+// Waits for the wave's accesses to memory.
+__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // Input of channel c at position p of prompt s (t0 = its first row; p < 0: its history).
 __device__ __forceinline__ uint16_t raw_at(const SsmScanArgs& a, int s, int t0, int p, int c) {
@@ -485,7 +488,7 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
   char* const tabs = xs + 2 * L::X + (OUT ? hpw * 2048 : 0);
   const int hb = l.H / hpw, per_group = hb / l.G;
   int unit, b;
-  if (grouped) {   // the workgroups that read the same B and C go to one XCD
+  if (grouped) {   // the workgroups that read the same B and C go to one XCD (4 x 8,192 tokens: 492 -> 481 us)
     const int q = blockIdx.x / (8 * per_group), rem = blockIdx.x % (8 * per_group), cell = 8 * q + rem % 8;
     unit = cell / l.G;
     b = cell % l.G * per_group + rem / 8;
@@ -507,9 +510,7 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
   const int st_at = (32 * half + 2 * r) * N + 8 * g;       // this lane's entries of a head's state
   // A chunk is fetched while others are worked on, to LDS directly, 16 bytes a
   // lane: its operands once the ones before are through with the products, its
-  // x a chunk earlier.  Nothing waits for the outputs' way to memory: the waits
-  // leave the two newest accesses, the chunk's two stores, out (waiting for them
-  // cost 117 us of 364 at 32 x 1,024 tokens of 64 heads of 64 on 128).
+  // x a chunk earlier.
   auto fetch = [&](int c) __attribute__((always_inline)) {
     const int64_t sg = (slot0 + c) * l.G + grp;
     const char* src = w.bc + sg * 3 * OPS;
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
     }
   };
   float seg_sum = 0.f;
-  arrived<0>();
+  arrived();
   __syncthreads();   // the first chunk is whole
   if (CONV && c_first == 0 && c_end > 0) {
     // the window takes the place of the three rows before the prompt (rows 0 to 2: not swapped)
@@ -685,9 +686,12 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
     // a checkpoint at the chunk's start gets the state that enters it, and so
     // does one inside, to which a launch behind this one adds the tokens
     if (OUT) keep_until(t0 + c * kChunk + left);
-    arrived<OUT ? 2 : 0>();
+    arrived();
     __syncthreads();   // the chunk's operands and the next x are whole; x is in registers; the last outputs are through with M
     if (c + 2 < c_end) fetch_x(c + 2);
+    // the half with the operands goes first on a SIMD: behind its end wait the
+    // workgroup's fetches (307 -> 297 us at 32 x 1,024 tokens)
+    __builtin_amdgcn_s_setprio(1);
     const int2 kk = *reinterpret_cast<const int2*>(gts + GT - 512);
     const int kbt = __builtin_amdgcn_readfirstlane(kk.x), kb = kbt - kTopBt + kTopB, kc = __builtin_amdgcn_readfirstlane(kk.y);
     const float* tab = reinterpret_cast<const float*>(tabs + (c & 1) * L::TABS) + hl * kTab;
@@ -811,6 +815,7 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt) fe[tt] = f1 * __builtin_amdgcn_exp2f(tab[32 + 16 * tt + r]);
     }
+    __builtin_amdgcn_s_setprio(0);
     __syncthreads();   // M is whole; the products are through with the operands
     if (c + 1 < c_end) fetch(c + 1);
     if (OUT) {
