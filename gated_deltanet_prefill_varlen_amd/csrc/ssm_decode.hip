@@ -12,7 +12,7 @@
 // computed once per workgroup and token (for four tokens at once, 64 sequences
 // of one took 57.0 us for 46.5).  64 rows a workgroup took 47.0 us there, 6.5 us
 // for 6.0 with one sequence and 11.8 us for 10.5 with four tokens of one.
-// 64 sequences, 268 MB: 5.8 TB/s with the windows' launch.
+// 64 sequences, 268 MB from and to memory: 50 us with the windows' launch, 5.5 TB/s.
 #include "ssm_device.h"
 
 namespace gdn {
@@ -22,7 +22,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRows = 32;
 
-template <int N, int P, bool CONV, bool ONCE>
+template <int N, int P, bool CONV>
 __global__ void __launch_bounds__(kRows * (N / 16)) ssm_decode_kernel(const SsmDecodeArgs a) {
   constexpr int LPR = N / 16, THREADS = kRows * LPR, NCH = kRows + 2 * N;
   const SsmLayer& l = a.l;
@@ -31,11 +31,15 @@ __global__ void __launch_bounds__(kRows * (N / 16)) ssm_decode_kernel(const SsmD
   const int grp = h / (l.H / l.G), inner = l.H * P;
   const int r = a.slot ? a.slot[b] : b;
 
-  // the row of the state is asked for before the token's inputs
+  // The row of the state is asked for before the token's inputs.  A layer's states
+  // are met again only after all other layers' have passed, so they stay out of
+  // the caches: 64 sequences on states that come from memory 57.6 -> 50.0 us, 256
+  // 214 -> 184.  (One pool over and over, which no model does, would find half of
+  // it in the last cache: 46.5 us for 49.0.)
   f32x4* const sp = reinterpret_cast<f32x4*>(a.state + (((size_t)r * l.H + h) * P + row0 + rg) * N + 4 * jl);
   f32x4 S[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) S[k] = ONCE ? __builtin_nontemporal_load(sp + LPR * k) : sp[LPR * k];
+  for (int k = 0; k < 4; ++k) S[k] = __builtin_nontemporal_load(sp + LPR * k);
 
   __shared__ float u[NCH];   // the token's x of these rows, B, C
   const float A = l.A[h], D = l.D ? l.D[h] : 0.f;
@@ -77,16 +81,14 @@ __global__ void __launch_bounds__(kRows * (N / 16)) ssm_decode_kernel(const SsmD
     y = group_sum<LPR>(y);
     if (jl == 0) a.out[(t * l.H + h) * P + row0 + rg] = (uint16_t)f32_to_bf16(fmaf(D, x, y));
     if (a.snap) {
+      // (through the caches: 23.0 us for 16 sequences of 4 tokens, past them 31.1)
       f32x4* q = reinterpret_cast<f32x4*>(a.snap + ((t * l.H + h) * P + row0 + rg) * N + 4 * jl);
 #pragma unroll
       for (int k = 0; k < 4; ++k) q[LPR * k] = S[k];
     }
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (ONCE) __builtin_nontemporal_store(S[k], sp + LPR * k);
-    else sp[LPR * k] = S[k];
-  }
+  for (int k = 0; k < 4; ++k) __builtin_nontemporal_store(S[k], sp + LPR * k);
 }
 
 // Each slot's window moves on by n_tok inputs: a launch of its own, since
@@ -109,18 +111,12 @@ __global__ void __launch_bounds__(256) ssm_window_kernel(const SsmDecodeArgs a) 
 
 template <int N, int P>
 hipError_t launch(const SsmDecodeArgs& a, hipStream_t st) {
-  // States that the last cache (256 MB) cannot hold to the next call pass it by:
-  // 128 sequences of 64 heads of 64 on 128 take 92 us for 99, 256 take 184 for
-  // 214; 64, whose 134 MB it holds, would take 49 for 46.5.
-  const bool once = (int64_t)a.batch * a.l.H * P * N * 4 >= 256 << 20;
   const dim3 grid(a.batch, a.l.H, P / kRows), blk(kRows * (N / 16));
   if (!a.l.conv_w) {
-    if (once) hipLaunchKernelGGL((ssm_decode_kernel<N, P, false, true>), grid, blk, 0, st, a);
-    else hipLaunchKernelGGL((ssm_decode_kernel<N, P, false, false>), grid, blk, 0, st, a);
+    hipLaunchKernelGGL((ssm_decode_kernel<N, P, false>), grid, blk, 0, st, a);
     return hipGetLastError();
   }
-  if (once) hipLaunchKernelGGL((ssm_decode_kernel<N, P, true, true>), grid, blk, 0, st, a);
-  else hipLaunchKernelGGL((ssm_decode_kernel<N, P, true, false>), grid, blk, 0, st, a);
+  hipLaunchKernelGGL((ssm_decode_kernel<N, P, true>), grid, blk, 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(ssm_window_kernel, dim3(a.batch, (a.l.conv_dim + 1023) / 1024), dim3(256), 0, st, a);

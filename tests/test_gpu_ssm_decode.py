@@ -167,7 +167,7 @@ def test_prefill_then_decode_then_norm():
 
 
 def test_states_past_the_last_cache_as_within_it():
-    """256 MB of states take another way to memory: the same bits as in parts."""
+    """More states than the last cache holds: the same bits as in parts."""
     H, G, P, N, B = 64, 4, 64, 128, 130
     y = Layer(H, G, P, N, [B], seed=21)
     state, window = pools(y, B + 2, 9)
