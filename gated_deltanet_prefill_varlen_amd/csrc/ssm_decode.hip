@@ -9,9 +9,10 @@
 // float4 each, so a load instruction reads whole 128-byte (N = 128) pieces of
 // rows, and the sum S C of a row is a reduction over LPR lanes in a fixed
 // order.  The convolved x (this workgroup's rows), B and C go through LDS,
-// computed once per workgroup and token (for four tokens at once, 64 sequences
-// of one took 57.0 us for 46.5).  64 rows a workgroup took 47.0 us there, 6.5 us
-// for 6.0 with one sequence and 11.8 us for 10.5 with four tokens of one.
+// computed once per workgroup and token.  On one pool over and over: with four
+// tokens computed at once 64 sequences of one token took 57.0 us for 46.5, with 64
+// rows a workgroup 47.0; one sequence then took 6.5 us for 6.0, four tokens of one
+// 11.8 for 10.5.
 // 64 sequences, 268 MB from and to memory: 50 us with the windows' launch, 5.5 TB/s.
 #include "ssm_device.h"
 
