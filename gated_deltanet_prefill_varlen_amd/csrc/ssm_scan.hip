@@ -794,7 +794,10 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
     float mul[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      mul[q] = ldexpf(alpha, e_new[q] - e[q]);
+      // A state of zeros has no power of its own, and the change from any to the
+      // next may pass 2^127, whose infinity would make NaN of its zeros.  (Where
+      // it holds anything, mul times an entry of 2^e bound stays below 2^90.)
+      mul[q] = ldexpf(alpha, bound[q] == 0.f ? -126 : e_new[q] - e[q]);
       e[q] = e_new[q];
       bound[q] = grown[q];
     }
