@@ -164,8 +164,8 @@ gdn_status check_ssm(const gdn_ssm_shape* s, gdn::SsmLayer* l) {
   if (s->flags & ~GDN_SSM_SOFTPLUS) return GDN_ERR_UNSUPPORTED;
   if (!(s->dt_min <= s->dt_max)) return GDN_ERR_SHAPE;   // also NaN
   const int64_t dim = (int64_t)s->num_heads * s->head_dim + 2 * (int64_t)s->num_groups * s->state_dim;
-  // the kernels' grids take a head, or a group and four heads, along their second axis
-  if (s->num_heads > 65535 || s->num_groups + (s->num_heads + 3) / 4 > 65535 || dim >= (1 << 23)) return GDN_ERR_SHAPE;
+  // the kernels' grids take a head, or a group and eight heads, along their second axis
+  if (s->num_heads > 65535 || s->num_groups + (s->num_heads + 7) / 8 > 65535 || dim >= (1 << 23)) return GDN_ERR_SHAPE;
   l->H = s->num_heads; l->G = s->num_groups; l->P = s->head_dim; l->N = s->state_dim; l->conv_dim = (int32_t)dim;
   l->softplus = (s->flags & GDN_SSM_SOFTPLUS) != 0;
   l->dt_min = s->dt_min; l->dt_max = s->dt_max;
@@ -683,7 +683,7 @@ gdn_status gdn_ssm_prefill_packed(
   const void* ptrs[] = {conv_state_in, conv_state_out, conv_ckpt, init_state, final_state, ckpt_buf, workspace};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return GDN_ERR_SHAPE;
-  if (!fits_grid(gdn::ssm_scan_groups(a.l, n_seqs, n_tokens), 512) || !fits_grid((int64_t)n_ckpt + n_seqs, 256)) return GDN_ERR_SHAPE;
+  if (!fits_grid(gdn::ssm_scan_groups(a.l, n_seqs, n_tokens), 256) || !fits_grid((int64_t)n_ckpt + n_seqs, 256)) return GDN_ERR_SHAPE;
   const int64_t windows = (int64_t)n_seqs * 3 * a.l.conv_dim * 2;
   if (conv_state_in != conv_state_out && overlap(conv_state_in, windows, conv_state_out, windows)) return GDN_ERR_SHAPE;
   const int64_t need = gdn::ssm_scan_bytes(a.l, n_seqs, cu_seqlens_host);
