@@ -124,6 +124,27 @@ bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
   return x && y && x < y + b_bytes && y < x + a_bytes;
 }
 
+// A buffer of a call.  One that is written may be its input `twin`, in place.
+struct Span {
+  const void* p;
+  int64_t bytes;
+  int twin = -1;
+};
+
+// Whether something that is written overlaps an input or something else that
+// is written (rows of a stride as a whole, from the first to the last).
+template <size_t W, size_t R>
+bool overlaps(const Span (&to)[W], const Span (&in)[R]) {
+  auto meet = [](const Span& a, const Span& b) { return a.bytes > 0 && b.bytes > 0 && overlap(a.p, a.bytes, b.p, b.bytes); };
+  for (size_t i = 0; i < W; ++i) {
+    for (size_t j = 0; j < R; ++j)
+      if (meet(to[i], in[j]) && !(to[i].twin == (int)j && to[i].p == in[j].p)) return true;
+    for (size_t j = 0; j < i; ++j)
+      if (meet(to[i], to[j])) return true;
+  }
+  return false;
+}
+
 // A launch holds fewer than 2^32 threads along its first axis.
 bool fits_grid(int64_t groups, int64_t threads) { return groups * threads <= UINT32_MAX; }
 
@@ -183,10 +204,7 @@ gdn_status check_ssm_rows(int64_t rows, int64_t x_given, const void* x, int32_t 
   *dts = dt_given == 0 ? l->H : dt_given;
   if (*dts < l->H || *dts > INT32_MAX || *xs >= (1 << 23)) return GDN_ERR_SHAPE;
   if ((x && !aligned16(x)) || (conv_w && !aligned16(conv_w)) || (conv_b && !aligned16(conv_b)) || (out && !aligned16(out))) return GDN_ERR_SHAPE;
-  if (rows > 0) {
-    if (!x || !dt || !A || !out) return GDN_ERR_NULL;
-    if (overlap(x, ((rows - 1) * *xs + l->conv_dim) * 2, out, rows * l->H * l->P * 2)) return GDN_ERR_SHAPE;
-  }
+  if (rows > 0 && (!x || !dt || !A || !out)) return GDN_ERR_NULL;
   l->dt_f32 = dt_dtype == GDN_F32;
   l->A = A; l->dt_bias = dt_bias; l->D = D; l->conv_w = conv_w; l->conv_bias = conv_b;
   return GDN_OK;
@@ -684,18 +702,16 @@ gdn_status gdn_ssm_prefill_packed(
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return GDN_ERR_SHAPE;
   if (!fits_grid(gdn::ssm_scan_groups(a.l, n_seqs, n_tokens), 256) || !fits_grid((int64_t)n_ckpt + n_seqs, 256)) return GDN_ERR_SHAPE;
-  const int64_t windows = (int64_t)n_seqs * 3 * a.l.conv_dim * 2;
-  if (conv_state_in != conv_state_out && overlap(conv_state_in, windows, conv_state_out, windows)) return GDN_ERR_SHAPE;
   const int64_t need = gdn::ssm_scan_bytes(a.l, n_seqs, cu_seqlens_host);
   if (need > 0 && !workspace) return GDN_ERR_NULL;
   if (workspace_bytes < need) return GDN_ERR_CAPACITY;
-  if (n_tokens > 0 && (overlap(workspace, need, x, ((n_tokens - 1) * a.x_stride + a.l.conv_dim) * 2) ||
-                       overlap(workspace, need, out, (int64_t)n_tokens * a.l.H * a.l.P * 2))) return GDN_ERR_SHAPE;
-  const int64_t head = (int64_t)a.l.H * a.l.P * a.l.N * 4, states = n_seqs * head, kept = n_ckpt * head;
-  if (init_state != final_state && overlap(init_state, states, final_state, states)) return GDN_ERR_SHAPE;
-  if (overlap(ckpt_buf, kept, init_state, states) || overlap(ckpt_buf, kept, final_state, states)) return GDN_ERR_SHAPE;
-  if (overlap(workspace, need, init_state, states) || overlap(workspace, need, final_state, states) ||
-      overlap(workspace, need, ckpt_buf, kept)) return GDN_ERR_SHAPE;
+  const int64_t T = n_tokens, n = n_seqs, H = a.l.H, dim = a.l.conv_dim, head = H * a.l.P * a.l.N * 4;
+  const Span in[] = {{x, T > 0 ? ((T - 1) * a.x_stride + dim) * 2 : 0}, {dt, T > 0 ? ((T - 1) * a.dt_stride + H) * (a.l.dt_f32 ? 4 : 2) : 0},
+                     {init_state, n * head}, {conv_state_in, n * 6 * dim}, {A, H * 4}, {dt_bias, H * 4}, {D, H * 4},
+                     {conv_weight, dim * 16}, {conv_bias, dim * 4}, {cu_seqlens, (n + 1) * 4}, {ckpt_positions, (int64_t)n_ckpt * 4}};
+  const Span to[] = {{out, T * H * a.l.P * 2}, {final_state, n * head, 2}, {ckpt_buf, n_ckpt * head}, {conv_state_out, n * 6 * dim, 3},
+                     {conv_ckpt, (int64_t)n_ckpt * 6 * dim}, {workspace, need}};
+  if (overlaps(to, in)) return GDN_ERR_SHAPE;
   if (n_seqs == 0) return GDN_OK;
   a.cu = cu_seqlens; a.n_seqs = n_seqs; a.n_tokens = n_tokens;
   a.x = static_cast<const uint16_t*>(x); a.dt = dt;
@@ -734,6 +750,11 @@ gdn_status gdn_ssm_decode(const gdn_ssm_shape* shape, int32_t batch, int32_t n_t
   } else if (batch > pool_slots) {
     return GDN_ERR_CAPACITY;
   }
+  const int64_t T = (int64_t)batch * n_tok, H = a.l.H, dim = a.l.conv_dim, head = H * a.l.P * a.l.N * 4;
+  const Span in[] = {{x, ((T - 1) * a.x_stride + dim) * 2}, {dt, ((T - 1) * a.dt_stride + H) * (a.l.dt_f32 ? 4 : 2)},
+                     {A, H * 4}, {dt_bias, H * 4}, {D, H * 4}, {conv_weight, dim * 16}, {conv_bias, dim * 4}, {slot, (int64_t)batch * 4}};
+  const Span to[] = {{out, T * H * a.l.P * 2}, {state, pool_slots * head}, {conv_state, pool_slots * 6 * dim}, {snapshots, T * head}};
+  if (overlaps(to, in)) return GDN_ERR_SHAPE;
   a.batch = batch; a.n_tok = n_tok;
   a.x = static_cast<const uint16_t*>(x); a.dt = dt; a.state = state; a.slot = slot;
   a.out = static_cast<uint16_t*>(out); a.snap = snapshots;

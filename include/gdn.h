@@ -594,8 +594,10 @@ GDN_API gdn_status gdn_ssm_prefill_workspace(const gdn_ssm_shape* shape, const i
  *                     each.
  * A prompt's bits do not depend on the pack.  A prompt continued from a
  * checkpoint agrees with the unbroken one to fp32's rounding.  init_state may be
- * final_state; other overlaps of what is written are not allowed.
- * Errors: as gdn_prefill_packed; GDN_ERR_CAPACITY (workspace too short). */
+ * final_state; other overlaps of what is written, with inputs or each other, are
+ * refused, rows taken as whole spans from the first to the last.
+ * Errors: as gdn_prefill_packed; GDN_ERR_CAPACITY (workspace too short);
+ * GDN_ERR_SHAPE (also: overlaps). */
 GDN_API gdn_status gdn_ssm_prefill_packed(
     const gdn_ssm_shape* shape, const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, int32_t n_seqs,
     int32_t n_tokens, const void* x, int64_t x_tok_stride, const float* conv_weight, const float* conv_bias,
@@ -614,7 +616,9 @@ GDN_API gdn_status gdn_ssm_prefill_packed(
  *                bf16 [pool_slots, 3, conv_dim], which moves on by n_tok inputs.
  *   out:         device bf16 [batch * n_tok, H, P].
  *   snapshots:   device fp32 [batch, n_tok, H, P, N] or NULL.
- * Errors: as gdn_decode_tokens. */
+ * What is written (state and conv_state as whole pools) must overlap neither an
+ * input nor another buffer that is written.
+ * Errors: as gdn_decode_tokens; GDN_ERR_SHAPE (also: overlaps). */
 GDN_API gdn_status gdn_ssm_decode(const gdn_ssm_shape* shape, int32_t batch, int32_t n_tok, const void* x,
                                   int64_t x_tok_stride, const float* conv_weight, const float* conv_bias,
                                   void* conv_state, int32_t dt_dtype, const void* dt, int64_t dt_tok_stride,
