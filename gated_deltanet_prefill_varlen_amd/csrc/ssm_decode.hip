@@ -14,6 +14,7 @@
 // rows a workgroup 47.0; one sequence then took 6.5 us for 6.0, four tokens of one
 // 11.8 for 10.5.
 // 64 sequences, 268 MB from and to memory: 50 us with the windows' launch, 5.5 TB/s.
+#include "cache_device.h"
 #include "ssm_device.h"
 
 namespace gdn {
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(kRows * (N / 16)) ssm_decode_kernel(const SsmD
       }
     }
     y = group_sum<LPR>(y);
-    if (jl == 0) a.out[(t * l.H + h) * P + row0 + rg] = (uint16_t)f32_to_bf16(fmaf(D, x, y));
+    if (jl == 0) a.out[(t * l.H + h) * P + row0 + rg] = (uint16_t)pack_bf16(fmaf(D, x, y), 0.f);   // (keeps every NaN)
     if (a.snap) {
       // (through the caches: 23.0 us for 16 sequences of 4 tokens, past them 31.1)
       f32x4* q = reinterpret_cast<f32x4*>(a.snap + ((t * l.H + h) * P + row0 + rg) * N + 4 * jl);
