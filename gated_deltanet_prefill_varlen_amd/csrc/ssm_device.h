@@ -7,15 +7,17 @@
 
 namespace gdn {
 
-// silu(bias + the four taps), taps and bias scaled by -log2(e) (conv_tap), in
-// the order of conv4_silu; not rounded.
+// 2^POW2 silu(bias + the four taps), taps and bias scaled by -log2(e)
+// (conv_tap), in the order of conv4_silu; not rounded.
+template <int POW2 = 0>
 __device__ __forceinline__ float conv4_bias_silu(float b, float w0, float w1, float w2, float w3, float x0, float x1,
                                                  float x2, float x3) {
+  constexpr float k = kNegLog2e / (1 << POW2);
   float zs = fmaf(w0, x0, b);
   zs = fmaf(w1, x1, zs);
   zs = fmaf(w2, x2, zs);
   zs = fmaf(w3, x3, zs);
-  return zs * __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_exp2f(zs), kNegLog2e, kNegLog2e));
+  return zs * __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_exp2f(zs), k, k));
 }
 
 // The step of a head at a token: clamp(softplus(raw + bias)).  softplus(v) =

@@ -20,11 +20,13 @@
 // Precision.  States come back in fp32 and are held to it: x w and B enter
 // their product as fp16 pairs hi + lo (hi hi + hi lo + lo hi: 2^-21).  What only
 // ends in the bf16 outputs (M, x, C, S as operands) is fp16 once, 2^-11 of the
-// value.  fp16's range is met by powers of two: B and C per chunk and group, x
-// per chunk and channel, S per channel by a bound of its largest entry that is
-// carried along.  A channel's x, as an operand, and its state, as an
-// accumulator, lie in the same lanes, so a channel's scale never leaves them
-// but for the outputs.
+// value.  fp16's range is met by powers of two: B and C per chunk and group, x, x w
+// and S per channel, by the largest x and x w of the chunk and by a bound of S's
+// largest entry that is carried along.  Below them fp16's smallest step is felt:
+// half of it is at most 2^-28 of a channel's largest x in the chunk, 2^-29 of its
+// largest x w and 2^-27 of S's bound.  A channel's x, as an operand, and its
+// state, as an accumulator, lie in the same lanes, so a channel's scale never
+// leaves them but for the outputs.
 //
 // Measured: 32 x 1,024 tokens of 64 heads of 64 on 128 with the convolution (0.63
 // GB) 290 us, prepare 32 of them; 4 x 8,192 tokens of 32 heads of 128 on 128 in 16
@@ -48,6 +50,7 @@ constexpr int kTiles = 3;                 // 16 x 16 tiles of C . B on and below
 // state (and S, where a chunk's products of x w and B fill it), B and C in C . B (whose
 // sums over N, times a step's share, fit fp16).
 constexpr int kTopBt = 14, kTopS = 30, kTopS16 = 14, kTopB = 4, kTopC = 4;
+constexpr int kPlainX = 11;               // x as it is used where no channel asks for another power: below 2^4
 constexpr float kLog2e = 1.44269504088896341f;
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -234,10 +237,10 @@ __device__ __forceinline__ void load_x(const XRef& f, int c, int g, RawX& x) {
   }
 }
 
-// The convolution of a channel pair; v[q][run][i]: channel 2 r + q at token
-// 16 run + 4 g + i.
+// The convolution of a channel pair, times 2^POW2; v[q][run][i]: channel 2 r + q
+// at token 16 run + 4 g + i.
 struct ConvW { float w0[2], w1[2], w2[2], w3[2], b[2]; };
-template <bool CONV>
+template <bool CONV, int POW2 = 0>
 __device__ __forceinline__ void conv_run(const uint32_t (&x)[7], const ConvW& k, float (&v0)[4], float (&v1)[4]) {
   float in[2][7];
 #pragma unroll
@@ -246,8 +249,8 @@ __device__ __forceinline__ void conv_run(const uint32_t (&x)[7], const ConvW& k,
   for (int q = 0; q < 2; ++q)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      (q ? v1 : v0)[i] = CONV ? conv4_bias_silu(k.b[q], k.w0[q], k.w1[q], k.w2[q], k.w3[q], in[q][i], in[q][i + 1], in[q][i + 2], in[q][i + 3])
-                              : in[q][i + 3];
+      (q ? v1 : v0)[i] = CONV ? conv4_bias_silu<POW2>(k.b[q], k.w0[q], k.w1[q], k.w2[q], k.w3[q], in[q][i], in[q][i + 1], in[q][i + 2], in[q][i + 3])
+                              : POW2 == 0 ? in[q][i + 3] : in[q][i + 3] * (float)(1 << POW2);
 }
 
 __device__ __forceinline__ void load_conv(const SsmLayer& l, int ch, ConvW& k) {
@@ -389,14 +392,13 @@ __device__ __forceinline__ void prepare_steps(const SsmScanArgs& a, const Ws& w,
   float* tab = w.tab + ((int64_t)(t0 / kChunk + s + c) * a.l.H + h) * kTab;
   tab[lane] = dt;
   tab[32 + lane] = cum;
-  const int kw = 10 - pow2_above(wmax);
+  const int kw = -pow2_above(wmax);      // the weights below 1
   tab[64 + lane] = ldexpf(wt, kw);
-  if (lane < 5)
+  if (lane < 4)
     tab[96 + lane] = lane == 0   ? total
-                     : lane == 1 ? wmax * kChunk
+                     : lane == 1 ? __int_as_float(kw)
                      : lane == 2 ? __int_as_float(pow2_above(dmax))
-                     : lane == 3 ? __builtin_amdgcn_exp2f(total)
-                                 : __int_as_float(kw);
+                                 : __builtin_amdgcn_exp2f(total);
 }
 
 template <int N, bool CONV>
@@ -640,8 +642,10 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
   const f16x8* bh = reinterpret_cast<const f16x8*>(ops + OPS - FIRST) + lane;
   const f16x8* bl = reinterpret_cast<const f16x8*>(ops + (CONV ? 2 * OPS : OPS) - FIRST) + lane;
 
-  // A chunk's x through the convolution, and the largest of each channel.
-  float xv[2][2][4], xmax[2];
+  // A chunk's x through the convolution, times 2^kPlainX; x_plain: every channel of
+  // the wave is 0, or its largest lies where that power serves it.
+  float xv[2][2][4];
+  bool x_plain = false;
   auto take_x = [&](int c) __attribute__((always_inline)) {
     // row 16 run + 4 g + j of the tile, from one address for j below 4 and one beyond
     ConvW cw;
@@ -665,24 +669,21 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
         const int j = i - (CONV ? 0 : 3);
         x[i] = xr[j / 4][16 * nw * (16 * run + j)];
       }
-      conv_run<CONV>(x, cw, xv[0][run], xv[1][run]);
+      conv_run<CONV, kPlainX>(x, cw, xv[0][run], xv[1][run]);
     }
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      xmax[q] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) xmax[q] = fmaxf(xmax[q], fabsf(xv[q][i / 4][i % 4]));   // (NaN is passed over)
-    }
-    if (__ballot(!(fmaxf(xmax[0], xmax[1]) < __builtin_inff()))) {
+    if (OUT) {
+      // of each channel, over the lane groups: is any value not 0, is any as large as wanted
+      x_plain = true;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        xmax[q] = 0.f;
+        float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) xmax[q] = fmaxf(xmax[q], finite_abs(xv[q][i / 4][i % 4]));
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(xv[q][i / 4][i % 4]));   // (NaN is passed over)
+        auto fold = [](uint64_t m) { m |= m >> 32; return (uint32_t)(m | m >> 16) & 0xFFFFu; };
+        const uint32_t any = fold(__ballot(top > 0.f)), large = fold(__ballot(top >= ldexpf(1.f, kPlainX - 8)));
+        x_plain = x_plain && (any & ~large) == 0 && __ballot(!(top < 32768.f)) == 0;
       }
     }
-#pragma unroll
-    for (int q = 0; q < 2; ++q) xmax[q] = over_groups(xmax[q]);
   };
   const int pd_max = 14 - pow2_above(fabsf(D));
   if (c_first < c_end) take_x(c_first);
@@ -702,17 +703,28 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
     const int kbt = __builtin_amdgcn_readfirstlane(kk.x), kb = kbt - kTopBt + kTopB, kc = __builtin_amdgcn_readfirstlane(kk.y);
     const float* tab = reinterpret_cast<const float*>(tabs + (c & 1) * L::TABS) + hl * kTab;
     const float alpha = tab[99];
-    const int kw = __float_as_int(tab[100]), ad = min(-__float_as_int(tab[98]), pd_max - (kb + kc)), m = kb + kc + ad;
+    const int kw = __float_as_int(tab[97]), ad = min(-__float_as_int(tab[98]), pd_max - (kb + kc)), m = kb + kc + ad;
     __builtin_amdgcn_sched_barrier(0);
 
-    // the entering state with C: S as an operand times 2^es, one power for the
-    // wave; y[tt][q]: channel 2 (4 g + i) + q at token 16 tt + r
+    // the entering state with C: S as an operand times 2^es; y[tt][q]: channel
+    // 2 (4 g + i) + q at token 16 tt + r.  One power for the wave and one for x
+    // (plain) serve where they leave each channel 2^-27 of its own largest value:
+    // where no channel's x, or state, lies far below the wave's.  Else each channel
+    // has its own, which the outputs' rows then take from its lanes.
     f32x4 y[2][2];
-    float f1 = 0.f;
+    int es[2];
+    bool plain = false;
     if (OUT) {
-      const int es = kTopS16 - pow2_above(over_wave16(fmaxf(bound[0], bound[1])));
-      f1 = ldexpf(1.f, max(-126, min(126, -(es + kc))));
-      const float down[2] = {ldexpf(1.f, es - e[0]), ldexpf(1.f, es - e[1])};
+      const float top = over_wave16(fmaxf(bound[0], bound[1]));
+      const uint32_t low = __float_as_uint(top * 0x1p-12f) - 1u;       // (a bound of 0 passes)
+      plain = x_plain && (top == 0.f || (top >= 0x1p-60f && top < 0x1p60f)) &&
+              __ballot(__float_as_uint(bound[0]) - 1u < low || __float_as_uint(bound[1]) - 1u < low) == 0;
+      float down[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        es[q] = kTopS16 - pow2_above(plain ? top : bound[q]);
+        down[q] = bound[q] == 0.f ? 0.f : ldexpf(1.f, es[q] - e[q]);
+      }
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
@@ -739,55 +751,78 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
     }
     __builtin_amdgcn_sched_barrier(0);
 
-    // x as operand of the outputs: times 2^kx, one power for the wave; x w of
-    // the state, in pairs: times 2^(kw + ks), one power for the channel
-    const float xw = OUT ? over_wave16(fmaxf(xmax[0], xmax[1])) : 0.f;
-    const int kx = !OUT || (xw >= 0.125f && xw < 32768.f) ? 0 : 14 - pow2_above(xw);
-    int ks[2], e_new[2];
-    float grown[2];
-    const float wmax = ldexpf(tab[97], kTopBt - kbt);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      grown[q] = fmaf(alpha, bound[q], wmax * xmax[q]);
-      ks[q] = xmax[q] >= 0x1p-6f && xmax[q] < 16.f ? 0 : 4 - pow2_above(xmax[q]);
-      ks[q] = min(ks[q], 90 - pow2_above(grown[q]) - kbt - kw);     // the state stays inside fp32
-      e_new[q] = kbt + kw + ks[q];
-    }
-    const bool plain = __ballot((kx | ks[0] | ks[1]) != 0) == 0;
+    // x as operand of the outputs, times 2^kx
+    int kx[2] = {kPlainX, kPlainX};
     f16x8 xo[2], xh[2], xl[2];
     if (OUT) {
-      if (!plain) {
-        const float f = ldexpf(1.f, kx);
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+      for (int q = 0; q < 2; ++q) {
+        if (plain) {
+          xo[q] = join(pack_f16(xv[q][0][0], xv[q][0][1]), pack_f16(xv[q][0][2], xv[q][0][3]), pack_f16(xv[q][1][0], xv[q][1][1]),
+                       pack_f16(xv[q][1][2], xv[q][1][3]));
+          continue;
+        }
+        float top = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) xv[q][i / 4][i % 4] *= f;
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, finite_abs(xv[q][i / 4][i % 4]));
+        const int k = 15 - pow2_above(over_groups(top));
+        kx[q] += k;
+        f16x2 o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = pack_f16(ldexpf(xv[q][i / 2][2 * (i % 2)], k), ldexpf(xv[q][i / 2][2 * (i % 2) + 1], k));
+        xo[q] = join(o[0], o[1], o[2], o[3]);
       }
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        xo[q] = join(pack_f16(xv[q][0][0], xv[q][0][1]), pack_f16(xv[q][0][2], xv[q][0][3]), pack_f16(xv[q][1][0], xv[q][1][1]),
-                     pack_f16(xv[q][1][2], xv[q][1][3]));
     }
-    if (!plain) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) xv[q][i / 4][i % 4] = ldexpf(xv[q][i / 4][i % 4], ks[q] - kx);
-    }
+    // x w of the state, in pairs: times 2^(kPlainX + kw + ks), ks a channel's own, and
+    // 0 where half the pairs' smallest step is 2^-29 of its largest x w at most
+    float grown[2], pmax[2];
+    int ks[2], e_new[2];
     {
       const f32x4 wt[2] = {*reinterpret_cast<const f32x4*>(tab + 64 + 4 * g), *reinterpret_cast<const f32x4*>(tab + 80 + 4 * g)};
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        f16x2 hi[4], lo[4];
+        pmax[q] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x0 = xv[q][i / 2][2 * (i % 2)], x1 = xv[q][i / 2][2 * (i % 2) + 1], w0 = wt[i / 2][2 * (i % 2)], w1 = wt[i / 2][2 * (i % 2) + 1];
-          hi[i] = pack_f16(x0 * w0, x1 * w1);
-          lo[i] = pack_f16(fmaf(x0, w0, -(float)hi[i][0]), fmaf(x1, w1, -(float)hi[i][1]));
+        for (int i = 0; i < 8; ++i) {
+          xv[q][i / 4][i % 4] *= wt[i / 4][i % 4];
+          pmax[q] = fmaxf(pmax[q], fabsf(xv[q][i / 4][i % 4]));      // (NaN is passed over)
         }
-        xh[q] = join(hi[0], hi[1], hi[2], hi[3]);
-        xl[q] = join(lo[0], lo[1], lo[2], lo[3]);
       }
+    }
+    if (__ballot(!(fmaxf(pmax[0], pmax[1]) < __builtin_inff()))) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        pmax[q] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pmax[q] = fmaxf(pmax[q], finite_abs(xv[q][i / 4][i % 4]));
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      pmax[q] = over_groups(pmax[q]);
+      // no entry of the channel will be larger: 32 products below 2^(kTopBt - kbt) each
+      grown[q] = fmaf(alpha, bound[q], ldexpf(pmax[q], 5 + kTopBt - kbt - kw - kPlainX));
+      ks[q] = pmax[q] == 0.f || (pmax[q] >= 16.f && pmax[q] < 32768.f) ? 0 : 15 - pow2_above(pmax[q]);
+      ks[q] = min(ks[q], 90 - pow2_above(grown[q]) - kbt - kw - kPlainX);     // the state stays inside fp32
+      e_new[q] = kbt + kw + kPlainX + ks[q];
+    }
+    if (__ballot((ks[0] | ks[1]) != 0)) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) xv[q][i / 4][i % 4] = ldexpf(xv[q][i / 4][i % 4], ks[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      f16x2 hi[4], lo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float p0 = xv[q][i / 2][2 * (i % 2)], p1 = xv[q][i / 2][2 * (i % 2) + 1];
+        hi[i] = pack_f16(p0, p1);
+        lo[i] = pack_f16(fmaf((float)hi[i][0], -1.f, p0), fmaf((float)hi[i][1], -1.f, p1));
+      }
+      xh[q] = join(hi[0], hi[1], hi[2], hi[3]);
+      xl[q] = join(lo[0], lo[1], lo[2], lo[3]);
     }
 
     // the state: S^T[n, p] += B^T[n, s] (x w)^T[s, p]
@@ -818,11 +853,11 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
     }
     __builtin_amdgcn_sched_barrier(0);
     if (!OUT) seg_sum += tab[96];
-    // the outputs' decays, before the tables may be fetched over: from the start of the chunk
+    // the outputs' decays from the start of the chunk, before the tables may be fetched over
     float fe[2];
     if (OUT) {
 #pragma unroll
-      for (int tt = 0; tt < 2; ++tt) fe[tt] = f1 * __builtin_amdgcn_exp2f(tab[32 + 16 * tt + r]);
+      for (int tt = 0; tt < 2; ++tt) fe[tt] = __builtin_amdgcn_exp2f(tab[32 + 16 * tt + r]);
     }
     __builtin_amdgcn_s_setprio(0);
     __syncthreads();   // M is whole; the products are through with the operands
@@ -848,18 +883,27 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
           first_bad[q] = min(first_bad[q], from_lane(first_bad[q], lane2 ^ 32));
         }
       }
-      const float f2 = ldexpf(1.f, max(-126, min(126, -(m + kx))));
       uint16_t* to = a.out + ((int64_t)(t0 + c * kChunk) * l.H + h) * P + 32 * half;
       const uint32_t out_at = (uint32_t)(r * l.H * P + 8 * g);
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt) {
         const f16x8 mf = fm[tt][lane];
         float o[8];
+        const f32x4 z = {0.f, 0.f, 0.f, 0.f}, y2[2] = {mma(xo[0], mf, z), mma(xo[1], mf, z)};
+        if (plain) {
+          const float f1 = ldexpf(fe[tt], -(es[0] + kc)), f2 = ldexpf(1.f, -(m + kPlainX));
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const f32x4 y2 = mma(xo[q], mf, f32x4{0.f, 0.f, 0.f, 0.f});
+          for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[2 * i + q] = fmaf(y2[i], f2, y[tt][q][i] * fe[tt]);
+            for (int i = 0; i < 4; ++i) o[2 * i + q] = fmaf(y2[q][i], f2, y[tt][q][i] * f1);
+        } else {
+          const int row = anew(4 * g);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              o[2 * i + q] = ldexpf(y2[q][i], -(m + from_lane(kx[q], row + i))) +
+                             ldexpf(y[tt][q][i] * fe[tt], -(from_lane(es[q], row + i) + kc));
         }
         const int t = 16 * tt + r;
         if (bad) {
