@@ -20,13 +20,16 @@
 // Precision.  States come back in fp32 and are held to it: x w and B enter
 // their product as fp16 pairs hi + lo (hi hi + hi lo + lo hi: 2^-21).  What only
 // ends in the bf16 outputs (M, x, C, S as operands) is fp16 once, 2^-11 of the
-// value.  fp16's range is met by powers of two: B and C per chunk and group, x, x w
-// and S per channel, by the largest x and x w of the chunk and by a bound of S's
-// largest entry that is carried along.  Below them fp16's smallest step is felt:
-// half of it is at most 2^-28 of a channel's largest x in the chunk, 2^-29 of its
-// largest x w and 2^-27 of S's bound.  A channel's x, as an operand, and its
-// state, as an accumulator, lie in the same lanes, so a channel's scale never
-// leaves them but for the outputs.
+// value.  fp16's range is met by powers of two: per token on C and, for the state,
+// on B (which x w takes back), per chunk on B in C . B, per chunk and channel on x and
+// x w, and per channel on S, by a bound of its largest entry that is carried along.
+// Below them fp16's smallest step is felt.  Half of it is at most, of x, 2^-28 of its
+// channel's largest in the chunk; of x w, 2^-29 of its channel's largest with its
+// token's largest B; of B for the state, 2^-38 of its token's largest; of S, 2^-27 of
+// its bound; and of the weights M, twice, 2^-30 of the largest C of the token, B of
+// the chunk and step together.  A channel's x, as an operand, and its state, as an
+// accumulator, lie in the same lanes, so a channel's scale never leaves them but for
+// the outputs.
 //
 // Measured: 32 x 1,024 tokens of 64 heads of 64 on 128 with the convolution (0.63
 // GB) 290 us, prepare 32 of them; 4 x 8,192 tokens of 32 heads of 128 on 128 in 16
@@ -46,10 +49,10 @@ namespace {
 constexpr int kChunk = 32;
 constexpr int kTab = 128;                 // floats of a (chunk, head)'s table: dt, cum, w, scalars
 constexpr int kTiles = 3;                 // 16 x 16 tiles of C . B on and below the diagonal
-// Powers of two that the largest values are brought to: B^T in the update of the
-// state (and S, where a chunk's products of x w and B fill it), B and C in C . B (whose
-// sums over N, times a step's share, fit fp16).
-constexpr int kTopBt = 14, kTopS = 30, kTopS16 = 14, kTopB = 4, kTopC = 4;
+// Powers of two that the largest values are brought to: B of a token for the state
+// and of a chunk for C . B (and S, where the products of x w and B fill it), C of a
+// token, and the products C . B, whose sums over N stay below 2^(kTopB + kTopC + 7).
+constexpr int kTopB = 14, kTopS = 30, kTopS16 = 14, kTopC = 14, kTopCB = 15, kCB = kTopB + kTopC + 7 - kTopCB;
 constexpr int kPlainX = 11;               // x as it is used where no channel asks for another power: below 2^4
 constexpr float kLog2e = 1.44269504088896341f;
 
@@ -117,8 +120,9 @@ struct AddOp { __device__ __forceinline__ float operator()(float a, float b) con
 // and none passes n_tokens / 32 + n_seqs.  Segments alike, by 256 tokens.
 struct Ws {
   char* bc;              // [slots][G]: C operands, B^T hi, B^T lo (32 N halves each)
-  _Float16* gt;          // [slots][G][4][64][4]: the tiles of C . B on and below the diagonal; the powers of
-                         // two on B^T and C in the first 8 bytes of the fourth
+  _Float16* gt;          // [slots][G][4][64][4]: the tiles of C . B on and below the diagonal; in place of the
+                         // fourth kb, the power of two on the chunk's B, and per token (from the 32nd dword on)
+                         // that on C and (from the 64th on) 2^(kb - that on B), which stands with x w
   float* tab;            // [slots][H][kTab]
   float* seg;            // [segment slots][H][P][N]
   float* seg_sum;        // [segment slots][H]: log2 of the segment's decay
@@ -273,7 +277,7 @@ __device__ __forceinline__ void prepare_bc(const SsmScanArgs& a, const Ws& w, in
   const int t0 = a.cu[s], len = a.cu[s + 1] - t0, inner = l.H * l.P, left = len - c * kChunk;
   const int64_t sg = (int64_t)(t0 / kChunk + s + c) * l.G + grp;
   float v[TILES][2][2][4];
-  float m[2] = {0.f, 0.f};
+  float top[TILES][2][4] = {};        // the largest of each token in a tile
   RawX x[TILES];
   auto tile_of = [&](int k) { return wave + 4 * k; };     // below PAIRS: of B, then of C
   auto col_of = [&](int t) { return t < PAIRS ? inner + grp * N + 32 * t : inner + (l.G + grp) * N + 32 * (t - PAIRS); };
@@ -289,46 +293,61 @@ __device__ __forceinline__ void prepare_bc(const SsmScanArgs& a, const Ws& w, in
     if (tile_of(k) >= 2 * PAIRS) continue;
     ConvW cw;
     if (CONV) load_conv(l, col_of(tile_of(k)) + 2 * r, cw);
-    float top = 0.f;
 #pragma unroll
     for (int run = 0; run < 2; ++run) {
       conv_run<CONV>(x[k].v[run], cw, v[k][0][run], v[k][1][run]);
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float& u = v[k][q][run][i];
-          if (16 * run + 4 * g + i >= left) u = 0.f;
-          top = fmaxf(top, finite_abs(u));
-        }
+      for (int i = 0; i < 4; ++i) {
+        float& u0 = v[k][0][run][i];
+        float& u1 = v[k][1][run][i];
+        if (16 * run + 4 * g + i >= left) u0 = u1 = 0.f;
+        top[k][run][i] = fmaxf(finite_abs(u0), finite_abs(u1));
+      }
     }
-    m[tile_of(k) >= PAIRS] = fmaxf(m[tile_of(k) >= PAIRS], top);
   }
+  // [B, C][token][tile]
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    m[i] = over_wave(m[i], MaxOp{});
-    if (lane == 0) red[4 * i + wave] = m[i];
+  for (int k = 0; k < TILES; ++k) {
+    if (tile_of(k) >= 2 * PAIRS) continue;
+    float* const to = red + (tile_of(k) / PAIRS * kChunk + 4 * g) * PAIRS + tile_of(k) % PAIRS;
+#pragma unroll
+    for (int run = 0; run < 2; ++run)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float m = over_wave16(top[k][run][i]);
+        if (r == 0) to[(16 * run + i) * PAIRS] = m;
+      }
   }
   __syncthreads();
+  // lane t of each wave: token t's power on B, lane 32 + t: on C
+  float most = red[lane * PAIRS];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) m[i] = fmaxf(fmaxf(red[4 * i], red[4 * i + 1]), fmaxf(red[4 * i + 2], red[4 * i + 3]));
-  const int kb = kTopBt - pow2_above(m[0]), kc = kTopC - pow2_above(m[1]);
-  if (tid == 0) *reinterpret_cast<int2*>(w.gt + sg * 4 * 256 + 3 * 256) = make_int2(kb, kc);
+  for (int i = 1; i < PAIRS; ++i) most = fmaxf(most, red[lane * PAIRS + i]);
+  const int power = (lane < 32 ? kTopB : kTopC) - pow2_above(most);
+  int kb = lane < 32 ? power : INT_MAX;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) kb = min(kb, from_lane(kb, lane ^ d));
+  kb = __builtin_amdgcn_readfirstlane(kb);
+  if (wave == 0) {
+    int* const powers = reinterpret_cast<int*>(w.gt + sg * 4 * 256 + 3 * 256);
+    if (lane == 0) powers[0] = kb;
+    powers[32 + (lane ^ 32)] = lane < 32 ? __float_as_int(ldexpf(1.f, kb - power)) : power;
+  }
   f16x8* ops = reinterpret_cast<f16x8*>(w.bc + sg * 3 * kChunk * N * 2);
 #pragma unroll
   for (int k = 0; k < TILES; ++k) {
     const int t = tile_of(k);
     if (t >= 2 * PAIRS) continue;
     const bool is_c = t >= PAIRS;
-    const float f = ldexpf(1.f, is_c ? kc : kb), down = is_c ? 1.f : 1.f / (1 << (kTopBt - kTopB));
     _Float16* to = rows + (is_c ? kChunk * ROW + 32 * (t - PAIRS) : 32 * t) + 2 * r;
 #pragma unroll
     for (int run = 0; run < 2; ++run)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[k][0][run][i] *= f;
-        v[k][1][run][i] *= f;
-        *reinterpret_cast<f16x2*>(to + (16 * run + 4 * g + i) * ROW) = pack_f16(v[k][0][run][i] * down, v[k][1][run][i] * down);
+        const int own = from_lane(power, (is_c ? 32 : 0) + 16 * run + 4 * g + i), all = is_c ? own : kb;
+        *reinterpret_cast<f16x2*>(to + (16 * run + 4 * g + i) * ROW) = pack_f16(ldexpf(v[k][0][run][i], all), ldexpf(v[k][1][run][i], all));
+        v[k][0][run][i] = ldexpf(v[k][0][run][i], own);
+        v[k][1][run][i] = ldexpf(v[k][1][run][i], own);
       }
     if (!is_c) {
       f16x8* bt = ops + kChunk * N / 8;
@@ -358,6 +377,7 @@ __device__ __forceinline__ void prepare_bc(const SsmScanArgs& a, const Ws& w, in
     for (int ks = 0; ks < KN; ++ks)
       acc = mma(*reinterpret_cast<const f16x8*>(rows + (16 * st + r) * ROW + 8 * g + 32 * ks),
                 *reinterpret_cast<const f16x8*>(rc + 16 * tt * ROW + 32 * ks), acc);
+    acc *= 1.f / (1 << kCB);
     const f16x2 p0 = pack_f16(acc[0], acc[1]), p1 = pack_f16(acc[2], acc[3]);
     reinterpret_cast<f16x4*>(w.gt + sg * 4 * 256)[wave * 64 + lane] = f16x4{p0[0], p0[1], p1[0], p1[1]};
   }
@@ -404,7 +424,7 @@ __device__ __forceinline__ void prepare_steps(const SsmScanArgs& a, const Ws& w,
 template <int N, bool CONV>
 __global__ void __launch_bounds__(256) ssm_prepare_kernel(const SsmScanArgs a, const Ws w) {
   __shared__ __align__(16) _Float16 rows[2 * kChunk * (N + 8)];
-  __shared__ float red[8];
+  __shared__ __align__(16) float red[2 * kChunk * 4];
   const int b = blockIdx.x, s = owner(a.cu, a.n_seqs, kChunk, b), c = b - (a.cu[s] / kChunk + s);
   if (c * kChunk >= a.cu[s + 1] - a.cu[s]) return;
   if ((int)blockIdx.y < a.l.G) {
@@ -442,10 +462,16 @@ __device__ __forceinline__ void move_window(const SsmScanArgs& a, int s, int t0,
   for (int j = 0; j < 3; ++j) reinterpret_cast<uint32_t*>(a.conv_out + ((int64_t)s * 3 + j) * a.l.conv_dim)[pair] = v[j];
 }
 
-// The operand of M^T for 16 tokens t (tile row TT): both tiles of s.
+// The power of two on a token's weights: from those on C . B (with C's own, kc)
+// and the chunk's steps (ad), or what D leaves.
+__device__ __forceinline__ int weight_power(int kb, int kc, int ad, int pd_max) { return min(kb + kc - kCB + ad, pd_max); }
+
+// The operand of M^T for 16 tokens t (tile row TT): both tiles of s.  m: the power
+// on the weights of this lane's token, cb: the one that they have from C . B.
 template <int TT>
-__device__ __forceinline__ f16x8 weigh(const f16x4* gt, const float* tab, int lane, int ad, float dm) {
-  const int r = lane & 15, g = lane >> 4;
+__device__ __forceinline__ f16x8 weigh(const f16x4* gt, const float* tab, int lane, int m, int cb, float D) {
+  const int r = lane & 15, g = lane >> 4, ad = m - cb;
+  const float dm = ldexpf(D, m);
   const float ct = tab[32 + 16 * TT + r] + (float)ad;
   f16x2 o[4];
 #pragma unroll
@@ -699,11 +725,19 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
     // the half with the operands goes first on a SIMD: behind its end wait the
     // workgroup's fetches (307 -> 297 us at 32 x 1,024 tokens)
     __builtin_amdgcn_s_setprio(1);
-    const int2 kk = *reinterpret_cast<const int2*>(gts + GT - 512);
-    const int kbt = __builtin_amdgcn_readfirstlane(kk.x), kb = kbt - kTopBt + kTopB, kc = __builtin_amdgcn_readfirstlane(kk.y);
+    const int* const powers = reinterpret_cast<const int*>(gts + GT - 512);
+    const int kbt = __builtin_amdgcn_readfirstlane(powers[0]);
     const float* tab = reinterpret_cast<const float*>(tabs + (c & 1) * L::TABS) + hl * kTab;
     const float alpha = tab[99];
-    const int kw = __float_as_int(tab[97]), ad = min(-__float_as_int(tab[98]), pd_max - (kb + kc)), m = kb + kc + ad;
+    const int kw = __float_as_int(tab[97]);
+    int kc[2], m[2];           // the powers on C and on the weights of tokens r and 16 + r
+    if (OUT) {
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt) {
+        kc[tt] = powers[32 + 16 * tt + r];
+        m[tt] = weight_power(kbt, kc[tt], -__float_as_int(tab[98]), pd_max);
+      }
+    }
     __builtin_amdgcn_sched_barrier(0);
 
     // the entering state with C: S as an operand times 2^es; y[tt][q]: channel
@@ -744,10 +778,9 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
       }
       __builtin_amdgcn_sched_barrier(0);
       // the weights inside the chunk, as operands: element (t = column, s) of M^T
-      const float dm = ldexpf(D, m);
       const f16x4* gt = reinterpret_cast<const f16x4*>(gts);
-      if (0 == half) fm[0][lane] = weigh<0>(gt, tab, lane, ad, dm);
-      if (1 % WPH == half) fm[1][lane] = weigh<1>(gt, tab, lane, ad, dm);
+      if (0 == half) fm[0][lane] = weigh<0>(gt, tab, lane, m[0], kbt + kc[0] - kCB, D);
+      if (1 % WPH == half) fm[1][lane] = weigh<1>(gt, tab, lane, m[1], kbt + kc[1] - kCB, D);
     }
     __builtin_amdgcn_sched_barrier(0);
 
@@ -778,7 +811,9 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
     float grown[2], pmax[2];
     int ks[2], e_new[2];
     {
-      const f32x4 wt[2] = {*reinterpret_cast<const f32x4*>(tab + 64 + 4 * g), *reinterpret_cast<const f32x4*>(tab + 80 + 4 * g)};
+      const float* const fb = reinterpret_cast<const float*>(powers) + 64;
+      const f32x4 wt[2] = {*reinterpret_cast<const f32x4*>(tab + 64 + 4 * g) * *reinterpret_cast<const f32x4*>(fb + 4 * g),
+                           *reinterpret_cast<const f32x4*>(tab + 80 + 4 * g) * *reinterpret_cast<const f32x4*>(fb + 16 + 4 * g)};
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         pmax[q] = 0.f;
@@ -800,8 +835,8 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       pmax[q] = over_groups(pmax[q]);
-      // no entry of the channel will be larger: 32 products below 2^(kTopBt - kbt) each
-      grown[q] = fmaf(alpha, bound[q], ldexpf(pmax[q], 5 + kTopBt - kbt - kw - kPlainX));
+      // no entry of the channel will be larger: 32 products below 2^(kTopB - kbt) each
+      grown[q] = fmaf(alpha, bound[q], ldexpf(pmax[q], 5 + kTopB - kbt - kw - kPlainX));
       ks[q] = pmax[q] == 0.f || (pmax[q] >= 16.f && pmax[q] < 32768.f) ? 0 : 15 - pow2_above(pmax[q]);
       ks[q] = min(ks[q], 90 - pow2_above(grown[q]) - kbt - kw - kPlainX);     // the state stays inside fp32
       e_new[q] = kbt + kw + kPlainX + ks[q];
@@ -891,7 +926,7 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
         float o[8];
         const f32x4 z = {0.f, 0.f, 0.f, 0.f}, y2[2] = {mma(xo[0], mf, z), mma(xo[1], mf, z)};
         if (plain) {
-          const float f1 = ldexpf(fe[tt], -(es[0] + kc)), f2 = ldexpf(1.f, -(m + kPlainX));
+          const float f1 = ldexpf(fe[tt], -(es[0] + kc[tt])), f2 = ldexpf(1.f, -(m[tt] + kPlainX));
 #pragma unroll
           for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -902,8 +937,8 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
           for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              o[2 * i + q] = ldexpf(y2[q][i], -(m + from_lane(kx[q], row + i))) +
-                             ldexpf(y[tt][q][i] * fe[tt], -(from_lane(es[q], row + i) + kc));
+              o[2 * i + q] = ldexpf(y2[q][i], -(m[tt] + from_lane(kx[q], row + i))) +
+                             ldexpf(y[tt][q][i] * fe[tt], -(from_lane(es[q], row + i) + kc[tt]));
         }
         const int t = 16 * tt + r;
         if (bad) {

@@ -33,28 +33,68 @@ def test_zeros(what, conv, init):
     y.check(y.run(ck), y.oracle(ck), ck)
 
 
-def check(y, ck=()):
-    """Against the oracle, with what fp16's smallest step adds to an output.  x is an operand times a power of
-    two: half the smallest step, 2^-25, is 2^-28 of the largest |x| of its channel in the chunk of 32 tokens,
-    or less (the power is 2^11 where that largest is 2^-8 or more, else it is brought to 2^14).  Outputs are
-    sums of weights times x: 2^-28 of the same sum of absolute values with each |x| at its chunk's largest."""
-    r, want = y.run(ck), y.oracle(ck)
+def floors(y):
+    """What fp16's smallest step, whose half is 2^-25, may add to each output.
+    - x is an operand times a power of two: 2^11 where the channel's largest |x| in the chunk of 32 tokens is
+      2^-8 or more, else the power that brings that largest to 2^14 or more.  2^-25 is 2^-28 of that largest,
+      or less: 2^-28 of the sum of absolute terms with each |x| at its chunk's largest.
+    - A token's weights are products of C, brought to 2^13 or more by its largest, of B, by the chunk's largest, of
+      steps, by the largest that is left of any, and of 2^-20, and round twice at 2^-25: in units of these
+      three largest 2 * 2^-25 / 2^(13 + 13 - 20) / 2^-1 = 2^-29, times the sum of the chunk's |x| up to the token.
+      Where D is larger it is brought to 2^13 or more instead, 2^-38 of it, times 32 tokens' |x|: 2^-5 of the first."""
     H, G, P, N = y.dims
-    u = []
+    A, dt = f64(y.A), y.steps()
+    rows, weights = [], np.zeros((int(y.cu[-1]), H, P))
     for s, n in enumerate(y.lens):
-        rows = f64(y.x[y.cu[s]:y.cu[s + 1]])
+        u = f64(y.x[y.cu[s]:y.cu[s + 1]])
         if y.w is not None:
-            rows = O.conv(rows, f64(y.w), f64(y.b), np.zeros((3, y.C)) if y.window is None else f64(y.window)[s])[0]
-        rows = np.abs(rows)
+            u = O.conv(u, f64(y.w), f64(y.b), np.zeros((3, y.C)) if y.window is None else f64(y.window)[s])[0]
+        u = np.abs(u)
         for c in range(0, n, 32):
-            rows[c:c + 32, :H * P] = rows[c:c + 32, :H * P].max(0)
-        u.append(rows)
-    top = O.prefill(H, G, P, N, y.cu, np.concatenate(u), y.steps(), f64(y.A), None if y.D is None else np.abs(f64(y.D)))["out"]
+            part, at = u[c:c + 32], slice(y.cu[s] + c, min(y.cu[s] + c + 32, y.cu[s + 1]))
+            x, b, k = part[:, :H * P].reshape(-1, H, P), part[:, H * P:H * P + G * N].reshape(-1, G, N), part[:, H * P + G * N:].reshape(-1, G, N)
+            al = A * dt[at]
+            left = np.abs(dt[at]).max(0) * np.exp(np.maximum(al, 0).sum(0))
+            weights[at] = np.cumsum(x, 0) * (np.repeat(b.max((0, 2)) * k.max(2), H // G, 1) * left)[:, :, None]
+            part[:, :H * P] = part[:, :H * P].max(0)
+        rows.append(u)
+    D = None if y.D is None else np.abs(f64(y.D))
+    return 2.0 ** -28 * (1 + 2.0 ** -5) * O.prefill(H, G, P, N, y.cu, np.concatenate(rows), dt, A, D)["out"] + 2.0 ** -29 * weights
+
+
+def state_floors(y, ck):
+    """The same for states, of final and kept ones: [.., H, P, 1].  Of a chunk's products x w (w: the steps, decayed to
+    its end) a channel's largest, each with its token's largest |B|, is brought to 2^4 or more, and each is off by
+    2^-25: 2^-28 of that largest with its |B| (2^-29, and a power of two's slack in the |B|), 32 times at most.  B itself, brought
+    to 2^13 or more in each token, is off by 2^-38 of that, far less.  Kept states inside a chunk come from the one at its start."""
+    H, G, P, N = y.dims
+    A, dt, final, kept = f64(y.A), y.steps(), [], []
+    for s, n in enumerate(y.lens):
+        u = f64(y.x[y.cu[s]:y.cu[s + 1]])
+        if y.w is not None:
+            u = O.conv(u, f64(y.w), f64(y.b), np.zeros((3, y.C)) if y.window is None else f64(y.window)[s])[0]
+        u, F = np.abs(u), np.zeros((H, P, 1))
+        for c in range(0, n, 32):
+            L = min(32, n - c)
+            kept += [F] * sum(int(y.cu[s]) + c < k < int(y.cu[s]) + c + L for k in ck)
+            part, d = u[c:c + L], dt[y.cu[s] + c:y.cu[s] + c + L]
+            cum = np.cumsum(A * d, 0)
+            w = np.abs(d) * np.exp(cum[-1] - cum)
+            b = np.repeat(part[:, H * P:H * P + G * N].reshape(L, G, N).max(2), H // G, 1)
+            F = np.exp(cum[-1])[:, None, None] * F + 2.0 ** -23 * (part[:, :H * P].reshape(L, H, P) * (w * b)[..., None]).max(0)[..., None]
+            kept += [F] * (int(y.cu[s]) + c + L in ck)
+        final.append(F)
+    return np.array(final), np.array(kept)
+
+
+def check(y, ck=()):
+    r, want = y.run(ck), y.oracle(ck)
     T, longest = int(y.cu[-1]), max(y.lens)
-    close(r["out"][:T], want["out"], out_tol(want["out"], want["out_mass"]) + 2.0 ** -28 * top, "out")
-    close(r["final"], want["final"], state_tol(want["final_mass"], longest), "final")
+    final, kept = state_floors(y, ck)
+    close(r["out"][:T], want["out"], out_tol(want["out"], want["out_mass"]) + floors(y), "out")
+    close(r["final"], want["final"], state_tol(want["final_mass"], longest) + final, "final")
     if len(ck):
-        close(r["kept"], want["kept"], state_tol(want["kept_mass"], longest), "kept")
+        close(r["kept"], want["kept"], state_tol(want["kept_mass"], longest) + kept, "kept")
 
 
 def spread(shape, low, seed):
@@ -95,5 +135,20 @@ def test_x_of_tokens_apart(D, a_scale):
     f[[0, 70, 1270]] = 2.0 ** -25
     f[[69, 1269, 1302]] = 2.0 ** -20
     y.x[:, :256] = (y.x[:, :256].float() * f).bfloat16()
+    ck = [20, 70, 70 + 1024, 1303]
+    check(y, ck)
+
+
+@pytest.mark.parametrize("low", [-17, -20, -40])
+@pytest.mark.parametrize("a_scale", [1.0, 50.0])
+@pytest.mark.parametrize("what", ["B and C", "C"])
+def test_b_and_c_of_tokens_apart(low, a_scale, what):
+    """Tokens whose B and C, or C alone, are far below those of others in the chunk: a prompt's first, whose
+    output is nothing but their product, and, with decays that leave nothing, any."""
+    y = Layer(4, 2, 64, 64, [70, 1200, 33], seed=54, conv=False, D=False, a_scale=a_scale, dt_shift=4.0 if a_scale > 1 else 0.0)
+    f = spread((1303, 1), low, 4)
+    f[[0, 70, 1270, 69, 1302]] = 2.0 ** low
+    at = 384 if what == "C" else 256
+    y.x[:, at:] = (y.x[:, at:].float() * f).bfloat16()
     ck = [20, 70, 70 + 1024, 1303]
     check(y, ck)
