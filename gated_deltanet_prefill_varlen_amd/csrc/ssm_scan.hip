@@ -27,7 +27,7 @@
 // channel's largest in the chunk; of x w, 2^-29 of its channel's largest with its
 // token's largest B; of B for the state, 2^-38 of its token's largest; of S, 2^-27 of
 // its bound; and of the weights M, twice, 2^-30 of the largest C of the token, B of
-// the chunk and step together.  A channel's x, as an operand, and its state, as an
+// the chunk and step (as far as it is left at the token) together.  A channel's x, as an operand, and its state, as an
 // accumulator, lie in the same lanes, so a channel's scale never leaves them but for
 // the outputs.
 //
@@ -47,7 +47,7 @@ namespace gdn {
 namespace {
 
 constexpr int kChunk = 32;
-constexpr int kTab = 128;                 // floats of a (chunk, head)'s table: dt, cum, w, scalars
+constexpr int kTab = 128;                 // floats of a (chunk, head)'s table: dt, cum, w, scalars, 32 powers as int8
 constexpr int kTiles = 3;                 // 16 x 16 tiles of C . B on and below the diagonal
 // Powers of two that the largest values are brought to: B of a token for the state
 // and of a chunk for C . B (and S, where the products of x w and B fill it), C of a
@@ -80,15 +80,6 @@ __device__ __forceinline__ int anew(int x) {
 }
 
 template <typename Op>
-__device__ __forceinline__ float over_wave(float x, Op op) {
-  x = op(x, dpp_f32<0xB1>(x));
-  x = op(x, dpp_f32<0x4E>(x));
-  x = op(x, dpp_f32<0x141>(x));
-  x = op(x, dpp_f32<0x140>(x));
-  x = op(x, __shfl_xor(x, 16));
-  return op(x, __shfl_xor(x, 32));
-}
-template <typename Op>
 __device__ __forceinline__ float over_half(float x, Op op) {
   x = op(x, dpp_f32<0xB1>(x));
   x = op(x, dpp_f32<0x4E>(x));
@@ -113,7 +104,6 @@ __device__ __forceinline__ float over_groups(float v) {
 __device__ __forceinline__ float over_wave16(float v) {
   return __uint_as_float(max_dpp<0x140>(max_dpp<0x141>(max_dpp<0x4E>(max_dpp<0xB1>(__float_as_uint(v))))));
 }
-struct AddOp { __device__ __forceinline__ float operator()(float a, float b) const { return a + b; } };
 
 // ------------------------------------------------------------ the layout --
 // Chunk c of prompt s has slot cu[s] / 32 + s + c: no two chunks share one,
@@ -406,19 +396,22 @@ __device__ __forceinline__ void prepare_steps(const SsmScanArgs& a, const Ws& w,
   after = __shfl_down(after, 1, 32);
   if (lane == 31) after = 0.f;
   const float wt = __builtin_amdgcn_exp2f(after) * dt;
-  const float grow = over_half(fmaxf(al, 0.f), AddOp{});
   const float wmax = over_half(finite_abs(wt), MaxOp{});
-  const float dmax = over_half(finite_abs(dt), MaxOp{}) * __builtin_amdgcn_exp2f(fminf(grow, 60.f));
+  // the power of two above the largest step of this token and those before it,
+  // decayed (or grown) to this token: what the token's weights hold besides C . B
+  float most = (float)pow2_above(finite_abs(dt)) - cum;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const float x = __shfl_up(most, d, 32);
+    if (lane >= d) most = fmaxf(most, x);      // (NaN, of later tokens' sums alone, is passed over)
+  }
   float* tab = w.tab + ((int64_t)(t0 / kChunk + s + c) * a.l.H + h) * kTab;
   tab[lane] = dt;
   tab[32 + lane] = cum;
   const int kw = -pow2_above(wmax);      // the weights below 1
   tab[64 + lane] = ldexpf(wt, kw);
-  if (lane < 4)
-    tab[96 + lane] = lane == 0   ? total
-                     : lane == 1 ? __int_as_float(kw)
-                     : lane == 2 ? __int_as_float(pow2_above(dmax))
-                                 : __builtin_amdgcn_exp2f(total);
+  if (lane < 3) tab[96 + lane] = lane == 0 ? total : lane == 1 ? __int_as_float(kw) : __builtin_amdgcn_exp2f(total);
+  reinterpret_cast<int8_t*>(tab + 100)[lane] = (int8_t)fminf(fmaxf(ceilf(most + cum), -100.f), 127.f);
 }
 
 template <int N, bool CONV>
@@ -463,7 +456,7 @@ __device__ __forceinline__ void move_window(const SsmScanArgs& a, int s, int t0,
 }
 
 // The power of two on a token's weights: from those on C . B (with C's own, kc)
-// and the chunk's steps (ad), or what D leaves.
+// and its steps (ad), or what D leaves.
 __device__ __forceinline__ int weight_power(int kb, int kc, int ad, int pd_max) { return min(kb + kc - kCB + ad, pd_max); }
 
 // The operand of M^T for 16 tokens t (tile row TT): both tiles of s.  m: the power
@@ -728,14 +721,14 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
     const int* const powers = reinterpret_cast<const int*>(gts + GT - 512);
     const int kbt = __builtin_amdgcn_readfirstlane(powers[0]);
     const float* tab = reinterpret_cast<const float*>(tabs + (c & 1) * L::TABS) + hl * kTab;
-    const float alpha = tab[99];
+    const float alpha = tab[98];
     const int kw = __float_as_int(tab[97]);
     int kc[2], m[2];           // the powers on C and on the weights of tokens r and 16 + r
     if (OUT) {
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt) {
         kc[tt] = powers[32 + 16 * tt + r];
-        m[tt] = weight_power(kbt, kc[tt], -__float_as_int(tab[98]), pd_max);
+        m[tt] = weight_power(kbt, kc[tt], -reinterpret_cast<const int8_t*>(tab + 100)[16 * tt + r], pd_max);
       }
     }
     __builtin_amdgcn_sched_barrier(0);

@@ -39,8 +39,8 @@ def floors(y):
       2^-8 or more, else the power that brings that largest to 2^14 or more.  2^-25 is 2^-28 of that largest,
       or less: 2^-28 of the sum of absolute terms with each |x| at its chunk's largest.
     - A token's weights are products of C, brought to 2^13 or more by its largest, of B, by the chunk's largest, of
-      steps, by the largest that is left of any, and of 2^-20, and round twice at 2^-25: in units of these
-      three largest 2 * 2^-25 / 2^(13 + 13 - 20) / 2^-1 = 2^-29, times the sum of the chunk's |x| up to the token.
+      steps, by the largest that is left of any up to the token, and of 2^-20, and round twice at 2^-25: in units of
+      these three largest 2 * 2^-25 / 2^(13 + 13 - 20) / 2^-1 = 2^-29, times the sum of the chunk's |x| up to the token.
       Where D is larger it is brought to 2^13 or more instead, 2^-38 of it, times 32 tokens' |x|: 2^-5 of the first."""
     H, G, P, N = y.dims
     A, dt = f64(y.A), y.steps()
@@ -53,8 +53,9 @@ def floors(y):
         for c in range(0, n, 32):
             part, at = u[c:c + 32], slice(y.cu[s] + c, min(y.cu[s] + c + 32, y.cu[s + 1]))
             x, b, k = part[:, :H * P].reshape(-1, H, P), part[:, H * P:H * P + G * N].reshape(-1, G, N), part[:, H * P + G * N:].reshape(-1, G, N)
-            al = A * dt[at]
-            left = np.abs(dt[at]).max(0) * np.exp(np.maximum(al, 0).sum(0))
+            left = np.abs(dt[at])
+            for i in range(1, len(left)):
+                left[i] = np.maximum(left[i], left[i - 1] * np.exp(A * dt[y.cu[s] + c + i]))
             weights[at] = np.cumsum(x, 0) * (np.repeat(b.max((0, 2)) * k.max(2), H // G, 1) * left)[:, :, None]
             part[:, :H * P] = part[:, :H * P].max(0)
         rows.append(u)
@@ -87,14 +88,14 @@ def state_floors(y, ck):
     return np.array(final), np.array(kept)
 
 
-def check(y, ck=()):
+def check(y, ck=(), decays=0.0):
     r, want = y.run(ck), y.oracle(ck)
     T, longest = int(y.cu[-1]), max(y.lens)
     final, kept = state_floors(y, ck)
     close(r["out"][:T], want["out"], out_tol(want["out"], want["out_mass"]) + floors(y), "out")
-    close(r["final"], want["final"], state_tol(want["final_mass"], longest) + final, "final")
+    close(r["final"], want["final"], state_tol(want["final_mass"], longest) + decays * want["final_mass"] + final, "final")
     if len(ck):
-        close(r["kept"], want["kept"], state_tol(want["kept_mass"], longest) + kept, "kept")
+        close(r["kept"], want["kept"], state_tol(want["kept_mass"], longest) + decays * want["kept_mass"] + kept, "kept")
 
 
 def spread(shape, low, seed):
@@ -150,5 +151,27 @@ def test_b_and_c_of_tokens_apart(low, a_scale, what):
     f[[0, 70, 1270, 69, 1302]] = 2.0 ** low
     at = 384 if what == "C" else 256
     y.x[:, at:] = (y.x[:, at:].float() * f).bfloat16()
+    ck = [20, 70, 70 + 1024, 1303]
+    check(y, ck)
+
+
+@pytest.mark.parametrize("lens", [[32], [20, 39, 32]], ids=str)
+@pytest.mark.parametrize("D", [False, True])
+def test_growth(lens, D):
+    """States that grow by 2^100 in a chunk.  The running sums of the exponents, below 128, round at 2^-18 in each of five
+    additions, and each exponent at 2^-22 in two products: 2^-15 of a decay, ln 2 counted."""
+    y = Layer(2, 1, 64, 64, lens, seed=55, conv=False, D=D, softplus=False, dt_bias=False, x_scale=2.0 ** -8)
+    y.dt[:] = 0.75
+    y.A[:] = 2.9
+    check(y, [10, sum(lens)], decays=2.0 ** -15)
+
+
+@pytest.mark.parametrize("low", [-20, -40])
+def test_steps_apart(low):
+    """Steps of a prompt's first tokens far below those of the others: their outputs are products with them alone."""
+    y = Layer(4, 2, 64, 64, [70, 1200, 33], seed=56, conv=False, D=False, softplus=False, dt_bias=False, dt_f32=True)
+    f = spread((1303, 1), low, 5)
+    f[[0, 1, 2, 70, 71, 1270]] = 2.0 ** low
+    y.dt = y.dt * f
     ck = [20, 70, 70 + 1024, 1303]
     check(y, ck)
