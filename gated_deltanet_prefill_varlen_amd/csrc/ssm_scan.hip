@@ -66,8 +66,8 @@ __device__ __forceinline__ f32x4 mma(f16x8 a, f16x8 b, f32x4 c) { return __built
 
 __device__ __forceinline__ f16x2 pack_f16(float a, float b) { return __builtin_convertvector(f32x2{a, b}, f16x2); }
 
-// x < 2^pow2_above(x) for finite x >= 0, within -100 .. 110.
-__device__ __forceinline__ int pow2_above(float x) { return min(max((int)(__float_as_uint(x) >> 23) - 126, -100), 110); }
+// x < 2^pow2_above(x) for finite x >= 0; -100 at least.
+__device__ __forceinline__ int pow2_above(float x) { return max((int)(__float_as_uint(x) >> 23 & 0xFF) - 126, -100); }
 
 // x of another lane.
 __device__ __forceinline__ int from_lane(int x, int src) { return __builtin_amdgcn_ds_bpermute(src << 2, x); }
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
         for (int i = 0; i < 4; ++i) bound[q] = fmaxf(bound[q], finite_abs(S[nt][q][i]));
       bound[q] = over_groups(bound[q]);
       e[q] = kTopS - pow2_above(bound[q]);
-      const float f = ldexpf(1.f, e[q]);     // (e is within -80 .. 130: past 127 by parts)
+      const float f = ldexpf(1.f, e[q]);     // (e is within -98 .. 130: past 127 by parts)
       const float f0 = e[q] > 126 ? 0x1p100f : f, f1 = e[q] > 126 ? ldexpf(1.f, e[q] - 100) : 1.f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)

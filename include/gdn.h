@@ -553,7 +553,10 @@ GDN_API gdn_status gdn_attn_decode_workspace(const gdn_cache* cache, int32_t num
  *                          raw_t + dt_bias).
  *   dt_min, dt_max:        0 and infinity for no clamp.
  * A is below 0 in a trained layer; steps of A dt below -138 (2^-200) count as
- * that. */
+ * that, and growth (A above 0) over any 32 tokens must stay below 2^127.
+ * In the scan, |x| of 2^116 and more, and what is not finite in x, makes NaN of
+ * its channel's state and outputs from that token on, also where the formulas
+ * give infinities; values below 2^-100 may count as 0. */
 #define GDN_SSM_SOFTPLUS 1u
 typedef struct gdn_ssm_shape {
   int32_t num_heads;

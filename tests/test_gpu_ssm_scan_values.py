@@ -175,3 +175,26 @@ def test_steps_apart(low):
     y.dt = y.dt * f
     ck = [20, 70, 70 + 1024, 1303]
     check(y, ck)
+
+
+@pytest.mark.parametrize("power", [110, 100, -100])
+@pytest.mark.parametrize("conv", [False, True])
+@pytest.mark.parametrize("what", ["x", "B", "C"])
+def test_ends_of_the_range(power, conv, what):
+    """x, B or C of about 2^110, beside others that keep products and outputs in fp32; and of 2^-100."""
+    y = Layer(2, 1, 64, 64, [70, 33], seed=57, conv=conv, bias=False, D=False)
+    parts = dict(x=slice(0, 128), B=slice(128, 192), C=slice(192, 256))
+    f = 2.0 ** (power - 2)
+    y.x[:, parts[what]] = (y.x[:, parts[what]].float() * f).bfloat16()
+    if what == "C" and power > 0:
+        y.x[:, parts["B"]] = (y.x[:, parts["B"]].float() * 2.0 ** -20).bfloat16()
+    check(y, [20, 103])
+
+
+@pytest.mark.parametrize("power", [110, -100])
+def test_large_and_small_states(power):
+    """States that enter at 2^110 and 2^-100."""
+    y = Layer(2, 1, 64, 64, [70, 33], seed=58, conv=False, init=True, D=False)
+    y.init *= 2.0 ** power
+    y.x[:, :128] = (y.x[:, :128].float() * 2.0 ** (power if power < 0 else 0)).bfloat16()
+    check(y, [20, 103])
