@@ -690,6 +690,16 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
       }
       conv_run<CONV, kPlainX>(x, cw, xv[0][run], xv[1][run]);
     }
+    if (CONV && len - c * kChunk < kChunk) {
+      // behind the prompt's last row stands that row again, whose convolution may
+      // be what no token's is: infinite, say, which a weight of 0 would make NaN
+      const int past = len - c * kChunk - anew(4 * g);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (16 * (i / 4) + i % 4 >= past) xv[q][i / 4][i % 4] = 0.f;
+    }
     if (OUT) {
       // of each channel, over the lane groups: is any value not 0, is any as large as wanted
       x_plain = true;

@@ -198,3 +198,16 @@ def test_large_and_small_states(power):
     y.init *= 2.0 ** power
     y.x[:, :128] = (y.x[:, :128].float() * 2.0 ** (power if power < 0 else 0)).bfloat16()
     check(y, [20, 103])
+
+
+@pytest.mark.parametrize("n", [5, 31, 33, 60, 1100])
+def test_rows_that_do_not_exist(n):
+    """Inputs that cancel in every token's convolution, but would not in tokens behind the last: those play no part."""
+    y = Layer(2, 1, 64, 64, [n, 40], seed=59, bias=False, D=False)
+    sign = 1.0 - 2.0 * (torch.arange(n + 40, device=DEV)[:, None] % 2).float()
+    y.x[:, 3:100:7] = (sign * 2.0 ** 115).bfloat16()
+    y.w[3:100:7] = 1.0
+    r, want = y.run(), y.oracle()
+    # the sums are exact, so what an output holds is its own largest products
+    close(r["out"][:n + 40], want["out"], out_tol(want["out"], want["out_mass"]), "out")
+    close(r["final"], want["final"], state_tol(want["final_mass"], n), "final")
