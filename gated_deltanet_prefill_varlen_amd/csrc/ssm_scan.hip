@@ -123,14 +123,22 @@ struct Ws {
 constexpr int kSegUnit = 8;               // chunks a segment has at least
 
 // Chunks of a segment for a prompt of nc chunks whose chunk row takes hb
-// workgroups: as many segments as make 256 workgroups of the prompt alone, from
-// 1,024 tokens on.  The rule looks at one prompt, so that its bits do not depend
-// on the pack, and stands between a lone prompt and several.  With 128 and 512 in
-// 256's place, 32 heads of 128 on 128: one prompt of 8,192 tokens takes 281 and
-// 144 us for 177, four take 484 and 547 for 508; one of 2,048 takes 86 and 64 for
-// 64, sixteen take 490 and 598 for 598.
+// workgroups: as many segments as make 256 workgroups of the prompt alone, where
+// it has more than 40 chunks.  The rule looks at one prompt, so that its bits do
+// not depend on the pack, and stands between a lone prompt, which gains, and many,
+// which pay for states that they did not need early.
+// The 40: from there on a lone prompt gains more than 32 at once lose.  Uncut and
+// cut, us, of 64 heads of 64 on 128, and of 32 heads of 128 in 16 groups:
+//   tokens      768      1,024      1,280       1,536       2,048
+//   1 prompt    89 / 70  115 / 72   140 / 73    166 / 75    217 / 80
+//   32          242 / 590  313 / 589  390 / 793   458 / 886   599 / 1211
+//   1 prompt    76 / 60  99 / 63    120 / 65    140 / 67    182 / 70
+//   32          263 / 440  348 / 594  433 / 755   521 / 931   685 / 1260
+// The 256: with 128 and 512 in its place, 32 heads of 128 in 16 groups, one prompt
+// of 8,192 tokens takes 311 and 147 us for 191, four take 487 and 534 for 483; one
+// of 2,048 takes 96 and 69 for 69, sixteen take 509 and 611 for 609.
 __host__ __device__ inline int seg_chunks(int nc, int hb) {
-  if (nc <= 32) return nc > 0 ? nc : 1;
+  if (nc <= 40) return nc > 0 ? nc : 1;
   const int want = (256 + hb - 1) / hb, most = nc / kSegUnit, n = want < most ? want : most;
   return (nc + n - 1) / n;
 }

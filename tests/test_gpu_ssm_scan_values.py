@@ -108,12 +108,12 @@ def spread(shape, low, seed):
 @pytest.mark.parametrize("init", [False, True])
 def test_channels_apart(low, conv, init):
     """Channels of one head that differ by up to 2^25: each is held to its own size."""
-    y = Layer(4, 2, 64, 64, [70, 1200, 33], seed=51, conv=conv, bias=False, init=init)
+    y = Layer(4, 2, 64, 64, [70, 1400, 33], seed=51, conv=conv, bias=False, init=init)
     f = spread((4 * 64,), low, 1)
     y.x[:, :256] = (y.x[:, :256].float() * f).bfloat16()
     if init:
         y.init *= f.view(4, 64, 1)
-    ck = [20, 70, 70 + 1024, 1303]
+    ck = [20, 70, 70 + 1024, 1503]
     check(y, ck)
 
 
@@ -131,12 +131,12 @@ def test_states_apart(low):
 def test_x_of_tokens_apart(D, a_scale):
     """x of a prompt's first tokens, and of others, 2^-20 to 2^-25 of its channel's largest in a chunk; with
     decays that leave nothing of a token, the next stands alone in the state too."""
-    y = Layer(4, 2, 64, 64, [70, 1200, 33], seed=53, conv=False, D=D, a_scale=a_scale, dt_shift=4.0 if a_scale > 1 else 0.0)
-    f = spread((1303, 1), -25, 3)
-    f[[0, 70, 1270]] = 2.0 ** -25
-    f[[69, 1269, 1302]] = 2.0 ** -20
+    y = Layer(4, 2, 64, 64, [70, 1400, 33], seed=53, conv=False, D=D, a_scale=a_scale, dt_shift=4.0 if a_scale > 1 else 0.0)
+    f = spread((1503, 1), -25, 3)
+    f[[0, 70, 1470]] = 2.0 ** -25
+    f[[69, 1469, 1502]] = 2.0 ** -20
     y.x[:, :256] = (y.x[:, :256].float() * f).bfloat16()
-    ck = [20, 70, 70 + 1024, 1303]
+    ck = [20, 70, 70 + 1024, 1503]
     check(y, ck)
 
 
@@ -146,12 +146,12 @@ def test_x_of_tokens_apart(D, a_scale):
 def test_b_and_c_of_tokens_apart(low, a_scale, what):
     """Tokens whose B and C, or C alone, are far below those of others in the chunk: a prompt's first, whose
     output is nothing but their product, and, with decays that leave nothing, any."""
-    y = Layer(4, 2, 64, 64, [70, 1200, 33], seed=54, conv=False, D=False, a_scale=a_scale, dt_shift=4.0 if a_scale > 1 else 0.0)
-    f = spread((1303, 1), low, 4)
-    f[[0, 70, 1270, 69, 1302]] = 2.0 ** low
+    y = Layer(4, 2, 64, 64, [70, 1400, 33], seed=54, conv=False, D=False, a_scale=a_scale, dt_shift=4.0 if a_scale > 1 else 0.0)
+    f = spread((1503, 1), low, 4)
+    f[[0, 70, 1470, 69, 1502]] = 2.0 ** low
     at = 384 if what == "C" else 256
     y.x[:, at:] = (y.x[:, at:].float() * f).bfloat16()
-    ck = [20, 70, 70 + 1024, 1303]
+    ck = [20, 70, 70 + 1024, 1503]
     check(y, ck)
 
 
@@ -169,11 +169,11 @@ def test_growth(lens, D):
 @pytest.mark.parametrize("low", [-20, -40])
 def test_steps_apart(low):
     """Steps of a prompt's first tokens far below those of the others: their outputs are products with them alone."""
-    y = Layer(4, 2, 64, 64, [70, 1200, 33], seed=56, conv=False, D=False, softplus=False, dt_bias=False, dt_f32=True)
-    f = spread((1303, 1), low, 5)
-    f[[0, 1, 2, 70, 71, 1270]] = 2.0 ** low
+    y = Layer(4, 2, 64, 64, [70, 1400, 33], seed=56, conv=False, D=False, softplus=False, dt_bias=False, dt_f32=True)
+    f = spread((1503, 1), low, 5)
+    f[[0, 1, 2, 70, 71, 1470]] = 2.0 ** low
     y.dt = y.dt * f
-    ck = [20, 70, 70 + 1024, 1303]
+    ck = [20, 70, 70 + 1024, 1503]
     check(y, ck)
 
 
