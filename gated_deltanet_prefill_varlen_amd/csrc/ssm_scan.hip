@@ -69,6 +69,11 @@ __device__ __forceinline__ f16x2 pack_f16(float a, float b) { return __builtin_c
 // x < 2^pow2_above(x) for finite x >= 0; -100 at least.
 __device__ __forceinline__ int pow2_above(float x) { return max((int)(__float_as_uint(x) >> 23 & 0xFF) - 126, -100); }
 
+// Whether one of two values >= 0 lies below `low`, other than 0 itself.
+__device__ __forceinline__ bool small_but_not_0(const float (&x)[2], float low) {
+  return min(__float_as_uint(x[0]) - 1u, __float_as_uint(x[1]) - 1u) < __float_as_uint(low) - 1u;
+}
+
 // x of another lane.
 __device__ __forceinline__ int from_lane(int x, int src) { return __builtin_amdgcn_ds_bpermute(src << 2, x); }
 __device__ __forceinline__ float from_lane(float x, int src) { return __int_as_float(from_lane(__float_as_int(x), src)); }
@@ -669,10 +674,10 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
   const f16x8* bh = reinterpret_cast<const f16x8*>(ops + OPS - FIRST) + lane;
   const f16x8* bl = reinterpret_cast<const f16x8*>(ops + (CONV ? 2 * OPS : OPS) - FIRST) + lane;
 
-  // A chunk's x through the convolution, times 2^kPlainX; x_plain: every channel of
-  // the wave is 0, or its largest lies where that power serves it.
+  // A chunk's x through the convolution, times 2^kPlainX; x_wide: that power does
+  // not serve this lane's values.
   float xv[2][2][4];
-  bool x_plain = false;
+  bool x_wide = false;
   auto take_x = [&](int c) __attribute__((always_inline)) {
     // row 16 run + 4 g + j of the tile, from one address for j below 4 and one beyond
     ConvW cw;
@@ -709,17 +714,12 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
           if (16 * (i / 4) + i % 4 >= past) xv[q][i / 4][i % 4] = 0.f;
     }
     if (OUT) {
-      // of each channel, over the lane groups: is any value not 0, is any as large as wanted
-      x_plain = true;
+      float top[2] = {0.f, 0.f};
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        float top = 0.f;
+      for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(xv[q][i / 4][i % 4]));   // (NaN is passed over)
-        auto fold = [](uint64_t m) { m |= m >> 32; return (uint32_t)(m | m >> 16) & 0xFFFFu; };
-        const uint32_t any = fold(__ballot(top > 0.f)), large = fold(__ballot(top >= ldexpf(1.f, kPlainX - 8)));
-        x_plain = x_plain && (any & ~large) == 0 && __ballot(!(top < 32768.f)) == 0;
-      }
+        for (int i = 0; i < 8; ++i) top[q] = fmaxf(top[q], fabsf(xv[q][i / 4][i % 4]));   // (NaN is passed over)
+      x_wide = small_but_not_0(top, ldexpf(1.f, kPlainX - 8)) || fmaxf(top[0], top[1]) >= 32768.f;
     }
   };
   const int pd_max = 14 - pow2_above(fabsf(D));
@@ -761,9 +761,7 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
     bool plain = false;
     if (OUT) {
       const float top = over_wave16(fmaxf(bound[0], bound[1]));
-      const uint32_t low = __float_as_uint(top * 0x1p-12f) - 1u;       // (a bound of 0 passes)
-      plain = x_plain && (top == 0.f || (top >= 0x1p-60f && top < 0x1p60f)) &&
-              __ballot(__float_as_uint(bound[0]) - 1u < low || __float_as_uint(bound[1]) - 1u < low) == 0;
+      plain = __ballot(x_wide || small_but_not_0(bound, top * 0x1p-12f) || top >= 0x1p60f) == 0;
       float down[2];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
