@@ -26,16 +26,17 @@
 // Below them fp16's smallest step is felt.  Half of it is at most, of x, 2^-28 of its
 // channel's largest in the chunk; of x w, 2^-29 of its channel's largest with its
 // token's largest B; of B for the state, 2^-38 of its token's largest; of S, 2^-27 of
-// its bound; and of the weights M, twice, 2^-30 of the largest C of the token, B of
-// the chunk and step (as far as it is left at the token) together.  A channel's x, as an operand, and its state, as an
-// accumulator, lie in the same lanes, so a channel's scale never leaves them but for
-// the outputs.
+// its bound; and of the weights M, with the products C . B and their operands,
+// 2^-28 of the largest C of the token, B of the chunk and step (as far as it is
+// left at the token) together.  A channel's x, as an operand, and its state, as an
+// accumulator, lie in the same lanes, so a channel's scale never leaves them but
+// for the outputs.  Values below 2^-100 and decays below 2^-126 may count as 0.
 //
 // Measured: 32 x 1,024 tokens of 64 heads of 64 on 128 with the convolution (0.63
-// GB) 290 us, prepare 32 of them; 4 x 8,192 tokens of 32 heads of 128 on 128 in 16
-// groups (0.82 GB) 480 us: prepare 112, segments 150 + 20.  Bound by the vector
-// instructions of the scan, 660 a wave and chunk beside 68 products, on two waves
-// a SIMD (190 registers); a third wave's 168 would spill into the loop.
+// GB) 305 us, prepare 32 of them; 4 x 8,192 tokens of 32 heads of 128 on 128 in 16
+// groups (0.82 GB) 485 us: prepare 114, segments 128 + 19.  Bound by the vector
+// instructions of the scan, 715 a wave and chunk beside 68 products, on two waves
+// a SIMD (189 registers); a third wave's 168 would spill into the loop.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -755,7 +756,8 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_chunk_kernel(const SsmScanArgs
     // 2 (4 g + i) + q at token 16 tt + r.  One power for the wave and one for x
     // (plain) serve where they leave each channel 2^-27 of its own largest value:
     // where no channel's x, or state, lies far below the wave's.  Else each channel
-    // has its own, which the outputs' rows then take from its lanes.
+    // has its own, which the outputs' rows then take from its lanes (in every chunk:
+    // 32 x 1,024 tokens 302 -> 346 us).
     f32x4 y[2][2];
     int es[2];
     bool plain = false;

@@ -556,7 +556,15 @@ GDN_API gdn_status gdn_attn_decode_workspace(const gdn_cache* cache, int32_t num
  * that, and growth (A above 0) over any 32 tokens must stay below 2^127.
  * In the scan, |x| of 2^116 and more, and what is not finite in x, makes NaN of
  * its channel's state and outputs from that token on, also where the formulas
- * give infinities; values below 2^-100 may count as 0. */
+ * give infinities; values below 2^-100 and decays below 2^-126 may count as 0.
+ * Roundings.  The decode step is fp32 throughout.  The scan takes chunks of 32
+ * tokens.  Into states it multiplies x w (w: the steps, decayed to the chunk's end)
+ * and B as pairs of fp16, 2^-21 of each product and, in all of a chunk, 2^-23 of a
+ * channel's largest |x w B|; sums are fp32.  For outputs, x, C, the state and the
+ * weights of a token's sum over the chunk are fp16 once, 2^-11 of each, or where
+ * that is more 2^-28 of the largest |x| of the channel in the chunk, or of the
+ * largest |C| of the token times |B| and step of the chunk; sums are fp32, and out
+ * is rounded to bf16 once. */
 #define GDN_SSM_SOFTPLUS 1u
 typedef struct gdn_ssm_shape {
   int32_t num_heads;

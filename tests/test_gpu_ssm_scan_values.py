@@ -39,8 +39,10 @@ def floors(y):
       2^-8 or more, else the power that brings that largest to 2^14 or more.  2^-25 is 2^-28 of that largest,
       or less: 2^-28 of the sum of absolute terms with each |x| at its chunk's largest.
     - A token's weights are products of C, brought to 2^13 or more by its largest, of B, by the chunk's largest, of
-      steps, by the largest that is left of any up to the token, and of 2^-20, and round twice at 2^-25: in units of
-      these three largest 2 * 2^-25 / 2^(13 + 13 - 20) / 2^-1 = 2^-29, times the sum of the chunk's |x| up to the token.
+      steps, by the largest that is left of any up to the token, and of 2^-20.  The products round at 2^-25, in units of
+      the three largest 2^-25 / 2^(13 + 13 - 20) = 2^-31; the weights at twice that (a step is brought to 1/2 or
+      more); C and B at 2^-25 in each of N products with values below 2^14, N 2^-31 / 2^6, 2^-30 each for N = 128.
+      Together less than 2^-28, times the sum of the chunk's |x| up to the token.
       Where D is larger it is brought to 2^13 or more instead, 2^-38 of it, times 32 tokens' |x|: 2^-5 of the first."""
     H, G, P, N = y.dims
     A, dt = f64(y.A), y.steps()
@@ -60,7 +62,7 @@ def floors(y):
             part[:, :H * P] = part[:, :H * P].max(0)
         rows.append(u)
     D = None if y.D is None else np.abs(f64(y.D))
-    return 2.0 ** -28 * (1 + 2.0 ** -5) * O.prefill(H, G, P, N, y.cu, np.concatenate(rows), dt, A, D)["out"] + 2.0 ** -29 * weights
+    return 2.0 ** -28 * (1 + 2.0 ** -5) * O.prefill(H, G, P, N, y.cu, np.concatenate(rows), dt, A, D)["out"] + 2.0 ** -28 * weights
 
 
 def state_floors(y, ck):
