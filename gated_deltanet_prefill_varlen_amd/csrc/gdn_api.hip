@@ -753,8 +753,17 @@ gdn_status gdn_ssm_decode(const gdn_ssm_shape* shape, int32_t batch, int32_t n_t
   const int64_t T = (int64_t)batch * n_tok, H = a.l.H, dim = a.l.conv_dim, head = H * a.l.P * a.l.N * 4;
   const Span in[] = {{x, ((T - 1) * a.x_stride + dim) * 2}, {dt, ((T - 1) * a.dt_stride + H) * (a.l.dt_f32 ? 4 : 2)},
                      {A, H * 4}, {dt_bias, H * 4}, {D, H * 4}, {conv_weight, dim * 16}, {conv_bias, dim * 4}, {slot, (int64_t)batch * 4}};
-  const Span to[] = {{out, T * H * a.l.P * 2}, {state, pool_slots * head}, {conv_state, pool_slots * 6 * dim}, {snapshots, T * head}};
-  if (overlaps(to, in)) return GDN_ERR_SHAPE;
+  Span to[] = {{out, T * H * a.l.P * 2}, {snapshots, T * head}, {state, pool_slots * head}, {conv_state, pool_slots * 6 * dim}};
+  if (overlaps(to, in)) {
+    // the pools as a whole meet something: may be in slots that the call leaves alone
+    if (overlap(state, pool_slots * head, conv_state, pool_slots * 6 * dim)) return GDN_ERR_SHAPE;
+    for (int32_t b = 0; b < batch; ++b) {
+      const int64_t r = slot ? slot_host[b] : b;
+      to[2] = {state + r * head / 4, head};
+      to[3] = {conv_state ? static_cast<const char*>(conv_state) + r * 6 * dim : nullptr, 6 * dim};
+      if (overlaps(to, in)) return GDN_ERR_SHAPE;
+    }
+  }
   a.batch = batch; a.n_tok = n_tok;
   a.x = static_cast<const uint16_t*>(x); a.dt = dt; a.state = state; a.slot = slot;
   a.out = static_cast<uint16_t*>(out); a.snap = snapshots;

@@ -627,8 +627,9 @@ GDN_API gdn_status gdn_ssm_prefill_packed(
  *                bf16 [pool_slots, 3, conv_dim], which moves on by n_tok inputs.
  *   out:         device bf16 [batch * n_tok, H, P].
  *   snapshots:   device fp32 [batch, n_tok, H, P, N] or NULL.
- * What is written (state and conv_state as whole pools) must overlap neither an
- * input nor another buffer that is written.
+ * What is written (of state and conv_state the addressed slots) must overlap
+ * neither an input nor another buffer that is written; the two pools must not
+ * overlap.
  * Errors: as gdn_decode_tokens; GDN_ERR_SHAPE (also: overlaps). */
 GDN_API gdn_status gdn_ssm_decode(const gdn_ssm_shape* shape, int32_t batch, int32_t n_tok, const void* x,
                                   int64_t x_tok_stride, const float* conv_weight, const float* conv_bias,

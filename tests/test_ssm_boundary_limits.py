@@ -60,8 +60,28 @@ def test_scan_overlaps():
 
 @no_gpu
 def test_step_overlaps():
-    H, P, N, B, pool = 4, 64, 64, 2, 5
+    H, P, N, B, pool = 4, 64, 64, 2, 2
     C = H * P + 2 * 2 * N
     spans = dict(x=B * 3 * C * 2, dt=B * 3 * H * 2, A=H * 4, bias=H * 4, D=H * 4, w=C * 16, b=C * 4, slot=B * 4, state=pool * H * P * N * 4,
                  cs=pool * 3 * C * 2, out=B * 3 * H * P * 2, snap=B * 3 * H * P * N * 4)
-    check_overlaps(lambda **kw: step(n_tok=3, **kw), spans, ("out", "state", "cs", "snap"), set())
+    check_overlaps(lambda **kw: step(n_tok=3, slots=(1, 0), pool=pool, **kw), spans, ("out", "state", "cs", "snap"), set())
+    check_overlaps(lambda **kw: step(n_tok=3, slots=None, pool=pool, **{**kw, "slot": None}), {k: v for k, v in spans.items() if k != "slot"},
+                   ("out", "state", "cs", "snap"), set())
+
+
+@no_gpu
+def test_step_in_spare_slots():
+    """Slots that the call does not address are neither read nor written: they may hold its snapshots, or its rows."""
+    head, window, pool = 4 * 64 * 64 * 4, 3 * (4 * 64 + 2 * 2 * 64) * 2, 8
+    base = 1 << 43
+    for slots in ((3, 0), (0, 3), (7, 6), None):
+        kw = dict(pool=pool, slots=slots, **({"slot": None} if slots is None else {}))
+        used = set(slots or (0, 1))
+        for first in range(pool - 1):
+            spare = not used & {first, first + 1}                        # the snapshots of two sequences
+            assert step(state=base, snap=base + first * head, **kw) == (HIP if spare else SHAPE), (slots, first)
+        for first in range(pool):
+            want = SHAPE if first in used else HIP
+            assert step(state=base, out=base + first * head, **kw) == want and step(cs=base, out=base + first * window, **kw) == want, (slots, first)
+            assert step(state=base, x=base + first * head, **kw) == want, (slots, first)
+    assert step(state=base, cs=base + 7 * head, pool=pool, slots=(3, 0)) == SHAPE
