@@ -799,19 +799,12 @@ gdn_status gdn_rms_norm(const gdn_norm_shape* shape, int32_t n_rows, int32_t x_d
   const uintptr_t odd = (uintptr_t)x | (uintptr_t)gate | (uintptr_t)out, rodd = (uintptr_t)residual | (uintptr_t)residual_out;
   if (odd % xb != 0 || rodd % rb != 0 || ((uintptr_t)weight | (uintptr_t)scales) % 4 != 0) return GDN_ERR_SHAPE;
   // what is written overlaps nothing, but residual_out may be residual and out a dense x
-  struct Span { const void* p; int64_t bytes; };
   const int64_t scale_n = shape->scale_block ? d / 128 : 1;
   const Span in[] = {{x, ((rows - 1) * xs + d) * xb}, {residual, ((rows - 1) * rs + d) * rb},
                      {gate, ((rows - 1) * zs + d) * xb}, {weight, shape->weight_dim * 4}};
-  const Span to[] = {{out, rows * d * xb}, {residual_out, ((rows - 1) * rs + d) * rb}, {codes, rows * d}, {scales, rows * scale_n * 4}};
-  for (int i = 0; i < 4; ++i) {
-    for (int j = 0; j < 4; ++j) {
-      if ((i == 0 && j == 0 && out == x && xs == d) || (i == 1 && j == 1 && residual_out == residual)) continue;
-      if (overlap(to[i].p, to[i].bytes, in[j].p, in[j].bytes)) return GDN_ERR_SHAPE;
-    }
-    for (int j = 0; j < i; ++j)
-      if (overlap(to[i].p, to[i].bytes, to[j].p, to[j].bytes)) return GDN_ERR_SHAPE;
-  }
+  const Span to[] = {{out, rows * d * xb, xs == d ? 0 : -1}, {residual_out, ((rows - 1) * rs + d) * rb, 1},
+                     {codes, rows * d}, {scales, rows * scale_n * 4}};
+  if (overlaps(to, in)) return GDN_ERR_SHAPE;
   if (!fits_grid(rows, d <= 512 ? 64 : d <= 2048 ? 256 : d <= 4096 ? 512 : 1024)) return GDN_ERR_SHAPE;
   gdn::NormArgs a{};
   a.dim = (int32_t)d; a.groups = shape->groups; a.group_dim = (int32_t)gd; a.scale_block = shape->scale_block;
